@@ -1,4 +1,4 @@
-"""Build and load libmlp_chain.so (the CUDA library behind include/mlp_chain.h).
+"""Build and load libmlp_chain.so (the CUDA library behind include/mlp_chain.h and mlp_block.h).
 
 The library is compiled in-tree with nvcc for sm_103a only. Loading it never falls back to
 anything else: if the shared object is missing, ``load()`` raises.
@@ -7,7 +7,9 @@ from __future__ import annotations
 
 import ctypes
 import os
+import shutil
 import subprocess
+import tempfile
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -15,13 +17,14 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libmlp_chain.so")
-SOURCES = [os.path.join(CSRC, "mlp_chain.cu"), os.path.join(CSRC, "host_protocol.cpp")]
-DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("chain_kernel.cuh", "ptx.cuh", "protocol.h", "dep_groups.h")] + [
-    os.path.join(INCLUDE, "mlp_chain.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("mlp_chain.cu", "host_protocol.cpp", "linear.cu", "layer_norm.cu")]
+DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("chain_kernel.cuh", "ptx.cuh", "protocol.h", "dep_groups.h",
+                                                     "linear_kernel.cuh")] + [
+    os.path.join(INCLUDE, f) for f in ("mlp_chain.h", "mlp_block.h")]
 
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo",
-    "-Xcompiler", "-fPIC", "-Xcompiler", "-pthread", "-shared", "--threads", "0",
+    "-Xcompiler", "-fPIC", "-Xcompiler", "-pthread",
 ]
 
 _lock = threading.Lock()
@@ -40,11 +43,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if force or _stale():
         nvcc = os.environ.get("NVCC", "nvcc")
         tmp = LIB_PATH + f".tmp{os.getpid()}"
-        cmd = [nvcc, *NVCC_FLAGS, "-I", INCLUDE, "-o", tmp, *SOURCES]
-        if verbose:
-            print(" ".join(cmd))
-        subprocess.run(cmd, check=True)
-        os.replace(tmp, LIB_PATH)
+        work = tempfile.mkdtemp(prefix="mlp_chain_build")
+        try:   # one compiler per source, side by side
+            objs = [os.path.join(work, os.path.basename(f) + ".o") for f in SOURCES]
+            cmds = [[nvcc, *NVCC_FLAGS, "-I", INCLUDE, "-c", "-o", o, f] for f, o in zip(SOURCES, objs)]
+            link = [nvcc, *NVCC_FLAGS, "-shared", "-o", tmp, *objs]
+            if verbose:
+                print("\n".join(" ".join(c) for c in cmds + [link]))
+            procs = [subprocess.Popen(c) for c in cmds]
+            for rc, c in zip([p.wait() for p in procs], cmds):
+                if rc:
+                    raise subprocess.CalledProcessError(rc, c)
+            subprocess.run(link, check=True)
+            os.replace(tmp, LIB_PATH)
+        finally:
+            shutil.rmtree(work, ignore_errors=True)
     return LIB_PATH
 
 
@@ -82,13 +95,22 @@ class ChainInfo(ctypes.Structure):
     ]
 
 
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("K", i64), ("N", i64), ("experts", i32), ("weight_layout", i32), ("activation", ctypes.c_int),
+                ("bias_dtype", ctypes.c_int), ("dw_dtype", ctypes.c_int), ("device", i32), ("timeout_us", u32)]
+
+
+class LinearPlan(ctypes.Structure):
+    _fields_ = [("form", i32), ("cta_pair", i32), ("tile_cols", i32), ("k_split", i32), ("pipe_stages", i32)]
+
+
 class Scoreboard(ctypes.Structure):
     _fields_ = [("producers", i32), ("consumers", i32), ("groups", i32), ("edges", i32),
                 ("releases_per_producer", i32), ("pg_off", vp), ("pg_tgt", vp), ("grp_off", vp),
                 ("grp_mem", vp), ("grp_target", vp), ("cons_grp", vp)]
 
 
-# every symbol include/mlp_chain.h declares: name -> (restype, argtypes)
+# every symbol include/mlp_chain.h and include/mlp_block.h declare: name -> (restype, argtypes)
 SIGNATURES = {
     "mlp_chain_create": (ctypes.c_int, [ctypes.POINTER(ChainDesc), ctypes.POINTER(vp)]),
     "mlp_chain_workspace_size": (ctypes.c_int, [vp, ctypes.POINTER(szt)]),
@@ -107,6 +129,18 @@ SIGNATURES = {
     "mlp_protocol_model_slices": (ctypes.c_int, [i32, i32, vp, vp, i32, i32, i32, u64, i32, i32, u32, vp]),
     "mlp_chain_run_noalloc": (ctypes.c_int, [i64, i64, i64, i64, vp, vp, vp, vp, i32, vp]),
     "mlp_status_str": (ctypes.c_char_p, [ctypes.c_int]),
+    "mlp_layernorm_forward": (ctypes.c_int, [i64, i64, vp, i64, ctypes.c_int, vp, vp, ctypes.c_int, ctypes.c_float, vp,
+                                             i64, vp, vp, vp]),
+    "mlp_layernorm_backward": (ctypes.c_int, [i64, i64, vp, i64, vp, i64, ctypes.c_int, vp, ctypes.c_int, vp, vp, vp,
+                                              i64, vp, i64, vp, vp, vp, vp]),
+    "mlp_layernorm_workspace_size": (ctypes.c_int, [i64, i64, ctypes.POINTER(szt)]),
+    "mlp_linear_create": (ctypes.c_int, [ctypes.POINTER(LinearDesc), ctypes.POINTER(vp)]),
+    "mlp_linear_destroy": (ctypes.c_int, [vp]),
+    "mlp_linear_workspace_size": (ctypes.c_int, [vp, i64, ctypes.POINTER(szt)]),
+    "mlp_linear_forward": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, vp, i64, vp, vp, i64, vp, i64, vp]),
+    "mlp_linear_backward": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, vp, vp, vp]),
+    "mlp_linear_check": (ctypes.c_int, [vp, vp]),
+    "mlp_linear_get_plan": (ctypes.c_int, [vp, i64, i32, ctypes.POINTER(LinearPlan)]),
 }
 
 

@@ -1,0 +1,597 @@
+// linear.cu -- C ABI of mlp_linear (include/mlp_block.h): handle, choice of the kernel variant, tensor
+// maps, launches, and the elementwise part of the backward pass.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+#include <new>
+
+#include "../../include/mlp_block.h"
+#include "linear_kernel.cuh"
+
+using namespace mlpl;
+
+namespace {
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                             const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder()
+{
+    static const EncodeFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// View (inner, outer, group) of bf16 rows of `inner` elements, `ld` apart, `outer` per group.
+bool encode(CUtensorMap *map, const void *ptr, int64_t inner, int64_t outer, int64_t groups, int64_t ld, int box_outer)
+{
+    EncodeFn fn = encoder();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer), static_cast<cuuint64_t>(groups)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * 2 * static_cast<cuuint64_t>(outer)};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_outer), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr size_t kSmemLimit = 227 * 1024;
+
+struct Plan {
+    int form, pair, bn, split, pipe;
+    uint32_t slot;
+};
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+struct mlp_linear {
+    mlp_linear_desc d;
+    int groups;
+    int num_sms;
+    int max_clusters[9];   // co-resident clusters of 1, 2, 4, 8 CTAs
+    uint32_t *status;
+};
+
+namespace {
+
+void finish_plan(const mlp_linear *h, Plan &pl)
+{
+    pl.slot = kPBytes + static_cast<uint32_t>(pl.bn / pl.pair) * kKB * 2;
+    const size_t fixed = linear_smem_bytes(0, pl.slot, h->groups);
+    pl.pipe = static_cast<int>(std::min<size_t>(kMaxRing, (kSmemLimit - fixed) / pl.slot));
+}
+
+// rows: of the whole call; out_cols, red: output columns and reduction extent of a rows product.
+Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red)
+{
+    const int64_t avg = cdiv(rows, h->groups);
+    const int64_t kb = cdiv(red, kKB);
+    Plan pl{kRows, 1, 256, 1, 0, 0};
+    if (avg <= 64) {
+        pl.form = kRowsT;
+        pl.bn = avg <= 32 ? 32 : 64;
+        const int64_t items = std::min<int64_t>(h->groups, rows) * cdiv(out_cols, kPRows);
+        while (pl.split < (pl.bn == 32 ? 4 : 8) && items * pl.split * 2 <= h->num_sms && kb >= 4 * pl.split * 2)
+            pl.split *= 2;
+    } else {
+        // time of the variants in units of one 128 x 256 x 64 step of an SM
+        double best = 1e300;
+        for (int v = 0; v < 3; ++v) {
+            const int pair = v == 0 ? 2 : 1, bn = v == 2 ? 128 : 256;
+            const double step = v == 0 ? 1.0 : v == 1 ? 1.1 : 0.65;
+            const int64_t items = h->groups * cdiv(avg, kPRows * pair) * cdiv(out_cols, bn);
+            for (int s = 1; s <= (pair == 2 ? 1 : 4); s *= 2) {
+                const int64_t at_once = h->max_clusters[pair * s];
+                const double t = static_cast<double>(cdiv(items, at_once)) * (step * static_cast<double>(cdiv(kb, s)) + (s > 1 ? 10.0 : 2.0)) + 4.0;
+                if (t < best) {
+                    best = t;
+                    pl.pair = pair;
+                    pl.bn = bn;
+                    pl.split = s;
+                }
+            }
+        }
+    }
+    finish_plan(h, pl);
+    return pl;
+}
+
+Plan plan_reduce(const mlp_linear *h, int64_t p_ext, int64_t q_ext)
+{
+    Plan pl{kReduce, 2, 256, 1, 0, 0};
+    if (h->groups * cdiv(p_ext, 256) * cdiv(q_ext, 256) * 2 < h->num_sms)
+        pl = Plan{kReduce, 1, 128, 1, 0, 0};
+    finish_plan(h, pl);
+    return pl;
+}
+
+template <int kForm, int kPair>
+bool launch_one(const LinearParams &p, int clusters, int cs, size_t smem, cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * cs), 1, 1);
+    cfg.blockDim = dim3(kLThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = cs > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, linear_kernel<kForm, kPair>, p) == cudaSuccess;
+}
+
+// items: an upper bound on the items of this launch (the counts of groups are on the device).
+mlp_status launch(const mlp_linear *h, LinearParams &p, const Plan &pl, int64_t items, cudaStream_t st)
+{
+    p.groups = h->groups;
+    p.bn = pl.bn;
+    p.split = pl.split;
+    p.raster = 16 / pl.pair;
+    p.num_pipe = pl.pipe;
+    p.slot_bytes = pl.slot;
+    // two accumulators; a split tile's parts may be narrower than the 32 columns read at a time
+    const uint32_t cols = 2u * static_cast<uint32_t>(pl.bn) + (pl.bn / pl.split < 32 ? 32u : 0u);
+    p.tmem_cols = 32;
+    while (p.tmem_cols < cols)
+        p.tmem_cols *= 2;
+    p.status = h->status;
+    p.timeout_ns = static_cast<uint64_t>(h->d.timeout_us ? h->d.timeout_us : 2000000u) * 1000ull;
+    const int cs = pl.pair * pl.split;
+    const int clusters = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(items, h->max_clusters[cs])));
+    const size_t smem = linear_smem_bytes(pl.pipe, pl.slot, h->groups);
+    bool ok = false;
+    if (pl.form == kRows)
+        ok = pl.pair == 2 ? launch_one<kRows, 2>(p, clusters, cs, smem, st) : launch_one<kRows, 1>(p, clusters, cs, smem, st);
+    else if (pl.form == kRowsT)
+        ok = launch_one<kRowsT, 1>(p, clusters, cs, smem, st);
+    else
+        ok = pl.pair == 2 ? launch_one<kReduce, 2>(p, clusters, cs, smem, st) : launch_one<kReduce, 1>(p, clusters, cs, smem, st);
+    return ok ? MLP_OK : MLP_ERR_CUDA;
+}
+
+// out[rows, out_cols] = A[rows, red] * B, B stored out_cols-major (b_mn: red x out_cols) or red-major.
+mlp_status rows_product(const mlp_linear *h, LinearParams &p, int64_t rows, const void *A, int64_t lda, const void *B,
+                        int64_t out_cols, int64_t red, bool b_mn, cudaStream_t st)
+{
+    const Plan pl = plan_rows(h, rows, out_cols, red);
+    p.rows = static_cast<int32_t>(rows);
+    p.k_ext = static_cast<int32_t>(red);
+    CUtensorMap *mapA = pl.form == kRows ? &p.mapP : &p.mapQ, *mapB = pl.form == kRows ? &p.mapQ : &p.mapP;
+    const int b_rows = pl.form == kRows ? pl.bn / pl.pair : kPRows;
+    if (!encode(mapA, A, red, rows, 1, lda, pl.form == kRows ? kPRows : pl.bn))
+        return MLP_ERR_CUDA;
+    if (!(b_mn ? encode(mapB, B, out_cols, red, h->groups, out_cols, kKB) : encode(mapB, B, red, out_cols, h->groups, red, b_rows)))
+        return MLP_ERR_CUDA;
+    int64_t items;
+    if (pl.form == kRows) {
+        p.p_mn = 0;
+        p.q_mn = b_mn;
+        p.q_ext = static_cast<int32_t>(out_cols);
+        items = (cdiv(rows, kPRows * pl.pair) + h->groups - 1) * cdiv(out_cols, pl.bn);
+    } else {
+        p.p_mn = b_mn;
+        p.q_mn = 0;
+        p.p_ext = static_cast<int32_t>(out_cols);
+        items = (cdiv(rows, pl.bn) + h->groups - 1) * cdiv(out_cols, kPRows);
+    }
+    return launch(h, p, pl, items, st);
+}
+
+// ------------------------------------------------------- dZ = dY act'(Z) and the bias gradient --
+// With e = e^-t and s = sigmoid(t) = 1 / (1 + e): 1 - s = e s, without cancellation.
+//   silu'(z) = s + z s (1 - s), t = z;   gelu'(z) = s + z s (1 - s) t', t = 2u.
+// Where |t| is past 60 the second term is below any value that counts and e may overflow: dropped.
+template <int kAct>
+__device__ __forceinline__ float act_grad(float dy, float z)
+{
+    if (kAct == kActRelu)
+        return z <= 0.0f ? 0.0f : dy;
+    if (kAct == kActSilu) {
+        const float e = __expf(-z), s = __fdividef(1.0f, 1.0f + e);
+        return dy * (s + (fabsf(z) > 60.0f ? 0.0f : z * s * (e * s)));
+    }
+    if (kAct == kActGelu) {
+        const float z2 = z * z;
+        const float t = z * fmaf(2.0f * kGeluC * kGeluA, z2, 2.0f * kGeluC);
+        const float e = __expf(-t), s = __fdividef(1.0f, 1.0f + e);
+        const float dt = fmaf(6.0f * kGeluC * kGeluA, z2, 2.0f * kGeluC);
+        return dy * (s + (fabsf(t) > 60.0f ? 0.0f : z * s * (e * s) * dt));
+    }
+    return dy;
+}
+
+constexpr int kStrip = 256;    // columns per CTA: 32 lanes x 8
+
+struct GradParams {
+    const __nv_bfloat16 *dy, *z;
+    __nv_bfloat16 *dz;          // rows x N contiguous, or null
+    int64_t ld_dy, ld_z;
+    int32_t rows, N, groups, block_rows, blocks;
+    const int32_t *offsets;
+    float *part;                // (blocks + groups) x N column sums, or null
+    void *dbias;
+    int32_t bias_f32;
+};
+
+__device__ __forceinline__ void group_range(const GradParams &p, int32_t e, int32_t &lo, int32_t &hi)
+{
+    lo = p.offsets ? min(max(p.offsets[e], 0), p.rows) : 0;
+    hi = p.offsets ? min(max(p.offsets[e + 1], lo), p.rows) : p.rows;
+}
+
+// One CTA: a block of rows x 256 columns.  Memory-bound: reads dY and Z once, writes dZ once; the column
+// sums stay in registers and leave as one fp32 row per (block, group) pair.  Blocks and groups are both
+// ascending ranges, so block + group numbers those pairs without collisions.
+template <int kAct>
+__global__ void __launch_bounds__(256) act_grad_kernel(const GradParams p)
+{
+    __shared__ float red[8][kStrip];
+    const int32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int32_t col = blockIdx.x * kStrip + lane * 8;
+    const bool col_ok = col < p.N;
+    const int32_t b_lo = blockIdx.y * p.block_rows, b_hi = min(b_lo + p.block_rows, p.rows);
+    int32_t e = 0;
+    if (p.offsets) {   // first group that ends past the block's start
+        int32_t lo = 0, hi = p.groups;
+        while (lo < hi) {
+            const int32_t mid = (lo + hi) / 2;
+            if (p.offsets[mid + 1] > b_lo)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        e = lo;
+    }
+    for (; e < p.groups; ++e) {
+        int32_t g_lo, g_hi;
+        group_range(p, e, g_lo, g_hi);
+        if (g_lo >= b_hi)
+            break;
+        const int32_t lo = max(g_lo, b_lo), hi = min(g_hi, b_hi);
+        if (lo >= hi)
+            continue;
+        float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (col_ok) {
+#pragma unroll 4
+            for (int32_t r = lo + warp; r < hi; r += 8) {
+                const uint4 dyv = *reinterpret_cast<const uint4 *>(p.dy + r * p.ld_dy + col);
+                uint4 zv = make_uint4(0u, 0u, 0u, 0u);
+                if (kAct != kActNone)
+                    zv = *reinterpret_cast<const uint4 *>(p.z + r * p.ld_z + col);
+                const uint32_t dw[4] = {dyv.x, dyv.y, dyv.z, dyv.w}, zw[4] = {zv.x, zv.y, zv.z, zv.w};
+                uint32_t ow[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 a = unpack2(dw[j]), b = unpack2(zw[j]);
+                    const float g0 = act_grad<kAct>(a.x, b.x), g1 = act_grad<kAct>(a.y, b.y);
+                    acc[2 * j] += g0;
+                    acc[2 * j + 1] += g1;
+                    ow[j] = pack2(g0, g1);
+                }
+                if (kAct != kActNone && p.dz)
+                    *reinterpret_cast<uint4 *>(p.dz + static_cast<int64_t>(r) * p.N + col) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+            }
+        }
+        if (p.part) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                red[warp][lane * 8 + j] = acc[j];
+            __syncthreads();
+            const int32_t c = blockIdx.x * kStrip + threadIdx.x;
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+                s += red[w][threadIdx.x];
+            if (c < p.N)
+                p.part[static_cast<int64_t>(blockIdx.y + e) * p.N + c] = s;
+        }
+    }
+}
+
+// dbias[e, :]: the partial rows of the blocks that hold rows of group e, in block order.
+__global__ void __launch_bounds__(256) bias_grad_kernel(const GradParams p)
+{
+    const int32_t c = blockIdx.x * 256 + threadIdx.x, e = blockIdx.y;
+    if (c >= p.N)
+        return;
+    int32_t lo, hi;
+    group_range(p, e, lo, hi);
+    float s = 0.0f;
+    if (hi > lo) {
+        const int32_t b1 = (hi - 1) / p.block_rows;
+#pragma unroll 8
+        for (int32_t b = lo / p.block_rows; b <= b1; ++b)
+            s += p.part[static_cast<int64_t>(b + e) * p.N + c];
+    }
+    const int64_t o = static_cast<int64_t>(e) * p.N + c;
+    if (p.bias_f32)
+        static_cast<float *>(p.dbias)[o] = s;
+    else
+        static_cast<__nv_bfloat16 *>(p.dbias)[o] = __float2bfloat16_rn(s);
+}
+
+// Rows per block: about four CTAs per SM, at least 16 rows (two per warp).
+int32_t grad_block_rows(const mlp_linear *h, int64_t rows)
+{
+    const int64_t strips = cdiv(h->d.N, kStrip);
+    const int64_t blocks = std::max<int64_t>(1, cdiv(4 * h->num_sms, strips));
+    return static_cast<int32_t>(std::max<int64_t>(16, cdiv(cdiv(rows, blocks), 8) * 8));
+}
+
+size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+bool misaligned(const void *p, uintptr_t a = 16) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+bool bad_matrix(const void *p, int64_t ld, int64_t cols) { return !p || misaligned(p) || ld < cols || ld % 8 != 0; }
+
+bool bad_call(const mlp_linear *h, int64_t rows, const int32_t *offsets)
+{
+    return rows < 0 || rows > (int64_t{1} << 31) - 1024 || (h->d.experts > 0) != (offsets != nullptr) ||
+           (offsets && misaligned(offsets, 4));
+}
+
+}  // namespace
+
+extern "C" mlp_status mlp_linear_create(const mlp_linear_desc *d, mlp_linear_t *out)
+{
+    if (!d || !out)
+        return MLP_ERR_INVALID_ARG;
+    *out = nullptr;
+    const int64_t lim = (int64_t{1} << 31) - 1024;
+    if (d->K < 8 || d->N < 8 || d->K % 8 || d->N % 8 || d->K > lim || d->N > lim || d->experts < 0 ||
+        d->experts > MLP_MAX_EXPERTS || d->weight_layout < 0 || d->weight_layout > 1 || d->device < 0)
+        return MLP_ERR_INVALID_ARG;
+    if (d->activation < MLP_ACT_NONE || d->activation > MLP_ACT_SILU ||
+        (d->bias_dtype != MLP_DT_BF16 && d->bias_dtype != MLP_DT_F32) ||
+        (d->dw_dtype != MLP_DT_BF16 && d->dw_dtype != MLP_DT_F32))
+        return MLP_ERR_UNSUPPORTED;
+    if (cudaSetDevice(d->device) != cudaSuccess)
+        return MLP_ERR_CUDA;
+    mlp_linear *h = new (std::nothrow) mlp_linear();
+    if (!h)
+        return MLP_ERR_OOM;
+    h->d = *d;
+    h->groups = d->experts ? d->experts : 1;
+    h->status = nullptr;
+    mlp_status st = MLP_OK;
+    if (cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, d->device) != cudaSuccess ||
+        cudaFuncSetAttribute(linear_kernel<kRows, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
+        cudaFuncSetAttribute(linear_kernel<kRows, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
+        cudaFuncSetAttribute(linear_kernel<kRowsT, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
+        cudaFuncSetAttribute(linear_kernel<kReduce, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
+        cudaFuncSetAttribute(linear_kernel<kReduce, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) {
+        st = MLP_ERR_CUDA;
+    }
+    for (int cs = 1; cs <= 8 && st == MLP_OK; cs *= 2) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(cs), 1, 1);
+        cfg.blockDim = dim3(kLThreads, 1, 1);
+        cfg.dynamicSmemBytes = kSmemLimit;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<kRows, 1>, &cfg) != cudaSuccess || n < 1)
+            st = MLP_ERR_CUDA;
+        h->max_clusters[cs] = n;
+    }
+    if (st == MLP_OK && cudaMalloc(&h->status, 256) != cudaSuccess) {
+        h->status = nullptr;
+        st = MLP_ERR_OOM;
+    }
+    if (st == MLP_OK && cudaMemset(h->status, 0, 256) != cudaSuccess)
+        st = MLP_ERR_CUDA;
+    if (st != MLP_OK) {
+        cudaGetLastError();
+        if (h->status)
+            cudaFree(h->status);
+        delete h;
+        return st;
+    }
+    *out = h;
+    return MLP_OK;
+}
+
+extern "C" mlp_status mlp_linear_destroy(mlp_linear_t h)
+{
+    if (!h)
+        return MLP_ERR_INVALID_ARG;
+    cudaSetDevice(h->d.device);
+    cudaFree(h->status);
+    delete h;
+    return MLP_OK;
+}
+
+// dZ, then the partial column sums.
+static void workspace_layout(const mlp_linear *h, int64_t rows, size_t *part, size_t *total)
+{
+    const size_t dz = h->d.activation == MLP_ACT_NONE ? 0 : align256(static_cast<size_t>(rows) * h->d.N * 2);
+    const int64_t blocks = cdiv(rows, grad_block_rows(h, rows));
+    *part = dz;
+    *total = dz + align256(static_cast<size_t>(blocks + h->groups) * h->d.N * 4);
+}
+
+extern "C" mlp_status mlp_linear_workspace_size(mlp_linear_t h, int64_t rows, size_t *bytes)
+{
+    if (!h || !bytes || rows < 0)
+        return MLP_ERR_INVALID_ARG;
+    size_t part;
+    workspace_layout(h, rows, &part, bytes);
+    return MLP_OK;
+}
+
+extern "C" mlp_status mlp_linear_forward(mlp_linear_t h, int64_t rows, const void *X, int64_t ldx, const void *W,
+                                         const void *bias, const void *residual, int64_t ldr, const int32_t *offsets,
+                                         void *Z, int64_t ldz, void *Y, int64_t ldy, void *stream)
+{
+    if (!h || bad_call(h, rows, offsets))
+        return MLP_ERR_INVALID_ARG;
+    const int64_t K = h->d.K, N = h->d.N;
+    if (rows == 0)
+        return MLP_OK;
+    if (bad_matrix(X, ldx, K) || bad_matrix(Y, ldy, N) || !W || misaligned(W) || (residual && bad_matrix(residual, ldr, N)) ||
+        (Z && bad_matrix(Z, ldz, N)) || (bias && misaligned(bias, h->d.bias_dtype == MLP_DT_F32 ? 4 : 2)))
+        return MLP_ERR_INVALID_ARG;
+    if (cudaSetDevice(h->d.device) != cudaSuccess)
+        return MLP_ERR_CUDA;
+    LinearParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.offsets = offsets;
+    p.act = h->d.activation;
+    p.bias = bias;
+    p.bias_f32 = h->d.bias_dtype == MLP_DT_F32;
+    p.res = static_cast<const __nv_bfloat16 *>(residual);
+    p.ld_res = ldr;
+    p.z = static_cast<__nv_bfloat16 *>(Z);
+    p.ld_z = ldz;
+    p.out = Y;
+    p.ld_out = ldy;
+    return rows_product(h, p, rows, X, ldx, W, N, K, h->d.weight_layout == 0, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const void *dY, int64_t lddy, const void *X,
+                                          int64_t ldx, const void *W, const void *Z, int64_t ldz, const int32_t *offsets,
+                                          void *dX, int64_t lddx, void *dW, void *dbias, void *workspace, void *stream)
+{
+    if (!h || bad_call(h, rows, offsets))
+        return MLP_ERR_INVALID_ARG;
+    const int64_t K = h->d.K, N = h->d.N;
+    const bool act = h->d.activation != MLP_ACT_NONE;
+    const size_t bias_esz = h->d.bias_dtype == MLP_DT_F32 ? 4 : 2, dw_esz = h->d.dw_dtype == MLP_DT_F32 ? 4 : 2;
+    if ((dW && misaligned(dW)) || (dbias && misaligned(dbias, bias_esz)))
+        return MLP_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {
+        if (cudaSetDevice(h->d.device) != cudaSuccess ||
+            (dW && cudaMemsetAsync(dW, 0, static_cast<size_t>(h->groups) * K * N * dw_esz, st) != cudaSuccess) ||
+            (dbias && cudaMemsetAsync(dbias, 0, static_cast<size_t>(h->groups) * N * bias_esz, st) != cudaSuccess))
+            return MLP_ERR_CUDA;
+        return MLP_OK;
+    }
+    if (bad_matrix(dY, lddy, N) || (act && bad_matrix(Z, ldz, N)) || (dW && bad_matrix(X, ldx, K)) ||
+        (dX && (bad_matrix(dX, lddx, K) || !W || misaligned(W))) ||
+        (((act && (dX || dW)) || dbias) && (!workspace || misaligned(workspace, 256))))
+        return MLP_ERR_INVALID_ARG;
+    if (cudaSetDevice(h->d.device) != cudaSuccess)
+        return MLP_ERR_CUDA;
+    const void *dz = dY;
+    int64_t ld_dz = lddy;
+    if ((act && (dX || dW)) || dbias) {
+        size_t part, total;
+        workspace_layout(h, rows, &part, &total);
+        GradParams g;
+        std::memset(&g, 0, sizeof(g));
+        g.dy = static_cast<const __nv_bfloat16 *>(dY);
+        g.ld_dy = lddy;
+        g.z = static_cast<const __nv_bfloat16 *>(Z);
+        g.ld_z = ldz;
+        if (act && (dX || dW)) {
+            g.dz = static_cast<__nv_bfloat16 *>(workspace);
+            dz = workspace;
+            ld_dz = N;
+        }
+        g.rows = static_cast<int32_t>(rows);
+        g.N = static_cast<int32_t>(N);
+        g.groups = h->groups;
+        g.block_rows = grad_block_rows(h, rows);
+        g.blocks = static_cast<int32_t>(cdiv(rows, g.block_rows));
+        g.offsets = offsets;
+        g.part = dbias ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part) : nullptr;
+        g.dbias = dbias;
+        g.bias_f32 = bias_esz == 4;
+        const dim3 grid(static_cast<unsigned>(cdiv(N, kStrip)), static_cast<unsigned>(g.blocks));
+        switch (h->d.activation) {
+        case MLP_ACT_RELU: act_grad_kernel<kActRelu><<<grid, 256, 0, st>>>(g); break;
+        case MLP_ACT_GELU_TANH: act_grad_kernel<kActGelu><<<grid, 256, 0, st>>>(g); break;
+        case MLP_ACT_SILU: act_grad_kernel<kActSilu><<<grid, 256, 0, st>>>(g); break;
+        default: act_grad_kernel<kActNone><<<grid, 256, 0, st>>>(g); break;
+        }
+        if (cudaGetLastError() != cudaSuccess)
+            return MLP_ERR_CUDA;
+        if (dbias) {
+            bias_grad_kernel<<<dim3(static_cast<unsigned>(cdiv(N, 256)), static_cast<unsigned>(h->groups)), 256, 0, st>>>(g);
+            if (cudaGetLastError() != cudaSuccess)
+                return MLP_ERR_CUDA;
+        }
+    }
+    if (dX) {
+        LinearParams p;
+        std::memset(&p, 0, sizeof(p));
+        p.offsets = offsets;
+        p.out = dX;
+        p.ld_out = lddx;
+        // dX[m, k] = sum_n dZ[m, n] W(k, n): W stored K x N has the reduction inside
+        const mlp_status r = rows_product(h, p, rows, dz, ld_dz, W, K, N, h->d.weight_layout == 1, st);
+        if (r != MLP_OK)
+            return r;
+    }
+    if (dW) {
+        const bool kn = h->d.weight_layout == 0;
+        const int64_t pe = kn ? K : N, qe = kn ? N : K;
+        const Plan pl = plan_reduce(h, pe, qe);
+        LinearParams p;
+        std::memset(&p, 0, sizeof(p));
+        p.offsets = offsets;
+        p.rows = static_cast<int32_t>(rows);
+        p.p_ext = static_cast<int32_t>(pe);
+        p.q_ext = static_cast<int32_t>(qe);
+        p.p_mn = p.q_mn = 1;
+        p.out = dW;
+        p.out_f32 = dw_esz == 4;
+        p.ld_out = qe;
+        if (!encode(&p.mapP, kn ? X : dz, pe, rows, 1, kn ? ldx : ld_dz, kKB) ||
+            !encode(&p.mapQ, kn ? dz : X, qe, rows, 1, kn ? ld_dz : ldx, kKB))
+            return MLP_ERR_CUDA;
+        return launch(h, p, pl, h->groups * cdiv(pe, kPRows * pl.pair) * cdiv(qe, pl.bn), st);
+    }
+    return MLP_OK;
+}
+
+extern "C" mlp_status mlp_linear_check(mlp_linear_t h, void *stream)
+{
+    if (!h)
+        return MLP_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint32_t v = 0;
+    if (cudaSetDevice(h->d.device) != cudaSuccess ||
+        cudaMemcpyAsync(&v, h->status, 4, cudaMemcpyDeviceToHost, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
+        return MLP_ERR_CUDA;
+    if (v && (cudaMemsetAsync(h->status, 0, 4, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess))
+        return MLP_ERR_CUDA;
+    return static_cast<mlp_status>(v);
+}
+
+extern "C" mlp_status mlp_linear_get_plan(mlp_linear_t h, int64_t rows, int32_t pass, mlp_linear_plan *plan)
+{
+    if (!h || !plan || rows < 1 || pass < 0 || pass > 2)
+        return MLP_ERR_INVALID_ARG;
+    const bool kn = h->d.weight_layout == 0;
+    const Plan pl = pass == 0   ? plan_rows(h, rows, h->d.N, h->d.K)
+                    : pass == 1 ? plan_rows(h, rows, h->d.K, h->d.N)
+                                : plan_reduce(h, kn ? h->d.K : h->d.N, kn ? h->d.N : h->d.K);
+    plan->form = pl.form;
+    plan->cta_pair = pl.pair;
+    plan->tile_cols = pl.bn;
+    plan->k_split = pl.split;
+    plan->pipe_stages = pl.pipe;
+    return MLP_OK;
+}

@@ -1,0 +1,894 @@
+// linear_kernel.cuh -- the persistent, warp-specialised tcgen05 kernel behind mlp_linear: products of
+// bf16 matrices with fp32 accumulators in TMEM, in three forms that differ in which dimension is
+// ragged (the row ranges [start_e, start_e + cnt_e) of the groups; a dense product is one group):
+//
+//   kRows    D[rows of e, n] = sum_k A[row, k] B_e[k, n]      forward, and the input's gradient
+//            (MMA rows = activation rows, MMA columns = weight columns)
+//   kRowsT   the same product with the operands exchanged: MMA rows = weight columns, MMA columns =
+//            activation rows.  An MMA always works on 128 rows; with few activation rows they are the
+//            narrow operand here, so a tile reads 128 weight columns and 32 to 128 activation rows
+//            per k block instead of 128 mostly empty activation rows.
+//   kReduce  D_e[i, j] = sum_{rows of e} A[row, i] B[row, j]  the weights' gradient
+//
+// In MMA terms every form is D[p, q] = sum_k P[p, k] Q[q, k] with operands that are K-major or
+// MN-major in memory (the descriptors' and the TMA boxes' business only).
+//
+// Roles (256 threads): warp 0 TMA producer, warp 1 MMA issuer and TMEM owner, warp 2 group tables
+// and the masking of ragged reduction tails, warps 4-7 epilogue (one TMEM lane quarter each).  The
+// accumulator is double buffered, so a tile's epilogue runs under the next tile's MMAs.  Tiles are
+// dealt out statically, in an order that lets the CTAs running at one time share operand panels in L2.
+//
+// kPair = 2 runs 256-row tiles on CTA pairs (cta_group::2): each CTA loads its 128 rows of P and half
+// of Q's tile, a third less to fetch per SM and flop.  split > 1 shares one tile's reduction among the
+// CTAs of a cluster: partial sums travel through distributed shared memory into the ring, which is
+// idle by then, and are added in slice order, so the result does not depend on timing.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "ptx.cuh"
+
+namespace mlpl {
+
+using namespace mlpc;
+
+enum Form { kRows = 0, kRowsT = 1, kReduce = 2 };
+enum Act { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3 };
+
+constexpr int kLThreads = 256;
+constexpr int kPRows = 128;                    // rows of P per CTA (= TMEM lanes)
+constexpr int kKB = 64;                        // reduction depth of one ring slot: 128 bytes of bf16
+constexpr uint32_t kPBytes = kPRows * kKB * 2;
+constexpr uint32_t kBoxBytes = kKB * 128;      // one MN-major box: 64 k rows of 64 columns
+constexpr int kMaxRing = 10;
+constexpr uint32_t kStageWarpBytes = 32 * 128; // epilogue staging: 32 rows x 128 bytes per warp
+constexpr uint32_t kStTimeout = 5, kStBadOffsets = 1;
+
+struct LinearParams {
+    CUtensorMap mapP, mapQ;         // (inner, outer, group) views
+    const int32_t *offsets;         // device, groups + 1 entries, or null: one group of `rows` rows
+    int32_t groups, rows;
+    int32_t p_ext, q_ext, k_ext;    // extents of the dimensions that are not ragged
+    int32_t p_mn, q_mn;             // operand stored MN-major (else K-major)
+    int32_t bn;                     // columns of a tile (the pair's)
+    int32_t split;                  // CTAs (kPair = 1) sharing a tile's reduction
+    int32_t raster;                 // row panels sharing a sweep over the column tiles
+    int32_t num_pipe;
+    uint32_t slot_bytes;
+    uint32_t tmem_cols;
+    int32_t act;
+    int32_t bias_f32, out_f32;
+    const void *bias;               // groups x (output columns), or null
+    const __nv_bfloat16 *res;       // or null
+    __nv_bfloat16 *z;               // pre-activation output, or null
+    void *out;
+    int64_t ld_out, ld_res, ld_z;   // row strides in elements
+    uint32_t *status;
+    uint64_t timeout_ns;
+};
+
+struct __align__(8) LCtrl {
+    uint64_t full[kMaxRing], empty[kMaxRing], go[kMaxRing], tail[kMaxRing];
+    uint64_t tfull[2], tempty[2];
+    uint64_t drain, rdy, got, ringfree;
+    uint32_t tmem_base;
+    volatile int32_t abort_flag;
+    int32_t skip;
+    int32_t n_items;
+};
+
+// Shared memory: ring (1024-byte aligned), epilogue staging, bias tile per epilogue warp, control
+// block, group tables.
+__host__ __device__ inline uint32_t ls_stage(int num_pipe, uint32_t slot) { return static_cast<uint32_t>(num_pipe) * slot; }
+__host__ __device__ inline uint32_t ls_bias(int num_pipe, uint32_t slot) { return ls_stage(num_pipe, slot) + 4u * kStageWarpBytes; }
+__host__ __device__ inline uint32_t ls_ctrl(int num_pipe, uint32_t slot) { return ls_bias(num_pipe, slot) + 4u * 256u * 4u; }
+__host__ __device__ inline uint32_t ls_tab(int num_pipe, uint32_t slot)
+{
+    return ls_ctrl(num_pipe, slot) + static_cast<uint32_t>((sizeof(LCtrl) + 15) / 16 * 16);
+}
+__host__ inline size_t linear_smem_bytes(int num_pipe, uint32_t slot, int groups)
+{
+    return 1024 + ls_tab(num_pipe, slot) + (3 * static_cast<size_t>(groups) + 1) * 4;
+}
+
+__device__ __forceinline__ uint64_t policy_evict_normal()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+// Each thread of the warp reads 8 consecutive 32-bit columns of its own TMEM lane.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// Order this thread's generic-proxy accesses of its CTA's shared memory with later async-proxy ones
+// (TMA copies, MMA operand reads).
+__device__ __forceinline__ void fence_proxy_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ------------------------------------------------------------------------------ bounded waits --
+// On expiry: first error wins in the status word, the CTA's abort flag stops the other roles.  Drain
+// waits (own copies and MMAs in flight after an abort) ignore the flag and use a short limit.
+__device__ __forceinline__ bool lwait(uint64_t *bar, uint32_t parity, LCtrl *c, const LinearParams &p,
+                                      bool cluster = false, bool draining = false)
+{
+    auto probe = [&]() { return cluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+    if (probe())
+        return true;
+    const uint64_t t0 = globaltimer_ns();
+    const uint64_t limit = draining ? 200000000ull : p.timeout_ns;
+    while (true) {
+        if (probe())
+            return true;
+        if (!draining && c->abort_flag)
+            return false;
+        if (globaltimer_ns() - t0 > limit) {
+            atomicCAS(p.status, 0u, kStTimeout);
+            c->abort_flag = 1;
+            return false;
+        }
+    }
+}
+
+// Lane 0 waits, then every lane acquires the completed phase itself.
+__device__ __forceinline__ bool lwait_warp(uint64_t *bar, uint32_t parity, LCtrl *c, const LinearParams &p,
+                                           bool cluster = false)
+{
+    uint32_t ok = 0;
+    if ((threadIdx.x & 31) == 0)
+        ok = lwait(bar, parity, c, p, cluster) ? 1u : 0u;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (!ok)
+        return false;
+    if (cluster)
+        mbar_try_wait_cluster(bar, parity);
+    else
+        mbar_try_wait(bar, parity);
+    return true;
+}
+
+// ---------------------------------------------------------------------------------- activations --
+// x sigmoid(t) as x / (1 + e^-t): relative accuracy for every sign of t (a tanh form cancels for
+// t << 0); e^-t overflowing to infinity gives the limit 0.
+__device__ __forceinline__ float x_sigmoid(float x, float t) { return __fdividef(x, 1.0f + __expf(-t)); }
+
+constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+// gelu(x) = x (1 + tanh u) / 2 = x sigmoid(2u), u = c (x + a x^3)
+__device__ __forceinline__ float act_fwd(int act, float x)
+{
+    if (act == kActGelu)
+        return x_sigmoid(x, x * fmaf(2.0f * kGeluC * kGeluA, x * x, 2.0f * kGeluC));
+    if (act == kActSilu)
+        return x_sigmoid(x, x);
+    if (act == kActRelu)
+        return x < 0.0f ? 0.0f : x;   // NaN stays NaN
+    return x;
+}
+
+// ---------------------------------------------------------------------------------------- items --
+struct GroupTab {
+    int32_t *start, *cnt, *base;   // rows of each group; items before each group (groups + 1)
+};
+
+struct Tile {
+    int32_t e, start, cnt;
+    int32_t p0, q0;      // origin in the P and Q extents (inside the group's rows for a ragged one)
+    int32_t kb0, kb1;    // k blocks of this CTA's slice
+};
+
+template <int kForm, int kPair>
+__device__ __forceinline__ int32_t items_of(const LinearParams &p, int32_t cnt)
+{
+    constexpr int32_t bm = kPRows * kPair;
+    if (kForm == kRows)
+        return (cnt + bm - 1) / bm * ((p.q_ext + p.bn - 1) / p.bn);
+    if (kForm == kRowsT)
+        return (cnt + p.bn - 1) / p.bn * ((p.p_ext + bm - 1) / bm);
+    return (p.p_ext + bm - 1) / bm * ((p.q_ext + p.bn - 1) / p.bn);
+}
+
+// One role's walk over its CTA's items: ids grow, so the group only ever advances.
+template <int kForm, int kPair>
+struct Walk {
+    int32_t id, step, e, slice;
+    __device__ __forceinline__ Walk(const LinearParams &p)
+        : id(static_cast<int32_t>(cluster_id_x())), step(static_cast<int32_t>(num_clusters_x())), e(0),
+          slice(kPair == 1 && p.split > 1 ? static_cast<int32_t>(cluster_ctarank()) : 0)
+    {
+    }
+    __device__ __forceinline__ bool next(const LinearParams &p, const GroupTab &g, int32_t n_items, Tile &t)
+    {
+        if (id >= n_items)
+            return false;
+        while (id >= g.base[e + 1])
+            ++e;
+        constexpr int32_t bm = kPRows * kPair;
+        t.e = e;
+        t.start = g.start[e];
+        t.cnt = g.cnt[e];
+        const int32_t i = id - g.base[e];
+        id += step;
+        const int32_t kext = kForm == kReduce ? t.cnt : p.k_ext;
+        const int32_t nkb = (kext + kKB - 1) / kKB;
+        if (kForm == kRowsT) {
+            const int32_t tq = (t.cnt + p.bn - 1) / p.bn;
+            t.p0 = i / tq * bm;
+            t.q0 = i % tq * p.bn;
+        } else {
+            const int32_t tp = ((kForm == kRows ? t.cnt : p.p_ext) + bm - 1) / bm;
+            const int32_t tq = (p.q_ext + p.bn - 1) / p.bn;
+            const int32_t band = i / (p.raster * tq), first = band * p.raster;
+            const int32_t h = min(p.raster, tp - first), r = i - first * tq;
+            t.q0 = r / h * p.bn;
+            t.p0 = (first + r % h) * bm;
+        }
+        if (kPair == 1 && p.split > 1) {
+            const int32_t per = (nkb + p.split - 1) / p.split;
+            t.kb0 = min(slice * per, nkb);
+            t.kb1 = min(t.kb0 + per, nkb);
+        } else {
+            t.kb0 = 0;
+            t.kb1 = nkb;
+        }
+        return true;
+    }
+};
+
+// A group's last k block holds rows of the next group when the reduction runs over a group's rows:
+// they are zeroed in shared memory.  (At the very end of the matrix the copy fills zeros itself.)
+template <int kForm>
+__device__ __forceinline__ int32_t masked_rows(const LinearParams &p, const Tile &t, int32_t kb)
+{
+    if (kForm != kReduce)
+        return 0;
+    const int32_t have = t.cnt - kb * kKB;
+    return have < kKB && t.start + t.cnt < p.rows ? kKB - have : 0;
+}
+
+// -------------------------------------------------------------------------------- TMA producer --
+template <int kForm, int kPair>
+__device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring)
+{
+    const int32_t num_pipe = p.num_pipe;
+    const uint32_t slot_bytes = p.slot_bytes;
+    const uint32_t half = kPair == 2 ? (cluster_ctarank() & 1u) : 0u;
+    const uint32_t full_lead0 = kPair == 2 ? map_to_rank(&c->full[0], 0) : 0u;
+    const uint32_t go_peer0 = kPair == 2 ? map_to_rank(&c->go[0], 1) : 0u;
+    const uint32_t tail_own0 = kPair == 2 ? map_to_rank(&c->tail[0], half) : 0u;
+    const int32_t bn_cta = p.bn / kPair;
+    const uint32_t q_bytes = static_cast<uint32_t>(bn_cta) * kKB * 2;
+    const bool p_mn = p.p_mn != 0, q_mn = p.q_mn != 0;
+    const int32_t n_items = c->n_items;
+    // the ragged operand is read by many tiles, weights by the row panels of one group at a time
+    const uint64_t pol = policy_evict_normal();
+    uint32_t issued = 0, tail_use = 0, tail_ph = 0;
+    int32_t ps = 0;
+    uint32_t pph = 0;
+    Walk<kForm, kPair> w(p);
+    Tile t;
+    bool ok = true;
+    uint32_t item_ph = 0;
+    bool first = true;
+    while (ok && w.next(p, g, n_items, t)) {
+        if (kPair == 1 && p.split > 1) {   // the ring was the exchange buffer of the previous item
+            if (!first) {
+                if (!lwait(&c->ringfree, item_ph, c, p))
+                    break;
+                item_ph ^= 1;
+            }
+            first = false;
+        }
+        const int32_t p_row = (kForm == kRows ? t.start : 0) + t.p0 + static_cast<int32_t>(half) * kPRows;
+        const int32_t q_row = (kForm == kRowsT ? t.start : 0) + t.q0 + static_cast<int32_t>(half) * bn_cta;
+        const int32_t p_grp = kForm == kRowsT ? t.e : 0, q_grp = kForm == kRows ? t.e : 0;
+        for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
+            if (kPair == 2 && half) {
+                if (!lwait(&c->go[ps], pph, c, p, true)) {   // the leader armed this fill
+                    ok = false;
+                    break;
+                }
+            } else if (!lwait(&c->empty[ps], pph ^ 1, c, p)) {
+                ok = false;
+                break;
+            }
+            const bool masked = masked_rows<kForm>(p, t, kb) != 0;
+            if (masked) {
+                // completes on this CTA's own tail barrier; warp 2 zeroes the rows and completes `full`
+                mbar_arrive_expect_tx(&c->tail[ps], kPBytes + q_bytes);
+                tail_use |= 1u << ps;
+                tail_ph ^= 1u << ps;
+            } else if (!half) {
+                mbar_arrive_expect_tx(&c->full[ps], kPair * (kPBytes + q_bytes));
+                if (kForm == kReduce && kPair == 2)
+                    mbar_arrive(&c->full[ps]);   // (the count is 2: one per CTA's warp 2 on a masked fill)
+            }
+            if (kPair == 2 && !half)
+                mbar_arrive_cluster(go_peer0 + 8u * static_cast<uint32_t>(ps));
+            uint8_t *a = ring + static_cast<size_t>(ps) * slot_bytes;
+            uint8_t *b = a + kPBytes;
+            const int32_t k = (kForm == kReduce ? t.start : 0) + kb * kKB;
+            const uint32_t fb = kPair == 2 ? (masked ? tail_own0 : full_lead0) + 8u * static_cast<uint32_t>(ps) : 0u;
+            uint64_t *lb = masked ? &c->tail[ps] : &c->full[ps];
+            auto load = [&](uint8_t *dst, const CUtensorMap *m, int32_t c0, int32_t c1, int32_t c2) {
+                if (kPair == 2)
+                    tma_load_3d_pair(dst, m, fb, c0, c1, c2, pol);
+                else
+                    tma_load_3d(dst, m, lb, c0, c1, c2, pol);
+            };
+            if (p_mn) {
+                load(a, &p.mapP, p_row, k, p_grp);
+                load(a + kBoxBytes, &p.mapP, p_row + 64, k, p_grp);
+            } else {
+                load(a, &p.mapP, k, p_row, p_grp);
+            }
+            if (q_mn) {
+                for (int32_t j = 0; j < bn_cta; j += 64)
+                    load(b + (j >> 6) * kBoxBytes, &p.mapQ, q_row + j, k, q_grp);
+            } else {
+                load(b, &p.mapQ, k, q_row, q_grp);
+            }
+            ++issued;
+            if (++ps == num_pipe) {
+                ps = 0;
+                pph ^= 1;
+            }
+        }
+    }
+    if (c->abort_flag) {
+        // Let the copies land before the shared memory goes away.  Unmasked fills of a pair complete on
+        // the leader's barriers (the peer fills only what the leader armed, and keeps its shared memory
+        // until the final cluster barrier); masked fills complete on each CTA's own.
+        for (int32_t i = 0; i < num_pipe; ++i) {
+            if (tail_use >> i & 1u)
+                lwait(&c->tail[i], (tail_ph >> i & 1u) ^ 1u, c, p, false, true);
+            const uint32_t n = static_cast<uint32_t>(num_pipe), u = static_cast<uint32_t>(i);
+            const uint32_t fills = issued / n + (u < issued % n ? 1u : 0u);
+            if (!half && fills > 0)
+                lwait(&c->full[i], (fills - 1) & 1, c, p, false, true);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------- MMA issuer --
+template <int kForm, int kPair>
+__device__ __forceinline__ void l_role_mma(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring,
+                                           uint32_t tmem_base)
+{
+    if (kPair == 2 && (cluster_ctarank() & 1u))
+        return;   // the leader issues for both
+    const int32_t num_pipe = p.num_pipe;
+    const uint32_t bn = static_cast<uint32_t>(p.bn);
+    const uint32_t tfull_peer0 = kPair == 2 ? map_to_rank(&c->tfull[0], 1) : 0u;
+    const uint32_t idesc = idesc_bf16_f32(kPRows * kPair, bn, p.q_mn ? 1u : 0u) | (p.p_mn ? 1u << 15 : 0u);
+    const uint32_t base = smem_u32(ring);
+    // K-major: 8-row groups 1024 bytes apart, a 16-deep k step 32 bytes along the row.  MN-major: 64
+    // columns x 64 k per box, boxes kBoxBytes apart, a k step 16 rows of 128 bytes.  Slot offsets add to
+    // the 14-bit address field in 16-byte units (shared memory is below 2^18 bytes: no carry).
+    const uint64_t pd = p.p_mn ? smem_desc(base, kBoxBytes, 1024u, 2u) : smem_desc(base, 16u, 1024u, 2u);
+    const uint64_t qd = p.q_mn ? smem_desc(base + kPBytes, kBoxBytes, 1024u, 2u) : smem_desc(base + kPBytes, 16u, 1024u, 2u);
+    const uint64_t pstep = p.p_mn ? 128u : 2u, qstep = p.q_mn ? 128u : 2u;
+    const uint64_t slot16 = p.slot_bytes >> 4;
+    const int32_t n_items = c->n_items;
+    int32_t ps = 0;
+    uint32_t pph = 0, tiles = 0;
+    bool issued = false, ok = true;
+    Walk<kForm, kPair> w(p);
+    Tile t;
+    while (w.next(p, g, n_items, t)) {
+        const uint32_t acc = tiles & 1u;
+        if (!lwait(&c->tempty[acc], ((tiles >> 1) & 1u) ^ 1u, c, p, kPair == 2))
+            break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + acc * bn;
+        uint32_t accum = 0;
+        for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
+            if (!lwait(&c->full[ps], pph, c, p, kPair == 2)) {
+                ok = false;
+                break;
+            }
+            const uint64_t off = static_cast<uint64_t>(ps) * slot16;
+#pragma unroll
+            for (uint32_t kk = 0; kk < kKB / 16; ++kk) {
+                mma_bf16_ss_g<kPair>(d, pd + off + pstep * kk, qd + off + qstep * kk, idesc, accum);
+                accum = 1u;
+            }
+            issued = true;
+            mma_commit_g<kPair>(smem_u32(&c->empty[ps]));
+            if (++ps == num_pipe) {
+                ps = 0;
+                pph ^= 1;
+            }
+        }
+        if (!ok)
+            break;
+        mma_commit_g<kPair>(smem_u32(&c->tfull[acc]));
+        if (kPair == 2)
+            mma_commit_g<kPair>(tfull_peer0 + acc * 8u);
+        ++tiles;
+    }
+    if (c->abort_flag && issued) {
+        mma_commit_g<kPair>(smem_u32(&c->drain));
+        lwait(&c->drain, 0, c, p, false, true);
+    }
+}
+
+// ---------------------------------------------------------------- ragged reduction tails (warp 2) --
+template <int kPair>
+__device__ __forceinline__ void l_role_mask(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring)
+{
+    const int32_t lane = threadIdx.x & 31;
+    const int32_t num_pipe = p.num_pipe;
+    const uint32_t boxes = 2u + static_cast<uint32_t>(p.bn / kPair) / 64u;   // P's two, then Q's
+    const uint32_t full_lead0 = kPair == 2 ? map_to_rank(&c->full[0], 0) : 0u;
+    const int32_t n_items = c->n_items;
+    uint32_t fills = 0, tail_ph = 0;
+    Walk<kReduce, kPair> w(p);
+    Tile t;
+    while (w.next(p, g, n_items, t)) {
+        if (t.kb1 <= t.kb0)
+            continue;
+        const int32_t zero = masked_rows<kReduce>(p, t, t.kb1 - 1);
+        fills += static_cast<uint32_t>(t.kb1 - t.kb0);
+        if (!zero)
+            continue;
+        const int32_t ps = static_cast<int32_t>((fills - 1) % static_cast<uint32_t>(num_pipe));
+        if (!lwait_warp(&c->tail[ps], (tail_ph >> ps) & 1u, c, p))
+            return;
+        tail_ph ^= 1u << ps;
+        // a k row is 128 contiguous bytes of each box (the swizzle permutes inside them)
+        uint8_t *s = ring + static_cast<size_t>(ps) * p.slot_bytes;
+        const uint32_t segs = static_cast<uint32_t>(zero) * 8u;
+        for (uint32_t b = 0; b < boxes; ++b)
+            for (uint32_t i = lane; i < segs; i += 32)
+                *reinterpret_cast<uint4 *>(s + b * kBoxBytes + (kKB - zero) * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            if (kPair == 2)
+                mbar_arrive_cluster(full_lead0 + 8u * static_cast<uint32_t>(ps));
+            else
+                mbar_arrive(&c->full[ps]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------- epilogue --
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ float2 unpack2(uint32_t w)
+{
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// Offset of 16-byte segment `seg` of row `row` in a warp's 32 x 128-byte staging buffer; the XOR keeps
+// row-wise and segment-wise accesses off each other's banks.
+__device__ __forceinline__ uint32_t stg(int row, int seg) { return static_cast<uint32_t>(row * 128 + ((seg ^ (row & 7)) * 16)); }
+
+// The staged 32 rows x 8 segments to (or from) global memory, whole 128-byte row pieces at a time.
+// esz: bytes of an element; rows and columns past the limits are skipped (columns are multiples of a
+// segment).
+template <bool kLoad>
+__device__ __forceinline__ void stage_move(uint8_t *stage, uint8_t *gbase, int64_t ld_bytes, int32_t row_lim,
+                                           int32_t seg_lim, int32_t lane)
+{
+    const int32_t sg = lane & 7;
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+        const int32_t rr = it * 4 + (lane >> 3);
+        uint4 *s = reinterpret_cast<uint4 *>(stage + stg(rr, sg));
+        uint4 *q = reinterpret_cast<uint4 *>(gbase + rr * ld_bytes + sg * 16);
+        if (rr < row_lim && sg < seg_lim) {
+            if (kLoad)
+                *s = *q;
+            else
+                *q = *s;
+        }
+    }
+}
+
+// Arrive at the leader's accumulator-empty barrier.
+template <int kPair>
+__device__ __forceinline__ void free_acc(LCtrl *c, uint32_t acc)
+{
+    if (kPair == 2)
+        mbar_arrive_cluster(map_to_rank(&c->tempty[acc], 0));
+    else
+        mbar_arrive(&c->tempty[acc]);
+}
+
+// 32 x kW part of a tile's row chunk in the orientation TMEM lane = output row: bias, activation,
+// residual, rounding and stores of 64 bf16 (or 32 fp32) columns.
+template <int kAct>
+__device__ __forceinline__ void finish_bf16(const LinearParams &p, float (&v)[64], uint8_t *stage, const float *bias,
+                                            int64_t row, int32_t row_lim, int32_t col, int32_t col_lim, int32_t lane)
+{
+    const int32_t seg_lim = min(8, (col_lim - col) / 8);
+    if (p.bias) {
+#pragma unroll
+        for (int j = 0; j < 64; j += 4) {
+            const float4 b = *reinterpret_cast<const float4 *>(bias + j);
+            v[j] += b.x;
+            v[j + 1] += b.y;
+            v[j + 2] += b.z;
+            v[j + 3] += b.w;
+        }
+    }
+    if (p.z) {
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            *reinterpret_cast<uint4 *>(stage + stg(lane, s)) =
+                make_uint4(pack2(v[8 * s], v[8 * s + 1]), pack2(v[8 * s + 2], v[8 * s + 3]),
+                           pack2(v[8 * s + 4], v[8 * s + 5]), pack2(v[8 * s + 6], v[8 * s + 7]));
+        __syncwarp();
+        stage_move<false>(stage, reinterpret_cast<uint8_t *>(p.z + row * p.ld_z + col), p.ld_z * 2, row_lim, seg_lim, lane);
+        __syncwarp();
+    }
+    if (p.res) {
+        stage_move<true>(stage, reinterpret_cast<uint8_t *>(const_cast<__nv_bfloat16 *>(p.res) + row * p.ld_res + col),
+                         p.ld_res * 2, row_lim, seg_lim, lane);
+        __syncwarp();
+    }
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+        uint4 *q = reinterpret_cast<uint4 *>(stage + stg(lane, s));
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            y[j] = act_fwd(kAct, v[8 * s + j]);
+        if (p.res) {
+            const uint4 x = *q;
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = unpack2(xw[j]);
+                y[2 * j] += f.x;
+                y[2 * j + 1] += f.y;
+            }
+        }
+        *q = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+    }
+    __syncwarp();
+    stage_move<false>(stage, reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(p.out) + row * p.ld_out + col),
+                      p.ld_out * 2, row_lim, seg_lim, lane);
+    __syncwarp();
+}
+
+__device__ __forceinline__ void finish_f32(const LinearParams &p, const float *v, uint8_t *stage, int64_t row,
+                                           int32_t row_lim, int32_t col, int32_t col_lim, int32_t lane)
+{
+    const int32_t seg_lim = min(8, (col_lim - col) / 4);
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+        *reinterpret_cast<float4 *>(stage + stg(lane, s)) = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
+    __syncwarp();
+    stage_move<false>(stage, reinterpret_cast<uint8_t *>(static_cast<float *>(p.out) + row * p.ld_out + col),
+                      p.ld_out * 4, row_lim, seg_lim, lane);
+    __syncwarp();
+}
+
+__device__ __forceinline__ float load_bias(const LinearParams &p, int64_t i)
+{
+    return p.bias_f32 ? static_cast<const float *>(p.bias)[i]
+                      : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.bias)[i]);
+}
+
+// Output column `n` of up to 32 activation rows, lane = output column.
+template <int kAct>
+__device__ __forceinline__ void finish_rows_t(const LinearParams &p, float (&v)[32], float bias, int64_t row, int32_t n_rows,
+                                              int32_t n, bool n_ok)
+{
+    if (!n_ok)
+        return;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row * p.ld_out + n;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        if (j < n_rows) {
+            const float z = v[j] + bias;
+            if (p.z)
+                p.z[(row + j) * p.ld_z + n] = __float2bfloat16_rn(z);
+            float y = act_fwd(kAct, z);
+            if (p.res)
+                y += __bfloat162float(p.res[(row + j) * p.ld_res + n]);
+            out[j * p.ld_out] = __float2bfloat16_rn(y);
+        }
+    }
+}
+
+template <int kForm, int kPair>
+__device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring,
+                                                uint8_t *stage_all, float *bias_all, uint32_t tmem_base)
+{
+    const int32_t ew = static_cast<int32_t>(threadIdx.x / 32) - 4;   // = warp % 4: its TMEM lane quarter
+    const int32_t lane = threadIdx.x & 31;
+    const uint32_t half = kPair == 2 ? (cluster_ctarank() & 1u) : 0u;
+    uint8_t *stage = stage_all + ew * kStageWarpBytes;
+    float *bias_s = bias_all + ew * 256;
+    const int32_t bn = p.bn;
+    const int32_t n_items = c->n_items;
+    const bool splitk = kPair == 1 && p.split > 1;
+    const int32_t S = splitk ? p.split : 1;
+    const int32_t part = bn / S;                 // columns this CTA finishes
+    const int32_t me = splitk ? static_cast<int32_t>(cluster_ctarank()) : 0;
+    const uint32_t lane_base = static_cast<uint32_t>(ew * 32) << 16;
+    uint32_t tiles = 0;
+    Walk<kForm, kPair> w(p);
+    Tile t;
+    while (w.next(p, g, n_items, t)) {
+        const uint32_t acc = tiles & 1u;
+        const uint32_t ph = (tiles >> 1) & 1u;
+        const int32_t c_lo = me * part, c_hi = c_lo + part;   // this CTA's columns of the tile
+        // ---- bias of the tile, while its MMAs run
+        float bias_t = 0.0f;
+        const int32_t n_t = t.p0 + ew * 32 + lane;             // kRowsT: this lane's output column
+        if (p.bias) {
+            if (kForm == kRowsT) {
+                if (n_t < p.p_ext)
+                    bias_t = load_bias(p, static_cast<int64_t>(t.e) * p.p_ext + n_t);
+            } else {
+                __syncwarp();
+                for (int32_t j = c_lo + lane; j < c_hi; j += 32)
+                    bias_s[j] = t.q0 + j < p.q_ext ? load_bias(p, static_cast<int64_t>(t.e) * p.q_ext + t.q0 + j) : 0.0f;
+                __syncwarp();
+            }
+        }
+        if (!lwait_warp(&c->tfull[acc], ph, c, p, kPair == 2))
+            return;
+        tc_fence_after();
+        const uint32_t d = tmem_base + acc * static_cast<uint32_t>(bn) + lane_base;
+        const bool have_k = t.kb1 > t.kb0;
+        const uint32_t item_ph = tiles & 1u;
+        if (splitk) {
+            // Every CTA's MMAs of this item are done, so every ring is free to receive.
+            if (lane == 0) {
+                for (int32_t r = 0; r < S; ++r)
+                    mbar_arrive_cluster(map_to_rank(&c->rdy, static_cast<uint32_t>(r)));
+            }
+            if (!lwait_warp(&c->rdy, item_ph, c, p, true))
+                return;
+            // parts of 8 columns: [source slot][4-column block][128 lanes] float4
+            for (int32_t o = 1; o < S; ++o) {
+                const int32_t r = (me + o) % S;
+                const uint32_t dst = map_to_rank(ring, static_cast<uint32_t>(r));
+                const int32_t slot = me < r ? me : me - 1;
+                for (int32_t j = 0; j < part; j += 8) {
+                    uint32_t x[8];
+                    tmem_ld_32x32b_x8(d + static_cast<uint32_t>(r * part + j), x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const uint32_t off =
+                            (static_cast<uint32_t>(slot * (part / 4) + j / 4 + b) * 128u + static_cast<uint32_t>(ew * 32 + lane)) * 16u;
+                        st_cluster_v4_f32(dst + off, have_k ? __uint_as_float(x[4 * b]) : 0.0f,
+                                          have_k ? __uint_as_float(x[4 * b + 1]) : 0.0f,
+                                          have_k ? __uint_as_float(x[4 * b + 2]) : 0.0f,
+                                          have_k ? __uint_as_float(x[4 * b + 3]) : 0.0f);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                for (int32_t o = 1; o < S; ++o)
+                    mbar_arrive_cluster(map_to_rank(&c->got, static_cast<uint32_t>((me + o) % S)));
+            if (!lwait_warp(&c->got, item_ph, c, p, true))
+                return;
+        }
+        // Accumulator columns [col, col + 32) of this lane, partial sums of all slices in slice order.
+        auto fetch = [&](int32_t col, float *v) {
+            uint32_t x[32];
+            tmem_ld_32x32b_x32(d + static_cast<uint32_t>(col), x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] = have_k ? __uint_as_float(x[j]) : 0.0f;
+            if (splitk) {
+                float own[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    own[j] = v[j];
+                    v[j] = 0.0f;
+                }
+                const int32_t blocks = min(8, (c_hi - col) / 4);
+                for (int32_t s = 0; s < S; ++s) {
+                    if (s == me) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] += own[j];
+                        continue;
+                    }
+                    const int32_t slot = s < me ? s : s - 1;
+#pragma unroll
+                    for (int b = 0; b < 8; ++b) {
+                        if (b < blocks) {
+                            const float4 q = *reinterpret_cast<const float4 *>(
+                                ring + (static_cast<uint32_t>(slot * (part / 4) + (col - c_lo) / 4 + b) * 128u +
+                                        static_cast<uint32_t>(ew * 32 + lane)) * 16u);
+                            v[4 * b] += q.x;
+                            v[4 * b + 1] += q.y;
+                            v[4 * b + 2] += q.z;
+                            v[4 * b + 3] += q.w;
+                        }
+                    }
+                }
+            }
+        };
+        if (kForm == kRowsT) {
+            for (int32_t col = c_lo; col < c_hi; col += 32) {
+                const int32_t rows_here = min(min(32, c_hi - col), t.cnt - t.q0 - col);
+                if (rows_here <= 0)
+                    break;
+                float v[32];
+                fetch(col, v);
+                const int64_t row = static_cast<int64_t>(t.start) + t.q0 + col;
+                const bool n_ok = n_t < p.p_ext;
+                switch (p.act) {
+                case kActGelu: finish_rows_t<kActGelu>(p, v, bias_t, row, rows_here, n_t, n_ok); break;
+                case kActSilu: finish_rows_t<kActSilu>(p, v, bias_t, row, rows_here, n_t, n_ok); break;
+                case kActRelu: finish_rows_t<kActRelu>(p, v, bias_t, row, rows_here, n_t, n_ok); break;
+                default: finish_rows_t<kActNone>(p, v, bias_t, row, rows_here, n_t, n_ok); break;
+                }
+            }
+        } else {
+            const int32_t prow = t.p0 + static_cast<int32_t>(half) * kPRows + ew * 32;   // first row of this warp
+            const int32_t row_lim = min(32, (kForm == kRows ? t.cnt : p.p_ext) - prow);
+            const int64_t row = (kForm == kRows ? static_cast<int64_t>(t.start) : static_cast<int64_t>(t.e) * p.p_ext) + prow;
+            for (int32_t col = c_lo; col < c_hi && t.q0 + col < p.q_ext && row_lim > 0; col += 64) {
+                float v[64];
+                fetch(col, v);
+                if (col + 32 < c_hi) {
+                    fetch(col + 32, v + 32);
+                } else {
+#pragma unroll
+                    for (int j = 32; j < 64; ++j)
+                        v[j] = 0.0f;
+                }
+                const int32_t gcol = t.q0 + col, col_lim = min(p.q_ext, t.q0 + c_hi);
+                if (kForm == kReduce) {
+                    if (p.out_f32) {
+                        finish_f32(p, v, stage, row, row_lim, gcol, col_lim, lane);
+                        if (gcol + 32 < col_lim)
+                            finish_f32(p, v + 32, stage, row, row_lim, gcol + 32, col_lim, lane);
+                    } else {
+                        finish_bf16<kActNone>(p, v, stage, bias_s + col, row, row_lim, gcol, col_lim, lane);
+                    }
+                } else {
+                    switch (p.act) {
+                    case kActGelu: finish_bf16<kActGelu>(p, v, stage, bias_s + col, row, row_lim, gcol, col_lim, lane); break;
+                    case kActSilu: finish_bf16<kActSilu>(p, v, stage, bias_s + col, row, row_lim, gcol, col_lim, lane); break;
+                    case kActRelu: finish_bf16<kActRelu>(p, v, stage, bias_s + col, row, row_lim, gcol, col_lim, lane); break;
+                    default: finish_bf16<kActNone>(p, v, stage, bias_s + col, row, row_lim, gcol, col_lim, lane); break;
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (splitk) {
+            fence_proxy_async_shared();   // these reads of the ring before the producer's next copies
+            __syncwarp();
+        }
+        if (lane == 0) {
+            free_acc<kPair>(c, acc);
+            if (splitk)
+                mbar_arrive(&c->ringfree);
+        }
+        ++tiles;
+    }
+}
+
+// --------------------------------------------------------------------------------------- kernel --
+template <int kForm, int kPair>
+__global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_constant__ LinearParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t base = smem_u32(smem_raw);
+    uint8_t *ring = smem_raw + (((base + 1023u) & ~1023u) - base);
+    LCtrl *c = reinterpret_cast<LCtrl *>(ring + ls_ctrl(p.num_pipe, p.slot_bytes));
+    GroupTab g;
+    g.start = reinterpret_cast<int32_t *>(ring + ls_tab(p.num_pipe, p.slot_bytes));
+    g.cnt = g.start + p.groups;
+    g.base = g.cnt + p.groups;
+    const int32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_tensormap(&p.mapP);
+            prefetch_tensormap(&p.mapQ);
+        }
+        for (int32_t i = lane; i < p.num_pipe; i += 32) {
+            mbar_init(&c->full[i], kForm == kReduce ? kPair : 1);
+            mbar_init(&c->empty[i], 1);
+            mbar_init(&c->go[i], 1);
+            mbar_init(&c->tail[i], 1);
+        }
+        if (lane < 2) {
+            mbar_init(&c->tfull[lane], 1);
+            mbar_init(&c->tempty[lane], 4 * kPair);
+        }
+        if (lane == 0) {
+            const int32_t S = p.split > 1 ? p.split : 1;
+            mbar_init(&c->drain, 1);
+            mbar_init(&c->rdy, 4 * S);                       // every CTA's four epilogue warps
+            mbar_init(&c->got, S > 1 ? 4 * (S - 1) : 1);     // the other CTAs' four warps
+            mbar_init(&c->ringfree, 4);
+            c->abort_flag = 0;
+            c->skip = ld_relaxed_gpu_u32(p.status) != 0;     // sticky error: do nothing
+        }
+        fence_barrier_init();
+    } else if (warp == 1) {
+        tmem_alloc_g<kPair>(&c->tmem_base, p.tmem_cols);
+        tmem_relinquish_g<kPair>();
+    } else if (warp == 2) {
+        // Group tables.  Offsets come from device memory: anything out of order or out of range is
+        // clamped, so no access can leave the matrices, and reported through the status word.
+        int32_t carry = 0;
+        bool bad = false;
+        for (int32_t e0 = 0; e0 < p.groups; e0 += 32) {
+            const int32_t e = e0 + lane;
+            int32_t items = 0;
+            if (e < p.groups) {
+                const int32_t lo0 = p.offsets ? p.offsets[e] : 0, hi0 = p.offsets ? p.offsets[e + 1] : p.rows;
+                const int32_t lo = min(max(lo0, 0), p.rows), hi = min(max(hi0, lo), p.rows);
+                bad |= lo != lo0 || hi != hi0;
+                g.start[e] = lo;
+                g.cnt[e] = hi - lo;
+                items = items_of<kForm, kPair>(p, hi - lo);
+            }
+            int32_t sum = items;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o)
+                    sum += v;
+            }
+            if (e < p.groups)
+                g.base[e] = carry + sum - items;
+            carry += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) {
+            g.base[p.groups] = carry;
+            c->n_items = carry;
+        }
+        if (__any_sync(0xffffffffu, bad) && lane == 0)
+            atomicCAS(p.status, 0u, kStBadOffsets);
+    }
+    tc_fence_before();
+    cluster_sync_all();   // barriers initialised before any remote arrival
+    tc_fence_after();
+    const uint32_t tmem_base = c->tmem_base;
+    if (!c->skip) {
+        if (warp == 0) {
+            if (lane == 0)
+                l_role_tma<kForm, kPair>(p, c, g, ring);
+        } else if (warp == 1) {
+            if (lane == 0)
+                l_role_mma<kForm, kPair>(p, c, g, ring, tmem_base);
+        } else if (warp == 2) {
+            if (kForm == kReduce && p.offsets)
+                l_role_mask<kPair>(p, c, g, ring);
+        } else if (warp >= 4) {
+            l_role_epilogue<kForm, kPair>(p, c, g, ring, ring + ls_stage(p.num_pipe, p.slot_bytes),
+                                          reinterpret_cast<float *>(ring + ls_bias(p.num_pipe, p.slot_bytes)), tmem_base);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();   // MMAs, epilogues and exchanges of every CTA of the cluster are over
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_g<kPair>(tmem_base, p.tmem_cols);
+    }
+    cluster_sync_all();
+}
+
+}  // namespace mlpl
