@@ -309,7 +309,7 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
                     mbar_arrive(&c->full[ps]);   // (the count is 2: one per CTA's warp 2 on a masked fill)
             }
             if (kPair == 2 && !half)
-                mbar_arrive_cluster(go_peer0 + 8u * static_cast<uint32_t>(ps));
+                mbar_arrive_relaxed_cluster(go_peer0 + 8u * static_cast<uint32_t>(ps), 1);   // publishes no data
             uint8_t *a = ring + static_cast<size_t>(ps) * slot_bytes;
             uint8_t *b = a + kPBytes;
             const int32_t k = (kForm == kReduce ? t.start : 0) + kb * kKB;
