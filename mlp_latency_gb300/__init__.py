@@ -14,5 +14,6 @@ _BLOCK = ("Linear", "layer_norm_forward", "layer_norm_backward", "layer_norm_wor
 def __getattr__(name):   # the operators take torch tensors: torch is imported with the first use of one
     if name in _BLOCK:
         from . import block
-        return getattr(block, name)
+        globals().update({n: getattr(block, n) for n in _BLOCK})
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

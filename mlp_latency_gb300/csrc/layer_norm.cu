@@ -54,15 +54,27 @@ __device__ __forceinline__ void store(T *p, const float (&f)[V])
     *reinterpret_cast<Vec<T, V> *>(p) = x;
 }
 
-// gamma or beta, columns c .. c + V - 1 (NULL: `none`)
+// gamma or beta, columns c .. c + V - 1 (NULL: `none`).  kind: 0 bf16, 1 fp32; + 2: aligned to V of them
+// (at most 16 bytes), read in vectors.
 template <int V>
-__device__ __forceinline__ void load_w(const void *w, bool f32, int64_t c, float none, float (&f)[V])
+__device__ __forceinline__ void load_w(const void *w, int kind, int64_t c, float none, float (&f)[V])
 {
+    constexpr int V4 = V < 4 ? V : 4;
     if (!w) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
             f[j] = none;
-    } else if (f32) {
+    } else if (kind == 2) {
+        load<__nv_bfloat16, V>(static_cast<const __nv_bfloat16 *>(w) + c, f);
+    } else if (kind == 3) {
+#pragma unroll
+        for (int j = 0; j < V; j += V4) {
+            const Vec<float, V4> x = *reinterpret_cast<const Vec<float, V4> *>(static_cast<const float *>(w) + c + j);
+#pragma unroll
+            for (int k = 0; k < V4; ++k)
+                f[j + k] = x.v[k];
+        }
+    } else if (kind == 1) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
             f[j] = static_cast<const float *>(w)[c + j];
@@ -110,15 +122,15 @@ struct NormParams {
     const float *mean_in, *rstd_in;
     int64_t rows, cols, ldx, ldy, lddy, ldadd, lddx;
     float eps, inv_cols;
-    int32_t w_f32;
+    int32_t w_f32, w_kind;         // dtype of the weights; how load_w reads them
     float *part;                   // column sums: blocks x 2 x cols
     int64_t block_rows;
     int32_t blocks;
 };
 
 // One row per team, the row in registers (kItems vectors of V per thread): moments, then the output.
-template <typename T, int V, int kItems, bool kWarpTeam>
-__global__ void __launch_bounds__(kMaxThreads) norm_forward_kernel(const NormParams p)
+template <typename T, int V, int kItems, bool kWarpTeam, int kThreads>
+__global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormParams p)
 {
     __shared__ float scratch[32];
     const int team = kWarpTeam ? 32 : static_cast<int>(blockDim.x);
@@ -166,8 +178,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_forward_kernel(const NormPar
         const int64_t c = (static_cast<int64_t>(i) * team + t) * V;
         if (c < p.cols) {
             float g[V], b[V], o[V];
-            load_w<V>(p.gamma, p.w_f32, c, 1.0f, g);
-            load_w<V>(p.beta, p.w_f32, c, 0.0f, b);
+            load_w<V>(p.gamma, p.w_kind, c, 1.0f, g);
+            load_w<V>(p.beta, p.w_kind, c, 0.0f, b);
 #pragma unroll
             for (int j = 0; j < V; ++j)
                 o[j] = fmaf((v[i][j] - mean) * rstd, g[j], b[j]);
@@ -204,8 +216,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_forward_wide_kernel(const No
     T *y = static_cast<T *>(p.y) + row * p.ldy;
     for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) {
         float g[1], b[1];
-        load_w<1>(p.gamma, p.w_f32, c, 1.0f, g);
-        load_w<1>(p.beta, p.w_f32, c, 0.0f, b);
+        load_w<1>(p.gamma, p.w_kind, c, 1.0f, g);
+        load_w<1>(p.beta, p.w_kind, c, 0.0f, b);
         y[c] = from_f32<T>(fmaf((to_f32<T>(x[c]) - mean) * rstd, g[0], b[0]));
     }
 }
@@ -227,7 +239,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormParams p
         float a[V], d[V], g[V];
         load<T, V>(x + c, a);
         load<T, V>(dy + c, d);
-        load_w<V>(p.gamma, p.w_f32, c, 1.0f, g);
+        load_w<V>(p.gamma, p.w_kind, c, 1.0f, g);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const float gd = g[j] * d[j];
@@ -241,7 +253,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormParams p
         float a[V], d[V], g[V], o[V];
         load<T, V>(x + c, a);
         load<T, V>(dy + c, d);
-        load_w<V>(p.gamma, p.w_f32, c, 1.0f, g);
+        load_w<V>(p.gamma, p.w_kind, c, 1.0f, g);
 #pragma unroll
         for (int j = 0; j < V; ++j)
             o[j] = rstd * (fmaf(g[j], d[j], -m0) - (a[j] - mean) * rstd * m1);
@@ -345,29 +357,36 @@ bool bad_rows(const void *p, int64_t ld, int64_t cols, size_t esz)
     return !p || reinterpret_cast<uintptr_t>(p) % esz != 0 || ld < cols;
 }
 
-template <typename T, int V, int kItems>
+template <typename T, int V, int kItems, int kThreads>
 void launch_forward(const NormParams &p, int64_t nvec, cudaStream_t st)
 {
     if (nvec <= 32 * kItems) {
         const int teams = 4;
-        norm_forward_kernel<T, V, kItems, true><<<static_cast<unsigned>(cdiv(p.rows, teams)), 32 * teams, 0, st>>>(p);
+        norm_forward_kernel<T, V, kItems, true, 128><<<static_cast<unsigned>(cdiv(p.rows, teams)), 32 * teams, 0, st>>>(p);
     } else {
         const int threads = static_cast<int>(cdiv(cdiv(nvec, kItems), 32) * 32);
-        norm_forward_kernel<T, V, kItems, false><<<static_cast<unsigned>(p.rows), threads, 0, st>>>(p);
+        norm_forward_kernel<T, V, kItems, false, kThreads><<<static_cast<unsigned>(p.rows), threads, 0, st>>>(p);
     }
 }
 
+// Vectors per thread.  Few rows: one, so that a row's loads go out at once from as many threads as there
+// are.  Many rows: four, so that several rows share an SM and one row's reductions hide behind the others'
+// loads.  Wider rows take what fits a block's registers.
 template <typename T, int V>
 void forward_v(const NormParams &p, cudaStream_t st)
 {
     const int64_t nvec = cdiv(p.cols, V);
-    // vectors per thread: enough for the row to fit one block
-    if (nvec <= kMaxThreads)
-        launch_forward<T, V, 1>(p, nvec, st);
-    else if (nvec <= 4 * kMaxThreads)
-        launch_forward<T, V, 4>(p, nvec, st);
-    else if (V <= 2 && nvec <= 16 * kMaxThreads)
-        launch_forward<T, V, V <= 2 ? 16 : 1>(p, nvec, st);
+    const bool many = p.rows > 304;
+    if (nvec <= (many ? 64 : 1024))
+        launch_forward<T, V, 1, 1024>(p, nvec, st);
+    else if (nvec <= 4 * 256)
+        launch_forward<T, V, 4, 256>(p, nvec, st);
+    else if (nvec <= 4 * 512)
+        launch_forward<T, V, 4, 512>(p, nvec, st);
+    else if (nvec <= 4 * 1024)
+        launch_forward<T, V, 4, 1024>(p, nvec, st);
+    else if (V <= 2 && nvec <= 16 * 1024)
+        launch_forward<T, V, V <= 2 ? 16 : 1, 1024>(p, nvec, st);
     else
         norm_forward_wide_kernel<T><<<static_cast<unsigned>(p.rows), kMaxThreads, 0, st>>>(p);
 }
@@ -414,6 +433,7 @@ extern "C" mlp_status mlp_layernorm_forward(int64_t rows, int64_t cols, const vo
     p.inv_cols = 1.0f / static_cast<float>(cols);
     p.w_f32 = w_dtype == MLP_DT_F32;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    p.w_kind = p.w_f32 + (aligned(gamma, 0, wsz, 16) && aligned(beta, 0, wsz, 16) ? 2 : 0);
     auto wide = [&](size_t bytes) {
         return static_cast<size_t>(cols) * esz % bytes == 0 && aligned(x, ldx, esz, bytes) && aligned(y, ldy, esz, bytes);
     };
@@ -481,6 +501,7 @@ extern "C" mlp_status mlp_layernorm_backward(int64_t rows, int64_t cols, const v
     p.lddx = lddx;
     p.inv_cols = 1.0f / static_cast<float>(cols);
     p.w_f32 = w_dtype == MLP_DT_F32;
+    p.w_kind = p.w_f32 + (aligned(gamma, 0, wsz, 16) ? 2 : 0);
     p.part = static_cast<float *>(workspace);
     p.block_rows = std::max<int64_t>(cdiv(rows, kColsumBlocks), 8);
     p.blocks = static_cast<int32_t>(cdiv(rows, p.block_rows));

@@ -48,12 +48,13 @@ bool encode(CUtensorMap *map, const void *ptr, int64_t inner, int64_t outer, int
 
 constexpr size_t kSmemLimit = 227 * 1024;
 
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 struct Plan {
     int form, pair, bn, split, pipe;
-    uint32_t slot;
+    uint32_t slot, recv_bytes;
+    int recv_bufs, part_align;
 };
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
@@ -61,60 +62,76 @@ struct mlp_linear {
     mlp_linear_desc d;
     int groups;
     int num_sms;
-    int max_clusters[9];   // co-resident clusters of 1, 2, 4, 8 CTAs
+    int max_clusters[9];   // co-resident clusters of 1 to 8 CTAs
     uint32_t *status;
 };
 
 namespace {
 
-void finish_plan(const mlp_linear *h, Plan &pl)
+// Ring depth and exchange buffers of a chosen variant.
+void finish_plan(const mlp_linear *h, Plan &pl, bool q_mn)
 {
-    pl.slot = kPBytes + static_cast<uint32_t>(pl.bn / pl.pair) * kKB * 2;
-    const size_t fixed = linear_smem_bytes(0, pl.slot, h->groups);
+    const bool rows_t = pl.form == kRowsT;
+    pl.slot = kPBytes + q_tile_bytes(pl.bn / pl.pair, q_mn);
+    // an accumulator next to another one of full width leaves no columns to over-read
+    pl.part_align = 2 * pl.bn + 32 <= 512 && rows_t ? 8 : 32;
+    const int part = static_cast<int>(cdiv(cdiv(pl.bn, pl.split), pl.part_align)) * pl.part_align;
+    pl.recv_bytes = static_cast<uint32_t>((pl.split - 1) * part) * kPRows * 4;
+    pl.recv_bufs = pl.split > 1 && rows_t ? (pl.recv_bytes <= 24 * 1024 ? 2 : pl.recv_bytes <= 64 * 1024 ? 1 : 0) : 0;
+    const size_t fixed = linear_smem_bytes(rows_t, 0, static_cast<uint32_t>(pl.recv_bufs) * pl.recv_bytes, h->groups);
     pl.pipe = static_cast<int>(std::min<size_t>(kMaxRing, (kSmemLimit - fixed) / pl.slot));
 }
 
-// rows: of the whole call; out_cols, red: output columns and reduction extent of a rows product.
-Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red)
+// The variant of a rows product, by an estimate of its time in SM cycles.  rows: of the whole call; out_cols,
+// red: output columns and reduction extent; w_mn: the weights' tile is MN-major.
+Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red, bool w_mn)
 {
-    const int64_t avg = cdiv(rows, h->groups);
+    const int64_t groups = std::min<int64_t>(h->groups, rows), avg = cdiv(rows, groups);
     const int64_t kb = cdiv(red, kKB);
-    Plan pl{kRows, 1, 256, 1, 0, 0};
-    if (avg <= 64) {
-        pl.form = kRowsT;
-        pl.bn = avg <= 32 ? 32 : 64;
-        const int64_t items = std::min<int64_t>(h->groups, rows) * cdiv(out_cols, kPRows);
-        while (pl.split < (pl.bn == 32 ? 4 : 8) && items * pl.split * 2 <= h->num_sms && kb >= 4 * pl.split * 2)
-            pl.split *= 2;
-    } else {
-        // time of the variants in units of one 128 x 256 x 64 step of an SM
-        double best = 1e300;
-        for (int v = 0; v < 3; ++v) {
-            const int pair = v == 0 ? 2 : 1, bn = v == 2 ? 128 : 256;
-            const double step = v == 0 ? 1.0 : v == 1 ? 1.1 : 0.65;
-            const int64_t items = h->groups * cdiv(avg, kPRows * pair) * cdiv(out_cols, bn);
-            for (int s = 1; s <= (pair == 2 ? 1 : 4); s *= 2) {
-                const int64_t at_once = h->max_clusters[pair * s];
-                const double t = static_cast<double>(cdiv(items, at_once)) * (step * static_cast<double>(cdiv(kb, s)) + (s > 1 ? 10.0 : 2.0)) + 4.0;
-                if (t < best) {
-                    best = t;
-                    pl.pair = pair;
-                    pl.bn = bn;
-                    pl.split = s;
+    Plan best{kRowsT, 1, 32, 1, 0, 0, 0, 0, 0};
+    double best_t = 1e300;
+    for (int form = kRows; form <= kRowsT; ++form)
+        for (int pair = 1; pair <= 2; ++pair)
+            for (int bn = 32; bn <= 256; bn += 32)
+                for (int s = 1; s * pair <= 8 && s <= 4; ++s) {
+                    if (form == kRows && bn < 128)
+                        continue;
+                    const int64_t at_once = h->max_clusters[pair * s];
+                    if (at_once < 1 || (s > 1 && kb < 4 * s))
+                        continue;
+                    const int bm = kPRows * pair;
+                    // groups of ragged size end in a partial tile: half a tile on average
+                    int64_t items;
+                    double n = bn;
+                    if (form == kRows) {
+                        items = (h->groups > 1 ? cdiv(rows, bm) + groups / 2 : cdiv(rows, bm)) * cdiv(out_cols, bn);
+                    } else {
+                        const int64_t tq = groups > 1 ? groups * cdiv(avg, bn) : cdiv(rows, bn);
+                        items = tq * cdiv(out_cols, bm);
+                        n = std::min<double>(bn, static_cast<double>(rows) / static_cast<double>(tq) + 16 * pair);
+                    }
+                    const double mma = std::max(2.0 * n, 64.0);
+                    const double fill = (16384.0 + bn * 128.0 / pair) / 64.0;
+                    const double step = std::max(mma, fill);
+                    const double waves = static_cast<double>(cdiv(items, at_once));
+                    double t = waves * (static_cast<double>(cdiv(kb, s)) * step + 400.0) + 6.0 * n;
+                    if (s > 1)
+                        t += 2500.0 + n * 512.0 * (s - 1) / s / 16.0;
+                    if (t < best_t) {
+                        best_t = t;
+                        best = Plan{form, pair, bn, s, 0, 0, 0, 0, 0};
+                    }
                 }
-            }
-        }
-    }
-    finish_plan(h, pl);
-    return pl;
+    finish_plan(h, best, best.form == kRows && w_mn);
+    return best;
 }
 
 Plan plan_reduce(const mlp_linear *h, int64_t p_ext, int64_t q_ext)
 {
-    Plan pl{kReduce, 2, 256, 1, 0, 0};
+    Plan pl{kReduce, 2, 256, 1, 0, 0, 0, 0, 0};
     if (h->groups * cdiv(p_ext, 256) * cdiv(q_ext, 256) * 2 < h->num_sms)
-        pl = Plan{kReduce, 1, 128, 1, 0, 0};
-    finish_plan(h, pl);
+        pl.pair = 1, pl.bn = 128;
+    finish_plan(h, pl, true);
     return pl;
 }
 
@@ -144,8 +161,11 @@ mlp_status launch(const mlp_linear *h, LinearParams &p, const Plan &pl, int64_t 
     p.raster = 16 / pl.pair;
     p.num_pipe = pl.pipe;
     p.slot_bytes = pl.slot;
-    // two accumulators; a split tile's parts may be narrower than the 32 columns read at a time
-    const uint32_t cols = 2u * static_cast<uint32_t>(pl.bn) + (pl.bn / pl.split < 32 ? 32u : 0u);
+    p.part_align = pl.part_align;
+    p.recv_bufs = pl.recv_bufs;
+    p.recv_bytes = pl.recv_bytes;
+    // two accumulators; parts of a split tile that are no multiple of 32 columns are over-read
+    const uint32_t cols = 2u * static_cast<uint32_t>(pl.bn) + (pl.split > 1 && pl.part_align < 32 ? 32u : 0u);
     p.tmem_cols = 32;
     while (p.tmem_cols < cols)
         p.tmem_cols *= 2;
@@ -153,12 +173,13 @@ mlp_status launch(const mlp_linear *h, LinearParams &p, const Plan &pl, int64_t 
     p.timeout_ns = static_cast<uint64_t>(h->d.timeout_us ? h->d.timeout_us : 2000000u) * 1000ull;
     const int cs = pl.pair * pl.split;
     const int clusters = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(items, h->max_clusters[cs])));
-    const size_t smem = linear_smem_bytes(pl.pipe, pl.slot, h->groups);
+    const size_t smem = linear_smem_bytes(pl.form == kRowsT, static_cast<uint32_t>(pl.pipe) * pl.slot,
+                                          static_cast<uint32_t>(pl.recv_bufs) * pl.recv_bytes, h->groups);
     bool ok = false;
     if (pl.form == kRows)
         ok = pl.pair == 2 ? launch_one<kRows, 2>(p, clusters, cs, smem, st) : launch_one<kRows, 1>(p, clusters, cs, smem, st);
     else if (pl.form == kRowsT)
-        ok = launch_one<kRowsT, 1>(p, clusters, cs, smem, st);
+        ok = pl.pair == 2 ? launch_one<kRowsT, 2>(p, clusters, cs, smem, st) : launch_one<kRowsT, 1>(p, clusters, cs, smem, st);
     else
         ok = pl.pair == 2 ? launch_one<kReduce, 2>(p, clusters, cs, smem, st) : launch_one<kReduce, 1>(p, clusters, cs, smem, st);
     return ok ? MLP_OK : MLP_ERR_CUDA;
@@ -168,12 +189,12 @@ mlp_status launch(const mlp_linear *h, LinearParams &p, const Plan &pl, int64_t 
 mlp_status rows_product(const mlp_linear *h, LinearParams &p, int64_t rows, const void *A, int64_t lda, const void *B,
                         int64_t out_cols, int64_t red, bool b_mn, cudaStream_t st)
 {
-    const Plan pl = plan_rows(h, rows, out_cols, red);
+    const Plan pl = plan_rows(h, rows, out_cols, red, b_mn);
     p.rows = static_cast<int32_t>(rows);
     p.k_ext = static_cast<int32_t>(red);
     CUtensorMap *mapA = pl.form == kRows ? &p.mapP : &p.mapQ, *mapB = pl.form == kRows ? &p.mapQ : &p.mapP;
     const int b_rows = pl.form == kRows ? pl.bn / pl.pair : kPRows;
-    if (!encode(mapA, A, red, rows, 1, lda, pl.form == kRows ? kPRows : pl.bn))
+    if (!encode(mapA, A, red, rows, 1, lda, pl.form == kRows ? kPRows : pl.bn / pl.pair))
         return MLP_ERR_CUDA;
     if (!(b_mn ? encode(mapB, B, out_cols, red, h->groups, out_cols, kKB) : encode(mapB, B, red, out_cols, h->groups, red, b_rows)))
         return MLP_ERR_CUDA;
@@ -187,7 +208,7 @@ mlp_status rows_product(const mlp_linear *h, LinearParams &p, int64_t rows, cons
         p.p_mn = b_mn;
         p.q_mn = 0;
         p.p_ext = static_cast<int32_t>(out_cols);
-        items = (cdiv(rows, pl.bn) + h->groups - 1) * cdiv(out_cols, kPRows);
+        items = (cdiv(rows, pl.bn) + h->groups - 1) * cdiv(out_cols, kPRows * pl.pair);
     }
     return launch(h, p, pl, items, st);
 }
@@ -374,11 +395,12 @@ extern "C" mlp_status mlp_linear_create(const mlp_linear_desc *d, mlp_linear_t *
         cudaFuncSetAttribute(linear_kernel<kRows, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
         cudaFuncSetAttribute(linear_kernel<kRows, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
         cudaFuncSetAttribute(linear_kernel<kRowsT, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
+        cudaFuncSetAttribute(linear_kernel<kRowsT, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
         cudaFuncSetAttribute(linear_kernel<kReduce, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
         cudaFuncSetAttribute(linear_kernel<kReduce, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) {
         st = MLP_ERR_CUDA;
     }
-    for (int cs = 1; cs <= 8 && st == MLP_OK; cs *= 2) {
+    for (int cs = 1; cs <= 8 && st == MLP_OK; ++cs) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -390,7 +412,7 @@ extern "C" mlp_status mlp_linear_create(const mlp_linear_desc *d, mlp_linear_t *
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<kRows, 1>, &cfg) != cudaSuccess || n < 1)
+        if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<kRows, 1>, &cfg) != cudaSuccess || (n < 1 && cs <= 2))
             st = MLP_ERR_CUDA;
         h->max_clusters[cs] = n;
     }
@@ -585,8 +607,8 @@ extern "C" mlp_status mlp_linear_get_plan(mlp_linear_t h, int64_t rows, int32_t 
     if (!h || !plan || rows < 1 || pass < 0 || pass > 2)
         return MLP_ERR_INVALID_ARG;
     const bool kn = h->d.weight_layout == 0;
-    const Plan pl = pass == 0   ? plan_rows(h, rows, h->d.N, h->d.K)
-                    : pass == 1 ? plan_rows(h, rows, h->d.K, h->d.N)
+    const Plan pl = pass == 0   ? plan_rows(h, rows, h->d.N, h->d.K, kn)
+                    : pass == 1 ? plan_rows(h, rows, h->d.K, h->d.N, !kn)
                                 : plan_reduce(h, kn ? h->d.K : h->d.N, kn ? h->d.N : h->d.K);
     plan->form = pl.form;
     plan->cta_pair = pl.pair;

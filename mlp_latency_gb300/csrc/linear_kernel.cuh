@@ -20,8 +20,9 @@
 //
 // kPair = 2 runs 256-row tiles on CTA pairs (cta_group::2): each CTA loads its 128 rows of P and half
 // of Q's tile, a third less to fetch per SM and flop.  split > 1 shares one tile's reduction among the
-// CTAs of a cluster: partial sums travel through distributed shared memory into the ring, which is
-// idle by then, and are added in slice order, so the result does not depend on timing.
+// CTAs (or pairs) of a cluster, each taking a range of k blocks; every CTA then finishes a range of the
+// tile's columns, for which the others send it their partial sums through distributed shared memory, and
+// adds them in slice order, so the result does not depend on timing.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -43,6 +44,12 @@ constexpr int kMaxRing = 10;
 constexpr uint32_t kStageWarpBytes = 32 * 128; // epilogue staging: 32 rows x 128 bytes per warp
 constexpr uint32_t kStTimeout = 5, kStBadOffsets = 1;
 
+// Shared memory of one CTA's share of a Q tile: `cols` K-major rows of 128 bytes, or whole boxes of 64 columns.
+__host__ __device__ inline uint32_t q_tile_bytes(int32_t cols, bool mn)
+{
+    return mn ? static_cast<uint32_t>((cols + 63) / 64) * kBoxBytes : static_cast<uint32_t>(cols) * 128u;
+}
+
 struct LinearParams {
     CUtensorMap mapP, mapQ;         // (inner, outer, group) views
     const int32_t *offsets;         // device, groups + 1 entries, or null: one group of `rows` rows
@@ -50,7 +57,10 @@ struct LinearParams {
     int32_t p_ext, q_ext, k_ext;    // extents of the dimensions that are not ragged
     int32_t p_mn, q_mn;             // operand stored MN-major (else K-major)
     int32_t bn;                     // columns of a tile (the pair's)
-    int32_t split;                  // CTAs (kPair = 1) sharing a tile's reduction
+    int32_t split;                  // CTAs, or pairs, sharing a tile's reduction
+    int32_t part_align;             // granularity of the column ranges that they finish: 8 or 32
+    int32_t recv_bufs;              // receive buffers for partial sums, of recv_bytes each; 0: the ring
+    uint32_t recv_bytes;            // serves as the one buffer and the next tile's copies wait for it
     int32_t raster;                 // row panels sharing a sweep over the column tiles
     int32_t num_pipe;
     uint32_t slot_bytes;
@@ -69,25 +79,29 @@ struct LinearParams {
 struct __align__(8) LCtrl {
     uint64_t full[kMaxRing], empty[kMaxRing], go[kMaxRing], tail[kMaxRing];
     uint64_t tfull[2], tempty[2];
-    uint64_t drain, rdy, got, ringfree;
+    uint64_t drain, rdy[2], got[2], ringfree;
     uint32_t tmem_base;
     volatile int32_t abort_flag;
     int32_t skip;
     int32_t n_items;
 };
 
-// Shared memory: ring (1024-byte aligned), epilogue staging, bias tile per epilogue warp, control
-// block, group tables.
-__host__ __device__ inline uint32_t ls_stage(int num_pipe, uint32_t slot) { return static_cast<uint32_t>(num_pipe) * slot; }
-__host__ __device__ inline uint32_t ls_bias(int num_pipe, uint32_t slot) { return ls_stage(num_pipe, slot) + 4u * kStageWarpBytes; }
-__host__ __device__ inline uint32_t ls_ctrl(int num_pipe, uint32_t slot) { return ls_bias(num_pipe, slot) + 4u * 256u * 4u; }
-__host__ __device__ inline uint32_t ls_tab(int num_pipe, uint32_t slot)
+// Shared memory: ring (1024-byte aligned), receive buffers, epilogue staging and bias tile per epilogue
+// warp (kRowsT needs neither), control block, group tables.
+struct SmemMap {
+    uint32_t recv, stage, bias, ctrl, tab;
+    __host__ __device__ SmemMap(bool rows_t, uint32_t ring_bytes, uint32_t recv_total)
+    {
+        recv = ring_bytes;
+        stage = recv + recv_total;
+        bias = stage + (rows_t ? 0u : 4u * kStageWarpBytes);
+        ctrl = bias + (rows_t ? 0u : 4u * 256u * 4u);
+        tab = ctrl + static_cast<uint32_t>((sizeof(LCtrl) + 15) / 16 * 16);
+    }
+};
+__host__ inline size_t linear_smem_bytes(bool rows_t, uint32_t ring_bytes, uint32_t recv_total, int groups)
 {
-    return ls_ctrl(num_pipe, slot) + static_cast<uint32_t>((sizeof(LCtrl) + 15) / 16 * 16);
-}
-__host__ inline size_t linear_smem_bytes(int num_pipe, uint32_t slot, int groups)
-{
-    return 1024 + ls_tab(num_pipe, slot) + (3 * static_cast<size_t>(groups) + 1) * 4;
+    return 1024 + SmemMap(rows_t, ring_bytes, recv_total).tab + (3 * static_cast<size_t>(groups) + 1) * 4;
 }
 
 __device__ __forceinline__ uint64_t policy_evict_normal()
@@ -179,6 +193,7 @@ struct GroupTab {
 struct Tile {
     int32_t e, start, cnt;
     int32_t p0, q0;      // origin in the P and Q extents (inside the group's rows for a ragged one)
+    int32_t n;           // MMA columns: bn, or what is left of the group's rows for kRowsT
     int32_t kb0, kb1;    // k blocks of this CTA's slice
 };
 
@@ -199,7 +214,7 @@ struct Walk {
     int32_t id, step, e, slice;
     __device__ __forceinline__ Walk(const LinearParams &p)
         : id(static_cast<int32_t>(cluster_id_x())), step(static_cast<int32_t>(num_clusters_x())), e(0),
-          slice(kPair == 1 && p.split > 1 ? static_cast<int32_t>(cluster_ctarank()) : 0)
+          slice(p.split > 1 ? static_cast<int32_t>(cluster_ctarank()) / kPair : 0)
     {
     }
     __device__ __forceinline__ bool next(const LinearParams &p, const GroupTab &g, int32_t n_items, Tile &t)
@@ -220,6 +235,7 @@ struct Walk {
             const int32_t tq = (t.cnt + p.bn - 1) / p.bn;
             t.p0 = i / tq * bm;
             t.q0 = i % tq * p.bn;
+            t.n = min(p.bn, (t.cnt - t.q0 + 16 * kPair - 1) / (16 * kPair) * (16 * kPair));   // (the MMA's step)
         } else {
             const int32_t tp = ((kForm == kRows ? t.cnt : p.p_ext) + bm - 1) / bm;
             const int32_t tq = (p.q_ext + p.bn - 1) / p.bn;
@@ -227,8 +243,9 @@ struct Walk {
             const int32_t h = min(p.raster, tp - first), r = i - first * tq;
             t.q0 = r / h * p.bn;
             t.p0 = (first + r % h) * bm;
+            t.n = p.bn;
         }
-        if (kPair == 1 && p.split > 1) {
+        if (p.split > 1) {
             const int32_t per = (nkb + p.split - 1) / p.split;
             t.kb0 = min(slice * per, nkb);
             t.kb1 = min(t.kb0 + per, nkb);
@@ -257,13 +274,14 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
 {
     const int32_t num_pipe = p.num_pipe;
     const uint32_t slot_bytes = p.slot_bytes;
-    const uint32_t half = kPair == 2 ? (cluster_ctarank() & 1u) : 0u;
-    const uint32_t full_lead0 = kPair == 2 ? map_to_rank(&c->full[0], 0) : 0u;
-    const uint32_t go_peer0 = kPair == 2 ? map_to_rank(&c->go[0], 1) : 0u;
-    const uint32_t tail_own0 = kPair == 2 ? map_to_rank(&c->tail[0], half) : 0u;
-    const int32_t bn_cta = p.bn / kPair;
-    const uint32_t q_bytes = static_cast<uint32_t>(bn_cta) * kKB * 2;
+    const uint32_t rank = cluster_ctarank();
+    const uint32_t half = kPair == 2 ? (rank & 1u) : 0u;
+    const uint32_t full_lead0 = kPair == 2 ? map_to_rank(&c->full[0], rank & ~1u) : 0u;
+    const uint32_t go_peer0 = kPair == 2 ? map_to_rank(&c->go[0], rank | 1u) : 0u;
+    const uint32_t tail_own0 = kPair == 2 ? map_to_rank(&c->tail[0], rank) : 0u;
     const bool p_mn = p.p_mn != 0, q_mn = p.q_mn != 0;
+    const int32_t bn_cta = p.bn / kPair;
+    const uint32_t q_bytes = q_tile_bytes(bn_cta, q_mn);
     const int32_t n_items = c->n_items;
     // the ragged operand is read by many tiles, weights by the row panels of one group at a time
     const uint64_t pol = policy_evict_normal();
@@ -276,7 +294,7 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
     uint32_t item_ph = 0;
     bool first = true;
     while (ok && w.next(p, g, n_items, t)) {
-        if (kPair == 1 && p.split > 1) {   // the ring was the exchange buffer of the previous item
+        if (p.split > 1 && p.recv_bufs == 0) {   // the ring was the exchange buffer of the previous item
             if (!first) {
                 if (!lwait(&c->ringfree, item_ph, c, p))
                     break;
@@ -285,7 +303,7 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
             first = false;
         }
         const int32_t p_row = (kForm == kRows ? t.start : 0) + t.p0 + static_cast<int32_t>(half) * kPRows;
-        const int32_t q_row = (kForm == kRowsT ? t.start : 0) + t.q0 + static_cast<int32_t>(half) * bn_cta;
+        const int32_t q_row = (kForm == kRowsT ? t.start : 0) + t.q0 + static_cast<int32_t>(half) * (t.n / kPair);
         const int32_t p_grp = kForm == kRowsT ? t.e : 0, q_grp = kForm == kRows ? t.e : 0;
         for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
             if (kPair == 2 && half) {
@@ -364,8 +382,8 @@ __device__ __forceinline__ void l_role_mma(const LinearParams &p, LCtrl *c, cons
         return;   // the leader issues for both
     const int32_t num_pipe = p.num_pipe;
     const uint32_t bn = static_cast<uint32_t>(p.bn);
-    const uint32_t tfull_peer0 = kPair == 2 ? map_to_rank(&c->tfull[0], 1) : 0u;
-    const uint32_t idesc = idesc_bf16_f32(kPRows * kPair, bn, p.q_mn ? 1u : 0u) | (p.p_mn ? 1u << 15 : 0u);
+    const uint32_t tfull_peer0 = kPair == 2 ? map_to_rank(&c->tfull[0], cluster_ctarank() | 1u) : 0u;
+    const uint32_t idesc0 = idesc_bf16_f32(kPRows * kPair, 0, p.q_mn ? 1u : 0u) | (p.p_mn ? 1u << 15 : 0u);
     const uint32_t base = smem_u32(ring);
     // K-major: 8-row groups 1024 bytes apart, a 16-deep k step 32 bytes along the row.  MN-major: 64
     // columns x 64 k per box, boxes kBoxBytes apart, a k step 16 rows of 128 bytes.  Slot offsets add to
@@ -386,6 +404,7 @@ __device__ __forceinline__ void l_role_mma(const LinearParams &p, LCtrl *c, cons
             break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * bn;
+        const uint32_t idesc = idesc0 | (static_cast<uint32_t>(t.n) >> 3) << 17;
         uint32_t accum = 0;
         for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
             if (!lwait(&c->full[ps], pph, c, p, kPair == 2)) {
@@ -424,8 +443,8 @@ __device__ __forceinline__ void l_role_mask(const LinearParams &p, LCtrl *c, con
 {
     const int32_t lane = threadIdx.x & 31;
     const int32_t num_pipe = p.num_pipe;
-    const uint32_t boxes = 2u + static_cast<uint32_t>(p.bn / kPair) / 64u;   // P's two, then Q's
-    const uint32_t full_lead0 = kPair == 2 ? map_to_rank(&c->full[0], 0) : 0u;
+    const uint32_t boxes = (kPBytes + q_tile_bytes(p.bn / kPair, true)) / kBoxBytes;   // P's two, then Q's
+    const uint32_t full_lead0 = kPair == 2 ? map_to_rank(&c->full[0], cluster_ctarank() & ~1u) : 0u;
     const int32_t n_items = c->n_items;
     uint32_t fills = 0, tail_ph = 0;
     Walk<kReduce, kPair> w(p);
@@ -502,7 +521,7 @@ template <int kPair>
 __device__ __forceinline__ void free_acc(LCtrl *c, uint32_t acc)
 {
     if (kPair == 2)
-        mbar_arrive_cluster(map_to_rank(&c->tempty[acc], 0));
+        mbar_arrive_cluster(map_to_rank(&c->tempty[acc], cluster_ctarank() & ~1u));
     else
         mbar_arrive(&c->tempty[acc]);
 }
@@ -606,31 +625,37 @@ __device__ __forceinline__ void finish_rows_t(const LinearParams &p, float (&v)[
 }
 
 template <int kForm, int kPair>
-__device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring,
+__device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *recv_base,
                                                 uint8_t *stage_all, float *bias_all, uint32_t tmem_base)
 {
     const int32_t ew = static_cast<int32_t>(threadIdx.x / 32) - 4;   // = warp % 4: its TMEM lane quarter
     const int32_t lane = threadIdx.x & 31;
-    const uint32_t half = kPair == 2 ? (cluster_ctarank() & 1u) : 0u;
+    const uint32_t rank = cluster_ctarank();
+    const uint32_t half = kPair == 2 ? (rank & 1u) : 0u;
     uint8_t *stage = stage_all + ew * kStageWarpBytes;
     float *bias_s = bias_all + ew * 256;
     const int32_t bn = p.bn;
     const int32_t n_items = c->n_items;
-    const bool splitk = kPair == 1 && p.split > 1;
+    const bool splitk = p.split > 1;
     const int32_t S = splitk ? p.split : 1;
-    const int32_t part = bn / S;                 // columns this CTA finishes
-    const int32_t me = splitk ? static_cast<int32_t>(cluster_ctarank()) : 0;
+    const int32_t me = splitk ? static_cast<int32_t>(rank) / kPair : 0;
+    const int32_t nbuf = p.recv_bufs > 0 ? p.recv_bufs : 1;
+    auto cta_of = [&](int32_t slice) { return static_cast<uint32_t>(slice * kPair) + half; };   // same half, other slice
     const uint32_t lane_base = static_cast<uint32_t>(ew * 32) << 16;
     uint32_t tiles = 0;
+    int32_t buf = 0;           // receive buffer of this item, and how often it was used before (parity)
+    uint32_t buf_ph = 0;
     Walk<kForm, kPair> w(p);
     Tile t;
     while (w.next(p, g, n_items, t)) {
         const uint32_t acc = tiles & 1u;
         const uint32_t ph = (tiles >> 1) & 1u;
-        const int32_t c_lo = me * part, c_hi = c_lo + part;   // this CTA's columns of the tile
+        // the columns of the tile that this CTA finishes
+        const int32_t part = splitk ? ((t.n + S - 1) / S + p.part_align - 1) / p.part_align * p.part_align : t.n;
+        const int32_t c_lo = min(me * part, t.n), c_hi = min(c_lo + part, t.n);
         // ---- bias of the tile, while its MMAs run
         float bias_t = 0.0f;
-        const int32_t n_t = t.p0 + ew * 32 + lane;             // kRowsT: this lane's output column
+        const int32_t n_t = t.p0 + static_cast<int32_t>(half) * kPRows + ew * 32 + lane;   // kRowsT: this lane's output column
         if (p.bias) {
             if (kForm == kRowsT) {
                 if (n_t < p.p_ext)
@@ -647,23 +672,29 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
         tc_fence_after();
         const uint32_t d = tmem_base + acc * static_cast<uint32_t>(bn) + lane_base;
         const bool have_k = t.kb1 > t.kb0;
-        const uint32_t item_ph = tiles & 1u;
+        uint8_t *recv = recv_base + static_cast<uint32_t>(buf) * p.recv_bytes;
         if (splitk) {
-            // Every CTA's MMAs of this item are done, so every ring is free to receive.
-            if (lane == 0) {
-                for (int32_t r = 0; r < S; ++r)
-                    mbar_arrive_cluster(map_to_rank(&c->rdy, static_cast<uint32_t>(r)));
+            // Wait until the others can receive: with the ring as buffer, until every CTA's MMAs of this
+            // item are done; with buffers of their own, until they have read this one's previous content.
+            if (p.recv_bufs == 0) {
+                if (lane == 0)
+                    for (int32_t r = 0; r < S; ++r)
+                        mbar_arrive_cluster(map_to_rank(&c->rdy[0], cta_of(r)));
+                if (!lwait_warp(&c->rdy[0], buf_ph, c, p, true))
+                    return;
+            } else if (tiles >= static_cast<uint32_t>(nbuf)) {
+                if (!lwait_warp(&c->rdy[buf], buf_ph ^ 1u, c, p, true))
+                    return;
             }
-            if (!lwait_warp(&c->rdy, item_ph, c, p, true))
-                return;
-            // parts of 8 columns: [source slot][4-column block][128 lanes] float4
+            // layout: [source][4-column block][128 lanes] float4
             for (int32_t o = 1; o < S; ++o) {
                 const int32_t r = (me + o) % S;
-                const uint32_t dst = map_to_rank(ring, static_cast<uint32_t>(r));
+                const uint32_t dst = map_to_rank(recv, cta_of(r));
                 const int32_t slot = me < r ? me : me - 1;
-                for (int32_t j = 0; j < part; j += 8) {
+                const int32_t r_lo = min(r * part, t.n), r_n = min(part, t.n - r_lo);
+                for (int32_t j = 0; j < r_n; j += 8) {
                     uint32_t x[8];
-                    tmem_ld_32x32b_x8(d + static_cast<uint32_t>(r * part + j), x);
+                    tmem_ld_32x32b_x8(d + static_cast<uint32_t>(r_lo + j), x);
                     tmem_ld_wait();
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
@@ -679,8 +710,8 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
             __syncwarp();
             if (lane == 0)
                 for (int32_t o = 1; o < S; ++o)
-                    mbar_arrive_cluster(map_to_rank(&c->got, static_cast<uint32_t>((me + o) % S)));
-            if (!lwait_warp(&c->got, item_ph, c, p, true))
+                    mbar_arrive_cluster(map_to_rank(&c->got[buf], cta_of((me + o) % S)));
+            if (!lwait_warp(&c->got[buf], buf_ph, c, p, true))
                 return;
         }
         // Accumulator columns [col, col + 32) of this lane, partial sums of all slices in slice order.
@@ -698,7 +729,7 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                     own[j] = v[j];
                     v[j] = 0.0f;
                 }
-                const int32_t blocks = min(8, (c_hi - col) / 4);
+                const int32_t blocks = min(8, (c_hi - col + 3) / 4);
                 for (int32_t s = 0; s < S; ++s) {
                     if (s == me) {
 #pragma unroll
@@ -711,7 +742,7 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                     for (int b = 0; b < 8; ++b) {
                         if (b < blocks) {
                             const float4 q = *reinterpret_cast<const float4 *>(
-                                ring + (static_cast<uint32_t>(slot * (part / 4) + (col - c_lo) / 4 + b) * 128u +
+                                recv + (static_cast<uint32_t>(slot * (part / 4) + (col - c_lo) / 4 + b) * 128u +
                                         static_cast<uint32_t>(ew * 32 + lane)) * 16u);
                             v[4 * b] += q.x;
                             v[4 * b + 1] += q.y;
@@ -773,16 +804,23 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
         }
         tc_fence_before();
         __syncwarp();
-        if (splitk) {
+        if (splitk && p.recv_bufs == 0) {
             fence_proxy_async_shared();   // these reads of the ring before the producer's next copies
             __syncwarp();
         }
         if (lane == 0) {
             free_acc<kPair>(c, acc);
-            if (splitk)
+            if (splitk && p.recv_bufs == 0)
                 mbar_arrive(&c->ringfree);
+            else if (splitk)
+                for (int32_t o = 1; o < S; ++o)
+                    mbar_arrive_cluster(map_to_rank(&c->rdy[buf], cta_of((me + o) % S)));
         }
         ++tiles;
+        if (++buf == nbuf) {
+            buf = 0;
+            buf_ph ^= 1u;
+        }
     }
 }
 
@@ -793,9 +831,11 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + (((base + 1023u) & ~1023u) - base);
-    LCtrl *c = reinterpret_cast<LCtrl *>(ring + ls_ctrl(p.num_pipe, p.slot_bytes));
+    const SmemMap sm(kForm == kRowsT, static_cast<uint32_t>(p.num_pipe) * p.slot_bytes,
+                     static_cast<uint32_t>(p.recv_bufs) * p.recv_bytes);
+    LCtrl *c = reinterpret_cast<LCtrl *>(ring + sm.ctrl);
     GroupTab g;
-    g.start = reinterpret_cast<int32_t *>(ring + ls_tab(p.num_pipe, p.slot_bytes));
+    g.start = reinterpret_cast<int32_t *>(ring + sm.tab);
     g.cnt = g.start + p.groups;
     g.base = g.cnt + p.groups;
     const int32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -818,8 +858,10 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
         if (lane == 0) {
             const int32_t S = p.split > 1 ? p.split : 1;
             mbar_init(&c->drain, 1);
-            mbar_init(&c->rdy, 4 * S);                       // every CTA's four epilogue warps
-            mbar_init(&c->got, S > 1 ? 4 * (S - 1) : 1);     // the other CTAs' four warps
+            for (int b = 0; b < 2; ++b) {   // four epilogue warps of the other CTAs (and, sharing the ring, this one)
+                mbar_init(&c->rdy[b], p.recv_bufs == 0 ? 4 * S : S > 1 ? 4 * (S - 1) : 1);
+                mbar_init(&c->got[b], S > 1 ? 4 * (S - 1) : 1);
+            }
             mbar_init(&c->ringfree, 4);
             c->abort_flag = 0;
             c->skip = ld_relaxed_gpu_u32(p.status) != 0;     // sticky error: do nothing
@@ -877,8 +919,8 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
             if (kForm == kReduce && p.offsets)
                 l_role_mask<kPair>(p, c, g, ring);
         } else if (warp >= 4) {
-            l_role_epilogue<kForm, kPair>(p, c, g, ring, ring + ls_stage(p.num_pipe, p.slot_bytes),
-                                          reinterpret_cast<float *>(ring + ls_bias(p.num_pipe, p.slot_bytes)), tmem_base);
+            l_role_epilogue<kForm, kPair>(p, c, g, ring + (p.recv_bufs ? sm.recv : 0u), ring + sm.stage,
+                                          reinterpret_cast<float *>(ring + sm.bias), tmem_base);
         }
     }
     __syncwarp();
