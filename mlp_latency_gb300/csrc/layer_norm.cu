@@ -128,6 +128,253 @@ struct NormParams {
     int32_t blocks;
 };
 
+// As team_sum over a block, once per row of a loop: the scratch alternates between two halves (`parity`), so
+// one barrier suffices (a thread cannot be two rows ahead of another).
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float (*scratch)[N][32], int parity)
+{
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, warps = blockDim.x / 32;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        v[n] = warp_sum(v[n]);
+    if (lane == 0)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            scratch[parity][n][warp] = v[n];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        v[n] = warp_sum(lane < warps ? scratch[parity][n][lane] : 0.0f);
+}
+
+// ------------------------------------------------------------------------- rows through a ring --
+// A block walks over rows; the next rows are on their way into shared memory while it works on one.  Each
+// thread copies exactly the columns that it reads, so the copies need no barrier, only the thread's own
+// wait_group.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void *dst, const void *src)
+{
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory"); }
+
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// kStages slots of kBufs rows; kStages = 0: no ring, rows are read where they are.
+template <typename T, int V, int kItems, int kStages>
+struct RowRing {
+    static constexpr int kBytes = V * static_cast<int>(sizeof(T));
+    uint8_t *base;
+    int bufs;
+    __device__ __forceinline__ uint8_t *slot(int stage, int buf, int i) const
+    {
+        return base + (static_cast<size_t>((stage * bufs + buf) * kItems + i) * blockDim.x + threadIdx.x) * kBytes;
+    }
+    __device__ __forceinline__ void fetch(int stage, int buf, const T *row, int cols) const
+    {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int c = (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
+            if (c < cols)
+                copy_async<kBytes>(slot(stage, buf, i), row + c);
+        }
+    }
+    __device__ __forceinline__ void read(int stage, int buf, int i, const T *row, int c, float (&f)[V]) const
+    {
+        if constexpr (kStages > 0)
+            load<T, V>(reinterpret_cast<const T *>(slot(stage, buf, i)), f);
+        else
+            load<T, V>(row + c, f);
+    }
+};
+
+// Forward over many rows: bounded by memory (2 C elements per row); measured below the estimate of one row per
+// block because a block's two reductions leave the memory system idle.
+template <typename T, int V, int kItems, int kStages>
+__global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float s1[2][1][32], s2[2][1][32];
+    const RowRing<T, V, kItems, kStages> ring{smem, 1};
+    const int64_t step = gridDim.x;
+    const int cols = static_cast<int>(p.cols);
+    const T *x = static_cast<const T *>(p.x);
+    int64_t row = blockIdx.x;
+    for (int s = 0; s < kStages - 1; ++s) {
+        if (row + s * step < p.rows)
+            ring.fetch(s, 0, x + (row + s * step) * p.ldx, cols);
+        copy_commit();
+    }
+    int stage = 0, parity = 0;
+    for (; row < p.rows; row += step, parity ^= 1) {
+        copy_wait<kStages - 2>();
+        const int64_t ahead = row + (kStages - 1) * step;
+        if (ahead < p.rows)
+            ring.fetch((stage + kStages - 1) % kStages, 0, x + ahead * p.ldx, cols);
+        copy_commit();
+        float v[kItems][V], s[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int c = (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
+            if (c < cols) {
+                ring.read(stage, 0, i, nullptr, c, v[i]);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    s[0] += v[i][j];
+            }
+        }
+        block_sum<1>(s, s1, parity);
+        const float mean = s[0] / static_cast<float>(p.cols);
+        s[0] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+            if ((i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V < cols)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float d = v[i][j] - mean;
+                    s[0] = fmaf(d, d, s[0]);
+                }
+        block_sum<1>(s, s2, parity);
+        const float rstd = rsqrtf(fmaf(s[0], p.inv_cols, p.eps));
+        if (threadIdx.x == 0) {
+            if (p.mean)
+                p.mean[row] = mean;
+            if (p.rstd)
+                p.rstd[row] = rstd;
+        }
+        T *y = static_cast<T *>(p.y) + row * p.ldy;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int c = (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
+            if (c < cols) {
+                float g[V], b[V], o[V];
+                load_w<V>(p.gamma, p.w_kind, c, 1.0f, g);
+                load_w<V>(p.beta, p.w_kind, c, 0.0f, b);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    o[j] = fmaf((v[i][j] - mean) * rstd, g[j], b[j]);
+                store<T, V>(y + c, o);
+            }
+        }
+        stage = (stage + 1) % kStages;
+    }
+}
+
+// Backward: dx of each row, and this block's column sums of dy xh and dy in registers (each thread keeps its
+// columns from row to row), so x and dy are read once for all three gradients.  The sums of the blocks are
+// added by norm_colsum_finish_kernel.
+template <typename T, int V, int kItems, int kStages>
+__global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float scratch[2][2][32];
+    constexpr int kS = kStages > 0 ? kStages : 1;
+    const RowRing<T, V, kItems, kStages> ring{smem, p.add ? 3 : 2};
+    const int64_t step = gridDim.x;
+    const int cols = static_cast<int>(p.cols);
+    const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy), *add = static_cast<const T *>(p.add);
+    griddep_launch_dependents();   // the finishing kernel waits for this grid by itself
+    float ag[kItems][V], ab[kItems][V];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            ag[i][j] = ab[i][j] = 0.0f;
+    auto fetch = [&](int stage, int64_t row) {
+        if (row < p.rows) {
+            ring.fetch(stage, 0, x + row * p.ldx, cols);
+            ring.fetch(stage, 1, dy + row * p.lddy, cols);
+            if (add)
+                ring.fetch(stage, 2, add + row * p.ldadd, cols);
+        }
+        copy_commit();
+    };
+    int64_t row = blockIdx.x;
+    if constexpr (kStages > 0)
+        for (int s = 0; s < kS - 1; ++s)
+            fetch(s, row + s * step);
+    float mean = row < p.rows ? p.mean_in[row] : 0.0f, rstd = row < p.rows ? p.rstd_in[row] : 0.0f;
+    int stage = 0, parity = 0;
+    for (; row < p.rows; row += step, parity ^= 1) {
+        if constexpr (kStages > 0) {
+            copy_wait<kS - 2>();
+            fetch((stage + kS - 1) % kS, row + (kS - 1) * step);
+        }
+        const int64_t next = row + step < p.rows ? row + step : row;
+        const float mean_next = p.mean_in[next], rstd_next = p.rstd_in[next];
+        const T *xr = x + row * p.ldx, *dr = dy + row * p.lddy;
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int c = (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
+            if (c < cols) {
+                float a[V], d[V], g[V];
+                ring.read(stage, 0, i, xr, c, a);
+                ring.read(stage, 1, i, dr, c, d);
+                load_w<V>(p.gamma, p.w_kind, c, 1.0f, g);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float xh = (a[j] - mean) * rstd, gd = g[j] * d[j];
+                    ab[i][j] += d[j];
+                    ag[i][j] = fmaf(d[j], xh, ag[i][j]);
+                    s[0] += gd;
+                    s[1] = fmaf(gd, xh, s[1]);
+                }
+            }
+        }
+        if (p.dx) {
+            block_sum<2>(s, scratch, parity);
+            const float m0 = s[0] * p.inv_cols, m1 = s[1] * p.inv_cols;
+            T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int c = (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
+                if (c < cols) {
+                    float a[V], d[V], g[V], o[V];
+                    ring.read(stage, 0, i, xr, c, a);
+                    ring.read(stage, 1, i, dr, c, d);
+                    load_w<V>(p.gamma, p.w_kind, c, 1.0f, g);
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        o[j] = rstd * (fmaf(g[j], d[j], -m0) - (a[j] - mean) * rstd * m1);
+                    if (add) {
+                        float r[V];
+                        ring.read(stage, 2, i, add + row * p.ldadd, c, r);
+#pragma unroll
+                        for (int j = 0; j < V; ++j)
+                            o[j] += r[j];
+                    }
+                    store<T, V>(dx + c, o);
+                }
+            }
+        }
+        mean = mean_next;
+        rstd = rstd_next;
+        stage = (stage + 1) % kS;
+    }
+    if (p.part) {
+        float *out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.cols;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int c = (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
+            if (c < cols)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {   // (cols may be odd: no vector store)
+                    out[c + j] = ag[i][j];
+                    out[cols + c + j] = ab[i][j];
+                }
+        }
+    }
+}
+
 // One row per team, the row in registers (kItems vectors of V per thread): moments, then the output.
 template <typename T, int V, int kItems, bool kWarpTeam, int kThreads>
 __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormParams p)
@@ -312,27 +559,29 @@ __global__ void __launch_bounds__(256) norm_colsum_kernel(const NormParams p)
     }
 }
 
-// dgamma and dbeta: the partial rows in block order.  32 columns per block, 8 interleaved row sets.
-__global__ void __launch_bounds__(256) norm_colsum_finish_kernel(const NormParams p, void *dgamma, void *dbeta)
+// dgamma and dbeta: the blocks' partial rows.  32 columns per block, 32 interleaved sets of rows (a column's
+// loads are few and go out together), added in a fixed order.
+__global__ void __launch_bounds__(1024) norm_colsum_finish_kernel(const NormParams p, void *dgamma, void *dbeta)
 {
-    __shared__ float red[8][33];
+    __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, set = threadIdx.x / 32;
     const int w = blockIdx.y;
     void *out = w ? dbeta : dgamma;
+    griddep_wait();
     if (!out)
         return;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float s = 0.0f;
     if (c < p.cols)
-#pragma unroll 4
-        for (int b = set; b < p.blocks; b += 8)
+#pragma unroll 8
+        for (int b = set; b < p.blocks; b += 32)
             s += p.part[(static_cast<int64_t>(b) * 2 + w) * p.cols + c];
     red[set][lane] = s;
     __syncthreads();
     if (set == 0 && c < p.cols) {
         s = 0.0f;
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
+        for (int q = 0; q < 32; ++q)
             s += red[q][lane];
         if (p.w_f32)
             static_cast<float *>(out)[c] = s;
@@ -343,7 +592,39 @@ __global__ void __launch_bounds__(256) norm_colsum_finish_kernel(const NormParam
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int kColsumBlocks = 64;   // row blocks of the column sums, at most
+constexpr int kSms = 152;
+constexpr int kColsumBlocks = 64;     // row blocks of the two-kernel backward pass, at most
+constexpr int kMaxBlocks = 8 * kSms;  // blocks of the fused one
+constexpr int64_t kFusedCols = 16384; // its widest rows
+constexpr size_t kRingLimit = 200 * 1024;
+
+// Vectors per thread of the kernels that walk over rows, for at most 512 threads and 32 columns a thread (16 of
+// the narrow kinds).  0: too wide.
+int ring_items(int64_t nvec, int v)
+{
+    if (v <= 2)
+        return nvec <= 4 * 512 ? 4 : nvec <= 16 * 512 ? 16 : 0;
+    if (nvec <= 256)
+        return 1;
+    for (int items = 2; items <= 32 / v; items *= 2)
+        if (nvec <= 512 * items)
+            return items;
+    return 0;
+}
+
+// Blocks of the fused backward kernel: small blocks share an SM, wide rows take one each.
+int fused_blocks(int64_t rows, int threads)
+{
+    const int per_sm = std::max(1, std::min(8, 768 / threads));
+    return static_cast<int>(std::min<int64_t>(rows, static_cast<int64_t>(per_sm) * kSms));
+}
+
+template <typename K>
+bool allow_smem(K *kernel, size_t bytes)
+{
+    return bytes <= 47 * 1024 ||   // (the blocks also hold up to 1 KB of static shared memory)
+           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess;
+}
 
 bool aligned(const void *p, int64_t ld, size_t esz, size_t bytes)
 {
@@ -369,15 +650,39 @@ void launch_forward(const NormParams &p, int64_t nvec, cudaStream_t st)
     }
 }
 
-// Vectors per thread.  Few rows: one, so that a row's loads go out at once from as many threads as there
-// are.  Many rows: four, so that several rows share an SM and one row's reductions hide behind the others'
-// loads.  Wider rows take what fits a block's registers.
+template <typename T, int V, int kItems>
+bool launch_forward_ring(const NormParams &p, int64_t nvec, cudaStream_t st)
+{
+    constexpr int kStages = 4;
+    const int threads = static_cast<int>(cdiv(cdiv(nvec, kItems), 32) * 32);
+    const size_t smem = static_cast<size_t>(kStages) * kItems * threads * V * sizeof(T);
+    const int per_sm = std::max(1, std::min({8, 1024 / threads, static_cast<int>(kRingLimit / smem)}));
+    auto kernel = norm_forward_ring_kernel<T, V, kItems, kStages>;
+    if (smem > kRingLimit || !allow_smem(kernel, smem))
+        return false;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.rows, static_cast<int64_t>(per_sm) * kSms));
+    kernel<<<grid, threads, smem, st>>>(p);
+    return true;
+}
+
+// Few rows: one vector per thread and one row per block, so that a row's loads go out at once from as many
+// threads as there are.  Many rows: narrow ones a warp each, wide ones through the ring.  What fits neither
+// (rows that are not 16-byte aligned, very wide ones) takes more vectors per thread, then three passes.
 template <typename T, int V>
 void forward_v(const NormParams &p, cudaStream_t st)
 {
     const int64_t nvec = cdiv(p.cols, V);
-    const bool many = p.rows > 304;
-    if (nvec <= (many ? 64 : 1024))
+    const bool many = p.rows > 2 * kSms;
+    if constexpr (V * sizeof(T) == 16) {
+        if (many && nvec > 128) {
+            const int items = ring_items(nvec, V);
+            if ((items == 1 && launch_forward_ring<T, V, 1>(p, nvec, st)) ||
+                (items == 2 && launch_forward_ring<T, V, 2>(p, nvec, st)) ||
+                (items >= 4 && nvec <= 2048 && launch_forward_ring<T, V, 4>(p, nvec, st)))
+                return;
+        }
+    }
+    if (nvec <= (many ? 32 : 1024))
         launch_forward<T, V, 1, 1024>(p, nvec, st);
     else if (nvec <= 4 * 256)
         launch_forward<T, V, 4, 256>(p, nvec, st);
@@ -391,15 +696,60 @@ void forward_v(const NormParams &p, cudaStream_t st)
         norm_forward_wide_kernel<T><<<static_cast<unsigned>(p.rows), kMaxThreads, 0, st>>>(p);
 }
 
-template <typename T, int V>
-void backward_v(const NormParams &p, bool want_w, cudaStream_t st)
+template <typename T, int V, int kItems, int kStages>
+bool launch_backward(const NormParams &p, int threads, size_t smem, cudaStream_t st)
 {
-    if (p.dx) {
-        const int threads = static_cast<int>(std::min<int64_t>(cdiv(cdiv(p.cols, V), 32) * 32, kMaxThreads));
-        norm_dx_kernel<T, V><<<static_cast<unsigned>(p.rows), threads, 0, st>>>(p);
+    auto kernel = norm_backward_kernel<T, V, kItems, kStages>;
+    if (!allow_smem(kernel, smem))
+        return false;
+    kernel<<<static_cast<unsigned>(p.blocks), threads, smem, st>>>(p);
+    return true;
+}
+
+// One pass for all gradients; false where the rows are too wide for it.  The ring has 4 slots, or 2 for wide
+// rows; rows in units of 2 bytes cannot be copied asynchronously and are read in place.
+template <typename T, int V, int kItems>
+bool backward_fused(NormParams &p, int64_t nvec, cudaStream_t st)
+{
+    const int threads = static_cast<int>(cdiv(cdiv(nvec, kItems), 32) * 32);
+    p.blocks = fused_blocks(p.rows, threads);
+    if constexpr (V * sizeof(T) == 2) {
+        return launch_backward<T, V, kItems, 0>(p, threads, 0, st);
+    } else {
+        const size_t slot = static_cast<size_t>(p.add ? 3 : 2) * kItems * threads * V * sizeof(T);
+        if (4 * slot * cdiv(p.blocks, kSms) <= kRingLimit)
+            return launch_backward<T, V, kItems, 4>(p, threads, 4 * slot, st);
+        return 2 * slot <= kRingLimit && launch_backward<T, V, kItems, 2>(p, threads, 2 * slot, st);
     }
-    if (want_w)
+}
+
+template <typename T, int V>
+bool backward_v(NormParams &p, cudaStream_t st)
+{
+    const int64_t nvec = cdiv(p.cols, V);
+    const int items = ring_items(nvec, V);
+    if constexpr (V <= 2) {
+        return items == 4 ? backward_fused<T, V, 4>(p, nvec, st) : items == 16 && backward_fused<T, V, 16>(p, nvec, st);
+    } else {
+        if constexpr (V == 4)
+            if (items == 8)
+                return backward_fused<T, V, 8>(p, nvec, st);
+        return items == 1   ? backward_fused<T, V, 1>(p, nvec, st)
+               : items == 2 ? backward_fused<T, V, 2>(p, nvec, st)
+                            : items == 4 && backward_fused<T, V, 4>(p, nvec, st);
+    }
+}
+
+// Rows wider than a block's registers: the column sums first (dx may overwrite what they read), then dx.
+template <typename T, int V>
+void backward_wide(NormParams &p, cudaStream_t st)
+{
+    p.block_rows = std::max<int64_t>(cdiv(p.rows, kColsumBlocks), 8);
+    p.blocks = static_cast<int32_t>(cdiv(p.rows, p.block_rows));
+    if (p.part)
         norm_colsum_kernel<T, V><<<dim3(static_cast<unsigned>(cdiv(p.cols, 32 * V)), static_cast<unsigned>(p.blocks)), 256, 0, st>>>(p);
+    if (p.dx)
+        norm_dx_kernel<T, V><<<static_cast<unsigned>(p.rows), kMaxThreads, 0, st>>>(p);
 }
 
 }  // namespace
@@ -456,7 +806,8 @@ extern "C" mlp_status mlp_layernorm_workspace_size(int64_t rows, int64_t cols, s
 {
     if (rows < 0 || cols < 1 || !bytes)
         return MLP_ERR_INVALID_ARG;
-    *bytes = static_cast<size_t>(kColsumBlocks) * 2 * static_cast<size_t>(cols) * 4;
+    const int64_t blocks = cols <= kFusedCols ? std::min<int64_t>(std::max<int64_t>(rows, kColsumBlocks), kMaxBlocks) : kColsumBlocks;
+    *bytes = static_cast<size_t>(blocks) * 2 * static_cast<size_t>(cols) * 4;
     return MLP_OK;
 }
 
@@ -502,33 +853,30 @@ extern "C" mlp_status mlp_layernorm_backward(int64_t rows, int64_t cols, const v
     p.inv_cols = 1.0f / static_cast<float>(cols);
     p.w_f32 = w_dtype == MLP_DT_F32;
     p.w_kind = p.w_f32 + (aligned(gamma, 0, wsz, 16) ? 2 : 0);
-    p.part = static_cast<float *>(workspace);
-    p.block_rows = std::max<int64_t>(cdiv(rows, kColsumBlocks), 8);
-    p.blocks = static_cast<int32_t>(cdiv(rows, p.block_rows));
-    // The column sums read dy and x, which dx may overwrite: they go first.
-    NormParams sums = p;
-    sums.dx = nullptr;
+    p.part = want_w ? static_cast<float *>(workspace) : nullptr;
     auto wide = [&](size_t bytes) {
         return static_cast<size_t>(cols) * esz % bytes == 0 && aligned(x, ldx, esz, bytes) && aligned(dy, lddy, esz, bytes) &&
                aligned(dx, lddx, esz, bytes) && aligned(dx_add, ldadd, esz, bytes);
     };
-    auto run = [&](auto vec) {
-        vec(sums, want_w);
-        vec(p, false);
-    };
     if (dtype == MLP_DT_BF16) {
-        if (wide(16))
-            run([&](const NormParams &q, bool w) { backward_v<__nv_bfloat16, 8>(q, w, st); });
-        else if (wide(4))
-            run([&](const NormParams &q, bool w) { backward_v<__nv_bfloat16, 2>(q, w, st); });
-        else
-            run([&](const NormParams &q, bool w) { backward_v<__nv_bfloat16, 1>(q, w, st); });
-    } else if (wide(16)) {
-        run([&](const NormParams &q, bool w) { backward_v<float, 4>(q, w, st); });
-    } else {
-        run([&](const NormParams &q, bool w) { backward_v<float, 1>(q, w, st); });
+        if (!(wide(16) ? backward_v<__nv_bfloat16, 8>(p, st) : wide(4) ? backward_v<__nv_bfloat16, 2>(p, st)
+                                                                       : backward_v<__nv_bfloat16, 1>(p, st)))
+            wide(16) ? backward_wide<__nv_bfloat16, 8>(p, st) : backward_wide<__nv_bfloat16, 1>(p, st);
+    } else if (!(wide(16) ? backward_v<float, 4>(p, st) : backward_v<float, 1>(p, st))) {
+        wide(16) ? backward_wide<float, 4>(p, st) : backward_wide<float, 1>(p, st);
     }
-    if (want_w)
-        norm_colsum_finish_kernel<<<dim3(static_cast<unsigned>(cdiv(cols, 32)), 2), 256, 0, st>>>(p, dgamma, dbeta);
+    if (want_w && cudaPeekAtLastError() == cudaSuccess) {
+        // launched while the kernel before it still runs; it waits for that one's results by itself
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(cdiv(cols, 32)), 2);
+        cfg.blockDim = dim3(1024);
+        cfg.stream = st;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        cudaLaunchKernelEx(&cfg, norm_colsum_finish_kernel, p, dgamma, dbeta);
+    }
     return cudaGetLastError() == cudaSuccess ? MLP_OK : MLP_ERR_CUDA;
 }
