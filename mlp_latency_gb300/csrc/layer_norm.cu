@@ -30,28 +30,70 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-    T v[V];
-};
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
 
+// V elements at an address aligned to V of them (at most 16 bytes), as one load or store.
 template <typename T, int V>
 __device__ __forceinline__ void load(const T *p, float (&f)[V])
 {
-    const Vec<T, V> x = *reinterpret_cast<const Vec<T, V> *>(p);
+    if constexpr (sizeof(T) == 2 && V == 8) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        f[j] = to_f32<T>(x.v[j]);
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = bf16_lo(w[j]);
+            f[2 * j + 1] = bf16_hi(w[j]);
+        }
+    } else if constexpr (sizeof(T) == 2 && V == 4) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        f[0] = bf16_lo(x.x);
+        f[1] = bf16_hi(x.x);
+        f[2] = bf16_lo(x.y);
+        f[3] = bf16_hi(x.y);
+    } else if constexpr (sizeof(T) == 2 && V == 2) {
+        const uint32_t x = *reinterpret_cast<const uint32_t *>(p);
+        f[0] = bf16_lo(x);
+        f[1] = bf16_hi(x);
+    } else if constexpr (sizeof(T) == 4 && V == 8) {
+        load<T, 4>(p, *reinterpret_cast<float(*)[4]>(&f[0]));
+        load<T, 4>(p + 4, *reinterpret_cast<float(*)[4]>(&f[4]));
+    } else if constexpr (sizeof(T) == 4 && V == 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(p);
+        f[0] = x.x;
+        f[1] = x.y;
+        f[2] = x.z;
+        f[3] = x.w;
+    } else if constexpr (sizeof(T) == 4 && V == 2) {
+        const float2 x = *reinterpret_cast<const float2 *>(p);
+        f[0] = x.x;
+        f[1] = x.y;
+    } else {
+        static_assert(V == 1, "no such vector");
+        f[0] = to_f32<T>(*p);
+    }
 }
 
 template <typename T, int V>
 __device__ __forceinline__ void store(T *p, const float (&f)[V])
 {
-    Vec<T, V> x;
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        x.v[j] = from_f32<T>(f[j]);
-    *reinterpret_cast<Vec<T, V> *>(p) = x;
+    if constexpr (sizeof(T) == 2 && V == 8)
+        *reinterpret_cast<uint4 *>(p) =
+            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    else if constexpr (sizeof(T) == 2 && V == 2)
+        *reinterpret_cast<uint32_t *>(p) = pack_bf16(f[0], f[1]);
+    else if constexpr (sizeof(T) == 4 && V == 4)
+        *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    else {
+        static_assert(V == 1, "no such vector");
+        *p = from_f32<T>(f[0]);
+    }
 }
 
 // gamma or beta, columns c .. c + V - 1 (NULL: `none`).  kind: 0 bf16, 1 fp32; + 2: aligned to V of them
@@ -59,7 +101,6 @@ __device__ __forceinline__ void store(T *p, const float (&f)[V])
 template <int V>
 __device__ __forceinline__ void load_w(const void *w, int kind, int64_t c, float none, float (&f)[V])
 {
-    constexpr int V4 = V < 4 ? V : 4;
     if (!w) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
@@ -67,13 +108,7 @@ __device__ __forceinline__ void load_w(const void *w, int kind, int64_t c, float
     } else if (kind == 2) {
         load<__nv_bfloat16, V>(static_cast<const __nv_bfloat16 *>(w) + c, f);
     } else if (kind == 3) {
-#pragma unroll
-        for (int j = 0; j < V; j += V4) {
-            const Vec<float, V4> x = *reinterpret_cast<const Vec<float, V4> *>(static_cast<const float *>(w) + c + j);
-#pragma unroll
-            for (int k = 0; k < V4; ++k)
-                f[j + k] = x.v[k];
-        }
+        load<float, V>(static_cast<const float *>(w) + c, f);
     } else if (kind == 1) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
@@ -128,12 +163,13 @@ struct NormParams {
     int32_t blocks;
 };
 
-// As team_sum over a block, once per row of a loop: the scratch alternates between two halves (`parity`), so
-// one barrier suffices (a thread cannot be two rows ahead of another).
+// As team_sum over a block of at most 512 threads, once per row of a loop: the scratch alternates between two
+// halves (`parity`), so one barrier suffices (a thread cannot be two rows ahead of another).  The warps' sums are
+// read back as vectors and added by every thread: a shorter chain than a second round of shuffles.
 template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float (*scratch)[N][32], int parity)
+__device__ __forceinline__ void block_sum(float (&v)[N], float (*scratch)[N][16], int parity)
 {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 #pragma unroll
     for (int n = 0; n < N; ++n)
         v[n] = warp_sum(v[n]);
@@ -143,8 +179,20 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*scratch)[N][32]
             scratch[parity][n][warp] = v[n];
     __syncthreads();
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-        v[n] = warp_sum(lane < warps ? scratch[parity][n][lane] : 0.0f);
+    for (int n = 0; n < N; ++n) {
+        const float4 *q = reinterpret_cast<const float4 *>(scratch[parity][n]);
+        const float4 a = q[0], b = q[1], c = q[2], d = q[3];   // (entries of absent warps are zero)
+        v[n] = (((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w))) +
+               (((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w)));
+    }
+}
+
+// Zero the scratch of block_sum (before its first use; followed by a barrier).
+template <int N>
+__device__ __forceinline__ void block_sum_init(float (*scratch)[N][16])
+{
+    for (int i = threadIdx.x; i < 2 * N * 16; i += blockDim.x)
+        (&scratch[0][0][0])[i] = 0.0f;
 }
 
 // ------------------------------------------------------------------------- rows through a ring --
@@ -196,51 +244,63 @@ struct RowRing {
     }
 };
 
-// Forward over many rows: bounded by memory (2 C elements per row); measured below the estimate of one row per
-// block because a block's two reductions leave the memory system idle.
+// Forward over many rows.  A thread keeps its columns from row to row, so gamma and beta stay in registers.
 template <typename T, int V, int kItems, int kStages>
 __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float s1[2][1][32], s2[2][1][32];
+    __shared__ __align__(16) float s1[2][1][16], s2[2][1][16];
     const RowRing<T, V, kItems, kStages> ring{smem, 1};
     const int64_t step = gridDim.x;
-    const int cols = static_cast<int>(p.cols);
-    const T *x = static_cast<const T *>(p.x);
-    int64_t row = blockIdx.x;
-    for (int s = 0; s < kStages - 1; ++s) {
-        if (row + s * step < p.rows)
-            ring.fetch(s, 0, x + (row + s * step) * p.ldx, cols);
+    const int cols = static_cast<int>(p.cols), c0 = static_cast<int>(threadIdx.x) * V, cstep = static_cast<int>(blockDim.x) * V;
+    const T *ahead = static_cast<const T *>(p.x) + blockIdx.x * p.ldx;   // next row to fetch
+    T *y = static_cast<T *>(p.y) + blockIdx.x * p.ldy;
+    int64_t left = (p.rows - blockIdx.x + step - 1) / step;              // rows of this block
+    int64_t to_fetch = left;
+    auto fetch = [&](int stage) {
+        if (to_fetch > 0)
+            ring.fetch(stage, 0, ahead, cols);
         copy_commit();
-    }
-    int stage = 0, parity = 0;
-    for (; row < p.rows; row += step, parity ^= 1) {
+        ahead += step * p.ldx;
+        --to_fetch;
+    };
+    for (int s = 0; s < kStages - 1; ++s)
+        fetch(s);
+    block_sum_init<1>(s1);
+    block_sum_init<1>(s2);
+    float g[kItems][V], b[kItems][V];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+        if (c0 + i * cstep < cols) {
+            load_w<V>(p.gamma, p.w_kind, c0 + i * cstep, 1.0f, g[i]);
+            load_w<V>(p.beta, p.w_kind, c0 + i * cstep, 0.0f, b[i]);
+        }
+    __syncthreads();
+    int stage = 0, into = kStages - 1, parity = 0;
+    for (int64_t row = blockIdx.x; left > 0; --left, row += step, parity ^= 1) {
         copy_wait<kStages - 2>();
-        const int64_t ahead = row + (kStages - 1) * step;
-        if (ahead < p.rows)
-            ring.fetch((stage + kStages - 1) % kStages, 0, x + ahead * p.ldx, cols);
-        copy_commit();
+        fetch(into);
+        into = into + 1 == kStages ? 0 : into + 1;
         float v[kItems][V], s[1] = {0.0f};
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int c = (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
-            if (c < cols) {
-                ring.read(stage, 0, i, nullptr, c, v[i]);
+        for (int i = 0; i < kItems; ++i)
+            if (c0 + i * cstep < cols) {
+                ring.read(stage, 0, i, nullptr, 0, v[i]);
 #pragma unroll
                 for (int j = 0; j < V; ++j)
                     s[0] += v[i][j];
             }
-        }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
         block_sum<1>(s, s1, parity);
-        const float mean = s[0] / static_cast<float>(p.cols);
+        const float mean = __fdividef(s[0], static_cast<float>(cols));
         s[0] = 0.0f;
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
-            if ((i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V < cols)
+            if (c0 + i * cstep < cols)
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float d = v[i][j] - mean;
-                    s[0] = fmaf(d, d, s[0]);
+                    v[i][j] -= mean;
+                    s[0] = fmaf(v[i][j], v[i][j], s[0]);
                 }
         block_sum<1>(s, s2, parity);
         const float rstd = rsqrtf(fmaf(s[0], p.inv_cols, p.eps));
@@ -250,44 +310,36 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams
             if (p.rstd)
                 p.rstd[row] = rstd;
         }
-        T *y = static_cast<T *>(p.y) + row * p.ldy;
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int c = (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
-            if (c < cols) {
-                float g[V], b[V], o[V];
-                load_w<V>(p.gamma, p.w_kind, c, 1.0f, g);
-                load_w<V>(p.beta, p.w_kind, c, 0.0f, b);
+        for (int i = 0; i < kItems; ++i)
+            if (c0 + i * cstep < cols) {
+                float o[V];
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    o[j] = fmaf((v[i][j] - mean) * rstd, g[j], b[j]);
-                store<T, V>(y + c, o);
+                    o[j] = fmaf(v[i][j] * rstd, g[i][j], b[i][j]);
+                store<T, V>(y + c0 + i * cstep, o);
             }
-        }
-        stage = (stage + 1) % kStages;
+        y += step * p.ldy;
     }
 }
 
 // Backward: dx of each row, and this block's column sums of dy xh and dy in registers (each thread keeps its
-// columns from row to row), so x and dy are read once for all three gradients.  The sums of the blocks are
-// added by norm_colsum_finish_kernel.
+// columns from row to row), so x and dy are read once for all three gradients.  Up to 16 columns a thread also
+// keep gamma and, over the row's reduction, g and xh; more columns are read and computed again.  The sums of the
+// blocks are added by norm_colsum_finish_kernel.
 template <typename T, int V, int kItems, int kStages>
 __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float scratch[2][2][32];
+    __shared__ __align__(16) float scratch[2][2][16];
     constexpr int kS = kStages > 0 ? kStages : 1;
+    constexpr bool kKeep = V * kItems <= 16;
+    constexpr int kK = kKeep ? kItems : 1;
     const RowRing<T, V, kItems, kStages> ring{smem, p.add ? 3 : 2};
     const int64_t step = gridDim.x;
-    const int cols = static_cast<int>(p.cols);
+    const int cols = static_cast<int>(p.cols), c0 = static_cast<int>(threadIdx.x) * V, cstep = static_cast<int>(blockDim.x) * V;
     const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy), *add = static_cast<const T *>(p.add);
     griddep_launch_dependents();   // the finishing kernel waits for this grid by itself
-    float ag[kItems][V], ab[kItems][V];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            ag[i][j] = ab[i][j] = 0.0f;
     auto fetch = [&](int stage, int64_t row) {
         if (row < p.rows) {
             ring.fetch(stage, 0, x + row * p.ldx, cols);
@@ -301,50 +353,72 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
     if constexpr (kStages > 0)
         for (int s = 0; s < kS - 1; ++s)
             fetch(s, row + s * step);
+    block_sum_init<2>(scratch);
+    float ag[kItems][V], ab[kItems][V], gk[kK][V];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            ag[i][j] = ab[i][j] = 0.0f;
+        if (kKeep && c0 + i * cstep < cols)
+            load_w<V>(p.gamma, p.w_kind, c0 + i * cstep, 1.0f, gk[kKeep ? i : 0]);
+    }
     float mean = row < p.rows ? p.mean_in[row] : 0.0f, rstd = row < p.rows ? p.rstd_in[row] : 0.0f;
-    int stage = 0, parity = 0;
+    __syncthreads();
+    int stage = 0, into = kS - 1, parity = 0;
     for (; row < p.rows; row += step, parity ^= 1) {
         if constexpr (kStages > 0) {
             copy_wait<kS - 2>();
-            fetch((stage + kS - 1) % kS, row + (kS - 1) * step);
+            fetch(into, row + (kS - 1) * step);
+            into = into + 1 == kS ? 0 : into + 1;
         }
         const int64_t next = row + step < p.rows ? row + step : row;
         const float mean_next = p.mean_in[next], rstd_next = p.rstd_in[next];
         const T *xr = x + row * p.ldx, *dr = dy + row * p.lddy;
-        float s[2] = {0.0f, 0.0f};
+        float s[2] = {0.0f, 0.0f}, gd[kK][V], xh[kK][V];
+        // g and xh of vector i
+        auto terms = [&](int i, float (&d)[V], float (&go)[V], float (&xo)[V]) {
+            const int c = c0 + i * cstep;
+            float a[V], w[V];
+            ring.read(stage, 0, i, xr, c, a);
+            ring.read(stage, 1, i, dr, c, d);
+            if constexpr (!kKeep)
+                load_w<V>(p.gamma, p.w_kind, c, 1.0f, w);
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int c = (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
-            if (c < cols) {
-                float a[V], d[V], g[V];
-                ring.read(stage, 0, i, xr, c, a);
-                ring.read(stage, 1, i, dr, c, d);
-                load_w<V>(p.gamma, p.w_kind, c, 1.0f, g);
+            for (int j = 0; j < V; ++j) {
+                xo[j] = (a[j] - mean) * rstd;
+                go[j] = (kKeep ? gk[kKeep ? i : 0][j] : w[j]) * d[j];
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+            if (c0 + i * cstep < cols) {
+                float d[V];
+                const int k = kKeep ? i : 0;
+                terms(i, d, gd[k], xh[k]);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float xh = (a[j] - mean) * rstd, gd = g[j] * d[j];
                     ab[i][j] += d[j];
-                    ag[i][j] = fmaf(d[j], xh, ag[i][j]);
-                    s[0] += gd;
-                    s[1] = fmaf(gd, xh, s[1]);
+                    ag[i][j] = fmaf(d[j], xh[k][j], ag[i][j]);
+                    s[0] += gd[k][j];
+                    s[1] = fmaf(gd[k][j], xh[k][j], s[1]);
                 }
             }
-        }
         if (p.dx) {
             block_sum<2>(s, scratch, parity);
             const float m0 = s[0] * p.inv_cols, m1 = s[1] * p.inv_cols;
             T *dx = static_cast<T *>(p.dx) + row * p.lddx;
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                const int c = (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
+                const int c = c0 + i * cstep;
                 if (c < cols) {
-                    float a[V], d[V], g[V], o[V];
-                    ring.read(stage, 0, i, xr, c, a);
-                    ring.read(stage, 1, i, dr, c, d);
-                    load_w<V>(p.gamma, p.w_kind, c, 1.0f, g);
+                    float o[V], d[V];
+                    const int k = kKeep ? i : 0;
+                    if constexpr (!kKeep)
+                        terms(i, d, gd[k], xh[k]);
 #pragma unroll
                     for (int j = 0; j < V; ++j)
-                        o[j] = rstd * (fmaf(g[j], d[j], -m0) - (a[j] - mean) * rstd * m1);
+                        o[j] = rstd * fmaf(-xh[k][j], m1, gd[k][j] - m0);
                     if (add) {
                         float r[V];
                         ring.read(stage, 2, i, add + row * p.ldadd, c, r);
@@ -358,19 +432,28 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
         }
         mean = mean_next;
         rstd = rstd_next;
-        stage = (stage + 1) % kS;
+        stage = stage + 1 == kS ? 0 : stage + 1;
     }
     if (p.part) {
-        float *out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.cols;
+        float *out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * cols;
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-            const int c = (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
-            if (c < cols)
+            const int c = c0 + i * cstep;
+            if (c < cols) {
+                if constexpr (V % 4 == 0) {   // cols is a multiple of V, and so of four
 #pragma unroll
-                for (int j = 0; j < V; ++j) {   // (cols may be odd: no vector store)
-                    out[c + j] = ag[i][j];
-                    out[cols + c + j] = ab[i][j];
+                    for (int j = 0; j < V; j += 4) {
+                        *reinterpret_cast<float4 *>(out + c + j) = make_float4(ag[i][j], ag[i][j + 1], ag[i][j + 2], ag[i][j + 3]);
+                        *reinterpret_cast<float4 *>(out + cols + c + j) = make_float4(ab[i][j], ab[i][j + 1], ab[i][j + 2], ab[i][j + 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        out[c + j] = ag[i][j];
+                        out[cols + c + j] = ab[i][j];
+                    }
                 }
+            }
         }
     }
 }
@@ -653,12 +736,20 @@ void launch_forward(const NormParams &p, int64_t nvec, cudaStream_t st)
 template <typename T, int V, int kItems>
 bool launch_forward_ring(const NormParams &p, int64_t nvec, cudaStream_t st)
 {
-    constexpr int kStages = 4;
+    constexpr int kStages = 3;
     const int threads = static_cast<int>(cdiv(cdiv(nvec, kItems), 32) * 32);
     const size_t smem = static_cast<size_t>(kStages) * kItems * threads * V * sizeof(T);
-    const int per_sm = std::max(1, std::min({8, 1024 / threads, static_cast<int>(kRingLimit / smem)}));
+    if (smem > kRingLimit)
+        return false;
+    // Blocks per SM: as many as fit registers (128 a thread) and rings, unless fewer leave the last round fuller
+    // (the blocks of an SM share its throughput, so a round of n rows per SM costs n).
+    const int most = std::max(1, std::min({8, 512 / threads, static_cast<int>(kRingLimit / smem)}));
+    int per_sm = most;
+    for (int n = most; n >= std::max(1, most / 2); --n)
+        if (cdiv(p.rows, static_cast<int64_t>(n) * kSms) * n < cdiv(p.rows, static_cast<int64_t>(per_sm) * kSms) * per_sm)
+            per_sm = n;
     auto kernel = norm_forward_ring_kernel<T, V, kItems, kStages>;
-    if (smem > kRingLimit || !allow_smem(kernel, smem))
+    if (!allow_smem(kernel, smem))
         return false;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.rows, static_cast<int64_t>(per_sm) * kSms));
     kernel<<<grid, threads, smem, st>>>(p);
@@ -675,10 +766,10 @@ void forward_v(const NormParams &p, cudaStream_t st)
     const bool many = p.rows > 2 * kSms;
     if constexpr (V * sizeof(T) == 16) {
         if (many && nvec > 128) {
-            const int items = ring_items(nvec, V);
-            if ((items == 1 && launch_forward_ring<T, V, 1>(p, nvec, st)) ||
-                (items == 2 && launch_forward_ring<T, V, 2>(p, nvec, st)) ||
-                (items >= 4 && nvec <= 2048 && launch_forward_ring<T, V, 4>(p, nvec, st)))
+            constexpr int kMost = 32 / V;   // 32 columns a thread
+            const int need = static_cast<int>(cdiv(nvec, 512));
+            if ((nvec <= 256 && launch_forward_ring<T, V, 1>(p, nvec, st)) ||
+                (need <= kMost && nvec > 256 && launch_forward_ring<T, V, kMost>(p, nvec, st)))
                 return;
         }
     }
