@@ -163,36 +163,180 @@ struct NormParams {
     int32_t blocks;
 };
 
-// As team_sum over a block of at most 512 threads, once per row of a loop: the scratch alternates between two
-// halves (`parity`), so one barrier suffices (a thread cannot be two rows ahead of another).  The warps' sums are
-// read back as vectors and added by every thread: a shorter chain than a second round of shuffles.
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float (*scratch)[N][16], int parity)
+// ---- element-wise arithmetic on a vector of V columns: pairs through the two-wide fp32 instructions of
+// sm_100 and later, which halve the instructions of kernels that are bound by issue as much as by memory.
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
 {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t d, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d)); }
+
+// d = a * b + c
+template <int V>
+__device__ __forceinline__ void fma_v(float (&d)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V])
+{
+    if constexpr (V % 2 == 0) {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-        v[n] = warp_sum(v[n]);
-    if (lane == 0)
+        for (int j = 0; j < V; j += 2) {
+            uint64_t r;
+            asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a[j], a[j + 1])), "l"(pair(b[j], b[j + 1])), "l"(pair(c[j], c[j + 1])));
+            unpair(r, d[j], d[j + 1]);
+        }
+    } else {
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-            scratch[parity][n][warp] = v[n];
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const float4 *q = reinterpret_cast<const float4 *>(scratch[parity][n]);
-        const float4 a = q[0], b = q[1], c = q[2], d = q[3];   // (entries of absent warps are zero)
-        v[n] = (((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w))) +
-               (((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w)));
+        for (int j = 0; j < V; ++j)
+            d[j] = fmaf(a[j], b[j], c[j]);
     }
 }
 
-// Zero the scratch of block_sum (before its first use; followed by a barrier).
-template <int N>
-__device__ __forceinline__ void block_sum_init(float (*scratch)[N][16])
+// d = a * b + c with scalars b, c
+template <int V>
+__device__ __forceinline__ void fma_s(float (&d)[V], const float (&a)[V], float b, float c)
 {
-    for (int i = threadIdx.x; i < 2 * N * 16; i += blockDim.x)
-        (&scratch[0][0][0])[i] = 0.0f;
+    float bv[V], cv[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        bv[j] = b;
+        cv[j] = c;
+    }
+    fma_v<V>(d, a, bv, cv);
+}
+
+template <int V>
+__device__ __forceinline__ void fma_sv(float (&d)[V], const float (&a)[V], float b, const float (&c)[V])
+{
+    float bv[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        bv[j] = b;
+    fma_v<V>(d, a, bv, c);
+}
+
+template <int V>
+__device__ __forceinline__ void mul_v(float (&d)[V], const float (&a)[V], const float (&b)[V])
+{
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            uint64_t r;
+            asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a[j], a[j + 1])), "l"(pair(b[j], b[j + 1])));
+            unpair(r, d[j], d[j + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            d[j] = a[j] * b[j];
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void mul_s(float (&d)[V], const float (&a)[V], float b)
+{
+    float bv[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        bv[j] = b;
+    mul_v<V>(d, a, bv);
+}
+
+template <int V>
+__device__ __forceinline__ void add_v(float (&d)[V], const float (&a)[V], const float (&b)[V])
+{
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            uint64_t r;
+            asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a[j], a[j + 1])), "l"(pair(b[j], b[j + 1])));
+            unpair(r, d[j], d[j + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            d[j] = a[j] + b[j];
+    }
+}
+
+// Running sums of a vector's columns, kept as min(V, 2) partial sums.
+template <int V>
+struct Sum {
+    static constexpr int kW = V % 2 == 0 ? 2 : 1;
+    float w[kW];
+    __device__ __forceinline__ Sum()
+    {
+#pragma unroll
+        for (int k = 0; k < kW; ++k)
+            w[k] = 0.0f;
+    }
+    __device__ __forceinline__ void add(const float (&a)[V])
+    {
+#pragma unroll
+        for (int j = 0; j < V; j += kW) {
+            float x[kW];
+#pragma unroll
+            for (int k = 0; k < kW; ++k)
+                x[k] = a[j + k];
+            add_v<kW>(w, w, x);
+        }
+    }
+    __device__ __forceinline__ void fma(const float (&a)[V], const float (&b)[V])
+    {
+#pragma unroll
+        for (int j = 0; j < V; j += kW) {
+            float x[kW], y[kW];
+#pragma unroll
+            for (int k = 0; k < kW; ++k) {
+                x[k] = a[j + k];
+                y[k] = b[j + k];
+            }
+            fma_v<kW>(w, x, y, w);
+        }
+    }
+    __device__ __forceinline__ float total() const { return kW == 2 ? w[0] + w[kW - 1] : w[0]; }
+};
+
+// ---- sums over a block of at most 512 threads, once per row of a loop.  The scratch (32 floats, zero where a warp
+// is absent) alternates between two halves, so one barrier suffices: no thread can be two rows ahead of another.
+__device__ __forceinline__ void block_sum_init(float (*scratch)[32])
+{
+    if (threadIdx.x < 32)
+        scratch[0][threadIdx.x] = scratch[1][threadIdx.x] = 0.0f;
+}
+
+__device__ __forceinline__ float block_sum(float v, float (*scratch)[32], int parity)
+{
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    v = warp_sum(v);
+    if (lane == 0)
+        scratch[parity][warp] = v;
+    __syncthreads();
+    v = scratch[parity][lane & 15];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Two sums at once: after the first exchange the lower half of a warp carries one value and the upper half the
+// other, so both take one chain of shuffles.
+__device__ __forceinline__ void block_sum2(float &a, float &b, float (*scratch)[32], int parity)
+{
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const bool upper = lane >= 16;
+    float v = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((lane & 15) == 0)
+        scratch[parity][(lane & 16) + warp] = v;
+    __syncthreads();
+    v = scratch[parity][lane];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    a = __shfl_sync(0xffffffffu, v, 0);
+    b = __shfl_sync(0xffffffffu, v, 16);
 }
 
 // ------------------------------------------------------------------------- rows through a ring --
@@ -200,13 +344,12 @@ __device__ __forceinline__ void block_sum_init(float (*scratch)[N][16])
 // thread copies exactly the columns that it reads, so the copies need no barrier, only the thread's own
 // wait_group.
 template <int kBytes>
-__device__ __forceinline__ void copy_async(void *dst, const void *src)
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
 {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
     if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -216,31 +359,66 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// kStages slots of kBufs rows; kStages = 0: no ring, rows are read where they are.
+// kStages slots of `bufs` rows, kItems vectors of V elements per thread and row.  kStages = 0: no ring, rows are
+// read where they are.
 template <typename T, int V, int kItems, int kStages>
 struct RowRing {
     static constexpr int kBytes = V * static_cast<int>(sizeof(T));
-    uint8_t *base;
-    int bufs;
-    __device__ __forceinline__ uint8_t *slot(int stage, int buf, int i) const
+    uint32_t first, last;        // this thread's place in the first and last slot
+    uint32_t rd, wr;             // ... in the slot to read and to fill next
+    uint32_t item, row, slot;    // strides of vectors, rows and slots
+    int cols, c0, cstep;         // this thread's first column, and the step to its next vector
+    __device__ __forceinline__ RowRing(const void *smem, int bufs, int n_cols) : cols(n_cols)
     {
-        return base + (static_cast<size_t>((stage * bufs + buf) * kItems + i) * blockDim.x + threadIdx.x) * kBytes;
+        item = blockDim.x * kBytes;
+        row = item * kItems;
+        slot = row * static_cast<uint32_t>(bufs);
+        first = rd = wr = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * kBytes;
+        last = first + slot * (kStages > 0 ? kStages - 1 : 0);
+        c0 = static_cast<int>(threadIdx.x) * V;
+        cstep = static_cast<int>(blockDim.x) * V;
     }
-    __device__ __forceinline__ void fetch(int stage, int buf, const T *row, int cols) const
+    __device__ __forceinline__ bool has(int i) const { return c0 + i * cstep < cols; }
+    __device__ __forceinline__ void advance(uint32_t &at) const { at = at == last ? first : at + slot; }
+    // one row into buffer `buf` of the slot to fill
+    __device__ __forceinline__ void fetch(int buf, const T *src) const
     {
+        src += c0;
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int c = (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
-            if (c < cols)
-                copy_async<kBytes>(slot(stage, buf, i), row + c);
-        }
+        for (int i = 0; i < kItems; ++i)
+            if (has(i))
+                copy_async<kBytes>(wr + buf * row + i * item, src + i * cstep);
     }
-    __device__ __forceinline__ void read(int stage, int buf, int i, const T *row, int c, float (&f)[V]) const
+    // vector i of buffer `buf` of the slot to read (of the row at src without a ring)
+    __device__ __forceinline__ void read(int buf, int i, const T *src, float (&f)[V]) const
     {
-        if constexpr (kStages > 0)
-            load<T, V>(reinterpret_cast<const T *>(slot(stage, buf, i)), f);
-        else
-            load<T, V>(row + c, f);
+        if constexpr (kStages == 0) {
+            load<T, V>(src + c0 + i * cstep, f);
+        } else {
+            const uint32_t at = rd + buf * row + i * item;
+            if constexpr (kBytes == 16) {
+                uint32_t w[4];
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (sizeof(T) == 2) {
+                        f[2 * j] = bf16_lo(w[j]);
+                        f[2 * j + 1] = bf16_hi(w[j]);
+                    } else {
+                        f[j] = __uint_as_float(w[j]);
+                    }
+                }
+            } else {
+                uint32_t w;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+                if constexpr (sizeof(T) == 2) {
+                    f[0] = bf16_lo(w);
+                    f[1] = bf16_hi(w);
+                } else {
+                    f[0] = __uint_as_float(w);
+                }
+            }
+        }
     }
 };
 
@@ -249,61 +427,54 @@ template <typename T, int V, int kItems, int kStages>
 __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ __align__(16) float s1[2][1][16], s2[2][1][16];
-    const RowRing<T, V, kItems, kStages> ring{smem, 1};
+    __shared__ float s1[2][32], s2[2][32];
+    RowRing<T, V, kItems, kStages> ring(smem, 1, static_cast<int>(p.cols));
     const int64_t step = gridDim.x;
-    const int cols = static_cast<int>(p.cols), c0 = static_cast<int>(threadIdx.x) * V, cstep = static_cast<int>(blockDim.x) * V;
     const T *ahead = static_cast<const T *>(p.x) + blockIdx.x * p.ldx;   // next row to fetch
-    T *y = static_cast<T *>(p.y) + blockIdx.x * p.ldy;
-    int64_t left = (p.rows - blockIdx.x + step - 1) / step;              // rows of this block
-    int64_t to_fetch = left;
-    auto fetch = [&](int stage) {
+    T *y = static_cast<T *>(p.y) + blockIdx.x * p.ldy + ring.c0;
+    int left = static_cast<int>((p.rows - blockIdx.x + step - 1) / step);   // rows of this block
+    int to_fetch = left;
+    auto fetch = [&] {
         if (to_fetch > 0)
-            ring.fetch(stage, 0, ahead, cols);
+            ring.fetch(0, ahead);
         copy_commit();
+        ring.advance(ring.wr);
         ahead += step * p.ldx;
         --to_fetch;
     };
     for (int s = 0; s < kStages - 1; ++s)
-        fetch(s);
-    block_sum_init<1>(s1);
-    block_sum_init<1>(s2);
+        fetch();
+    block_sum_init(s1);
+    block_sum_init(s2);
     float g[kItems][V], b[kItems][V];
 #pragma unroll
     for (int i = 0; i < kItems; ++i)
-        if (c0 + i * cstep < cols) {
-            load_w<V>(p.gamma, p.w_kind, c0 + i * cstep, 1.0f, g[i]);
-            load_w<V>(p.beta, p.w_kind, c0 + i * cstep, 0.0f, b[i]);
+        if (ring.has(i)) {
+            load_w<V>(p.gamma, p.w_kind, ring.c0 + i * ring.cstep, 1.0f, g[i]);
+            load_w<V>(p.beta, p.w_kind, ring.c0 + i * ring.cstep, 0.0f, b[i]);
         }
     __syncthreads();
-    int stage = 0, into = kStages - 1, parity = 0;
+    int parity = 0;
     for (int64_t row = blockIdx.x; left > 0; --left, row += step, parity ^= 1) {
         copy_wait<kStages - 2>();
-        fetch(into);
-        into = into + 1 == kStages ? 0 : into + 1;
-        float v[kItems][V], s[1] = {0.0f};
+        fetch();
+        float v[kItems][V];
+        Sum<V> sum, sq;
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
-            if (c0 + i * cstep < cols) {
-                ring.read(stage, 0, i, nullptr, 0, v[i]);
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    s[0] += v[i][j];
+            if (ring.has(i)) {
+                ring.read(0, i, nullptr, v[i]);
+                sum.add(v[i]);
             }
-        stage = stage + 1 == kStages ? 0 : stage + 1;
-        block_sum<1>(s, s1, parity);
-        const float mean = __fdividef(s[0], static_cast<float>(cols));
-        s[0] = 0.0f;
+        ring.advance(ring.rd);
+        const float mean = __fdiv_rn(block_sum(sum.total(), s1, parity), static_cast<float>(ring.cols));
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
-            if (c0 + i * cstep < cols)
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    v[i][j] -= mean;
-                    s[0] = fmaf(v[i][j], v[i][j], s[0]);
-                }
-        block_sum<1>(s, s2, parity);
-        const float rstd = rsqrtf(fmaf(s[0], p.inv_cols, p.eps));
+            if (ring.has(i)) {
+                fma_s<V>(v[i], v[i], 1.0f, -mean);
+                sq.fma(v[i], v[i]);
+            }
+        const float rstd = rsqrtf(fmaf(block_sum(sq.total(), s2, parity), p.inv_cols, p.eps));
         if (threadIdx.x == 0) {
             if (p.mean)
                 p.mean[row] = mean;
@@ -312,12 +483,10 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams
         }
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
-            if (c0 + i * cstep < cols) {
-                float o[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    o[j] = fmaf(v[i][j] * rstd, g[i][j], b[i][j]);
-                store<T, V>(y + c0 + i * cstep, o);
+            if (ring.has(i)) {
+                mul_s<V>(v[i], v[i], rstd);
+                fma_v<V>(v[i], v[i], g[i], b[i]);
+                store<T, V>(y + i * ring.cstep, v[i]);
             }
         y += step * p.ldy;
     }
@@ -325,121 +494,144 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams
 
 // Backward: dx of each row, and this block's column sums of dy xh and dy in registers (each thread keeps its
 // columns from row to row), so x and dy are read once for all three gradients.  Up to 16 columns a thread also
-// keep gamma and, over the row's reduction, g and xh; more columns are read and computed again.  The sums of the
-// blocks are added by norm_colsum_finish_kernel.
+// keep gamma and, over the row's reduction, g and xh; more columns are read and computed again.  (x rstd -
+// mean rstd would save an instruction, but leaves rounding errors where x = mean.)  The sums of the blocks are added
+// by norm_colsum_finish_kernel.
 template <typename T, int V, int kItems, int kStages>
 __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ __align__(16) float scratch[2][2][16];
-    constexpr int kS = kStages > 0 ? kStages : 1;
+    __shared__ float scratch[2][32];
     constexpr bool kKeep = V * kItems <= 16;
     constexpr int kK = kKeep ? kItems : 1;
-    const RowRing<T, V, kItems, kStages> ring{smem, p.add ? 3 : 2};
+    RowRing<T, V, kItems, kStages> ring(smem, p.add ? 3 : 2, static_cast<int>(p.cols));
     const int64_t step = gridDim.x;
-    const int cols = static_cast<int>(p.cols), c0 = static_cast<int>(threadIdx.x) * V, cstep = static_cast<int>(blockDim.x) * V;
-    const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy), *add = static_cast<const T *>(p.add);
+    const int cols = ring.cols;
+    const int64_t r0 = blockIdx.x;
+    const T *x = static_cast<const T *>(p.x) + r0 * p.ldx, *dy = static_cast<const T *>(p.dy) + r0 * p.lddy;
+    const T *add = p.add ? static_cast<const T *>(p.add) + r0 * p.ldadd : nullptr;
+    T *dx = p.dx ? static_cast<T *>(p.dx) + r0 * p.lddx + ring.c0 : nullptr;
+    const int mine = static_cast<int>((p.rows - r0 + step - 1) / step);   // rows of this block
+    int to_fetch = mine;
     griddep_launch_dependents();   // the finishing kernel waits for this grid by itself
-    auto fetch = [&](int stage, int64_t row) {
-        if (row < p.rows) {
-            ring.fetch(stage, 0, x + row * p.ldx, cols);
-            ring.fetch(stage, 1, dy + row * p.lddy, cols);
+    // with a ring x, dy and add run ahead: they point to the next row to fetch
+    auto fetch = [&] {
+        if (to_fetch > 0) {
+            ring.fetch(0, x);
+            ring.fetch(1, dy);
             if (add)
-                ring.fetch(stage, 2, add + row * p.ldadd, cols);
+                ring.fetch(2, add);
         }
         copy_commit();
+        ring.advance(ring.wr);
+        --to_fetch;
+        x += step * p.ldx;
+        dy += step * p.lddy;
+        if (add)
+            add += step * p.ldadd;
     };
-    int64_t row = blockIdx.x;
     if constexpr (kStages > 0)
-        for (int s = 0; s < kS - 1; ++s)
-            fetch(s, row + s * step);
-    block_sum_init<2>(scratch);
+        for (int s = 0; s < kStages - 1; ++s)
+            fetch();
+    block_sum_init(scratch);
     float ag[kItems][V], ab[kItems][V], gk[kK][V];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
             ag[i][j] = ab[i][j] = 0.0f;
-        if (kKeep && c0 + i * cstep < cols)
-            load_w<V>(p.gamma, p.w_kind, c0 + i * cstep, 1.0f, gk[kKeep ? i : 0]);
+        if (kKeep && ring.has(i))
+            load_w<V>(p.gamma, p.w_kind, ring.c0 + i * ring.cstep, 1.0f, gk[kKeep ? i : 0]);
     }
-    float mean = row < p.rows ? p.mean_in[row] : 0.0f, rstd = row < p.rows ? p.rstd_in[row] : 0.0f;
+    // mean and rstd of 32 rows at a time, a row a lane, the next 32 on their way: one row ahead is not enough for
+    // memory under load
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    auto load_stats = [&](int first, float &m, float &r) {
+        const int64_t q = r0 + static_cast<int64_t>(min(first + lane, mine - 1)) * step;
+        m = p.mean_in[q];
+        r = p.rstd_in[q];
+    };
+    float mean_c, rstd_c, mean_n, rstd_n;
+    load_stats(0, mean_c, rstd_c);
+    load_stats(32, mean_n, rstd_n);
     __syncthreads();
-    int stage = 0, into = kS - 1, parity = 0;
-    for (; row < p.rows; row += step, parity ^= 1) {
+    int parity = 0;
+    for (int it = 0; it < mine; ++it, parity ^= 1) {
         if constexpr (kStages > 0) {
-            copy_wait<kS - 2>();
-            fetch(into, row + (kS - 1) * step);
-            into = into + 1 == kS ? 0 : into + 1;
+            copy_wait<kStages - 2>();
+            fetch();
         }
-        const int64_t next = row + step < p.rows ? row + step : row;
-        const float mean_next = p.mean_in[next], rstd_next = p.rstd_in[next];
-        const T *xr = x + row * p.ldx, *dr = dy + row * p.lddy;
-        float s[2] = {0.0f, 0.0f}, gd[kK][V], xh[kK][V];
-        // g and xh of vector i
-        auto terms = [&](int i, float (&d)[V], float (&go)[V], float (&xo)[V]) {
-            const int c = c0 + i * cstep;
-            float a[V], w[V];
-            ring.read(stage, 0, i, xr, c, a);
-            ring.read(stage, 1, i, dr, c, d);
-            if constexpr (!kKeep)
-                load_w<V>(p.gamma, p.w_kind, c, 1.0f, w);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                xo[j] = (a[j] - mean) * rstd;
-                go[j] = (kKeep ? gk[kKeep ? i : 0][j] : w[j]) * d[j];
+        if (it > 0 && (it & 31) == 0) {
+            mean_c = mean_n;
+            rstd_c = rstd_n;
+            load_stats(it + 32, mean_n, rstd_n);
+        }
+        const float mean = __shfl_sync(0xffffffffu, mean_c, it & 31), rstd = __shfl_sync(0xffffffffu, rstd_c, it & 31);
+        Sum<V> sum0, sum1;
+        float gd[kK][V], xh[kK][V];
+        auto terms = [&](int i, float (&d)[V], float (&go)[V], float (&xo)[V]) {   // dy, g and xh of vector i
+            float a[V];
+            ring.read(0, i, x, a);
+            ring.read(1, i, dy, d);
+            fma_s<V>(xo, a, 1.0f, -mean);
+            mul_s<V>(xo, xo, rstd);
+            if constexpr (kKeep) {
+                mul_v<V>(go, gk[kKeep ? i : 0], d);
+            } else {
+                float w[V];
+                load_w<V>(p.gamma, p.w_kind, ring.c0 + i * ring.cstep, 1.0f, w);
+                mul_v<V>(go, w, d);
             }
         };
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
-            if (c0 + i * cstep < cols) {
+            if (ring.has(i)) {
                 float d[V];
                 const int k = kKeep ? i : 0;
                 terms(i, d, gd[k], xh[k]);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    ab[i][j] += d[j];
-                    ag[i][j] = fmaf(d[j], xh[k][j], ag[i][j]);
-                    s[0] += gd[k][j];
-                    s[1] = fmaf(gd[k][j], xh[k][j], s[1]);
-                }
+                add_v<V>(ab[i], ab[i], d);
+                fma_v<V>(ag[i], d, xh[k], ag[i]);
+                sum0.add(gd[k]);
+                sum1.fma(gd[k], xh[k]);
             }
-        if (p.dx) {
-            block_sum<2>(s, scratch, parity);
-            const float m0 = s[0] * p.inv_cols, m1 = s[1] * p.inv_cols;
-            T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+        if (dx) {
+            float m0 = sum0.total(), m1 = sum1.total();
+            block_sum2(m0, m1, scratch, parity);
+            m0 *= -rstd * p.inv_cols;   // dx = rstd g + (m0' + m1' xh), m' = -rstd * mean of g, of g xh
+            m1 *= -rstd * p.inv_cols;
 #pragma unroll
-            for (int i = 0; i < kItems; ++i) {
-                const int c = c0 + i * cstep;
-                if (c < cols) {
+            for (int i = 0; i < kItems; ++i)
+                if (ring.has(i)) {
                     float o[V], d[V];
                     const int k = kKeep ? i : 0;
                     if constexpr (!kKeep)
                         terms(i, d, gd[k], xh[k]);
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        o[j] = rstd * fmaf(-xh[k][j], m1, gd[k][j] - m0);
+                    fma_s<V>(o, xh[k], m1, m0);
+                    fma_sv<V>(o, gd[k], rstd, o);
                     if (add) {
                         float r[V];
-                        ring.read(stage, 2, i, add + row * p.ldadd, c, r);
-#pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            o[j] += r[j];
+                        ring.read(2, i, add, r);
+                        add_v<V>(o, o, r);
                     }
-                    store<T, V>(dx + c, o);
+                    store<T, V>(dx + i * ring.cstep, o);
                 }
-            }
+            dx += step * p.lddx;
         }
-        mean = mean_next;
-        rstd = rstd_next;
-        stage = stage + 1 == kS ? 0 : stage + 1;
+        if constexpr (kStages > 0) {
+            ring.advance(ring.rd);
+        } else {
+            x += step * p.ldx;
+            dy += step * p.lddy;
+            if (add)
+                add += step * p.ldadd;
+        }
     }
     if (p.part) {
-        float *out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+        float *out = p.part + r0 * 2 * cols;
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-            const int c = c0 + i * cstep;
-            if (c < cols) {
+            const int c = ring.c0 + i * ring.cstep;
+            if (ring.has(i)) {
                 if constexpr (V % 4 == 0) {   // cols is a multiple of V, and so of four
 #pragma unroll
                     for (int j = 0; j < V; j += 4) {
@@ -736,7 +928,7 @@ void launch_forward(const NormParams &p, int64_t nvec, cudaStream_t st)
 template <typename T, int V, int kItems>
 bool launch_forward_ring(const NormParams &p, int64_t nvec, cudaStream_t st)
 {
-    constexpr int kStages = 3;
+    constexpr int kStages = 3;   // (4 and 5 slots measured no faster at 2048 x 8192)
     const int threads = static_cast<int>(cdiv(cdiv(nvec, kItems), 32) * 32);
     const size_t smem = static_cast<size_t>(kStages) * kItems * threads * V * sizeof(T);
     if (smem > kRingLimit)
