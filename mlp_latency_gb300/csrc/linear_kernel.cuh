@@ -86,15 +86,15 @@ struct __align__(8) LCtrl {
     int32_t n_items;
 };
 
-// Shared memory: ring (1024-byte aligned), receive buffers, epilogue staging and bias tile per epilogue
-// warp (kRowsT needs neither), control block, group tables.
+// Shared memory: ring (1024-byte aligned), receive buffers, epilogue staging per epilogue warp (half as large for
+// kRowsT) and bias tile (not for kRowsT), control block, group tables.
 struct SmemMap {
     uint32_t recv, stage, bias, ctrl, tab;
     __host__ __device__ SmemMap(bool rows_t, uint32_t ring_bytes, uint32_t recv_total)
     {
         recv = ring_bytes;
         stage = recv + recv_total;
-        bias = stage + (rows_t ? 0u : 4u * kStageWarpBytes);
+        bias = stage + 4u * (rows_t ? kStageWarpBytes / 2 : kStageWarpBytes);
         ctrl = bias + (rows_t ? 0u : 4u * 256u * 4u);
         tab = ctrl + static_cast<uint32_t>((sizeof(LCtrl) + 15) / 16 * 16);
     }
@@ -602,26 +602,60 @@ __device__ __forceinline__ float load_bias(const LinearParams &p, int64_t i)
                       : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.bias)[i]);
 }
 
-// Output column `n` of up to 32 activation rows, lane = output column.
-template <int kAct>
-__device__ __forceinline__ void finish_rows_t(const LinearParams &p, float (&v)[32], float bias, int64_t row, int32_t n_rows,
-                                              int32_t n, bool n_ok)
+// kRowsT: 32 activation rows x this warp's 32 output columns (lane = column), transposed through the warp's
+// staging buffer: 32 rows of 64 bytes, moved to and from global memory 16 bytes a lane, four lanes a row.
+template <bool kLoad>
+__device__ __forceinline__ void stage_move_t(uint8_t *stage, uint8_t *gbase, int64_t ld_bytes, int32_t n_rows, int32_t seg_lim,
+                                             int32_t lane)
 {
-    if (!n_ok)
-        return;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row * p.ld_out + n;
+    const int32_t sg = lane & 3;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        if (j < n_rows) {
-            const float z = v[j] + bias;
-            if (p.z)
-                p.z[(row + j) * p.ld_z + n] = __float2bfloat16_rn(z);
-            float y = act_fwd(kAct, z);
-            if (p.res)
-                y += __bfloat162float(p.res[(row + j) * p.ld_res + n]);
-            out[j * p.ld_out] = __float2bfloat16_rn(y);
+    for (int it = 0; it < 4; ++it) {
+        const int32_t rr = it * 8 + (lane >> 2);
+        uint4 *s = reinterpret_cast<uint4 *>(stage + rr * 64 + sg * 16);
+        uint4 *q = reinterpret_cast<uint4 *>(gbase + rr * ld_bytes + sg * 16);
+        if (rr < n_rows && sg < seg_lim) {
+            if (kLoad)
+                *s = *q;
+            else
+                *q = *s;
         }
     }
+}
+
+template <int kAct>
+__device__ __forceinline__ void finish_rows_t(const LinearParams &p, float (&v)[32], float bias, uint8_t *stage, int64_t row,
+                                              int32_t n_rows, int32_t n0, int32_t lane)
+{
+    const int32_t seg_lim = min(4, (p.p_ext - n0) / 8);   // (columns are multiples of 8; may be negative)
+    __nv_bfloat16 *mine = reinterpret_cast<__nv_bfloat16 *>(stage) + lane;   // row j: mine[32 * j]
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        v[j] += bias;
+    if (p.z) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            mine[32 * j] = __float2bfloat16_rn(v[j]);
+        __syncwarp();
+        stage_move_t<false>(stage, reinterpret_cast<uint8_t *>(p.z + row * p.ld_z + n0), p.ld_z * 2, n_rows, seg_lim, lane);
+        __syncwarp();
+    }
+    if (p.res) {
+        stage_move_t<true>(stage, reinterpret_cast<uint8_t *>(const_cast<__nv_bfloat16 *>(p.res) + row * p.ld_res + n0), p.ld_res * 2,
+                           n_rows, seg_lim, lane);
+        __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        float y = act_fwd(kAct, v[j]);
+        if (p.res)
+            y += __bfloat162float(mine[32 * j]);
+        mine[32 * j] = __float2bfloat16_rn(y);
+    }
+    __syncwarp();
+    stage_move_t<false>(stage, reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(p.out) + row * p.ld_out + n0), p.ld_out * 2,
+                        n_rows, seg_lim, lane);
+    __syncwarp();
 }
 
 template <int kForm, int kPair>
@@ -632,7 +666,7 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
     const int32_t lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const uint32_t half = kPair == 2 ? (rank & 1u) : 0u;
-    uint8_t *stage = stage_all + ew * kStageWarpBytes;
+    uint8_t *stage = stage_all + ew * (kForm == kRowsT ? kStageWarpBytes / 2 : kStageWarpBytes);
     float *bias_s = bias_all + ew * 256;
     const int32_t bn = p.bn;
     const int32_t n_items = c->n_items;
@@ -761,12 +795,12 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                 float v[32];
                 fetch(col, v);
                 const int64_t row = static_cast<int64_t>(t.start) + t.q0 + col;
-                const bool n_ok = n_t < p.p_ext;
+                const int32_t n0 = n_t - lane;
                 switch (p.act) {
-                case kActGelu: finish_rows_t<kActGelu>(p, v, bias_t, row, rows_here, n_t, n_ok); break;
-                case kActSilu: finish_rows_t<kActSilu>(p, v, bias_t, row, rows_here, n_t, n_ok); break;
-                case kActRelu: finish_rows_t<kActRelu>(p, v, bias_t, row, rows_here, n_t, n_ok); break;
-                default: finish_rows_t<kActNone>(p, v, bias_t, row, rows_here, n_t, n_ok); break;
+                case kActGelu: finish_rows_t<kActGelu>(p, v, bias_t, stage, row, rows_here, n0, lane); break;
+                case kActSilu: finish_rows_t<kActSilu>(p, v, bias_t, stage, row, rows_here, n0, lane); break;
+                case kActRelu: finish_rows_t<kActRelu>(p, v, bias_t, stage, row, rows_here, n0, lane); break;
+                default: finish_rows_t<kActNone>(p, v, bias_t, stage, row, rows_here, n0, lane); break;
                 }
             }
         } else {
