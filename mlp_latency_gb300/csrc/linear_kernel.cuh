@@ -120,6 +120,20 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
                  : "memory");
 }
 
+// True in one lane of a converged warp.  (elect.sync rather than a comparison of the lane number: the compiler then
+// knows that the code under it runs in a single thread, and the uniform operands of tcgen05 and TMA instructions need
+// no loop over the lanes.)
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t pred = 0;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 r;\n\t"
+        "elect.sync r|p, 0xffffffff;\n\t"
+        "@p mov.u32 %0, 1;\n\t}\n"
+        : "+r"(pred));
+    return pred != 0;
+}
+
 // Order this thread's generic-proxy accesses of its CTA's shared memory with later async-proxy ones
 // (TMA copies, MMA operand reads).
 __device__ __forceinline__ void fence_proxy_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -944,10 +958,10 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
     const uint32_t tmem_base = c->tmem_base;
     if (!c->skip) {
         if (warp == 0) {
-            if (lane == 0)
+            if (elect_one())
                 l_role_tma<kForm, kPair>(p, c, g, ring);
         } else if (warp == 1) {
-            if (lane == 0)
+            if (elect_one())
                 l_role_mma<kForm, kPair>(p, c, g, ring, tmem_base);
         } else if (warp == 2) {
             if (kForm == kReduce && p.offsets)
