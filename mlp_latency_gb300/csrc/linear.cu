@@ -31,7 +31,9 @@ EncodeFn encoder()
     return fn;
 }
 
-// View (inner, outer, group) of bf16 rows of `inner` elements, `ld` apart, `outer` per group.
+// Views of bf16 rows of `inner` elements, `ld` apart, `outer` per group: (inner, outer, group) with boxes of 64 x
+// box_outer; or, for tiles of several 64-column boxes that start on a box, (64, outer, inner / 64, group) with all of a
+// tile's boxes in one.
 bool encode(CUtensorMap *map, const void *ptr, int64_t inner, int64_t outer, int64_t groups, int64_t ld, int box_outer)
 {
     EncodeFn fn = encoder();
@@ -50,10 +52,42 @@ constexpr size_t kSmemLimit = 227 * 1024;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+bool encode_boxed(CUtensorMap *map, const void *ptr, int64_t inner, int64_t outer, int64_t groups, int64_t ld, int boxes)
+{
+    EncodeFn fn = encoder();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(outer), static_cast<cuuint64_t>(inner / 64), static_cast<cuuint64_t>(groups)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld) * 2, 128, static_cast<cuuint64_t>(ld) * 2 * static_cast<cuuint64_t>(outer)};
+    const cuuint32_t box[4] = {64, kKB, static_cast<cuuint32_t>(boxes), 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Operand `op` of a launch.  K-major: `outer` rows of the reduction extent `inner`, `cols` of them per tile.  MN-major:
+// `inner` columns, the reduction outside, `cols` columns per tile.
+bool operand(LinearParams &p, int op, bool mn, const void *ptr, int64_t inner, int64_t outer, int64_t groups, int64_t ld, int cols)
+{
+    p.mn[op] = mn;
+    if (!mn) {
+        p.copy_bytes[op] = static_cast<uint32_t>(cols) * 128u;
+        return encode(&p.map[op], ptr, inner, outer, groups, ld, cols);
+    }
+    p.copy_bytes[op] = q_tile_bytes(cols, true);
+    if (inner % 64 == 0 && cols % 64 == 0 && encode_boxed(&p.map[op], ptr, inner, outer, groups, ld, cols / 64)) {
+        p.boxed[op] = 1;
+        return true;
+    }
+    return encode(&p.map[op], ptr, inner, outer, groups, ld, kKB);
+}
+
 struct Plan {
     int form, pair, bn, split, pipe;
     uint32_t slot, recv_bytes;
     int recv_bufs, part_align;
+    int q_step;              // kRowsT: rows per tile
 };
 
 }  // namespace
@@ -88,14 +122,14 @@ Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red,
 {
     const int64_t groups = std::min<int64_t>(h->groups, rows), avg = cdiv(rows, groups);
     const int64_t kb = cdiv(red, kKB);
-    Plan best{kRowsT, 1, 32, 1, 0, 0, 0, 0, 0};
+    Plan best{kRowsT, 1, 32, 1, 0, 0, 0, 0, 0, 0};
     double best_t = 1e300;
     for (int form = kRows; form <= kRowsT; ++form)
         for (int pair = 1; pair <= 2; ++pair)
             for (int bn = 32; bn <= 256; bn += 32)
                 for (int s = 1; s * pair <= 8 && s <= 4; ++s) {
-                    if (form == kRows && bn < 128)
-                        continue;
+                    if ((form == kRows && bn < 128) || (pair == 2 && rows <= (form == kRows ? kPRows : 32)))
+                        continue;   // (a pair's second half would have no rows)
                     const int64_t at_once = h->max_clusters[pair * s];
                     if (at_once < 1 || (s > 1 && kb < 4 * s))
                         continue;
@@ -119,16 +153,18 @@ Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red,
                         t += 2500.0 + n * 512.0 * (s - 1) / s / 16.0;
                     if (t < best_t) {
                         best_t = t;
-                        best = Plan{form, pair, bn, s, 0, 0, 0, 0, 0};
+                        best = Plan{form, pair, bn, s, 0, 0, 0, 0, 0, 0};
                     }
                 }
     finish_plan(h, best, best.form == kRows && w_mn);
+    // rows of one group are dealt evenly over their tiles; those of several groups end where they end
+    best.q_step = h->groups > 1 ? best.bn : static_cast<int>(cdiv(rows, cdiv(rows, best.bn)));
     return best;
 }
 
 Plan plan_reduce(const mlp_linear *h, int64_t p_ext, int64_t q_ext)
 {
-    Plan pl{kReduce, 2, 256, 1, 0, 0, 0, 0, 0};
+    Plan pl{kReduce, 2, 256, 1, 0, 0, 0, 0, 0, 0};
     if (h->groups * cdiv(p_ext, 256) * cdiv(q_ext, 256) * 2 < h->num_sms)
         pl.pair = 1, pl.bn = 128;
     finish_plan(h, pl, true);
@@ -192,23 +228,24 @@ mlp_status rows_product(const mlp_linear *h, LinearParams &p, int64_t rows, cons
     const Plan pl = plan_rows(h, rows, out_cols, red, b_mn);
     p.rows = static_cast<int32_t>(rows);
     p.k_ext = static_cast<int32_t>(red);
-    CUtensorMap *mapA = pl.form == kRows ? &p.mapP : &p.mapQ, *mapB = pl.form == kRows ? &p.mapQ : &p.mapP;
-    const int b_rows = pl.form == kRows ? pl.bn / pl.pair : kPRows;
-    if (!encode(mapA, A, red, rows, 1, lda, pl.form == kRows ? kPRows : pl.bn / pl.pair))
-        return MLP_ERR_CUDA;
-    if (!(b_mn ? encode(mapB, B, out_cols, red, h->groups, out_cols, kKB) : encode(mapB, B, red, out_cols, h->groups, red, b_rows)))
-        return MLP_ERR_CUDA;
     int64_t items;
+    p.q_step = pl.q_step;
     if (pl.form == kRows) {
-        p.p_mn = 0;
-        p.q_mn = b_mn;
+        // (a box never reaches past the last row of a short matrix: copies that are mostly out of range measured
+        // several times slower than full ones)
+        const int prows = static_cast<int>(std::min<int64_t>(kPRows, rows));
+        if (!operand(p, 0, false, A, red, rows, 1, lda, prows) ||
+            !operand(p, 1, b_mn, B, b_mn ? out_cols : red, b_mn ? red : out_cols, h->groups, b_mn ? out_cols : red, pl.bn / pl.pair))
+            return MLP_ERR_CUDA;
         p.q_ext = static_cast<int32_t>(out_cols);
         items = (cdiv(rows, kPRows * pl.pair) + h->groups - 1) * cdiv(out_cols, pl.bn);
     } else {
-        p.p_mn = b_mn;
-        p.q_mn = 0;
+        const int qrows = static_cast<int>(std::min<int64_t>(pl.pair == 2 ? pl.bn / 2 : pl.q_step, rows));
+        if (!operand(p, 1, false, A, red, rows, 1, lda, qrows) ||
+            !operand(p, 0, b_mn, B, b_mn ? out_cols : red, b_mn ? red : out_cols, h->groups, b_mn ? out_cols : red, kPRows))
+            return MLP_ERR_CUDA;
         p.p_ext = static_cast<int32_t>(out_cols);
-        items = (cdiv(rows, pl.bn) + h->groups - 1) * cdiv(out_cols, kPRows * pl.pair);
+        items = (cdiv(rows, pl.q_step) + h->groups - 1) * cdiv(out_cols, kPRows * pl.pair);
     }
     return launch(h, p, pl, items, st);
 }
@@ -576,12 +613,11 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         p.rows = static_cast<int32_t>(rows);
         p.p_ext = static_cast<int32_t>(pe);
         p.q_ext = static_cast<int32_t>(qe);
-        p.p_mn = p.q_mn = 1;
         p.out = dW;
         p.out_f32 = dw_esz == 4;
         p.ld_out = qe;
-        if (!encode(&p.mapP, kn ? X : dz, pe, rows, 1, kn ? ldx : ld_dz, kKB) ||
-            !encode(&p.mapQ, kn ? dz : X, qe, rows, 1, kn ? ld_dz : ldx, kKB))
+        if (!operand(p, 0, true, kn ? X : dz, pe, rows, 1, kn ? ldx : ld_dz, kPRows) ||
+            !operand(p, 1, true, kn ? dz : X, qe, rows, 1, kn ? ld_dz : ldx, pl.bn / pl.pair))
             return MLP_ERR_CUDA;
         return launch(h, p, pl, h->groups * cdiv(pe, kPRows * pl.pair) * cdiv(qe, pl.bn), st);
     }

@@ -13,10 +13,11 @@
 // In MMA terms every form is D[p, q] = sum_k P[p, k] Q[q, k] with operands that are K-major or
 // MN-major in memory (the descriptors' and the TMA boxes' business only).
 //
-// Roles (256 threads): warp 0 TMA producer, warp 1 MMA issuer and TMEM owner, warp 2 group tables
-// and the masking of ragged reduction tails, warps 4-7 epilogue (one TMEM lane quarter each).  The
-// accumulator is double buffered, so a tile's epilogue runs under the next tile's MMAs.  Tiles are
-// dealt out statically, in an order that lets the CTAs running at one time share operand panels in L2.
+// Roles (384 threads): warps 0 and 3 copy P and Q tiles (one thread each: issuing a fill's copies from one
+// thread took longer than its MMAs), warp 1 issues MMAs and owns TMEM, warp 2 builds the group tables and masks
+// ragged reduction tails, warps 4-11 run the epilogue (two per TMEM lane quarter, on alternating column chunks).
+// The accumulator is double buffered, so a tile's epilogue runs under the next tile's MMAs.  Tiles are dealt out
+// statically, in an order that lets the CTAs running at one time share operand panels in L2.
 //
 // kPair = 2 runs 256-row tiles on CTA pairs (cta_group::2): each CTA loads its 128 rows of P and half
 // of Q's tile, a third less to fetch per SM and flop.  split > 1 shares one tile's reduction among the
@@ -35,13 +36,14 @@ using namespace mlpc;
 enum Form { kRows = 0, kRowsT = 1, kReduce = 2 };
 enum Act { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3 };
 
-constexpr int kLThreads = 256;
+constexpr int kLThreads = 384;
+constexpr int kEpi = 8;                        // epilogue warps
 constexpr int kPRows = 128;                    // rows of P per CTA (= TMEM lanes)
 constexpr int kKB = 64;                        // reduction depth of one ring slot: 128 bytes of bf16
 constexpr uint32_t kPBytes = kPRows * kKB * 2;
 constexpr uint32_t kBoxBytes = kKB * 128;      // one MN-major box: 64 k rows of 64 columns
 constexpr int kMaxRing = 10;
-constexpr uint32_t kStageWarpBytes = 32 * 128; // epilogue staging: 32 rows x 128 bytes per warp
+constexpr uint32_t kStageWarpBytes = 32 * 64;  // epilogue staging: 32 rows x 64 bytes per warp
 constexpr uint32_t kStTimeout = 5, kStBadOffsets = 1;
 
 // Shared memory of one CTA's share of a Q tile: `cols` K-major rows of 128 bytes, or whole boxes of 64 columns.
@@ -51,12 +53,15 @@ __host__ __device__ inline uint32_t q_tile_bytes(int32_t cols, bool mn)
 }
 
 struct LinearParams {
-    CUtensorMap mapP, mapQ;         // (inner, outer, group) views
+    CUtensorMap map[2];             // P and Q: (inner, outer, group) views, or (64, outer, inner / 64, group)
+    uint32_t copy_bytes[2];         // what one fill copies of each into a CTA
+    int32_t boxed[2];               // the four-dimensional view: all boxes of an MN-major tile in one copy
+    int32_t mn[2];                  // operand stored MN-major (else K-major)
     const int32_t *offsets;         // device, groups + 1 entries, or null: one group of `rows` rows
     int32_t groups, rows;
     int32_t p_ext, q_ext, k_ext;    // extents of the dimensions that are not ragged
-    int32_t p_mn, q_mn;             // operand stored MN-major (else K-major)
     int32_t bn;                     // columns of a tile (the pair's)
+    int32_t q_step;                 // kRowsT: rows from one tile to the next (<= bn)
     int32_t split;                  // CTAs, or pairs, sharing a tile's reduction
     int32_t part_align;             // granularity of the column ranges that they finish: 8 or 32
     int32_t recv_bufs;              // receive buffers for partial sums, of recv_bytes each; 0: the ring
@@ -77,7 +82,8 @@ struct LinearParams {
 };
 
 struct __align__(8) LCtrl {
-    uint64_t full[kMaxRing], empty[kMaxRing], go[kMaxRing], tail[kMaxRing];
+    uint64_t full[kMaxRing], empty[kMaxRing], tail[kMaxRing];
+    uint64_t go[2][kMaxRing];   // leader to peer, per operand: the fill is armed
     uint64_t tfull[2], tempty[2];
     uint64_t drain, rdy[2], got[2], ringfree;
     uint32_t tmem_base;
@@ -86,16 +92,16 @@ struct __align__(8) LCtrl {
     int32_t n_items;
 };
 
-// Shared memory: ring (1024-byte aligned), receive buffers, epilogue staging per epilogue warp (half as large for
-// kRowsT) and bias tile (not for kRowsT), control block, group tables.
+// Shared memory: ring (1024-byte aligned), receive buffers, staging per epilogue warp, bias tile (kRowsT: none),
+// control block, group tables.
 struct SmemMap {
     uint32_t recv, stage, bias, ctrl, tab;
     __host__ __device__ SmemMap(bool rows_t, uint32_t ring_bytes, uint32_t recv_total)
     {
         recv = ring_bytes;
         stage = recv + recv_total;
-        bias = stage + 4u * (rows_t ? kStageWarpBytes / 2 : kStageWarpBytes);
-        ctrl = bias + (rows_t ? 0u : 4u * 256u * 4u);
+        bias = stage + kEpi * kStageWarpBytes;
+        ctrl = bias + (rows_t ? 0u : kEpi * 32u * 4u);
         tab = ctrl + static_cast<uint32_t>((sizeof(LCtrl) + 15) / 16 * 16);
     }
 };
@@ -118,6 +124,16 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr)
                  : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1, int32_t c2,
+                                                 int32_t c3, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
+        : "memory");
 }
 
 // True in one lane of a converged warp.  (elect.sync rather than a comparison of the lane number: the compiler then
@@ -218,7 +234,7 @@ __device__ __forceinline__ int32_t items_of(const LinearParams &p, int32_t cnt)
     if (kForm == kRows)
         return (cnt + bm - 1) / bm * ((p.q_ext + p.bn - 1) / p.bn);
     if (kForm == kRowsT)
-        return (cnt + p.bn - 1) / p.bn * ((p.p_ext + bm - 1) / bm);
+        return (cnt + p.q_step - 1) / p.q_step * ((p.p_ext + bm - 1) / bm);
     return (p.p_ext + bm - 1) / bm * ((p.q_ext + p.bn - 1) / p.bn);
 }
 
@@ -246,10 +262,11 @@ struct Walk {
         const int32_t kext = kForm == kReduce ? t.cnt : p.k_ext;
         const int32_t nkb = (kext + kKB - 1) / kKB;
         if (kForm == kRowsT) {
-            const int32_t tq = (t.cnt + p.bn - 1) / p.bn;
-            t.p0 = i / tq * bm;
-            t.q0 = i % tq * p.bn;
-            t.n = min(p.bn, (t.cnt - t.q0 + 16 * kPair - 1) / (16 * kPair) * (16 * kPair));   // (the MMA's step)
+            const int32_t tq = (t.cnt + p.q_step - 1) / p.q_step;
+            const int32_t pi = i / tq;
+            t.p0 = pi * bm;
+            t.q0 = (i - pi * tq) * p.q_step;
+            t.n = (min(p.q_step, t.cnt - t.q0) + 16 * kPair - 1) / (16 * kPair) * (16 * kPair);   // (the MMA's step)
         } else {
             const int32_t tp = ((kForm == kRows ? t.cnt : p.p_ext) + bm - 1) / bm;
             const int32_t tq = (p.q_ext + p.bn - 1) / p.bn;
@@ -282,8 +299,10 @@ __device__ __forceinline__ int32_t masked_rows(const LinearParams &p, const Tile
     return have < kKB && t.start + t.cnt < p.rows ? kKB - have : 0;
 }
 
-// -------------------------------------------------------------------------------- TMA producer --
-template <int kForm, int kPair>
+// ------------------------------------------------------------------------------- TMA producers --
+// One thread per operand (kOp 0: P, 1: Q) fills its part of every ring slot; a slot's full barrier takes one arrival
+// and the bytes of each.
+template <int kForm, int kPair, int kOp>
 __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring)
 {
     const int32_t num_pipe = p.num_pipe;
@@ -291,24 +310,23 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
     const uint32_t rank = cluster_ctarank();
     const uint32_t half = kPair == 2 ? (rank & 1u) : 0u;
     const uint32_t full_lead0 = kPair == 2 ? map_to_rank(&c->full[0], rank & ~1u) : 0u;
-    const uint32_t go_peer0 = kPair == 2 ? map_to_rank(&c->go[0], rank | 1u) : 0u;
+    const uint32_t go_peer0 = kPair == 2 ? map_to_rank(&c->go[kOp][0], rank | 1u) : 0u;
     const uint32_t tail_own0 = kPair == 2 ? map_to_rank(&c->tail[0], rank) : 0u;
-    const bool p_mn = p.p_mn != 0, q_mn = p.q_mn != 0;
-    const int32_t bn_cta = p.bn / kPair;
-    const uint32_t q_bytes = q_tile_bytes(bn_cta, q_mn);
+    const CUtensorMap *const map = &p.map[kOp];
+    const bool mn = p.mn[kOp] != 0, boxed = p.boxed[kOp] != 0;
+    const uint32_t bytes = p.copy_bytes[kOp];
+    const int32_t boxes = mn ? static_cast<int32_t>(bytes / kBoxBytes) : 1;
+    const bool shared_ring = p.split > 1 && p.recv_bufs == 0;
     const int32_t n_items = c->n_items;
-    // the ragged operand is read by many tiles, weights by the row panels of one group at a time
     const uint64_t pol = policy_evict_normal();
-    uint32_t issued = 0, tail_use = 0, tail_ph = 0;
+    uint32_t issued = 0, tail_use = 0, tail_ph = 0, item_ph = 0;
     int32_t ps = 0;
     uint32_t pph = 0;
     Walk<kForm, kPair> w(p);
     Tile t;
-    bool ok = true;
-    uint32_t item_ph = 0;
-    bool first = true;
+    bool ok = true, first = true;
     while (ok && w.next(p, g, n_items, t)) {
-        if (p.split > 1 && p.recv_bufs == 0) {   // the ring was the exchange buffer of the previous item
+        if (shared_ring) {   // the ring was the exchange buffer of the previous item
             if (!first) {
                 if (!lwait(&c->ringfree, item_ph, c, p))
                     break;
@@ -316,12 +334,14 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
             }
             first = false;
         }
-        const int32_t p_row = (kForm == kRows ? t.start : 0) + t.p0 + static_cast<int32_t>(half) * kPRows;
-        const int32_t q_row = (kForm == kRowsT ? t.start : 0) + t.q0 + static_cast<int32_t>(half) * (t.n / kPair);
-        const int32_t p_grp = kForm == kRowsT ? t.e : 0, q_grp = kForm == kRows ? t.e : 0;
-        for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
+        // first row (column of an MN-major operand) of this CTA's share, and the group
+        const int32_t row = kOp == 0 ? (kForm == kRows ? t.start : 0) + t.p0 + static_cast<int32_t>(half) * kPRows
+                                     : (kForm == kRowsT ? t.start : 0) + t.q0 + static_cast<int32_t>(half) * (t.n / kPair);
+        const int32_t grp = (kOp == 0 ? kForm == kRowsT : kForm == kRows) ? t.e : 0;
+        int32_t k = (kForm == kReduce ? t.start : 0) + t.kb0 * kKB;
+        for (int32_t kb = t.kb0; kb < t.kb1; ++kb, k += kKB) {
             if (kPair == 2 && half) {
-                if (!lwait(&c->go[ps], pph, c, p, true)) {   // the leader armed this fill
+                if (!lwait(&c->go[kOp][ps], pph, c, p, true)) {   // the leader armed this fill
                     ok = false;
                     break;
                 }
@@ -332,38 +352,34 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
             const bool masked = masked_rows<kForm>(p, t, kb) != 0;
             if (masked) {
                 // completes on this CTA's own tail barrier; warp 2 zeroes the rows and completes `full`
-                mbar_arrive_expect_tx(&c->tail[ps], kPBytes + q_bytes);
+                mbar_arrive_expect_tx(&c->tail[ps], bytes);
                 tail_use |= 1u << ps;
                 tail_ph ^= 1u << ps;
             } else if (!half) {
-                mbar_arrive_expect_tx(&c->full[ps], kPair * (kPBytes + q_bytes));
-                if (kForm == kReduce && kPair == 2)
-                    mbar_arrive(&c->full[ps]);   // (the count is 2: one per CTA's warp 2 on a masked fill)
+                mbar_arrive_expect_tx(&c->full[ps], kPair * bytes);
             }
             if (kPair == 2 && !half)
                 mbar_arrive_relaxed_cluster(go_peer0 + 8u * static_cast<uint32_t>(ps), 1);   // publishes no data
-            uint8_t *a = ring + static_cast<size_t>(ps) * slot_bytes;
-            uint8_t *b = a + kPBytes;
-            const int32_t k = (kForm == kReduce ? t.start : 0) + kb * kKB;
+            uint8_t *dst = ring + static_cast<size_t>(ps) * slot_bytes + (kOp == 0 ? 0u : kPBytes);
             const uint32_t fb = kPair == 2 ? (masked ? tail_own0 : full_lead0) + 8u * static_cast<uint32_t>(ps) : 0u;
             uint64_t *lb = masked ? &c->tail[ps] : &c->full[ps];
-            auto load = [&](uint8_t *dst, const CUtensorMap *m, int32_t c0, int32_t c1, int32_t c2) {
+            if (boxed) {
                 if (kPair == 2)
-                    tma_load_3d_pair(dst, m, fb, c0, c1, c2, pol);
+                    tma_load_4d_pair(dst, map, fb, 0, k, row >> 6, grp, pol);
                 else
-                    tma_load_3d(dst, m, lb, c0, c1, c2, pol);
-            };
-            if (p_mn) {
-                load(a, &p.mapP, p_row, k, p_grp);
-                load(a + kBoxBytes, &p.mapP, p_row + 64, k, p_grp);
+                    tma_load_4d(dst, map, lb, 0, k, row >> 6, grp, pol);
+            } else if (mn) {
+                for (int32_t j = 0; j < boxes; ++j) {
+                    if (kPair == 2)
+                        tma_load_3d_pair(dst + j * kBoxBytes, map, fb, row + 64 * j, k, grp, pol);
+                    else
+                        tma_load_3d(dst + j * kBoxBytes, map, lb, row + 64 * j, k, grp, pol);
+                }
             } else {
-                load(a, &p.mapP, k, p_row, p_grp);
-            }
-            if (q_mn) {
-                for (int32_t j = 0; j < bn_cta; j += 64)
-                    load(b + (j >> 6) * kBoxBytes, &p.mapQ, q_row + j, k, q_grp);
-            } else {
-                load(b, &p.mapQ, k, q_row, q_grp);
+                if (kPair == 2)
+                    tma_load_3d_pair(dst, map, fb, k, row, grp, pol);
+                else
+                    tma_load_3d(dst, map, lb, k, row, grp, pol);
             }
             ++issued;
             if (++ps == num_pipe) {
@@ -397,14 +413,14 @@ __device__ __forceinline__ void l_role_mma(const LinearParams &p, LCtrl *c, cons
     const int32_t num_pipe = p.num_pipe;
     const uint32_t bn = static_cast<uint32_t>(p.bn);
     const uint32_t tfull_peer0 = kPair == 2 ? map_to_rank(&c->tfull[0], cluster_ctarank() | 1u) : 0u;
-    const uint32_t idesc0 = idesc_bf16_f32(kPRows * kPair, 0, p.q_mn ? 1u : 0u) | (p.p_mn ? 1u << 15 : 0u);
+    const uint32_t idesc0 = idesc_bf16_f32(kPRows * kPair, 0, p.mn[1] ? 1u : 0u) | (p.mn[0] ? 1u << 15 : 0u);
     const uint32_t base = smem_u32(ring);
     // K-major: 8-row groups 1024 bytes apart, a 16-deep k step 32 bytes along the row.  MN-major: 64
     // columns x 64 k per box, boxes kBoxBytes apart, a k step 16 rows of 128 bytes.  Slot offsets add to
     // the 14-bit address field in 16-byte units (shared memory is below 2^18 bytes: no carry).
-    const uint64_t pd = p.p_mn ? smem_desc(base, kBoxBytes, 1024u, 2u) : smem_desc(base, 16u, 1024u, 2u);
-    const uint64_t qd = p.q_mn ? smem_desc(base + kPBytes, kBoxBytes, 1024u, 2u) : smem_desc(base + kPBytes, 16u, 1024u, 2u);
-    const uint64_t pstep = p.p_mn ? 128u : 2u, qstep = p.q_mn ? 128u : 2u;
+    const uint64_t pd = p.mn[0] ? smem_desc(base, kBoxBytes, 1024u, 2u) : smem_desc(base, 16u, 1024u, 2u);
+    const uint64_t qd = p.mn[1] ? smem_desc(base + kPBytes, kBoxBytes, 1024u, 2u) : smem_desc(base + kPBytes, 16u, 1024u, 2u);
+    const uint64_t pstep = p.mn[0] ? 128u : 2u, qstep = p.mn[1] ? 128u : 2u;
     const uint64_t slot16 = p.slot_bytes >> 4;
     const int32_t n_items = c->n_items;
     int32_t ps = 0;
@@ -483,10 +499,12 @@ __device__ __forceinline__ void l_role_mask(const LinearParams &p, LCtrl *c, con
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-            if (kPair == 2)
+            if (kPair == 2) {   // (one arrival of each CTA; a single CTA makes both)
                 mbar_arrive_cluster(full_lead0 + 8u * static_cast<uint32_t>(ps));
-            else
+            } else {
                 mbar_arrive(&c->full[ps]);
+                mbar_arrive(&c->full[ps]);
+            }
         }
     }
 }
@@ -504,109 +522,48 @@ __device__ __forceinline__ float2 unpack2(uint32_t w)
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// Offset of 16-byte segment `seg` of row `row` in a warp's 32 x 128-byte staging buffer; the XOR keeps
-// row-wise and segment-wise accesses off each other's banks.
-__device__ __forceinline__ uint32_t stg(int row, int seg) { return static_cast<uint32_t>(row * 128 + ((seg ^ (row & 7)) * 16)); }
-
-// The staged 32 rows x 8 segments to (or from) global memory, whole 128-byte row pieces at a time.
-// esz: bytes of an element; rows and columns past the limits are skipped (columns are multiples of a
-// segment).
-template <bool kLoad>
-__device__ __forceinline__ void stage_move(uint8_t *stage, uint8_t *gbase, int64_t ld_bytes, int32_t row_lim,
-                                           int32_t seg_lim, int32_t lane)
+// Offset of 16-byte segment `seg` (0-3) of row `row` in a warp's 32 x 64-byte staging buffer.  kSwizzle: accessed a
+// row per lane, so the XOR spreads eight consecutive rows over all banks.
+template <bool kSwizzle>
+__device__ __forceinline__ uint32_t stg(int row, int seg)
 {
-    const int32_t sg = lane & 7;
+    return static_cast<uint32_t>(row * 64 + ((kSwizzle ? seg ^ ((row >> 1) & 3) : seg) * 16));
+}
+
+// The staged 32 rows x 4 segments to global memory, four lanes a row; rows and segments past the limits are skipped.
+template <bool kSwizzle>
+__device__ __forceinline__ void stage_store(const uint8_t *stage, uint8_t *gbase, int64_t ld_bytes, int32_t row_lim,
+                                            int32_t seg_lim, int32_t lane)
+{
+    const int32_t sg = lane & 3;
 #pragma unroll
-    for (int it = 0; it < 8; ++it) {
-        const int32_t rr = it * 4 + (lane >> 3);
-        uint4 *s = reinterpret_cast<uint4 *>(stage + stg(rr, sg));
-        uint4 *q = reinterpret_cast<uint4 *>(gbase + rr * ld_bytes + sg * 16);
-        if (rr < row_lim && sg < seg_lim) {
-            if (kLoad)
-                *s = *q;
-            else
-                *q = *s;
-        }
+    for (int it = 0; it < 4; ++it) {
+        const int32_t rr = it * 8 + (lane >> 2);
+        if (rr < row_lim && sg < seg_lim)
+            *reinterpret_cast<uint4 *>(gbase + rr * ld_bytes + sg * 16) =
+                *reinterpret_cast<const uint4 *>(stage + stg<kSwizzle>(rr, sg));
     }
 }
 
-// Arrive at the leader's accumulator-empty barrier.
-template <int kPair>
-__device__ __forceinline__ void free_acc(LCtrl *c, uint32_t acc)
+// The residual's piece of a chunk: requested early, staged when it is needed.
+__device__ __forceinline__ void res_load(uint4 (&x)[4], const uint8_t *gbase, int64_t ld_bytes, int32_t row_lim, int32_t seg_lim,
+                                         int32_t lane)
 {
-    if (kPair == 2)
-        mbar_arrive_cluster(map_to_rank(&c->tempty[acc], cluster_ctarank() & ~1u));
-    else
-        mbar_arrive(&c->tempty[acc]);
+    const int32_t sg = lane & 3;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int32_t rr = it * 8 + (lane >> 2);
+        x[it] = make_uint4(0u, 0u, 0u, 0u);
+        if (rr < row_lim && sg < seg_lim)
+            x[it] = *reinterpret_cast<const uint4 *>(gbase + rr * ld_bytes + sg * 16);
+    }
 }
-
-// 32 x kW part of a tile's row chunk in the orientation TMEM lane = output row: bias, activation,
-// residual, rounding and stores of 64 bf16 (or 32 fp32) columns.
-template <int kAct>
-__device__ __forceinline__ void finish_bf16(const LinearParams &p, float (&v)[64], uint8_t *stage, const float *bias,
-                                            int64_t row, int32_t row_lim, int32_t col, int32_t col_lim, int32_t lane)
+template <bool kSwizzle>
+__device__ __forceinline__ void res_stage(const uint4 (&x)[4], uint8_t *stage, int32_t lane)
 {
-    const int32_t seg_lim = min(8, (col_lim - col) / 8);
-    if (p.bias) {
 #pragma unroll
-        for (int j = 0; j < 64; j += 4) {
-            const float4 b = *reinterpret_cast<const float4 *>(bias + j);
-            v[j] += b.x;
-            v[j + 1] += b.y;
-            v[j + 2] += b.z;
-            v[j + 3] += b.w;
-        }
-    }
-    if (p.z) {
-#pragma unroll
-        for (int s = 0; s < 8; ++s)
-            *reinterpret_cast<uint4 *>(stage + stg(lane, s)) =
-                make_uint4(pack2(v[8 * s], v[8 * s + 1]), pack2(v[8 * s + 2], v[8 * s + 3]),
-                           pack2(v[8 * s + 4], v[8 * s + 5]), pack2(v[8 * s + 6], v[8 * s + 7]));
-        __syncwarp();
-        stage_move<false>(stage, reinterpret_cast<uint8_t *>(p.z + row * p.ld_z + col), p.ld_z * 2, row_lim, seg_lim, lane);
-        __syncwarp();
-    }
-    if (p.res) {
-        stage_move<true>(stage, reinterpret_cast<uint8_t *>(const_cast<__nv_bfloat16 *>(p.res) + row * p.ld_res + col),
-                         p.ld_res * 2, row_lim, seg_lim, lane);
-        __syncwarp();
-    }
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-        uint4 *q = reinterpret_cast<uint4 *>(stage + stg(lane, s));
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            y[j] = act_fwd(kAct, v[8 * s + j]);
-        if (p.res) {
-            const uint4 x = *q;
-            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = unpack2(xw[j]);
-                y[2 * j] += f.x;
-                y[2 * j + 1] += f.y;
-            }
-        }
-        *q = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
-    }
-    __syncwarp();
-    stage_move<false>(stage, reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(p.out) + row * p.ld_out + col),
-                      p.ld_out * 2, row_lim, seg_lim, lane);
-    __syncwarp();
-}
-
-__device__ __forceinline__ void finish_f32(const LinearParams &p, const float *v, uint8_t *stage, int64_t row,
-                                           int32_t row_lim, int32_t col, int32_t col_lim, int32_t lane)
-{
-    const int32_t seg_lim = min(8, (col_lim - col) / 4);
-#pragma unroll
-    for (int s = 0; s < 8; ++s)
-        *reinterpret_cast<float4 *>(stage + stg(lane, s)) = make_float4(v[4 * s], v[4 * s + 1], v[4 * s + 2], v[4 * s + 3]);
-    __syncwarp();
-    stage_move<false>(stage, reinterpret_cast<uint8_t *>(static_cast<float *>(p.out) + row * p.ld_out + col),
-                      p.ld_out * 4, row_lim, seg_lim, lane);
+    for (int it = 0; it < 4; ++it)
+        *reinterpret_cast<uint4 *>(stage + stg<kSwizzle>(it * 8 + (lane >> 2), lane & 3)) = x[it];
     __syncwarp();
 }
 
@@ -616,72 +573,105 @@ __device__ __forceinline__ float load_bias(const LinearParams &p, int64_t i)
                       : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.bias)[i]);
 }
 
-// kRowsT: 32 activation rows x this warp's 32 output columns (lane = column), transposed through the warp's
-// staging buffer: 32 rows of 64 bytes, moved to and from global memory 16 bytes a lane, four lanes a row.
-template <bool kLoad>
-__device__ __forceinline__ void stage_move_t(uint8_t *stage, uint8_t *gbase, int64_t ld_bytes, int32_t n_rows, int32_t seg_lim,
-                                             int32_t lane)
-{
-    const int32_t sg = lane & 3;
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int32_t rr = it * 8 + (lane >> 2);
-        uint4 *s = reinterpret_cast<uint4 *>(stage + rr * 64 + sg * 16);
-        uint4 *q = reinterpret_cast<uint4 *>(gbase + rr * ld_bytes + sg * 16);
-        if (rr < n_rows && sg < seg_lim) {
-            if (kLoad)
-                *s = *q;
-            else
-                *q = *s;
-        }
-    }
-}
+// A 32 x 32 chunk of the output on its way out.  Rows are output rows, so with TMEM lane = output row (kLaneRow) a
+// lane holds a row of the chunk, and with lane = output column (kRowsT) a column; both go through the staging buffer
+// so that global memory is touched in 64-byte row pieces.
+struct Chunk {
+    int64_t row;         // first output row and column
+    int32_t col;
+    int32_t row_lim, seg_lim;
+};
 
-template <int kAct>
-__device__ __forceinline__ void finish_rows_t(const LinearParams &p, float (&v)[32], float bias, uint8_t *stage, int64_t row,
-                                              int32_t n_rows, int32_t n0, int32_t lane)
+template <bool kLaneRow>
+__device__ __forceinline__ void put_bf16(const float (&v)[32], uint8_t *stage, int32_t lane)
 {
-    const int32_t seg_lim = min(4, (p.p_ext - n0) / 8);   // (columns are multiples of 8; may be negative)
-    __nv_bfloat16 *mine = reinterpret_cast<__nv_bfloat16 *>(stage) + lane;   // row j: mine[32 * j]
+    if (kLaneRow) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-        v[j] += bias;
-    if (p.z) {
+        for (int s = 0; s < 4; ++s)
+            *reinterpret_cast<uint4 *>(stage + stg<true>(lane, s)) =
+                make_uint4(pack2(v[8 * s], v[8 * s + 1]), pack2(v[8 * s + 2], v[8 * s + 3]),
+                           pack2(v[8 * s + 4], v[8 * s + 5]), pack2(v[8 * s + 6], v[8 * s + 7]));
+    } else {
+        __nv_bfloat16 *mine = reinterpret_cast<__nv_bfloat16 *>(stage) + lane;
 #pragma unroll
         for (int j = 0; j < 32; ++j)
             mine[32 * j] = __float2bfloat16_rn(v[j]);
+    }
+    __syncwarp();
+}
+
+template <int kAct, bool kLaneRow>
+__device__ __forceinline__ void finish_chunk(const LinearParams &p, float (&v)[32], uint8_t *stage, const Chunk &ch, const uint4 (&res)[4],
+                                             int32_t lane)
+{
+    if (p.z) {
+        put_bf16<kLaneRow>(v, stage, lane);
+        stage_store<kLaneRow>(stage, reinterpret_cast<uint8_t *>(p.z + ch.row * p.ld_z + ch.col), p.ld_z * 2, ch.row_lim, ch.seg_lim, lane);
         __syncwarp();
-        stage_move_t<false>(stage, reinterpret_cast<uint8_t *>(p.z + row * p.ld_z + n0), p.ld_z * 2, n_rows, seg_lim, lane);
-        __syncwarp();
+    }
+    if (kAct != kActNone) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            v[j] = act_fwd(kAct, v[j]);
     }
     if (p.res) {
-        stage_move_t<true>(stage, reinterpret_cast<uint8_t *>(const_cast<__nv_bfloat16 *>(p.res) + row * p.ld_res + n0), p.ld_res * 2,
-                           n_rows, seg_lim, lane);
+        res_stage<kLaneRow>(res, stage, lane);
+        if (kLaneRow) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(stage + stg<true>(lane, s));
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = unpack2(xw[j]);
+                    v[8 * s + 2 * j] += f.x;
+                    v[8 * s + 2 * j + 1] += f.y;
+                }
+            }
+        } else {
+            const __nv_bfloat16 *mine = reinterpret_cast<const __nv_bfloat16 *>(stage) + lane;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] += __bfloat162float(mine[32 * j]);
+        }
         __syncwarp();
     }
+    put_bf16<kLaneRow>(v, stage, lane);
+    stage_store<kLaneRow>(stage, reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(p.out) + ch.row * p.ld_out + ch.col),
+                          p.ld_out * 2, ch.row_lim, ch.seg_lim, lane);
+    __syncwarp();
+}
+
+// 32 x 32 fp32 values, 16 columns at a time.
+__device__ __forceinline__ void finish_f32(const LinearParams &p, const float (&v)[32], uint8_t *stage, const Chunk &ch, int32_t cols,
+                                           int32_t lane)
+{
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        float y = act_fwd(kAct, v[j]);
-        if (p.res)
-            y += __bfloat162float(mine[32 * j]);
-        mine[32 * j] = __float2bfloat16_rn(y);
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            *reinterpret_cast<float4 *>(stage + stg<true>(lane, s)) =
+                make_float4(v[16 * h + 4 * s], v[16 * h + 4 * s + 1], v[16 * h + 4 * s + 2], v[16 * h + 4 * s + 3]);
+        __syncwarp();
+        stage_store<true>(stage, reinterpret_cast<uint8_t *>(static_cast<float *>(p.out) + ch.row * p.ld_out + ch.col + 16 * h),
+                          p.ld_out * 4, ch.row_lim, (cols - 16 * h) / 4, lane);
+        __syncwarp();
     }
-    __syncwarp();
-    stage_move_t<false>(stage, reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(p.out) + row * p.ld_out + n0), p.ld_out * 2,
-                        n_rows, seg_lim, lane);
-    __syncwarp();
 }
 
 template <int kForm, int kPair>
 __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *recv_base,
                                                 uint8_t *stage_all, float *bias_all, uint32_t tmem_base)
 {
-    const int32_t ew = static_cast<int32_t>(threadIdx.x / 32) - 4;   // = warp % 4: its TMEM lane quarter
+    constexpr bool kLaneRow = kForm != kRowsT;
+    const int32_t ew = static_cast<int32_t>(threadIdx.x / 32) - 4;
+    const int32_t quarter = ew & 3;            // = warp % 4: the TMEM lanes this warp can read
+    const int32_t which = ew >> 2;             // of the quarter's two warps: even or odd chunks
     const int32_t lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const uint32_t half = kPair == 2 ? (rank & 1u) : 0u;
-    uint8_t *stage = stage_all + ew * (kForm == kRowsT ? kStageWarpBytes / 2 : kStageWarpBytes);
-    float *bias_s = bias_all + ew * 256;
+    uint8_t *stage = stage_all + ew * kStageWarpBytes;
+    float *bias_s = bias_all + ew * 32;
     const int32_t bn = p.bn;
     const int32_t n_items = c->n_items;
     const bool splitk = p.split > 1;
@@ -689,7 +679,8 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
     const int32_t me = splitk ? static_cast<int32_t>(rank) / kPair : 0;
     const int32_t nbuf = p.recv_bufs > 0 ? p.recv_bufs : 1;
     auto cta_of = [&](int32_t slice) { return static_cast<uint32_t>(slice * kPair) + half; };   // same half, other slice
-    const uint32_t lane_base = static_cast<uint32_t>(ew * 32) << 16;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tempty_lead0 = map_to_rank(&c->tempty[0], kPair == 2 ? rank & ~1u : rank);
     uint32_t tiles = 0;
     int32_t buf = 0;           // receive buffer of this item, and how often it was used before (parity)
     uint32_t buf_ph = 0;
@@ -701,20 +692,42 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
         // the columns of the tile that this CTA finishes
         const int32_t part = splitk ? ((t.n + S - 1) / S + p.part_align - 1) / p.part_align * p.part_align : t.n;
         const int32_t c_lo = min(me * part, t.n), c_hi = min(c_lo + part, t.n);
-        // ---- bias of the tile, while its MMAs run
-        float bias_t = 0.0f;
-        const int32_t n_t = t.p0 + static_cast<int32_t>(half) * kPRows + ew * 32 + lane;   // kRowsT: this lane's output column
-        if (p.bias) {
-            if (kForm == kRowsT) {
-                if (n_t < p.p_ext)
-                    bias_t = load_bias(p, static_cast<int64_t>(t.e) * p.p_ext + n_t);
+        // where chunk `col` (accumulator columns col .. col + 31 of this warp's lanes) goes
+        const int32_t prow = t.p0 + static_cast<int32_t>(half) * kPRows + quarter * 32;   // first MMA row of this warp
+        auto chunk_of = [&](int32_t col) {
+            Chunk ch;
+            if (kLaneRow) {
+                ch.row = (kForm == kRows ? static_cast<int64_t>(t.start) : static_cast<int64_t>(t.e) * p.p_ext) + prow;
+                ch.col = t.q0 + col;
+                ch.row_lim = min(32, (kForm == kRows ? t.cnt : p.p_ext) - prow);
+                ch.seg_lim = (min(min(32, c_hi - col), p.q_ext - ch.col)) / 8;   // (extents are multiples of 8)
             } else {
-                __syncwarp();
-                for (int32_t j = c_lo + lane; j < c_hi; j += 32)
-                    bias_s[j] = t.q0 + j < p.q_ext ? load_bias(p, static_cast<int64_t>(t.e) * p.q_ext + t.q0 + j) : 0.0f;
-                __syncwarp();
+                ch.row = static_cast<int64_t>(t.start) + t.q0 + col;
+                ch.col = prow;
+                ch.row_lim = min(min(32, c_hi - col), min(p.q_step, t.cnt - t.q0) - col);
+                ch.seg_lim = min(32, p.p_ext - prow) / 8;
             }
-        }
+            return ch;
+        };
+        auto valid = [&](const Chunk &ch) { return ch.row_lim > 0 && ch.seg_lim > 0; };
+        uint4 res[4];
+        auto request_res = [&](int32_t col) {
+            if (p.res && col < c_hi) {
+                const Chunk ch = chunk_of(col);
+                res_load(res, reinterpret_cast<const uint8_t *>(p.res + ch.row * p.ld_res + ch.col), p.ld_res * 2, ch.row_lim,
+                         ch.seg_lim, lane);
+            }
+        };
+        // ---- bias and residual of the first chunk are requested while the tile's MMAs run, of later ones a chunk
+        // ahead.  A lane holds one column's bias: its own for kRowsT, column col + lane of the chunk otherwise.
+        float bias = 0.0f;
+        auto request_bias = [&](int32_t col) {
+            const int32_t n = kLaneRow ? t.q0 + col + lane : prow + lane, ext = kLaneRow ? p.q_ext : p.p_ext;
+            if (p.bias && col < c_hi)
+                bias = n < ext ? load_bias(p, static_cast<int64_t>(t.e) * ext + n) : 0.0f;
+        };
+        request_bias(c_lo + 32 * which);
+        request_res(c_lo + 32 * which);
         if (!lwait_warp(&c->tfull[acc], ph, c, p, kPair == 2))
             return;
         tc_fence_after();
@@ -727,7 +740,7 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
             if (p.recv_bufs == 0) {
                 if (lane == 0)
                     for (int32_t r = 0; r < S; ++r)
-                        mbar_arrive_cluster(map_to_rank(&c->rdy[0], cta_of(r)));
+                        mbar_arrive_relaxed_cluster(map_to_rank(&c->rdy[0], cta_of(r)), 1);   // publishes no data
                 if (!lwait_warp(&c->rdy[0], buf_ph, c, p, true))
                     return;
             } else if (tiles >= static_cast<uint32_t>(nbuf)) {
@@ -740,14 +753,14 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                 const uint32_t dst = map_to_rank(recv, cta_of(r));
                 const int32_t slot = me < r ? me : me - 1;
                 const int32_t r_lo = min(r * part, t.n), r_n = min(part, t.n - r_lo);
-                for (int32_t j = 0; j < r_n; j += 8) {
+                for (int32_t j = 8 * which; j < r_n; j += 16) {
                     uint32_t x[8];
                     tmem_ld_32x32b_x8(d + static_cast<uint32_t>(r_lo + j), x);
                     tmem_ld_wait();
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const uint32_t off =
-                            (static_cast<uint32_t>(slot * (part / 4) + j / 4 + b) * 128u + static_cast<uint32_t>(ew * 32 + lane)) * 16u;
+                        const uint32_t off = (static_cast<uint32_t>(slot * (part / 4) + j / 4 + b) * 128u +
+                                              static_cast<uint32_t>(quarter * 32 + lane)) * 16u;
                         st_cluster_v4_f32(dst + off, have_k ? __uint_as_float(x[4 * b]) : 0.0f,
                                           have_k ? __uint_as_float(x[4 * b + 1]) : 0.0f,
                                           have_k ? __uint_as_float(x[4 * b + 2]) : 0.0f,
@@ -756,28 +769,42 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                 }
             }
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0) {   // one fence, then arrivals: together the release of the warp's stores
+                fence_acq_rel_cluster();
                 for (int32_t o = 1; o < S; ++o)
-                    mbar_arrive_cluster(map_to_rank(&c->got[buf], cta_of((me + o) % S)));
+                    mbar_arrive_relaxed_cluster(map_to_rank(&c->got[buf], cta_of((me + o) % S)), 1);
+            }
             if (!lwait_warp(&c->got[buf], buf_ph, c, p, true))
                 return;
         }
-        // Accumulator columns [col, col + 32) of this lane, partial sums of all slices in slice order.
-        auto fetch = [&](int32_t col, float *v) {
-            uint32_t x[32];
-            tmem_ld_32x32b_x32(d + static_cast<uint32_t>(col), x);
-            tmem_ld_wait();
+        bool freed = false;
+        for (int32_t col = c_lo + 32 * which; col < c_hi; col += 64) {
+            const Chunk ch = chunk_of(col);
+            // accumulator columns [col, col + 32) of this lane, partial sums of all slices in slice order
+            float v[32];
+            {
+                uint32_t x[32];
+                tmem_ld_32x32b_x32(d + static_cast<uint32_t>(col), x);
+                tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                v[j] = have_k ? __uint_as_float(x[j]) : 0.0f;
+                for (int j = 0; j < 32; ++j)
+                    v[j] = have_k ? __uint_as_float(x[j]) : 0.0f;
+            }
+            if (col + 64 >= c_hi) {   // this warp's last read of the accumulator
+                freed = true;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_relaxed_cluster(tempty_lead0 + 8u * acc, 1);
+            }
             if (splitk) {
+                const int32_t blocks = min(8, (c_hi - col + 3) / 4);
                 float own[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     own[j] = v[j];
                     v[j] = 0.0f;
                 }
-                const int32_t blocks = min(8, (c_hi - col + 3) / 4);
                 for (int32_t s = 0; s < S; ++s) {
                     if (s == me) {
 #pragma unroll
@@ -791,7 +818,7 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                         if (b < blocks) {
                             const float4 q = *reinterpret_cast<const float4 *>(
                                 recv + (static_cast<uint32_t>(slot * (part / 4) + (col - c_lo) / 4 + b) * 128u +
-                                        static_cast<uint32_t>(ew * 32 + lane)) * 16u);
+                                        static_cast<uint32_t>(quarter * 32 + lane)) * 16u);
                             v[4 * b] += q.x;
                             v[4 * b + 1] += q.y;
                             v[4 * b + 2] += q.z;
@@ -800,69 +827,60 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                     }
                 }
             }
-        };
-        if (kForm == kRowsT) {
-            for (int32_t col = c_lo; col < c_hi; col += 32) {
-                const int32_t rows_here = min(min(32, c_hi - col), t.cnt - t.q0 - col);
-                if (rows_here <= 0)
-                    break;
-                float v[32];
-                fetch(col, v);
-                const int64_t row = static_cast<int64_t>(t.start) + t.q0 + col;
-                const int32_t n0 = n_t - lane;
-                switch (p.act) {
-                case kActGelu: finish_rows_t<kActGelu>(p, v, bias_t, stage, row, rows_here, n0, lane); break;
-                case kActSilu: finish_rows_t<kActSilu>(p, v, bias_t, stage, row, rows_here, n0, lane); break;
-                case kActRelu: finish_rows_t<kActRelu>(p, v, bias_t, stage, row, rows_here, n0, lane); break;
-                default: finish_rows_t<kActNone>(p, v, bias_t, stage, row, rows_here, n0, lane); break;
+            if (kForm == kReduce) {
+                if (valid(ch)) {
+                    if (p.out_f32)
+                        finish_f32(p, v, stage, ch, 8 * ch.seg_lim, lane);
+                    else
+                        finish_chunk<kActNone, true>(p, v, stage, ch, res, lane);
                 }
+                continue;
             }
-        } else {
-            const int32_t prow = t.p0 + static_cast<int32_t>(half) * kPRows + ew * 32;   // first row of this warp
-            const int32_t row_lim = min(32, (kForm == kRows ? t.cnt : p.p_ext) - prow);
-            const int64_t row = (kForm == kRows ? static_cast<int64_t>(t.start) : static_cast<int64_t>(t.e) * p.p_ext) + prow;
-            for (int32_t col = c_lo; col < c_hi && t.q0 + col < p.q_ext && row_lim > 0; col += 64) {
-                float v[64];
-                fetch(col, v);
-                if (col + 32 < c_hi) {
-                    fetch(col + 32, v + 32);
-                } else {
+            if (p.bias) {
+                if (kLaneRow) {
+                    bias_s[lane] = bias;
+                    __syncwarp();
+                }
 #pragma unroll
-                    for (int j = 32; j < 64; ++j)
-                        v[j] = 0.0f;
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 b = kLaneRow ? *reinterpret_cast<const float4 *>(bias_s + j) : make_float4(bias, bias, bias, bias);
+                    v[j] += b.x;
+                    v[j + 1] += b.y;
+                    v[j + 2] += b.z;
+                    v[j + 3] += b.w;
                 }
-                const int32_t gcol = t.q0 + col, col_lim = min(p.q_ext, t.q0 + c_hi);
-                if (kForm == kReduce) {
-                    if (p.out_f32) {
-                        finish_f32(p, v, stage, row, row_lim, gcol, col_lim, lane);
-                        if (gcol + 32 < col_lim)
-                            finish_f32(p, v + 32, stage, row, row_lim, gcol + 32, col_lim, lane);
-                    } else {
-                        finish_bf16<kActNone>(p, v, stage, bias_s + col, row, row_lim, gcol, col_lim, lane);
-                    }
-                } else {
-                    switch (p.act) {
-                    case kActGelu: finish_bf16<kActGelu>(p, v, stage, bias_s + col, row, row_lim, gcol, col_lim, lane); break;
-                    case kActSilu: finish_bf16<kActSilu>(p, v, stage, bias_s + col, row, row_lim, gcol, col_lim, lane); break;
-                    case kActRelu: finish_bf16<kActRelu>(p, v, stage, bias_s + col, row, row_lim, gcol, col_lim, lane); break;
-                    default: finish_bf16<kActNone>(p, v, stage, bias_s + col, row, row_lim, gcol, col_lim, lane); break;
-                    }
+                if (kLaneRow) {
+                    __syncwarp();
+                    request_bias(col + 64);
                 }
             }
+            if (valid(ch)) {
+                switch (p.act) {
+                case kActGelu: finish_chunk<kActGelu, kLaneRow>(p, v, stage, ch, res, lane); break;
+                case kActSilu: finish_chunk<kActSilu, kLaneRow>(p, v, stage, ch, res, lane); break;
+                case kActRelu: finish_chunk<kActRelu, kLaneRow>(p, v, stage, ch, res, lane); break;
+                default: finish_chunk<kActNone, kLaneRow>(p, v, stage, ch, res, lane); break;
+                }
+            }
+            request_res(col + 64);
         }
-        tc_fence_before();
         __syncwarp();
         if (splitk && p.recv_bufs == 0) {
-            fence_proxy_async_shared();   // these reads of the ring before the producer's next copies
+            fence_proxy_async_shared();   // these reads of the ring before the producers' next copies
             __syncwarp();
         }
         if (lane == 0) {
-            free_acc<kPair>(c, acc);
-            if (splitk && p.recv_bufs == 0)
+            if (!freed) {
+                tc_fence_before();
+                mbar_arrive_relaxed_cluster(tempty_lead0 + 8u * acc, 1);
+            }
+            if (splitk && p.recv_bufs == 0) {
                 mbar_arrive(&c->ringfree);
-            else if (splitk)
+            } else if (splitk) {
+                fence_acq_rel_cluster();   // this warp's reads of the buffer before the others' next stores to it
                 for (int32_t o = 1; o < S; ++o)
-                    mbar_arrive_cluster(map_to_rank(&c->rdy[buf], cta_of((me + o) % S)));
+                    mbar_arrive_relaxed_cluster(map_to_rank(&c->rdy[buf], cta_of((me + o) % S)), 1);
+            }
         }
         ++tiles;
         if (++buf == nbuf) {
@@ -890,27 +908,28 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
 
     if (warp == 0) {
         if (lane == 0) {
-            prefetch_tensormap(&p.mapP);
-            prefetch_tensormap(&p.mapQ);
+            prefetch_tensormap(&p.map[0]);
+            prefetch_tensormap(&p.map[1]);
         }
         for (int32_t i = lane; i < p.num_pipe; i += 32) {
-            mbar_init(&c->full[i], kForm == kReduce ? kPair : 1);
+            mbar_init(&c->full[i], 2);
             mbar_init(&c->empty[i], 1);
-            mbar_init(&c->go[i], 1);
-            mbar_init(&c->tail[i], 1);
+            mbar_init(&c->go[0][i], 1);
+            mbar_init(&c->go[1][i], 1);
+            mbar_init(&c->tail[i], 2);
         }
         if (lane < 2) {
             mbar_init(&c->tfull[lane], 1);
-            mbar_init(&c->tempty[lane], 4 * kPair);
+            mbar_init(&c->tempty[lane], kEpi * kPair);
         }
         if (lane == 0) {
             const int32_t S = p.split > 1 ? p.split : 1;
             mbar_init(&c->drain, 1);
-            for (int b = 0; b < 2; ++b) {   // four epilogue warps of the other CTAs (and, sharing the ring, this one)
-                mbar_init(&c->rdy[b], p.recv_bufs == 0 ? 4 * S : S > 1 ? 4 * (S - 1) : 1);
-                mbar_init(&c->got[b], S > 1 ? 4 * (S - 1) : 1);
+            for (int b = 0; b < 2; ++b) {   // epilogue warps of the other CTAs (and, sharing the ring, of this one)
+                mbar_init(&c->rdy[b], p.recv_bufs == 0 ? kEpi * S : S > 1 ? kEpi * (S - 1) : 1);
+                mbar_init(&c->got[b], S > 1 ? kEpi * (S - 1) : 1);
             }
-            mbar_init(&c->ringfree, 4);
+            mbar_init(&c->ringfree, kEpi);
             c->abort_flag = 0;
             c->skip = ld_relaxed_gpu_u32(p.status) != 0;     // sticky error: do nothing
         }
@@ -959,14 +978,17 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
     if (!c->skip) {
         if (warp == 0) {
             if (elect_one())
-                l_role_tma<kForm, kPair>(p, c, g, ring);
+                l_role_tma<kForm, kPair, 0>(p, c, g, ring);
         } else if (warp == 1) {
             if (elect_one())
                 l_role_mma<kForm, kPair>(p, c, g, ring, tmem_base);
         } else if (warp == 2) {
             if (kForm == kReduce && p.offsets)
                 l_role_mask<kPair>(p, c, g, ring);
-        } else if (warp >= 4) {
+        } else if (warp == 3) {
+            if (elect_one())
+                l_role_tma<kForm, kPair, 1>(p, c, g, ring);
+        } else {
             l_role_epilogue<kForm, kPair>(p, c, g, ring + (p.recv_bufs ? sm.recv : 0u), ring + sm.stage,
                                           reinterpret_cast<float *>(ring + sm.bias), tmem_base);
         }
