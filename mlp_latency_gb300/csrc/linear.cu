@@ -87,7 +87,7 @@ struct Plan {
     int form, pair, bn, split, pipe;
     uint32_t slot, recv_bytes;
     int recv_bufs, part_align;
-    int q_step;              // kRowsT: rows per tile
+    int q_tiles;             // kRowsT, one group: tiles along the rows
 };
 
 }  // namespace
@@ -122,7 +122,7 @@ Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red,
 {
     const int64_t groups = std::min<int64_t>(h->groups, rows), avg = cdiv(rows, groups);
     const int64_t kb = cdiv(red, kKB);
-    Plan best{kRowsT, 1, 32, 1, 0, 0, 0, 0, 0, 0};
+    Plan best{kRowsT, 1, 32, 1, 0, 0, 0, 0, 0, 1};
     double best_t = 1e300;
     for (int form = kRows; form <= kRowsT; ++form)
         for (int pair = 1; pair <= 2; ++pair)
@@ -133,32 +133,41 @@ Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red,
                     const int64_t at_once = h->max_clusters[pair * s];
                     if (at_once < 1 || (s > 1 && kb < 4 * s))
                         continue;
-                    const int bm = kPRows * pair;
-                    // groups of ragged size end in a partial tile: half a tile on average
-                    int64_t items;
-                    double n = bn;
-                    if (form == kRows) {
-                        items = (h->groups > 1 ? cdiv(rows, bm) + groups / 2 : cdiv(rows, bm)) * cdiv(out_cols, bn);
-                    } else {
-                        const int64_t tq = groups > 1 ? groups * cdiv(avg, bn) : cdiv(rows, bn);
-                        items = tq * cdiv(out_cols, bm);
-                        n = std::min<double>(bn, static_cast<double>(rows) / static_cast<double>(tq) + 16 * pair);
-                    }
-                    const double mma = std::max(2.0 * n, 64.0);
-                    const double fill = (16384.0 + bn * 128.0 / pair) / 64.0;
-                    const double step = std::max(mma, fill);
-                    const double waves = static_cast<double>(cdiv(items, at_once));
-                    double t = waves * (static_cast<double>(cdiv(kb, s)) * step + 400.0) + 6.0 * n;
-                    if (s > 1)
-                        t += 2500.0 + n * 512.0 * (s - 1) / s / 16.0;
-                    if (t < best_t) {
-                        best_t = t;
-                        best = Plan{form, pair, bn, s, 0, 0, 0, 0, 0, 0};
+                    const int bm = kPRows * pair, u = 16 * pair;
+                    const int64_t least = form == kRowsT ? cdiv(rows, bn) : 1;
+                    // tiles along the rows: as few as hold them, or up to two more for a fuller last round (never more
+                    // than there are column steps: every tile gets at least one)
+                    const int64_t most = form == kRowsT && h->groups == 1 ? std::min<int64_t>(least + 2, cdiv(rows, u)) : least;
+                    for (int64_t tq = least; tq <= most; ++tq) {
+                        // groups of ragged size end in a partial tile: half a tile on average
+                        int64_t items;
+                        double n = bn;
+                        if (form == kRows) {
+                            items = (h->groups > 1 ? cdiv(rows, bm) + groups / 2 : cdiv(rows, bm)) * cdiv(out_cols, bn);
+                        } else if (h->groups > 1) {
+                            const int64_t tiles = groups * cdiv(avg, bn);
+                            items = tiles * cdiv(out_cols, bm);
+                            n = std::min<double>(bn, static_cast<double>(rows) / static_cast<double>(tiles) + u);
+                        } else {
+                            items = tq * cdiv(out_cols, bm);
+                            n = static_cast<double>(cdiv(rows, u) * u) / static_cast<double>(tq);
+                        }
+                        // MMA: 2 n cycles per k block, at least 310 to issue its four instructions; fill: what a CTA
+                        // loads per k block at 64 bytes a cycle
+                        const double mma = std::max(2.0 * n, 310.0);
+                        const double fill = (16384.0 + (form == kRows ? q_tile_bytes(bn / pair, w_mn) : n * 128.0 / pair)) / 64.0;
+                        const double step = std::max(mma, fill);
+                        const double waves = static_cast<double>(cdiv(items, at_once));
+                        double t = waves * (static_cast<double>(cdiv(kb, s)) * step + 400.0) + 12.0 * n;
+                        if (s > 1)
+                            t += 1500.0 + n * 512.0 * (s - 1) / s / 18.0;
+                        if (t < best_t) {
+                            best_t = t;
+                            best = Plan{form, pair, bn, s, 0, 0, 0, 0, 0, static_cast<int>(tq)};
+                        }
                     }
                 }
     finish_plan(h, best, best.form == kRows && w_mn);
-    // rows of one group are dealt evenly over their tiles; those of several groups end where they end
-    best.q_step = h->groups > 1 ? best.bn : static_cast<int>(cdiv(rows, cdiv(rows, best.bn)));
     return best;
 }
 
@@ -175,23 +184,28 @@ template <int kForm, int kPair>
 bool launch_one(const LinearParams &p, int clusters, int cs, size_t smem, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    // set up while the kernel before it on the stream ends (every role waits for that end before it touches
+    // global memory that a kernel may have written or may still read)
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cs);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * cs), 1, 1);
     cfg.blockDim = dim3(kLThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = cs > 1 ? 1 : 0;
+    cfg.numAttrs = cs > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, linear_kernel<kForm, kPair>, p) == cudaSuccess;
 }
 
-// items: an upper bound on the items of this launch (the counts of groups are on the device).
+// items: the items of this launch, or an upper bound where the counts of groups are on the device.
 mlp_status launch(const mlp_linear *h, LinearParams &p, const Plan &pl, int64_t items, cudaStream_t st)
 {
     p.groups = h->groups;
+    p.dense_items = static_cast<int32_t>(items);
     p.bn = pl.bn;
     p.split = pl.split;
     p.raster = 16 / pl.pair;
@@ -229,7 +243,6 @@ mlp_status rows_product(const mlp_linear *h, LinearParams &p, int64_t rows, cons
     p.rows = static_cast<int32_t>(rows);
     p.k_ext = static_cast<int32_t>(red);
     int64_t items;
-    p.q_step = pl.q_step;
     if (pl.form == kRows) {
         // (a box never reaches past the last row of a short matrix: copies that are mostly out of range measured
         // several times slower than full ones)
@@ -240,12 +253,14 @@ mlp_status rows_product(const mlp_linear *h, LinearParams &p, int64_t rows, cons
         p.q_ext = static_cast<int32_t>(out_cols);
         items = (cdiv(rows, kPRows * pl.pair) + h->groups - 1) * cdiv(out_cols, pl.bn);
     } else {
-        const int qrows = static_cast<int>(std::min<int64_t>(pl.pair == 2 ? pl.bn / 2 : pl.q_step, rows));
+        const int qrows = static_cast<int>(std::min<int64_t>(pl.bn / pl.pair, rows));
         if (!operand(p, 1, false, A, red, rows, 1, lda, qrows) ||
             !operand(p, 0, b_mn, B, b_mn ? out_cols : red, b_mn ? red : out_cols, h->groups, b_mn ? out_cols : red, kPRows))
             return MLP_ERR_CUDA;
         p.p_ext = static_cast<int32_t>(out_cols);
-        items = (cdiv(rows, pl.q_step) + h->groups - 1) * cdiv(out_cols, kPRows * pl.pair);
+        if (h->groups == 1 && !p.offsets)
+            p.dense_q_tiles = pl.q_tiles;
+        items = (p.dense_q_tiles ? pl.q_tiles : cdiv(rows, pl.bn) + h->groups - 1) * cdiv(out_cols, kPRows * pl.pair);
     }
     return launch(h, p, pl, items, st);
 }
@@ -253,7 +268,8 @@ mlp_status rows_product(const mlp_linear *h, LinearParams &p, int64_t rows, cons
 // ------------------------------------------------------- dZ = dY act'(Z) and the bias gradient --
 // With e = e^-t and s = sigmoid(t) = 1 / (1 + e): 1 - s = e s, without cancellation.
 //   silu'(z) = s + z s (1 - s), t = z;   gelu'(z) = s + z s (1 - s) t', t = 2u.
-// Where |t| is past 60 the second term is below any value that counts and e may overflow: dropped.
+// Where |t| is past 60 the second term is below any value that counts and e may overflow: dropped.  (__fmul_rn: the
+// product is also summed, and must not become part of an fma in one of the places where it is used.)
 template <int kAct>
 __device__ __forceinline__ float act_grad(float dy, float z)
 {
@@ -261,14 +277,14 @@ __device__ __forceinline__ float act_grad(float dy, float z)
         return z <= 0.0f ? 0.0f : dy;
     if (kAct == kActSilu) {
         const float e = __expf(-z), s = __fdividef(1.0f, 1.0f + e);
-        return dy * (s + (fabsf(z) > 60.0f ? 0.0f : z * s * (e * s)));
+        return __fmul_rn(dy, s + (fabsf(z) > 60.0f ? 0.0f : z * s * (e * s)));
     }
     if (kAct == kActGelu) {
         const float z2 = z * z;
         const float t = z * fmaf(2.0f * kGeluC * kGeluA, z2, 2.0f * kGeluC);
         const float e = __expf(-t), s = __fdividef(1.0f, 1.0f + e);
         const float dt = fmaf(6.0f * kGeluC * kGeluA, z2, 2.0f * kGeluC);
-        return dy * (s + (fabsf(t) > 60.0f ? 0.0f : z * s * (e * s) * dt));
+        return __fmul_rn(dy, s + (fabsf(t) > 60.0f ? 0.0f : z * s * (e * s) * dt));
     }
     return dy;
 }
@@ -299,6 +315,7 @@ template <int kAct>
 __global__ void __launch_bounds__(256) act_grad_kernel(const GradParams p)
 {
     __shared__ float red[8][kStrip];
+    griddep_launch_dependents();
     const int32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int32_t col = blockIdx.x * kStrip + lane * 8;
     const bool col_ok = col < p.N;
@@ -325,24 +342,41 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const GradParams p)
             continue;
         float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         if (col_ok) {
-#pragma unroll 4
-            for (int32_t r = lo + warp; r < hi; r += 8) {
-                const uint4 dyv = *reinterpret_cast<const uint4 *>(p.dy + r * p.ld_dy + col);
-                uint4 zv = make_uint4(0u, 0u, 0u, 0u);
-                if (kAct != kActNone)
-                    zv = *reinterpret_cast<const uint4 *>(p.z + r * p.ld_z + col);
-                const uint32_t dw[4] = {dyv.x, dyv.y, dyv.z, dyv.w}, zw[4] = {zv.x, zv.y, zv.z, zv.w};
-                uint32_t ow[4];
+            // four rows a round, all of their loads first: the stores of one could be the loads of the next for all
+            // the compiler knows
+            for (int32_t r = lo + warp; r < hi; r += 32) {
+                uint4 dyv[4], zv[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 a = unpack2(dw[j]), b = unpack2(zw[j]);
-                    const float g0 = act_grad<kAct>(a.x, b.x), g1 = act_grad<kAct>(a.y, b.y);
-                    acc[2 * j] += g0;
-                    acc[2 * j + 1] += g1;
-                    ow[j] = pack2(g0, g1);
+                for (int i = 0; i < 4; ++i) {
+                    const int32_t q = min(r + 8 * i, hi - 1);
+                    dyv[i] = __ldg(reinterpret_cast<const uint4 *>(p.dy + q * p.ld_dy + col));
+                    if (kAct != kActNone)
+                        zv[i] = __ldg(reinterpret_cast<const uint4 *>(p.z + q * p.ld_z + col));
                 }
-                if (kAct != kActNone && p.dz)
-                    *reinterpret_cast<uint4 *>(p.dz + static_cast<int64_t>(r) * p.N + col) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (r + 8 * i >= hi)
+                        break;
+                    const uint32_t dw[4] = {dyv[i].x, dyv[i].y, dyv[i].z, dyv[i].w};
+                    uint32_t zw[4] = {0u, 0u, 0u, 0u};
+                    if (kAct != kActNone) {
+                        zw[0] = zv[i].x;
+                        zw[1] = zv[i].y;
+                        zw[2] = zv[i].z;
+                        zw[3] = zv[i].w;
+                    }
+                    uint32_t ow[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 a = unpack2(dw[j]), b = unpack2(zw[j]);
+                        const float g0 = act_grad<kAct>(a.x, b.x), g1 = act_grad<kAct>(a.y, b.y);
+                        acc[2 * j] += g0;
+                        acc[2 * j + 1] += g1;
+                        ow[j] = pack2(g0, g1);
+                    }
+                    if (kAct != kActNone && p.dz)
+                        *reinterpret_cast<uint4 *>(p.dz + static_cast<int64_t>(r + 8 * i) * p.N + col) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+                }
             }
         }
         if (p.part) {
@@ -366,6 +400,8 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const GradParams p)
 __global__ void __launch_bounds__(256) bias_grad_kernel(const GradParams p)
 {
     const int32_t c = blockIdx.x * 256 + threadIdx.x, e = blockIdx.y;
+    griddep_wait();   // launched while act_grad_kernel runs
+    griddep_launch_dependents();
     if (c >= p.N)
         return;
     int32_t lo, hi;
@@ -587,8 +623,16 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         if (cudaGetLastError() != cudaSuccess)
             return MLP_ERR_CUDA;
         if (dbias) {
-            bias_grad_kernel<<<dim3(static_cast<unsigned>(cdiv(N, 256)), static_cast<unsigned>(h->groups)), 256, 0, st>>>(g);
-            if (cudaGetLastError() != cudaSuccess)
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.gridDim = dim3(static_cast<unsigned>(cdiv(N, 256)), static_cast<unsigned>(h->groups));
+            cfg.blockDim = dim3(256);
+            cfg.stream = st;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaLaunchKernelEx(&cfg, bias_grad_kernel, g) != cudaSuccess)
                 return MLP_ERR_CUDA;
         }
     }

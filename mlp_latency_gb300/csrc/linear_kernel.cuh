@@ -13,9 +13,10 @@
 // In MMA terms every form is D[p, q] = sum_k P[p, k] Q[q, k] with operands that are K-major or
 // MN-major in memory (the descriptors' and the TMA boxes' business only).
 //
-// Roles (384 threads): warps 0 and 3 copy P and Q tiles (one thread each: issuing a fill's copies from one
-// thread took longer than its MMAs), warp 1 issues MMAs and owns TMEM, warp 2 builds the group tables and masks
-// ragged reduction tails, warps 4-11 run the epilogue (two per TMEM lane quarter, on alternating column chunks).
+// Roles (384 threads): warps 0 and 3 copy P and Q tiles into a ring (one thread each, taking fills in turn: a thread
+// issues one 16 KB copy per ~400 cycles, longer than a fill's MMAs), warp 1 issues MMAs and owns TMEM, warp 2 builds
+// the group tables and masks ragged reduction tails, warps 4-11 run the epilogue (two per TMEM lane quarter, on
+// alternating column chunks).
 // The accumulator is double buffered, so a tile's epilogue runs under the next tile's MMAs.  Tiles are dealt out
 // statically, in an order that lets the CTAs running at one time share operand panels in L2.
 //
@@ -59,9 +60,10 @@ struct LinearParams {
     int32_t mn[2];                  // operand stored MN-major (else K-major)
     const int32_t *offsets;         // device, groups + 1 entries, or null: one group of `rows` rows
     int32_t groups, rows;
+    int32_t dense_items;            // items of a dense product (no offsets)
+    int32_t dense_q_tiles;          // kRowsT, dense: tiles along the rows, from rows / bn up to one per column step
     int32_t p_ext, q_ext, k_ext;    // extents of the dimensions that are not ragged
     int32_t bn;                     // columns of a tile (the pair's)
-    int32_t q_step;                 // kRowsT: rows from one tile to the next (<= bn)
     int32_t split;                  // CTAs, or pairs, sharing a tile's reduction
     int32_t part_align;             // granularity of the column ranges that they finish: 8 or 32
     int32_t recv_bufs;              // receive buffers for partial sums, of recv_bytes each; 0: the ring
@@ -83,7 +85,7 @@ struct LinearParams {
 
 struct __align__(8) LCtrl {
     uint64_t full[kMaxRing], empty[kMaxRing], tail[kMaxRing];
-    uint64_t go[2][kMaxRing];   // leader to peer, per operand: the fill is armed
+    uint64_t go[kMaxRing];   // leader to peer: the fill is armed
     uint64_t tfull[2], tempty[2];
     uint64_t drain, rdy[2], got[2], ringfree;
     uint32_t tmem_base;
@@ -227,6 +229,12 @@ struct Tile {
     int32_t kb0, kb1;    // k blocks of this CTA's slice
 };
 
+// kRowsT: tiles that a group's rows are dealt over.
+__device__ __forceinline__ int32_t q_tiles(const LinearParams &p, int32_t cnt)
+{
+    return p.dense_q_tiles ? p.dense_q_tiles : (cnt + p.bn - 1) / p.bn;
+}
+
 template <int kForm, int kPair>
 __device__ __forceinline__ int32_t items_of(const LinearParams &p, int32_t cnt)
 {
@@ -234,7 +242,7 @@ __device__ __forceinline__ int32_t items_of(const LinearParams &p, int32_t cnt)
     if (kForm == kRows)
         return (cnt + bm - 1) / bm * ((p.q_ext + p.bn - 1) / p.bn);
     if (kForm == kRowsT)
-        return (cnt + p.q_step - 1) / p.q_step * ((p.p_ext + bm - 1) / bm);
+        return q_tiles(p, cnt) * ((p.p_ext + bm - 1) / bm);
     return (p.p_ext + bm - 1) / bm * ((p.q_ext + p.bn - 1) / p.bn);
 }
 
@@ -251,22 +259,33 @@ struct Walk {
     {
         if (id >= n_items)
             return false;
-        while (id >= g.base[e + 1])
-            ++e;
         constexpr int32_t bm = kPRows * kPair;
+        int32_t base = 0;
+        if (p.offsets) {
+            while (id >= g.base[e + 1])
+                ++e;
+            base = g.base[e];
+            t.start = g.start[e];
+            t.cnt = g.cnt[e];
+        } else {
+            t.start = 0;
+            t.cnt = p.rows;
+        }
         t.e = e;
-        t.start = g.start[e];
-        t.cnt = g.cnt[e];
-        const int32_t i = id - g.base[e];
+        const int32_t i = id - base;
         id += step;
         const int32_t kext = kForm == kReduce ? t.cnt : p.k_ext;
         const int32_t nkb = (kext + kKB - 1) / kKB;
         if (kForm == kRowsT) {
-            const int32_t tq = (t.cnt + p.q_step - 1) / p.q_step;
-            const int32_t pi = i / tq;
+            // the group's rows in units of the MMA's column step, dealt evenly over the tiles
+            constexpr int32_t u = 16 * kPair;
+            const int32_t units = (t.cnt + u - 1) / u;
+            const int32_t tq = q_tiles(p, t.cnt);
+            const int32_t pi = i / tq, qi = i - pi * tq;
+            const int32_t each = units / tq, more = units - each * tq;
             t.p0 = pi * bm;
-            t.q0 = (i - pi * tq) * p.q_step;
-            t.n = (min(p.q_step, t.cnt - t.q0) + 16 * kPair - 1) / (16 * kPair) * (16 * kPair);   // (the MMA's step)
+            t.q0 = (qi * each + min(qi, more)) * u;
+            t.n = (each + (qi < more ? 1 : 0)) * u;
         } else {
             const int32_t tp = ((kForm == kRows ? t.cnt : p.p_ext) + bm - 1) / bm;
             const int32_t tq = (p.q_ext + p.bn - 1) / p.bn;
@@ -300,32 +319,29 @@ __device__ __forceinline__ int32_t masked_rows(const LinearParams &p, const Tile
 }
 
 // ------------------------------------------------------------------------------- TMA producers --
-// One thread per operand (kOp 0: P, 1: Q) fills its part of every ring slot; a slot's full barrier takes one arrival
-// and the bytes of each.
-template <int kForm, int kPair, int kOp>
-__device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring)
+// One of two threads, `which` = 0 or 1: the even or the odd fills of the ring.
+template <int kForm, int kPair>
+__device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring, uint32_t which,
+                                           Walk<kForm, kPair> w, Tile t, bool have)
 {
-    const int32_t num_pipe = p.num_pipe;
+    const uint32_t num_pipe = static_cast<uint32_t>(p.num_pipe);
     const uint32_t slot_bytes = p.slot_bytes;
     const uint32_t rank = cluster_ctarank();
     const uint32_t half = kPair == 2 ? (rank & 1u) : 0u;
     const uint32_t full_lead0 = kPair == 2 ? map_to_rank(&c->full[0], rank & ~1u) : 0u;
-    const uint32_t go_peer0 = kPair == 2 ? map_to_rank(&c->go[kOp][0], rank | 1u) : 0u;
+    const uint32_t go_peer0 = kPair == 2 ? map_to_rank(&c->go[0], rank | 1u) : 0u;
     const uint32_t tail_own0 = kPair == 2 ? map_to_rank(&c->tail[0], rank) : 0u;
-    const CUtensorMap *const map = &p.map[kOp];
-    const bool mn = p.mn[kOp] != 0, boxed = p.boxed[kOp] != 0;
-    const uint32_t bytes = p.copy_bytes[kOp];
-    const int32_t boxes = mn ? static_cast<int32_t>(bytes / kBoxBytes) : 1;
+    const bool p_mn = p.mn[0] != 0, q_mn = p.mn[1] != 0, p_boxed = p.boxed[0] != 0, q_boxed = p.boxed[1] != 0;
+    const uint32_t bytes = p.copy_bytes[0] + p.copy_bytes[1];
+    const int32_t q_boxes = static_cast<int32_t>(p.copy_bytes[1] / kBoxBytes);
     const bool shared_ring = p.split > 1 && p.recv_bufs == 0;
     const int32_t n_items = c->n_items;
     const uint64_t pol = policy_evict_normal();
-    uint32_t issued = 0, tail_use = 0, tail_ph = 0, item_ph = 0;
-    int32_t ps = 0;
-    uint32_t pph = 0;
-    Walk<kForm, kPair> w(p);
-    Tile t;
+    uint32_t fills = 0, tail_ph = 0, tail_use = 0, item_ph = 0;
+    uint32_t ps = 0, pph = 0;
     bool ok = true, first = true;
-    while (ok && w.next(p, g, n_items, t)) {
+    griddep_wait();   // a programmatic launch: the kernel before this one is complete from here on
+    for (; ok && have; have = w.next(p, g, n_items, t)) {
         if (shared_ring) {   // the ring was the exchange buffer of the previous item
             if (!first) {
                 if (!lwait(&c->ringfree, item_ph, c, p))
@@ -334,71 +350,87 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
             }
             first = false;
         }
-        // first row (column of an MN-major operand) of this CTA's share, and the group
-        const int32_t row = kOp == 0 ? (kForm == kRows ? t.start : 0) + t.p0 + static_cast<int32_t>(half) * kPRows
-                                     : (kForm == kRowsT ? t.start : 0) + t.q0 + static_cast<int32_t>(half) * (t.n / kPair);
-        const int32_t grp = (kOp == 0 ? kForm == kRowsT : kForm == kRows) ? t.e : 0;
+        // first row (column of an MN-major operand) of this CTA's share of each tile, and the group
+        const int32_t p_row = (kForm == kRows ? t.start : 0) + t.p0 + static_cast<int32_t>(half) * kPRows;
+        const int32_t q_row = (kForm == kRowsT ? t.start : 0) + t.q0 + static_cast<int32_t>(half) * (t.n / kPair);
+        const int32_t p_grp = kForm == kRowsT ? t.e : 0, q_grp = kForm == kRows ? t.e : 0;
         int32_t k = (kForm == kReduce ? t.start : 0) + t.kb0 * kKB;
         for (int32_t kb = t.kb0; kb < t.kb1; ++kb, k += kKB) {
-            if (kPair == 2 && half) {
-                if (!lwait(&c->go[kOp][ps], pph, c, p, true)) {   // the leader armed this fill
+            if ((fills & 1u) == which) {
+                if (kPair == 2 && half) {
+                    if (!lwait(&c->go[ps], pph, c, p, true)) {   // the leader armed this fill
+                        ok = false;
+                        break;
+                    }
+                } else if (!lwait(&c->empty[ps], pph ^ 1u, c, p)) {
                     ok = false;
                     break;
                 }
-            } else if (!lwait(&c->empty[ps], pph ^ 1, c, p)) {
-                ok = false;
-                break;
-            }
-            const bool masked = masked_rows<kForm>(p, t, kb) != 0;
-            if (masked) {
-                // completes on this CTA's own tail barrier; warp 2 zeroes the rows and completes `full`
-                mbar_arrive_expect_tx(&c->tail[ps], bytes);
-                tail_use |= 1u << ps;
-                tail_ph ^= 1u << ps;
-            } else if (!half) {
-                mbar_arrive_expect_tx(&c->full[ps], kPair * bytes);
-            }
-            if (kPair == 2 && !half)
-                mbar_arrive_relaxed_cluster(go_peer0 + 8u * static_cast<uint32_t>(ps), 1);   // publishes no data
-            uint8_t *dst = ring + static_cast<size_t>(ps) * slot_bytes + (kOp == 0 ? 0u : kPBytes);
-            const uint32_t fb = kPair == 2 ? (masked ? tail_own0 : full_lead0) + 8u * static_cast<uint32_t>(ps) : 0u;
-            uint64_t *lb = masked ? &c->tail[ps] : &c->full[ps];
-            if (boxed) {
-                if (kPair == 2)
-                    tma_load_4d_pair(dst, map, fb, 0, k, row >> 6, grp, pol);
-                else
-                    tma_load_4d(dst, map, lb, 0, k, row >> 6, grp, pol);
-            } else if (mn) {
-                for (int32_t j = 0; j < boxes; ++j) {
-                    if (kPair == 2)
-                        tma_load_3d_pair(dst + j * kBoxBytes, map, fb, row + 64 * j, k, grp, pol);
-                    else
-                        tma_load_3d(dst + j * kBoxBytes, map, lb, row + 64 * j, k, grp, pol);
+                const bool masked = masked_rows<kForm>(p, t, kb) != 0;
+                if (masked) {
+                    // completes on this CTA's own tail barrier; warp 2 zeroes the rows and completes `full`
+                    mbar_arrive_expect_tx(&c->tail[ps], bytes);
+                    tail_use |= 1u << ps;
+                } else if (!half) {
+                    mbar_arrive_expect_tx(&c->full[ps], kPair * bytes);
+                    if (kForm == kReduce && kPair == 2)
+                        mbar_arrive(&c->full[ps]);   // (the count is 2: one per CTA's warp 2 on a masked fill)
                 }
-            } else {
-                if (kPair == 2)
-                    tma_load_3d_pair(dst, map, fb, k, row, grp, pol);
-                else
-                    tma_load_3d(dst, map, lb, k, row, grp, pol);
+                if (kPair == 2 && !half)
+                    mbar_arrive_relaxed_cluster(go_peer0 + 8u * ps, 1);   // publishes no data
+                uint8_t *a = ring + ps * slot_bytes, *b = a + kPBytes;
+                const uint32_t fb = kPair == 2 ? (masked ? tail_own0 : full_lead0) + 8u * ps : 0u;
+                uint64_t *lb = masked ? &c->tail[ps] : &c->full[ps];
+                auto load3 = [&](uint8_t *dst, const CUtensorMap *m, int32_t c0, int32_t c1, int32_t c2) {
+                    if (kPair == 2)
+                        tma_load_3d_pair(dst, m, fb, c0, c1, c2, pol);
+                    else
+                        tma_load_3d(dst, m, lb, c0, c1, c2, pol);
+                };
+                auto load4 = [&](uint8_t *dst, const CUtensorMap *m, int32_t c1, int32_t c2, int32_t c3) {
+                    if (kPair == 2)
+                        tma_load_4d_pair(dst, m, fb, 0, c1, c2, c3, pol);
+                    else
+                        tma_load_4d(dst, m, lb, 0, c1, c2, c3, pol);
+                };
+                if (!p_mn) {
+                    load3(a, &p.map[0], k, p_row, p_grp);
+                } else if (p_boxed) {
+                    load4(a, &p.map[0], k, p_row >> 6, p_grp);
+                } else {
+                    load3(a, &p.map[0], p_row, k, p_grp);
+                    load3(a + kBoxBytes, &p.map[0], p_row + 64, k, p_grp);
+                }
+                if (!q_mn) {
+                    load3(b, &p.map[1], k, q_row, q_grp);
+                } else if (q_boxed) {
+                    load4(b, &p.map[1], k, q_row >> 6, q_grp);
+                } else {
+                    for (int32_t j = 0; j < q_boxes; ++j)
+                        load3(b + j * kBoxBytes, &p.map[1], q_row + 64 * j, k, q_grp);
+                }
             }
-            ++issued;
+            if (kForm == kReduce && masked_rows<kForm>(p, t, kb) != 0)
+                tail_ph ^= 1u << ps;   // (the other thread's too: the slot's tail barrier counts both)
+            ++fills;
             if (++ps == num_pipe) {
                 ps = 0;
-                pph ^= 1;
+                pph ^= 1u;
             }
         }
     }
     if (c->abort_flag) {
-        // Let the copies land before the shared memory goes away.  Unmasked fills of a pair complete on
+        // Let this thread's copies land before the shared memory goes away.  Unmasked fills of a pair complete on
         // the leader's barriers (the peer fills only what the leader armed, and keeps its shared memory
         // until the final cluster barrier); masked fills complete on each CTA's own.
-        for (int32_t i = 0; i < num_pipe; ++i) {
-            if (tail_use >> i & 1u)
-                lwait(&c->tail[i], (tail_ph >> i & 1u) ^ 1u, c, p, false, true);
-            const uint32_t n = static_cast<uint32_t>(num_pipe), u = static_cast<uint32_t>(i);
-            const uint32_t fills = issued / n + (u < issued % n ? 1u : 0u);
-            if (!half && fills > 0)
-                lwait(&c->full[i], (fills - 1) & 1, c, p, false, true);
+        for (uint32_t f = fills > num_pipe ? fills - num_pipe : 0u; f < fills; ++f) {
+            const uint32_t slot = f % num_pipe;
+            if ((f & 1u) != which)
+                continue;
+            if (tail_use >> slot & 1u)
+                lwait(&c->tail[slot], (tail_ph >> slot & 1u) ^ 1u, c, p, false, true);
+            if (!half)
+                lwait(&c->full[slot], (f / num_pipe) & 1u, c, p, false, true);
         }
     }
 }
@@ -499,12 +531,10 @@ __device__ __forceinline__ void l_role_mask(const LinearParams &p, LCtrl *c, con
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-            if (kPair == 2) {   // (one arrival of each CTA; a single CTA makes both)
+            if (kPair == 2)
                 mbar_arrive_cluster(full_lead0 + 8u * static_cast<uint32_t>(ps));
-            } else {
+            else
                 mbar_arrive(&c->full[ps]);
-                mbar_arrive(&c->full[ps]);
-            }
         }
     }
 }
@@ -535,13 +565,21 @@ template <bool kSwizzle>
 __device__ __forceinline__ void stage_store(const uint8_t *stage, uint8_t *gbase, int64_t ld_bytes, int32_t row_lim,
                                             int32_t seg_lim, int32_t lane)
 {
-    const int32_t sg = lane & 3;
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int32_t rr = it * 8 + (lane >> 2);
-        if (rr < row_lim && sg < seg_lim)
-            *reinterpret_cast<uint4 *>(gbase + rr * ld_bytes + sg * 16) =
-                *reinterpret_cast<const uint4 *>(stage + stg<kSwizzle>(rr, sg));
+    const int32_t r0 = lane >> 2, sg = lane & 3;
+    // (eight rows on, the swizzle is the same: (row >> 1) & 3 has period 8)
+    const uint4 *s = reinterpret_cast<const uint4 *>(stage + stg<kSwizzle>(r0, sg));
+    uint8_t *q = gbase + r0 * ld_bytes + sg * 16;
+    const int64_t step = 8 * ld_bytes;
+    const uint4 a = s[0], b = s[32], c = s[64], d = s[96];
+    if (sg < seg_lim) {
+        if (r0 < row_lim)
+            *reinterpret_cast<uint4 *>(q) = a;
+        if (r0 + 8 < row_lim)
+            *reinterpret_cast<uint4 *>(q + step) = b;
+        if (r0 + 16 < row_lim)
+            *reinterpret_cast<uint4 *>(q + 2 * step) = c;
+        if (r0 + 24 < row_lim)
+            *reinterpret_cast<uint4 *>(q + 3 * step) = d;
     }
 }
 
@@ -681,6 +719,7 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
     auto cta_of = [&](int32_t slice) { return static_cast<uint32_t>(slice * kPair) + half; };   // same half, other slice
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tempty_lead0 = map_to_rank(&c->tempty[0], kPair == 2 ? rank & ~1u : rank);
+    griddep_wait();
     uint32_t tiles = 0;
     int32_t buf = 0;           // receive buffer of this item, and how often it was used before (parity)
     uint32_t buf_ph = 0;
@@ -704,7 +743,7 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
             } else {
                 ch.row = static_cast<int64_t>(t.start) + t.q0 + col;
                 ch.col = prow;
-                ch.row_lim = min(min(32, c_hi - col), min(p.q_step, t.cnt - t.q0) - col);
+                ch.row_lim = min(min(32, c_hi - col), t.cnt - t.q0 - col);
                 ch.seg_lim = min(32, p.p_ext - prow) / 8;
             }
             return ch;
@@ -788,7 +827,12 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    v[j] = have_k ? __uint_as_float(x[j]) : 0.0f;
+                    v[j] = __uint_as_float(x[j]);
+                if (!have_k) {   // an empty reduction
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = 0.0f;
+                }
             }
             if (col + 64 >= c_hi) {   // this warp's last read of the accumulator
                 freed = true;
@@ -905,6 +949,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
     g.cnt = g.start + p.groups;
     g.base = g.cnt + p.groups;
     const int32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    griddep_launch_dependents();   // every wait of a dependent kernel is for this grid's end
 
     if (warp == 0) {
         if (lane == 0) {
@@ -912,11 +957,10 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
             prefetch_tensormap(&p.map[1]);
         }
         for (int32_t i = lane; i < p.num_pipe; i += 32) {
-            mbar_init(&c->full[i], 2);
+            mbar_init(&c->full[i], kForm == kReduce ? kPair : 1);
             mbar_init(&c->empty[i], 1);
-            mbar_init(&c->go[0][i], 1);
-            mbar_init(&c->go[1][i], 1);
-            mbar_init(&c->tail[i], 2);
+            mbar_init(&c->go[i], 1);
+            mbar_init(&c->tail[i], 1);
         }
         if (lane < 2) {
             mbar_init(&c->tfull[lane], 1);
@@ -937,7 +981,11 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
     } else if (warp == 1) {
         tmem_alloc_g<kPair>(&c->tmem_base, p.tmem_cols);
         tmem_relinquish_g<kPair>();
+    } else if (warp == 2 && !p.offsets) {
+        if (lane == 0)
+            c->n_items = p.dense_items;
     } else if (warp == 2) {
+        griddep_wait();
         // Group tables.  Offsets come from device memory: anything out of order or out of range is
         // clamped, so no access can leave the matrices, and reported through the status word.
         int32_t carry = 0;
@@ -946,7 +994,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
             const int32_t e = e0 + lane;
             int32_t items = 0;
             if (e < p.groups) {
-                const int32_t lo0 = p.offsets ? p.offsets[e] : 0, hi0 = p.offsets ? p.offsets[e + 1] : p.rows;
+                const int32_t lo0 = p.offsets[e], hi0 = p.offsets[e + 1];
                 const int32_t lo = min(max(lo0, 0), p.rows), hi = min(max(hi0, lo), p.rows);
                 bad |= lo != lo0 || hi != hi0;
                 g.start[e] = lo;
@@ -971,14 +1019,22 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
         if (__any_sync(0xffffffffu, bad) && lane == 0)
             atomicCAS(p.status, 0u, kStBadOffsets);
     }
+    // a dense product's first tile needs no tables: its coordinates are worked out before the barrier
+    Walk<kForm, kPair> w(p);
+    Tile t;
+    bool have = false;
+    if (!p.offsets && (warp == 0 || warp == 3))
+        have = w.next(p, g, p.dense_items, t);
     tc_fence_before();
     cluster_sync_all();   // barriers initialised before any remote arrival
     tc_fence_after();
     const uint32_t tmem_base = c->tmem_base;
     if (!c->skip) {
         if (warp == 0) {
+            if (p.offsets)
+                have = w.next(p, g, c->n_items, t);
             if (elect_one())
-                l_role_tma<kForm, kPair, 0>(p, c, g, ring);
+                l_role_tma<kForm, kPair>(p, c, g, ring, 0, w, t, have);
         } else if (warp == 1) {
             if (elect_one())
                 l_role_mma<kForm, kPair>(p, c, g, ring, tmem_base);
@@ -986,21 +1042,23 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
             if (kForm == kReduce && p.offsets)
                 l_role_mask<kPair>(p, c, g, ring);
         } else if (warp == 3) {
+            if (p.offsets)
+                have = w.next(p, g, c->n_items, t);
             if (elect_one())
-                l_role_tma<kForm, kPair, 1>(p, c, g, ring);
+                l_role_tma<kForm, kPair>(p, c, g, ring, 1, w, t, have);
         } else {
             l_role_epilogue<kForm, kPair>(p, c, g, ring + (p.recv_bufs ? sm.recv : 0u), ring + sm.stage,
                                           reinterpret_cast<float *>(ring + sm.bias), tmem_base);
         }
     }
     __syncwarp();
+    griddep_wait();       // (also after a skipped run: this grid must not end before the one it may have overtaken)
     tc_fence_before();
     cluster_sync_all();   // MMAs, epilogues and exchanges of every CTA of the cluster are over
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_g<kPair>(tmem_base, p.tmem_cols);
     }
-    cluster_sync_all();
 }
 
 }  // namespace mlpl
