@@ -560,40 +560,54 @@ __device__ __forceinline__ uint32_t stg(int row, int seg)
     return static_cast<uint32_t>(row * 64 + ((kSwizzle ? seg ^ ((row >> 1) & 3) : seg) * 16));
 }
 
-// The staged 32 rows x 4 segments to global memory, four lanes a row; rows and segments past the limits are skipped.
+// Where a lane's 16-byte pieces of a 32 x 64-byte chunk lie in global memory: rows (lane >> 2) + 8 i, segment lane & 3.
+struct Piece {
+    uint8_t *at;        // of the chunk at hand
+    int64_t step;       // eight rows
+    int64_t next;       // to this warp's next chunk
+    __device__ __forceinline__ void init(const void *base, int64_t row, int32_t col, int64_t ld, int32_t esz, bool down, int32_t lane)
+    {
+        const int64_t ldb = ld * esz;
+        at = const_cast<uint8_t *>(static_cast<const uint8_t *>(base)) + (row + (lane >> 2)) * ldb + static_cast<int64_t>(col) * esz +
+             (lane & 3) * 16;
+        step = 8 * ldb;
+        next = down ? 8 * step : 64 * esz;   // 64 rows or 64 columns on
+    }
+};
+
+// The staged 32 rows x 4 segments to global memory; rows and segments past the limits are skipped.
 template <bool kSwizzle>
-__device__ __forceinline__ void stage_store(const uint8_t *stage, uint8_t *gbase, int64_t ld_bytes, int32_t row_lim,
-                                            int32_t seg_lim, int32_t lane)
+__device__ __forceinline__ void stage_store(const uint8_t *stage, const Piece &g, int32_t row_lim, int32_t seg_lim, int32_t lane)
 {
     const int32_t r0 = lane >> 2, sg = lane & 3;
     // (eight rows on, the swizzle is the same: (row >> 1) & 3 has period 8)
     const uint4 *s = reinterpret_cast<const uint4 *>(stage + stg<kSwizzle>(r0, sg));
-    uint8_t *q = gbase + r0 * ld_bytes + sg * 16;
-    const int64_t step = 8 * ld_bytes;
     const uint4 a = s[0], b = s[32], c = s[64], d = s[96];
-    if (sg < seg_lim) {
+    if (row_lim >= 32 && seg_lim >= 4) {
+        *reinterpret_cast<uint4 *>(g.at) = a;
+        *reinterpret_cast<uint4 *>(g.at + g.step) = b;
+        *reinterpret_cast<uint4 *>(g.at + 2 * g.step) = c;
+        *reinterpret_cast<uint4 *>(g.at + 3 * g.step) = d;
+    } else if (sg < seg_lim) {
         if (r0 < row_lim)
-            *reinterpret_cast<uint4 *>(q) = a;
+            *reinterpret_cast<uint4 *>(g.at) = a;
         if (r0 + 8 < row_lim)
-            *reinterpret_cast<uint4 *>(q + step) = b;
+            *reinterpret_cast<uint4 *>(g.at + g.step) = b;
         if (r0 + 16 < row_lim)
-            *reinterpret_cast<uint4 *>(q + 2 * step) = c;
+            *reinterpret_cast<uint4 *>(g.at + 2 * g.step) = c;
         if (r0 + 24 < row_lim)
-            *reinterpret_cast<uint4 *>(q + 3 * step) = d;
+            *reinterpret_cast<uint4 *>(g.at + 3 * g.step) = d;
     }
 }
 
 // The residual's piece of a chunk: requested early, staged when it is needed.
-__device__ __forceinline__ void res_load(uint4 (&x)[4], const uint8_t *gbase, int64_t ld_bytes, int32_t row_lim, int32_t seg_lim,
-                                         int32_t lane)
+__device__ __forceinline__ void res_load(uint4 (&x)[4], const Piece &g, int32_t row_lim, int32_t seg_lim, int32_t lane)
 {
-    const int32_t sg = lane & 3;
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-        const int32_t rr = it * 8 + (lane >> 2);
         x[it] = make_uint4(0u, 0u, 0u, 0u);
-        if (rr < row_lim && sg < seg_lim)
-            x[it] = *reinterpret_cast<const uint4 *>(gbase + rr * ld_bytes + sg * 16);
+        if (it * 8 + (lane >> 2) < row_lim && (lane & 3) < seg_lim)
+            x[it] = *reinterpret_cast<const uint4 *>(g.at + it * g.step);
     }
 }
 template <bool kSwizzle>
@@ -614,12 +628,6 @@ __device__ __forceinline__ float load_bias(const LinearParams &p, int64_t i)
 // A 32 x 32 chunk of the output on its way out.  Rows are output rows, so with TMEM lane = output row (kLaneRow) a
 // lane holds a row of the chunk, and with lane = output column (kRowsT) a column; both go through the staging buffer
 // so that global memory is touched in 64-byte row pieces.
-struct Chunk {
-    int64_t row;         // first output row and column
-    int32_t col;
-    int32_t row_lim, seg_lim;
-};
-
 template <bool kLaneRow>
 __device__ __forceinline__ void put_bf16(const float (&v)[32], uint8_t *stage, int32_t lane)
 {
@@ -639,12 +647,12 @@ __device__ __forceinline__ void put_bf16(const float (&v)[32], uint8_t *stage, i
 }
 
 template <int kAct, bool kLaneRow>
-__device__ __forceinline__ void finish_chunk(const LinearParams &p, float (&v)[32], uint8_t *stage, const Chunk &ch, const uint4 (&res)[4],
-                                             int32_t lane)
+__device__ __forceinline__ void finish_chunk(const LinearParams &p, float (&v)[32], uint8_t *stage, const Piece &out, const Piece &zp,
+                                             const uint4 (&res)[4], int32_t row_lim, int32_t seg_lim, int32_t lane)
 {
     if (p.z) {
         put_bf16<kLaneRow>(v, stage, lane);
-        stage_store<kLaneRow>(stage, reinterpret_cast<uint8_t *>(p.z + ch.row * p.ld_z + ch.col), p.ld_z * 2, ch.row_lim, ch.seg_lim, lane);
+        stage_store<kLaneRow>(stage, zp, row_lim, seg_lim, lane);
         __syncwarp();
     }
     if (kAct != kActNone) {
@@ -675,14 +683,12 @@ __device__ __forceinline__ void finish_chunk(const LinearParams &p, float (&v)[3
         __syncwarp();
     }
     put_bf16<kLaneRow>(v, stage, lane);
-    stage_store<kLaneRow>(stage, reinterpret_cast<uint8_t *>(static_cast<__nv_bfloat16 *>(p.out) + ch.row * p.ld_out + ch.col),
-                          p.ld_out * 2, ch.row_lim, ch.seg_lim, lane);
+    stage_store<kLaneRow>(stage, out, row_lim, seg_lim, lane);
     __syncwarp();
 }
 
 // 32 x 32 fp32 values, 16 columns at a time.
-__device__ __forceinline__ void finish_f32(const LinearParams &p, const float (&v)[32], uint8_t *stage, const Chunk &ch, int32_t cols,
-                                           int32_t lane)
+__device__ __forceinline__ void finish_f32(const float (&v)[32], uint8_t *stage, Piece out, int32_t row_lim, int32_t cols, int32_t lane)
 {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -691,8 +697,8 @@ __device__ __forceinline__ void finish_f32(const LinearParams &p, const float (&
             *reinterpret_cast<float4 *>(stage + stg<true>(lane, s)) =
                 make_float4(v[16 * h + 4 * s], v[16 * h + 4 * s + 1], v[16 * h + 4 * s + 2], v[16 * h + 4 * s + 3]);
         __syncwarp();
-        stage_store<true>(stage, reinterpret_cast<uint8_t *>(static_cast<float *>(p.out) + ch.row * p.ld_out + ch.col + 16 * h),
-                          p.ld_out * 4, ch.row_lim, (cols - 16 * h) / 4, lane);
+        stage_store<true>(stage, out, row_lim, (cols - 16 * h) / 4, lane);
+        out.at += 64;
         __syncwarp();
     }
 }
@@ -731,31 +737,27 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
         // the columns of the tile that this CTA finishes
         const int32_t part = splitk ? ((t.n + S - 1) / S + p.part_align - 1) / p.part_align * p.part_align : t.n;
         const int32_t c_lo = min(me * part, t.n), c_hi = min(c_lo + part, t.n);
-        // where chunk `col` (accumulator columns col .. col + 31 of this warp's lanes) goes
+        // This warp's chunks: accumulator columns col .. col + 31 of its lanes, for col = first, first + 64, ...
+        const int32_t first = c_lo + 32 * which;
         const int32_t prow = t.p0 + static_cast<int32_t>(half) * kPRows + quarter * 32;   // first MMA row of this warp
-        auto chunk_of = [&](int32_t col) {
-            Chunk ch;
-            if (kLaneRow) {
-                ch.row = (kForm == kRows ? static_cast<int64_t>(t.start) : static_cast<int64_t>(t.e) * p.p_ext) + prow;
-                ch.col = t.q0 + col;
-                ch.row_lim = min(32, (kForm == kRows ? t.cnt : p.p_ext) - prow);
-                ch.seg_lim = (min(min(32, c_hi - col), p.q_ext - ch.col)) / 8;   // (extents are multiples of 8)
-            } else {
-                ch.row = static_cast<int64_t>(t.start) + t.q0 + col;
-                ch.col = prow;
-                ch.row_lim = min(min(32, c_hi - col), t.cnt - t.q0 - col);
-                ch.seg_lim = min(32, p.p_ext - prow) / 8;
-            }
-            return ch;
-        };
-        auto valid = [&](const Chunk &ch) { return ch.row_lim > 0 && ch.seg_lim > 0; };
+        const int64_t row0 = kForm == kRows     ? static_cast<int64_t>(t.start) + prow
+                             : kForm == kRowsT ? static_cast<int64_t>(t.start) + t.q0 + first
+                                               : static_cast<int64_t>(t.e) * p.p_ext + prow;
+        const int32_t col0 = kLaneRow ? t.q0 + first : prow;
+        Piece out, zp, rp;
+        out.init(p.out, row0, col0, p.ld_out, kForm == kReduce && p.out_f32 ? 4 : 2, !kLaneRow, lane);
+        if (p.z)
+            zp.init(p.z, row0, col0, p.ld_z, 2, !kLaneRow, lane);
+        if (p.res)
+            rp.init(p.res, row0, col0, p.ld_res, 2, !kLaneRow, lane);
+        // rows and 16-byte segments (of bf16) of a chunk that exist
+        const int32_t lim_fix = kLaneRow ? (kForm == kRows ? t.cnt : p.p_ext) - prow : (p.p_ext - prow) / 8;
+        auto row_lim_of = [&](int32_t col) { return kLaneRow ? lim_fix : min(c_hi - col, t.cnt - t.q0 - col); };
+        auto seg_lim_of = [&](int32_t col) { return kLaneRow ? min(c_hi - col, p.q_ext - t.q0 - col) / 8 : lim_fix; };
         uint4 res[4];
         auto request_res = [&](int32_t col) {
-            if (p.res && col < c_hi) {
-                const Chunk ch = chunk_of(col);
-                res_load(res, reinterpret_cast<const uint8_t *>(p.res + ch.row * p.ld_res + ch.col), p.ld_res * 2, ch.row_lim,
-                         ch.seg_lim, lane);
-            }
+            if (p.res && col < c_hi)
+                res_load(res, rp, row_lim_of(col), seg_lim_of(col), lane);
         };
         // ---- bias and residual of the first chunk are requested while the tile's MMAs run, of later ones a chunk
         // ahead.  A lane holds one column's bias: its own for kRowsT, column col + lane of the chunk otherwise.
@@ -765,8 +767,8 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
             if (p.bias && col < c_hi)
                 bias = n < ext ? load_bias(p, static_cast<int64_t>(t.e) * ext + n) : 0.0f;
         };
-        request_bias(c_lo + 32 * which);
-        request_res(c_lo + 32 * which);
+        request_bias(first);
+        request_res(first);
         if (!lwait_warp(&c->tfull[acc], ph, c, p, kPair == 2))
             return;
         tc_fence_after();
@@ -817,8 +819,8 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                 return;
         }
         bool freed = false;
-        for (int32_t col = c_lo + 32 * which; col < c_hi; col += 64) {
-            const Chunk ch = chunk_of(col);
+        for (int32_t col = first; col < c_hi; col += 64) {
+            const int32_t row_lim = row_lim_of(col), seg_lim = seg_lim_of(col);
             // accumulator columns [col, col + 32) of this lane, partial sums of all slices in slice order
             float v[32];
             {
@@ -872,12 +874,14 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                 }
             }
             if (kForm == kReduce) {
-                if (valid(ch)) {
-                    if (p.out_f32)
-                        finish_f32(p, v, stage, ch, 8 * ch.seg_lim, lane);
-                    else
-                        finish_chunk<kActNone, true>(p, v, stage, ch, res, lane);
+                if (p.out_f32) {
+                    finish_f32(v, stage, out, row_lim, 8 * seg_lim, lane);
+                } else {
+                    put_bf16<true>(v, stage, lane);
+                    stage_store<true>(stage, out, row_lim, seg_lim, lane);
+                    __syncwarp();
                 }
+                out.at += out.next;
                 continue;
             }
             if (p.bias) {
@@ -898,14 +902,19 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                     request_bias(col + 64);
                 }
             }
-            if (valid(ch)) {
+            if (row_lim > 0 && seg_lim > 0) {
                 switch (p.act) {
-                case kActGelu: finish_chunk<kActGelu, kLaneRow>(p, v, stage, ch, res, lane); break;
-                case kActSilu: finish_chunk<kActSilu, kLaneRow>(p, v, stage, ch, res, lane); break;
-                case kActRelu: finish_chunk<kActRelu, kLaneRow>(p, v, stage, ch, res, lane); break;
-                default: finish_chunk<kActNone, kLaneRow>(p, v, stage, ch, res, lane); break;
+                case kActGelu: finish_chunk<kActGelu, kLaneRow>(p, v, stage, out, zp, res, row_lim, seg_lim, lane); break;
+                case kActSilu: finish_chunk<kActSilu, kLaneRow>(p, v, stage, out, zp, res, row_lim, seg_lim, lane); break;
+                case kActRelu: finish_chunk<kActRelu, kLaneRow>(p, v, stage, out, zp, res, row_lim, seg_lim, lane); break;
+                default: finish_chunk<kActNone, kLaneRow>(p, v, stage, out, zp, res, row_lim, seg_lim, lane); break;
                 }
             }
+            out.at += out.next;
+            if (p.z)
+                zp.at += zp.next;
+            if (p.res)
+                rp.at += rp.next;
             request_res(col + 64);
         }
         __syncwarp();
