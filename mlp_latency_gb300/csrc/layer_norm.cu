@@ -39,45 +39,78 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return d;
 }
 
-// V elements at an address aligned to V of them (at most 16 bytes), as one load or store.
+// V elements at an address aligned to V of them (at most 16 bytes) as they are in memory.  Loads keep this form until
+// the values are used: a conversion next to the load would wait for memory before the next load goes out.
+template <int kBytes>
+struct RawOf;
+template <>
+struct RawOf<2> { using type = unsigned short; };
+template <>
+struct RawOf<4> { using type = uint32_t; };
+template <>
+struct RawOf<8> { using type = uint2; };
+template <>
+struct RawOf<16> { using type = uint4; };
+template <typename T, int V>
+using Raw = typename RawOf<static_cast<int>(sizeof(T)) * V>::type;
+
+template <typename T>
+__device__ __forceinline__ void unpack(unsigned short x, float (&f)[1]) { f[0] = bf16_lo(x); }
+template <typename T>
+__device__ __forceinline__ void unpack(uint32_t x, float (&f)[1]) { f[0] = __uint_as_float(x); }
+template <typename T>
+__device__ __forceinline__ void unpack(uint32_t x, float (&f)[2])
+{
+    f[0] = bf16_lo(x);
+    f[1] = bf16_hi(x);
+}
+template <typename T>
+__device__ __forceinline__ void unpack(uint2 x, float (&f)[2])
+{
+    f[0] = __uint_as_float(x.x);
+    f[1] = __uint_as_float(x.y);
+}
+template <typename T>
+__device__ __forceinline__ void unpack(uint2 x, float (&f)[4])
+{
+    f[0] = bf16_lo(x.x);
+    f[1] = bf16_hi(x.x);
+    f[2] = bf16_lo(x.y);
+    f[3] = bf16_hi(x.y);
+}
+template <typename T>
+__device__ __forceinline__ void unpack(uint4 x, float (&f)[4])
+{
+    f[0] = __uint_as_float(x.x);
+    f[1] = __uint_as_float(x.y);
+    f[2] = __uint_as_float(x.z);
+    f[3] = __uint_as_float(x.w);
+}
+template <typename T>
+__device__ __forceinline__ void unpack(uint4 x, float (&f)[8])
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = bf16_lo(w[j]);
+        f[2 * j + 1] = bf16_hi(w[j]);
+    }
+}
+
+// Vectors at columns c, c + step, ... below cols.
+template <typename T, int V, int N>
+__device__ __forceinline__ void load_batch(const T *p, int64_t c, int64_t step, int64_t cols, Raw<T, V> (&r)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (c + i * step < cols)
+            r[i] = *reinterpret_cast<const Raw<T, V> *>(p + c + i * step);
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void load(const T *p, float (&f)[V])
 {
-    if constexpr (sizeof(T) == 2 && V == 8) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[2 * j] = bf16_lo(w[j]);
-            f[2 * j + 1] = bf16_hi(w[j]);
-        }
-    } else if constexpr (sizeof(T) == 2 && V == 4) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(p);
-        f[0] = bf16_lo(x.x);
-        f[1] = bf16_hi(x.x);
-        f[2] = bf16_lo(x.y);
-        f[3] = bf16_hi(x.y);
-    } else if constexpr (sizeof(T) == 2 && V == 2) {
-        const uint32_t x = *reinterpret_cast<const uint32_t *>(p);
-        f[0] = bf16_lo(x);
-        f[1] = bf16_hi(x);
-    } else if constexpr (sizeof(T) == 4 && V == 8) {
-        load<T, 4>(p, *reinterpret_cast<float(*)[4]>(&f[0]));
-        load<T, 4>(p + 4, *reinterpret_cast<float(*)[4]>(&f[4]));
-    } else if constexpr (sizeof(T) == 4 && V == 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(p);
-        f[0] = x.x;
-        f[1] = x.y;
-        f[2] = x.z;
-        f[3] = x.w;
-    } else if constexpr (sizeof(T) == 4 && V == 2) {
-        const float2 x = *reinterpret_cast<const float2 *>(p);
-        f[0] = x.x;
-        f[1] = x.y;
-    } else {
-        static_assert(V == 1, "no such vector");
-        f[0] = to_f32<T>(*p);
-    }
+    unpack<T>(*reinterpret_cast<const Raw<T, V> *>(p), f);
 }
 
 template <typename T, int V>
@@ -96,28 +129,80 @@ __device__ __forceinline__ void store(T *p, const float (&f)[V])
     }
 }
 
-// gamma or beta, columns c .. c + V - 1 (NULL: `none`).  kind: 0 bf16, 1 fp32; + 2: aligned to V of them
-// (at most 16 bytes), read in vectors.
-template <int V>
-__device__ __forceinline__ void load_w(const void *w, int kind, int64_t c, float none, float (&f)[V])
+// gamma or beta: N vectors of V columns at c, c + step, ... below cols (NULL: `none`).  kind: 0 bf16, 1 fp32; + 2:
+// aligned to V of them (at most 16 bytes), read in vectors.  Nothing that a kernel stores is read this way, so these
+// loads may move above stores.
+template <typename U, int V, int N>
+__device__ __forceinline__ void load_w_as(const U *w, int64_t c, int64_t step, int64_t cols, float (&f)[N][V])
+{
+    if constexpr (sizeof(U) * V > 16) {   // two loads of half the columns
+        float lo[N][V / 2], hi[N][V / 2];
+        load_w_as<U, V / 2, N>(w, c, step, cols, lo);
+        load_w_as<U, V / 2, N>(w + V / 2, c, step, cols - V / 2, hi);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                f[i][j] = lo[i][j];
+                f[i][j + V / 2] = hi[i][j];
+            }
+    } else {
+        Raw<U, V> r[N] = {};
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (c + i * step < cols)
+                r[i] = __ldg(reinterpret_cast<const Raw<U, V> *>(w + c + i * step));
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            unpack<U>(r[i], f[i]);
+    }
+}
+
+template <typename U, int V, int N>
+__device__ __forceinline__ void load_w_scalar(const U *w, int64_t c, int64_t step, int64_t cols, float (&f)[N][V])
+{
+    Raw<U, 1> r[N][V] = {};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (c + i * step < cols)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                r[i][j] = __ldg(reinterpret_cast<const Raw<U, 1> *>(w + c + i * step + j));
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float x[1];
+            unpack<U>(r[i][j], x);
+            f[i][j] = x[0];
+        }
+}
+
+template <int V, int N>
+__device__ __forceinline__ void load_w(const void *w, int kind, int64_t c, int64_t step, int64_t cols, float none, float (&f)[N][V])
 {
     if (!w) {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            f[j] = none;
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                f[i][j] = none;
     } else if (kind == 2) {
-        load<__nv_bfloat16, V>(static_cast<const __nv_bfloat16 *>(w) + c, f);
+        load_w_as<__nv_bfloat16, V, N>(static_cast<const __nv_bfloat16 *>(w), c, step, cols, f);
     } else if (kind == 3) {
-        load<float, V>(static_cast<const float *>(w) + c, f);
+        load_w_as<float, V, N>(static_cast<const float *>(w), c, step, cols, f);
     } else if (kind == 1) {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            f[j] = static_cast<const float *>(w)[c + j];
+        load_w_scalar<float, V, N>(static_cast<const float *>(w), c, step, cols, f);
     } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            f[j] = __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[c + j]);
+        load_w_scalar<__nv_bfloat16, V, N>(static_cast<const __nv_bfloat16 *>(w), c, step, cols, f);
     }
+}
+
+// One vector.
+template <int V>
+__device__ __forceinline__ void load_w(const void *w, int kind, int64_t c, float none, float (&f)[V])
+{
+    load_w<V, 1>(w, kind, c, 0, c + 1, none, *reinterpret_cast<float(*)[1][V]>(&f));
 }
 
 __device__ __forceinline__ float warp_sum(float v)
@@ -343,13 +428,9 @@ __device__ __forceinline__ void block_sum2(float &a, float &b, float (*scratch)[
 // A block walks over rows; the next rows are on their way into shared memory while it works on one.  Each
 // thread copies exactly the columns that it reads, so the copies need no barrier, only the thread's own
 // wait_group.
-template <int kBytes>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
 {
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -359,11 +440,11 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// kStages slots of `bufs` rows, kItems vectors of V elements per thread and row.  kStages = 0: no ring, rows are
-// read where they are.
+// kStages slots of `bufs` rows, kItems vectors of V elements (16 bytes) per thread and row.
 template <typename T, int V, int kItems, int kStages>
 struct RowRing {
-    static constexpr int kBytes = V * static_cast<int>(sizeof(T));
+    static constexpr int kBytes = 16;
+    static_assert(V * sizeof(T) == 16, "rows in 16-byte units");
     uint32_t first, last;        // this thread's place in the first and last slot
     uint32_t rd, wr;             // ... in the slot to read and to fill next
     uint32_t item, row, slot;    // strides of vectors, rows and slots
@@ -374,7 +455,7 @@ struct RowRing {
         row = item * kItems;
         slot = row * static_cast<uint32_t>(bufs);
         first = rd = wr = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * kBytes;
-        last = first + slot * (kStages > 0 ? kStages - 1 : 0);
+        last = first + slot * (kStages - 1);
         c0 = static_cast<int>(threadIdx.x) * V;
         cstep = static_cast<int>(blockDim.x) * V;
     }
@@ -387,36 +468,23 @@ struct RowRing {
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
             if (has(i))
-                copy_async<kBytes>(wr + buf * row + i * item, src + i * cstep);
+                copy_async(wr + buf * row + i * item, src + i * cstep);
     }
-    // vector i of buffer `buf` of the slot to read (of the row at src without a ring)
-    __device__ __forceinline__ void read(int buf, int i, const T *src, float (&f)[V]) const
+    // vector i of buffer `buf` of the slot to read
+    __device__ __forceinline__ void read(int buf, int i, float (&f)[V]) const
     {
-        if constexpr (kStages == 0) {
-            load<T, V>(src + c0 + i * cstep, f);
-        } else {
-            const uint32_t at = rd + buf * row + i * item;
-            if constexpr (kBytes == 16) {
-                uint32_t w[4];
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(rd + buf * row + i * item)
+                     : "memory");
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (sizeof(T) == 2) {
-                        f[2 * j] = bf16_lo(w[j]);
-                        f[2 * j + 1] = bf16_hi(w[j]);
-                    } else {
-                        f[j] = __uint_as_float(w[j]);
-                    }
-                }
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (sizeof(T) == 2) {
+                f[2 * j] = bf16_lo(w[j]);
+                f[2 * j + 1] = bf16_hi(w[j]);
             } else {
-                uint32_t w;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
-                if constexpr (sizeof(T) == 2) {
-                    f[0] = bf16_lo(w);
-                    f[1] = bf16_hi(w);
-                } else {
-                    f[0] = __uint_as_float(w);
-                }
+                f[j] = __uint_as_float(w[j]);
             }
         }
     }
@@ -447,12 +515,8 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams
     block_sum_init(s1);
     block_sum_init(s2);
     float g[kItems][V], b[kItems][V];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i)
-        if (ring.has(i)) {
-            load_w<V>(p.gamma, p.w_kind, ring.c0 + i * ring.cstep, 1.0f, g[i]);
-            load_w<V>(p.beta, p.w_kind, ring.c0 + i * ring.cstep, 0.0f, b[i]);
-        }
+    load_w<V, kItems>(p.gamma, p.w_kind, ring.c0, ring.cstep, ring.cols, 1.0f, g);
+    load_w<V, kItems>(p.beta, p.w_kind, ring.c0, ring.cstep, ring.cols, 0.0f, b);
     __syncthreads();
     int parity = 0;
     for (int64_t row = blockIdx.x; left > 0; --left, row += step, parity ^= 1) {
@@ -463,7 +527,7 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
             if (ring.has(i)) {
-                ring.read(0, i, nullptr, v[i]);
+                ring.read(0, i, v[i]);
                 sum.add(v[i]);
             }
         ring.advance(ring.rd);
@@ -514,7 +578,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
     const int mine = static_cast<int>((p.rows - r0 + step - 1) / step);   // rows of this block
     int to_fetch = mine;
     griddep_launch_dependents();   // the finishing kernel waits for this grid by itself
-    // with a ring x, dy and add run ahead: they point to the next row to fetch
+    // x, dy and add run ahead: they point to the next row to fetch
     auto fetch = [&] {
         if (to_fetch > 0) {
             ring.fetch(0, x);
@@ -530,9 +594,8 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
         if (add)
             add += step * p.ldadd;
     };
-    if constexpr (kStages > 0)
-        for (int s = 0; s < kStages - 1; ++s)
-            fetch();
+    for (int s = 0; s < kStages - 1; ++s)
+        fetch();
     block_sum_init(scratch);
     float ag[kItems][V], ab[kItems][V], gk[kK][V];
 #pragma unroll
@@ -540,9 +603,9 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
 #pragma unroll
         for (int j = 0; j < V; ++j)
             ag[i][j] = ab[i][j] = 0.0f;
-        if (kKeep && ring.has(i))
-            load_w<V>(p.gamma, p.w_kind, ring.c0 + i * ring.cstep, 1.0f, gk[kKeep ? i : 0]);
     }
+    if constexpr (kKeep)
+        load_w<V, kItems>(p.gamma, p.w_kind, ring.c0, ring.cstep, cols, 1.0f, gk);
     // mean and rstd of 32 rows at a time, a row a lane, the next 32 on their way: one row ahead is not enough for
     // memory under load
     const int lane = static_cast<int>(threadIdx.x & 31);
@@ -557,10 +620,8 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
     __syncthreads();
     int parity = 0;
     for (int it = 0; it < mine; ++it, parity ^= 1) {
-        if constexpr (kStages > 0) {
-            copy_wait<kStages - 2>();
-            fetch();
-        }
+        copy_wait<kStages - 2>();
+        fetch();
         if (it > 0 && (it & 31) == 0) {
             mean_c = mean_n;
             rstd_c = rstd_n;
@@ -571,8 +632,8 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
         float gd[kK][V], xh[kK][V];
         auto terms = [&](int i, float (&d)[V], float (&go)[V], float (&xo)[V]) {   // dy, g and xh of vector i
             float a[V];
-            ring.read(0, i, x, a);
-            ring.read(1, i, dy, d);
+            ring.read(0, i, a);
+            ring.read(1, i, d);
             fma_s<V>(xo, a, 1.0f, -mean);
             mul_s<V>(xo, xo, rstd);
             if constexpr (kKeep) {
@@ -610,21 +671,14 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
                     fma_sv<V>(o, gd[k], rstd, o);
                     if (add) {
                         float r[V];
-                        ring.read(2, i, add, r);
+                        ring.read(2, i, r);
                         add_v<V>(o, o, r);
                     }
                     store<T, V>(dx + i * ring.cstep, o);
                 }
             dx += step * p.lddx;
         }
-        if constexpr (kStages > 0) {
-            ring.advance(ring.rd);
-        } else {
-            x += step * p.ldx;
-            dy += step * p.lddy;
-            if (add)
-                add += step * p.ldadd;
-        }
+        ring.advance(ring.rd);
     }
     if (p.part) {
         float *out = p.part + r0 * 2 * cols;
@@ -632,18 +686,10 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
         for (int i = 0; i < kItems; ++i) {
             const int c = ring.c0 + i * ring.cstep;
             if (ring.has(i)) {
-                if constexpr (V % 4 == 0) {   // cols is a multiple of V, and so of four
 #pragma unroll
-                    for (int j = 0; j < V; j += 4) {
-                        *reinterpret_cast<float4 *>(out + c + j) = make_float4(ag[i][j], ag[i][j + 1], ag[i][j + 2], ag[i][j + 3]);
-                        *reinterpret_cast<float4 *>(out + cols + c + j) = make_float4(ab[i][j], ab[i][j + 1], ab[i][j + 2], ab[i][j + 3]);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        out[c + j] = ag[i][j];
-                        out[cols + c + j] = ab[i][j];
-                    }
+                for (int j = 0; j < V; j += 4) {
+                    *reinterpret_cast<float4 *>(out + c + j) = make_float4(ag[i][j], ag[i][j + 1], ag[i][j + 2], ag[i][j + 3]);
+                    *reinterpret_cast<float4 *>(out + cols + c + j) = make_float4(ab[i][j], ab[i][j + 1], ab[i][j + 2], ab[i][j + 3]);
                 }
             }
         }
@@ -663,15 +709,23 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormParams
     const T *x = static_cast<const T *>(p.x) + row * p.ldx;
     float v[kItems][V];
     float s[1] = {0.0f};
+    const int64_t c0 = static_cast<int64_t>(t) * V, cstep = static_cast<int64_t>(team) * V;
+    Raw<T, V> raw[kItems] = {};
+    load_batch<T, V, kItems>(x, c0, cstep, p.cols, raw);
+    // The weights of at most 16 columns at a time; where that is all of them, they are on their way during the sums.
+    constexpr int kB = V * kItems <= 16 ? kItems : 16 / V > 0 ? 16 / V : 1;
+    constexpr bool kEarly = kB == kItems;
+    float g[kB][V], b[kB][V];
+    if (kEarly) {
+        load_w<V, kB>(p.gamma, p.w_kind, c0, cstep, p.cols, 1.0f, g);
+        load_w<V, kB>(p.beta, p.w_kind, c0, cstep, p.cols, 0.0f, b);
+    }
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        const int64_t c = (static_cast<int64_t>(i) * team + t) * V;
-        if (c < p.cols) {
-            load<T, V>(x + c, v[i]);
+        unpack<T>(raw[i], v[i]);   // (zeros past the row's end)
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                s[0] += v[i][j];
-        }
+        for (int j = 0; j < V; ++j)
+            s[0] += v[i][j];
     }
     team_sum<1, kWarpTeam>(s, scratch);
     const float mean = s[0] / static_cast<float>(p.cols);   // (a division: a constant row gives exact zeros)
@@ -696,21 +750,239 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormParams
     }
     T *y = static_cast<T *>(p.y) + row * p.ldy;
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const int64_t c = (static_cast<int64_t>(i) * team + t) * V;
-        if (c < p.cols) {
-            float g[V], b[V], o[V];
-            load_w<V>(p.gamma, p.w_kind, c, 1.0f, g);
-            load_w<V>(p.beta, p.w_kind, c, 0.0f, b);
+    for (int k = 0; k < kItems; k += kB) {
+        if (!kEarly) {
+            load_w<V, kB>(p.gamma, p.w_kind, c0 + k * cstep, cstep, p.cols, 1.0f, g);
+            load_w<V, kB>(p.beta, p.w_kind, c0 + k * cstep, cstep, p.cols, 0.0f, b);
+        }
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                o[j] = fmaf((v[i][j] - mean) * rstd, g[j], b[j]);
-            store<T, V>(y + c, o);
+        for (int i = 0; i < kB; ++i)
+            if (c0 + (k + i) * cstep < p.cols) {
+                float o[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    o[j] = fmaf((v[k + i][j] - mean) * rstd, g[i][j], b[i][j]);
+                store<T, V>(y + c0 + (k + i) * cstep, o);
+            }
+    }
+}
+
+// ------------------------------------------------------------------------ rows without 16-byte alignment --
+// Any width and stride, V elements (1, or 2 where rows are in 4-byte units) at a time, in loops over the columns.
+// Each round first requests the loads of kBatch vectors and then works on them: a loop that uses a value where it
+// loads it waits for memory once per vector (one row of 14876 columns took 28 us that way).
+
+// Forward: the row waits in shared memory in fp32 between its three passes.
+template <typename T, int V>
+__global__ void __launch_bounds__(512) norm_forward_staged_kernel(const NormParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float s1[2][32], s2[2][32];
+    constexpr int kBatch = 8;
+    float *buf = reinterpret_cast<float *>(smem);
+    const int cols = static_cast<int>(p.cols), c0 = static_cast<int>(threadIdx.x) * V, cstep = static_cast<int>(blockDim.x) * V;
+    block_sum_init(s1);
+    block_sum_init(s2);
+    __syncthreads();
+    int parity = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
+        const T *x = static_cast<const T *>(p.x) + row * p.ldx;
+        T *y = static_cast<T *>(p.y) + row * p.ldy;
+        float s = 0.0f;
+        for (int c = c0; c < cols; c += kBatch * cstep) {   // (each thread reads back only what it wrote: no barrier)
+            Raw<T, V> raw[kBatch];
+            load_batch<T, V, kBatch>(x, c, cstep, cols, raw);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (c + i * cstep < cols) {
+                    float v[V];
+                    unpack<T>(raw[i], v);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        s += v[j];
+                        buf[c + i * cstep + j] = v[j];
+                    }
+                }
+        }
+        const float mean = __fdiv_rn(block_sum(s, s1, parity), static_cast<float>(cols));
+        s = 0.0f;
+#pragma unroll 8
+        for (int c = c0; c < cols; c += cstep)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float d = buf[c + j] - mean;
+                s = fmaf(d, d, s);
+            }
+        const float rstd = rsqrtf(fmaf(block_sum(s, s2, parity), p.inv_cols, p.eps));
+        if (threadIdx.x == 0) {
+            if (p.mean)
+                p.mean[row] = mean;
+            if (p.rstd)
+                p.rstd[row] = rstd;
+        }
+        for (int c = c0; c < cols; c += kBatch * cstep) {
+            float g[kBatch][V], b[kBatch][V], o[V];
+            load_w<V, kBatch>(p.gamma, p.w_kind, c, cstep, cols, 1.0f, g);
+            load_w<V, kBatch>(p.beta, p.w_kind, c, cstep, cols, 0.0f, b);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (c + i * cstep < cols) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        o[j] = fmaf((buf[c + i * cstep + j] - mean) * rstd, g[i][j], b[i][j]);
+                    store<T, V>(y + c + i * cstep, o);
+                }
         }
     }
 }
 
-// Rows too wide for registers: three passes over the row (the later ones come from L2).
+// Backward, R rows at a time: a column's R contributions to dgamma and dbeta are added in registers and then to the
+// block's running sums in shared memory; dx reads its rows a second time (from L2).
+template <typename T, int V, int R>
+__global__ void __launch_bounds__(512) norm_backward_staged_kernel(const NormParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float scratch[2 * R][16];
+    constexpr int kBatch = R == 1 ? 8 / V : 4 / V;
+    const int cols = static_cast<int>(p.cols), c0 = static_cast<int>(threadIdx.x) * V, cstep = static_cast<int>(blockDim.x) * V;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    float *ag = reinterpret_cast<float *>(smem), *ab = ag + cols;   // (a thread touches only its own columns)
+    const bool sums = p.part != nullptr;
+    const bool once = static_cast<int64_t>(gridDim.x) * R >= p.rows;   // one round per block: no running sums
+    float *pg = p.part + static_cast<int64_t>(blockIdx.x) * 2 * cols, *pb = pg + cols;
+    griddep_launch_dependents();   // the finishing kernel waits for this grid by itself
+    if (sums && !once)
+        for (int c = c0; c < cols; c += cstep)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                ag[c + j] = ab[c + j] = 0.0f;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * R; row < p.rows; row += static_cast<int64_t>(gridDim.x) * R) {
+        const int n = static_cast<int>(min(p.rows - row, static_cast<int64_t>(R)));
+        const T *x = static_cast<const T *>(p.x) + row * p.ldx, *dy = static_cast<const T *>(p.dy) + row * p.lddy;
+        float mean[R], rstd[R], s0[R], s1[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mean[r] = p.mean_in[row + min(r, n - 1)];
+            rstd[r] = p.rstd_in[row + min(r, n - 1)];
+            s0[r] = s1[r] = 0.0f;
+        }
+        for (int c = c0; c < cols; c += kBatch * cstep) {
+            Raw<T, V> ra[R][kBatch], rd[R][kBatch];
+            float g[kBatch][V];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r < n) {
+                    load_batch<T, V, kBatch>(x + r * p.ldx, c, cstep, cols, ra[r]);
+                    load_batch<T, V, kBatch>(dy + r * p.lddy, c, cstep, cols, rd[r]);
+                }
+            load_w<V, kBatch>(p.gamma, p.w_kind, c, cstep, cols, 1.0f, g);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (c + i * cstep < cols) {
+                    float dg[V], db[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        dg[j] = db[j] = 0.0f;
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (r < n) {
+                            float a[V], d[V];
+                            unpack<T>(ra[r][i], a);
+                            unpack<T>(rd[r][i], d);
+#pragma unroll
+                            for (int j = 0; j < V; ++j) {
+                                const float xh = (a[j] - mean[r]) * rstd[r], gd = g[i][j] * d[j];
+                                db[j] += d[j];
+                                dg[j] = fmaf(d[j], xh, dg[j]);
+                                s0[r] += gd;
+                                s1[r] = fmaf(gd, xh, s1[r]);
+                            }
+                        }
+                    if (sums) {
+                        if (once)
+#pragma unroll
+                            for (int j = 0; j < V; ++j) {
+                                pg[c + i * cstep + j] = dg[j];
+                                pb[c + i * cstep + j] = db[j];
+                            }
+                        else
+#pragma unroll
+                            for (int j = 0; j < V; ++j) {
+                                ag[c + i * cstep + j] += dg[j];
+                                ab[c + i * cstep + j] += db[j];
+                            }
+                    }
+                }
+        }
+        if (!p.dx)
+            continue;
+        __syncthreads();   // the sums of the rows before have been read
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s0[r] = warp_sum(s0[r]);
+            s1[r] = warp_sum(s1[r]);
+            if (lane == 0) {
+                scratch[2 * r][warp] = s0[r];
+                scratch[2 * r + 1][warp] = s1[r];
+            }
+        }
+        __syncthreads();
+        float m0[R], m1[R];   // dx = rstd g + (m0 + m1 xh)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float u = (lane & 15) < warps ? scratch[2 * r][lane & 15] : 0.0f, w = (lane & 15) < warps ? scratch[2 * r + 1][lane & 15] : 0.0f;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) {
+                u += __shfl_xor_sync(0xffffffffu, u, o);
+                w += __shfl_xor_sync(0xffffffffu, w, o);
+            }
+            m0[r] = -rstd[r] * p.inv_cols * u;
+            m1[r] = -rstd[r] * p.inv_cols * w;
+        }
+        T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+        const T *add = p.add ? static_cast<const T *>(p.add) + row * p.ldadd : nullptr;
+        for (int c = c0; c < cols; c += kBatch * cstep) {
+            Raw<T, V> ra[R][kBatch], rd[R][kBatch], rq[R][kBatch];
+            float g[kBatch][V];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r < n) {
+                    load_batch<T, V, kBatch>(x + r * p.ldx, c, cstep, cols, ra[r]);
+                    load_batch<T, V, kBatch>(dy + r * p.lddy, c, cstep, cols, rd[r]);
+                    if (add)
+                        load_batch<T, V, kBatch>(add + r * p.ldadd, c, cstep, cols, rq[r]);
+                }
+            load_w<V, kBatch>(p.gamma, p.w_kind, c, cstep, cols, 1.0f, g);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (c + i * cstep < cols)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (r < n) {
+                            float o[V], a[V], d[V], q[V];
+                            unpack<T>(ra[r][i], a);
+                            unpack<T>(rd[r][i], d);
+                            unpack<T>(rq[r][i], q);
+#pragma unroll
+                            for (int j = 0; j < V; ++j) {
+                                o[j] = fmaf(g[i][j] * d[j], rstd[r], fmaf((a[j] - mean[r]) * rstd[r], m1[r], m0[r]));
+                                if (add)
+                                    o[j] += q[j];
+                            }
+                            store<T, V>(dx + r * p.lddx + c + i * cstep, o);
+                        }
+        }
+    }
+    if (sums && !once)
+        for (int c = c0; c < cols; c += cstep)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                pg[c + j] = ag[c + j];
+                pb[c + j] = ab[c + j];
+            }
+}
+
+// Rows too wide for registers and shared memory: three passes over the row (the later ones come from L2).
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads) norm_forward_wide_kernel(const NormParams p)
 {
@@ -869,16 +1141,12 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int kSms = 152;
 constexpr int kColsumBlocks = 64;     // row blocks of the two-kernel backward pass, at most
-constexpr int kMaxBlocks = 8 * kSms;  // blocks of the fused one
-constexpr int64_t kFusedCols = 16384; // its widest rows
 constexpr size_t kRingLimit = 200 * 1024;
+constexpr int64_t kFusedCols = kRingLimit / 8;   // its widest rows
 
-// Vectors per thread of the kernels that walk over rows, for at most 512 threads and 32 columns a thread (16 of
-// the narrow kinds).  0: too wide.
+// Vectors per thread of the backward ring kernel, for at most 512 threads and 32 columns a thread.  0: too wide.
 int ring_items(int64_t nvec, int v)
 {
-    if (v <= 2)
-        return nvec <= 4 * 512 ? 4 : nvec <= 16 * 512 ? 16 : 0;
     if (nvec <= 256)
         return 1;
     for (int items = 2; items <= 32 / v; items *= 2)
@@ -887,11 +1155,33 @@ int ring_items(int64_t nvec, int v)
     return 0;
 }
 
-// Blocks of the fused backward kernel: small blocks share an SM, wide rows take one each.
-int fused_blocks(int64_t rows, int threads)
+int ring_threads(int64_t nvec, int items) { return static_cast<int>(cdiv(cdiv(nvec, items), 32) * 32); }
+
+// Threads of the kernels that loop over columns, about `each` vectors apiece.
+int loop_threads(int64_t nvec, int each)
 {
-    const int per_sm = std::max(1, std::min(8, 768 / threads));
-    return static_cast<int>(std::min<int64_t>(rows, static_cast<int64_t>(per_sm) * kSms));
+    return static_cast<int>(std::min<int64_t>(512, std::max<int64_t>(64, cdiv(cdiv(nvec, each), 32) * 32)));
+}
+
+// Blocks per SM of the fused backward kernels: small blocks share an SM, wide rows take one each.
+int ring_per_sm(int threads) { return std::max(1, std::min(8, 768 / threads)); }
+int staged_per_sm(int threads, size_t smem, int at_a_time)
+{
+    return std::max(1, std::min({8, (at_a_time == 1 ? 1536 : 1024) / threads, static_cast<int>(kRingLimit / smem)}));
+}
+
+// The most blocks that a fused backward kernel uses at this width, over the kinds of alignment.
+int64_t most_fused_blocks(int64_t cols)
+{
+    int per_sm = 1;
+    for (int v = 1; v <= 8; v *= 2) {
+        const int64_t nvec = cdiv(cols, v);
+        if (v <= 2)
+            per_sm = std::max(per_sm, staged_per_sm(loop_threads(nvec, 4), static_cast<size_t>(cols) * 8, 1));
+        else if (const int items = ring_items(nvec, v))
+            per_sm = std::max(per_sm, ring_per_sm(ring_threads(nvec, items)));
+    }
+    return static_cast<int64_t>(per_sm) * kSms;
 }
 
 template <typename K>
@@ -948,35 +1238,48 @@ bool launch_forward_ring(const NormParams &p, int64_t nvec, cudaStream_t st)
     return true;
 }
 
-// Few rows: one vector per thread and one row per block, so that a row's loads go out at once from as many
-// threads as there are.  Many rows: narrow ones a warp each, wide ones through the ring.  What fits neither
-// (rows that are not 16-byte aligned, very wide ones) takes more vectors per thread, then three passes.
+template <typename T, int V>
+bool launch_forward_staged(const NormParams &p, cudaStream_t st)
+{
+    const int threads = loop_threads(cdiv(p.cols, V), 8);
+    const size_t smem = static_cast<size_t>(p.cols) * 4;
+    auto kernel = norm_forward_staged_kernel<T, V>;
+    if (smem > kRingLimit || !allow_smem(kernel, smem))
+        return false;
+    const int per_sm = std::max(1, std::min({16, 2048 / threads, static_cast<int>(kRingLimit / smem)}));
+    kernel<<<static_cast<unsigned>(std::min<int64_t>(p.rows, static_cast<int64_t>(per_sm) * kSms)), threads, smem, st>>>(p);
+    return true;
+}
+
+// Rows in 16-byte units.  Few rows: one vector per thread and one row per block, so that a row's loads go out at once
+// from as many threads as there are.  Many rows: narrow ones a warp each, wide ones through the ring.  Other rows:
+// narrow ones a warp each, wide ones staged.  What fits none of these takes three passes over the row.
 template <typename T, int V>
 void forward_v(const NormParams &p, cudaStream_t st)
 {
     const int64_t nvec = cdiv(p.cols, V);
     const bool many = p.rows > 2 * kSms;
     if constexpr (V * sizeof(T) == 16) {
-        if (many && nvec > 128) {
-            constexpr int kMost = 32 / V;   // 32 columns a thread
-            const int need = static_cast<int>(cdiv(nvec, 512));
-            if ((nvec <= 256 && launch_forward_ring<T, V, 1>(p, nvec, st)) ||
-                (need <= kMost && nvec > 256 && launch_forward_ring<T, V, kMost>(p, nvec, st)))
-                return;
-        }
+        constexpr int kMost = 32 / V;   // 32 columns a thread
+        if (many && nvec > 128 &&
+            ((nvec <= 256 && launch_forward_ring<T, V, 1>(p, nvec, st)) ||
+             (nvec > 256 && nvec <= 512 * kMost && launch_forward_ring<T, V, kMost>(p, nvec, st))))
+            return;
+        if (nvec <= (many ? 32 : 1024))
+            return launch_forward<T, V, 1, 1024>(p, nvec, st);
+        if (nvec <= 4 * 512)
+            return launch_forward<T, V, 4, 512>(p, nvec, st);
+        if (nvec <= 4 * 1024)
+            return launch_forward<T, V, 4, 1024>(p, nvec, st);
+    } else {
+        if (nvec <= 32)
+            return launch_forward<T, V, 1, 1024>(p, nvec, st);
+        if (nvec <= 128)
+            return launch_forward<T, V, 4, 512>(p, nvec, st);
+        if (launch_forward_staged<T, V>(p, st))
+            return;
     }
-    if (nvec <= (many ? 32 : 1024))
-        launch_forward<T, V, 1, 1024>(p, nvec, st);
-    else if (nvec <= 4 * 256)
-        launch_forward<T, V, 4, 256>(p, nvec, st);
-    else if (nvec <= 4 * 512)
-        launch_forward<T, V, 4, 512>(p, nvec, st);
-    else if (nvec <= 4 * 1024)
-        launch_forward<T, V, 4, 1024>(p, nvec, st);
-    else if (V <= 2 && nvec <= 16 * 1024)
-        launch_forward<T, V, V <= 2 ? 16 : 1, 1024>(p, nvec, st);
-    else
-        norm_forward_wide_kernel<T><<<static_cast<unsigned>(p.rows), kMaxThreads, 0, st>>>(p);
+    norm_forward_wide_kernel<T><<<static_cast<unsigned>(p.rows), kMaxThreads, 0, st>>>(p);
 }
 
 template <typename T, int V, int kItems, int kStages>
@@ -989,38 +1292,57 @@ bool launch_backward(const NormParams &p, int threads, size_t smem, cudaStream_t
     return true;
 }
 
-// One pass for all gradients; false where the rows are too wide for it.  The ring has 4 slots, or 2 for wide
-// rows; rows in units of 2 bytes cannot be copied asynchronously and are read in place.
+// Rows in 16-byte units through a ring of 4 slots, or 2 where the rows are wide; false where they are too wide.
 template <typename T, int V, int kItems>
-bool backward_fused(NormParams &p, int64_t nvec, cudaStream_t st)
+bool backward_ring(NormParams &p, int64_t nvec, cudaStream_t st)
 {
-    const int threads = static_cast<int>(cdiv(cdiv(nvec, kItems), 32) * 32);
-    p.blocks = fused_blocks(p.rows, threads);
-    if constexpr (V * sizeof(T) == 2) {
-        return launch_backward<T, V, kItems, 0>(p, threads, 0, st);
-    } else {
-        const size_t slot = static_cast<size_t>(p.add ? 3 : 2) * kItems * threads * V * sizeof(T);
-        if (4 * slot * cdiv(p.blocks, kSms) <= kRingLimit)
-            return launch_backward<T, V, kItems, 4>(p, threads, 4 * slot, st);
-        return 2 * slot <= kRingLimit && launch_backward<T, V, kItems, 2>(p, threads, 2 * slot, st);
-    }
+    const int threads = ring_threads(nvec, kItems);
+    p.blocks = static_cast<int32_t>(std::min<int64_t>(p.rows, static_cast<int64_t>(ring_per_sm(threads)) * kSms));
+    const size_t slot = static_cast<size_t>(p.add ? 3 : 2) * kItems * threads * 16;
+    if (4 * slot * cdiv(p.blocks, kSms) <= kRingLimit)
+        return launch_backward<T, V, kItems, 4>(p, threads, 4 * slot, st);
+    return 2 * slot <= kRingLimit && launch_backward<T, V, kItems, 2>(p, threads, 2 * slot, st);
 }
 
+template <typename T, int V, int R>
+bool backward_staged_r(NormParams &p, int threads, size_t smem, cudaStream_t st)
+{
+    auto kernel = norm_backward_staged_kernel<T, V, R>;
+    if (!allow_smem(kernel, smem))
+        return false;
+    kernel<<<static_cast<unsigned>(p.blocks), threads, smem, st>>>(p);
+    return true;
+}
+
+// Other rows, four at a time where there are enough to keep every SM busy.
+template <typename T, int V>
+bool backward_staged(NormParams &p, cudaStream_t st)
+{
+    const int threads = loop_threads(cdiv(p.cols, V), 4);
+    const size_t smem = p.part ? static_cast<size_t>(p.cols) * 8 : 0;
+    if (smem > kRingLimit)
+        return false;
+    auto most = [&](int r) { return static_cast<int64_t>(staged_per_sm(threads, static_cast<size_t>(p.cols) * 8, r)) * kSms; };
+    const bool four = p.rows >= 2 * most(4);
+    p.blocks = static_cast<int32_t>(four ? std::min(cdiv(p.rows, 4), most(4)) : std::min(p.rows, most(1)));
+    return four ? backward_staged_r<T, V, 4>(p, threads, smem, st) : backward_staged_r<T, V, 1>(p, threads, smem, st);
+}
+
+// One kernel for all gradients; false where the rows are too wide for it.
 template <typename T, int V>
 bool backward_v(NormParams &p, cudaStream_t st)
 {
-    const int64_t nvec = cdiv(p.cols, V);
-    const int items = ring_items(nvec, V);
-    if constexpr (V <= 2) {
-        return items == 4 ? backward_fused<T, V, 4>(p, nvec, st) : items == 16 && backward_fused<T, V, 16>(p, nvec, st);
-    } else {
+    if constexpr (V * sizeof(T) == 16) {
+        const int64_t nvec = cdiv(p.cols, V);
+        const int items = ring_items(nvec, V);
         if constexpr (V == 4)
-            if (items == 8)
-                return backward_fused<T, V, 8>(p, nvec, st);
-        return items == 1   ? backward_fused<T, V, 1>(p, nvec, st)
-               : items == 2 ? backward_fused<T, V, 2>(p, nvec, st)
-                            : items == 4 && backward_fused<T, V, 4>(p, nvec, st);
+            if (items == 8 && backward_ring<T, V, 8>(p, nvec, st))
+                return true;
+        if ((items == 1 && backward_ring<T, V, 1>(p, nvec, st)) || (items == 2 && backward_ring<T, V, 2>(p, nvec, st)) ||
+            (items == 4 && backward_ring<T, V, 4>(p, nvec, st)))
+            return true;
     }
+    return backward_staged<T, V * sizeof(T) == 16 ? (sizeof(T) == 2 ? 2 : 1) : V>(p, st);
 }
 
 // Rows wider than a block's registers: the column sums first (dx may overwrite what they read), then dx.
@@ -1089,7 +1411,8 @@ extern "C" mlp_status mlp_layernorm_workspace_size(int64_t rows, int64_t cols, s
 {
     if (rows < 0 || cols < 1 || !bytes)
         return MLP_ERR_INVALID_ARG;
-    const int64_t blocks = cols <= kFusedCols ? std::min<int64_t>(std::max<int64_t>(rows, kColsumBlocks), kMaxBlocks) : kColsumBlocks;
+    const int64_t blocks = cols <= kFusedCols ? std::min<int64_t>(std::max<int64_t>(rows, kColsumBlocks), std::max<int64_t>(most_fused_blocks(cols), kColsumBlocks))
+                                              : kColsumBlocks;
     *bytes = static_cast<size_t>(blocks) * 2 * static_cast<size_t>(cols) * 4;
     return MLP_OK;
 }

@@ -120,7 +120,7 @@ void finish_plan(const mlp_linear *h, Plan &pl, bool q_mn)
 // red: output columns and reduction extent; w_mn: the weights' tile is MN-major.
 Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red, bool w_mn)
 {
-    const int64_t groups = std::min<int64_t>(h->groups, rows), avg = cdiv(rows, groups);
+    const int64_t groups = std::min<int64_t>(h->groups, rows);
     const int64_t kb = cdiv(red, kKB);
     Plan best{kRowsT, 1, 32, 1, 0, 0, 0, 0, 0, 1};
     double best_t = 1e300;
@@ -139,15 +139,15 @@ Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red,
                     // than there are column steps: every tile gets at least one)
                     const int64_t most = form == kRowsT && h->groups == 1 ? std::min<int64_t>(least + 2, cdiv(rows, u)) : least;
                     for (int64_t tq = least; tq <= most; ++tq) {
-                        // groups of ragged size end in a partial tile: half a tile on average
+                        // groups of ragged size: at least a tile each, and half a tile (a column step) too much
                         int64_t items;
                         double n = bn;
                         if (form == kRows) {
-                            items = (h->groups > 1 ? cdiv(rows, bm) + groups / 2 : cdiv(rows, bm)) * cdiv(out_cols, bn);
+                            items = (h->groups > 1 ? std::max(groups, cdiv(rows, bm) + groups / 2) : cdiv(rows, bm)) * cdiv(out_cols, bn);
                         } else if (h->groups > 1) {
-                            const int64_t tiles = groups * cdiv(avg, bn);
+                            const int64_t tiles = std::max(groups, cdiv(rows, bn) + groups / 2);
                             items = tiles * cdiv(out_cols, bm);
-                            n = std::min<double>(bn, static_cast<double>(rows) / static_cast<double>(tiles) + u);
+                            n = std::min<double>(bn, static_cast<double>(rows) / static_cast<double>(tiles) + u / 2);
                         } else {
                             items = tq * cdiv(out_cols, bm);
                             n = static_cast<double>(cdiv(rows, u) * u) / static_cast<double>(tq);
@@ -158,9 +158,10 @@ Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red,
                         const double fill = (16384.0 + (form == kRows ? q_tile_bytes(bn / pair, w_mn) : n * 128.0 / pair)) / 64.0;
                         const double step = std::max(mma, fill);
                         const double waves = static_cast<double>(cdiv(items, at_once));
+                        // the last epilogue of a CTA is not hidden, nor are the exchanges of a split tile
                         double t = waves * (static_cast<double>(cdiv(kb, s)) * step + 400.0) + 12.0 * n;
                         if (s > 1)
-                            t += 1500.0 + n * 512.0 * (s - 1) / s / 18.0;
+                            t += waves * (1500.0 + n * 512.0 * (s - 1) / s / 18.0);
                         if (t < best_t) {
                             best_t = t;
                             best = Plan{form, pair, bn, s, 0, 0, 0, 0, 0, static_cast<int>(tq)};
