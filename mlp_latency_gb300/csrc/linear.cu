@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <new>
 
@@ -52,6 +53,13 @@ constexpr size_t kSmemLimit = 227 * 1024;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+template <int kForm, int kFormB>
+bool allow_smem()
+{
+    return cudaFuncSetAttribute(linear_kernel<kForm, kFormB, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess &&
+           cudaFuncSetAttribute(linear_kernel<kForm, kFormB, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess;
+}
+
 bool encode_boxed(CUtensorMap *map, const void *ptr, int64_t inner, int64_t outer, int64_t groups, int64_t ld, int boxes)
 {
     EncodeFn fn = encoder();
@@ -68,7 +76,7 @@ bool encode_boxed(CUtensorMap *map, const void *ptr, int64_t inner, int64_t oute
 
 // Operand `op` of a launch.  K-major: `outer` rows of the reduction extent `inner`, `cols` of them per tile.  MN-major:
 // `inner` columns, the reduction outside, `cols` columns per tile.
-bool operand(LinearParams &p, int op, bool mn, const void *ptr, int64_t inner, int64_t outer, int64_t groups, int64_t ld, int cols)
+bool operand(Problem &p, int op, bool mn, const void *ptr, int64_t inner, int64_t outer, int64_t groups, int64_t ld, int cols)
 {
     p.mn[op] = mn;
     if (!mn) {
@@ -112,59 +120,77 @@ void finish_plan(const mlp_linear *h, Plan &pl, bool q_mn)
     const int part = static_cast<int>(cdiv(cdiv(pl.bn, pl.split), pl.part_align)) * pl.part_align;
     pl.recv_bytes = static_cast<uint32_t>((pl.split - 1) * part) * kPRows * 4;
     pl.recv_bufs = pl.split > 1 && rows_t ? (pl.recv_bytes <= 24 * 1024 ? 2 : pl.recv_bytes <= 64 * 1024 ? 1 : 0) : 0;
-    const size_t fixed = linear_smem_bytes(rows_t, 0, static_cast<uint32_t>(pl.recv_bufs) * pl.recv_bytes, h->groups);
+    const size_t fixed = linear_smem_bytes(pl.form != kRows, 0, static_cast<uint32_t>(pl.recv_bufs) * pl.recv_bytes, h->groups);
     pl.pipe = static_cast<int>(std::min<size_t>(kMaxRing, (kSmemLimit - fixed) / pl.slot));
 }
 
-// The variant of a rows product, by an estimate of its time in SM cycles.  rows: of the whole call; out_cols,
-// red: output columns and reduction extent; w_mn: the weights' tile is MN-major.
-Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red, bool w_mn)
+// An estimate of a product's time in SM cycles: of all its tiles on the whole GPU, of one tile, and the sum over the
+// tiles divided by the tiles that run at a time.
+struct Estimate {
+    double time, tile, work;
+};
+
+// A rows product.  rows: of the whole call; out_cols, red: output columns and reduction extent; w_mn: the weights' tile
+// is MN-major.
+Estimate estimate_rows(const mlp_linear *h, const Plan &pl, int64_t rows, int64_t out_cols, int64_t red, bool w_mn)
 {
-    const int64_t groups = std::min<int64_t>(h->groups, rows);
+    const int64_t groups = std::min<int64_t>(h->groups, rows), kb = cdiv(red, kKB);
+    const int bm = kPRows * pl.pair, u = 16 * pl.pair;
+    // groups of ragged size: at least a tile each, and half a tile (a column step) too much
+    int64_t items;
+    double n = pl.bn;
+    if (pl.form == kRows) {
+        items = (h->groups > 1 ? std::max(groups, cdiv(rows, bm) + groups / 2) : cdiv(rows, bm)) * cdiv(out_cols, pl.bn);
+    } else if (h->groups > 1) {
+        const int64_t tiles = std::max(groups, cdiv(rows, pl.bn) + groups / 2);
+        items = tiles * cdiv(out_cols, bm);
+        n = std::min<double>(pl.bn, static_cast<double>(rows) / static_cast<double>(tiles) + u / 2);
+    } else {
+        items = pl.q_tiles * cdiv(out_cols, bm);
+        n = static_cast<double>(cdiv(rows, u) * u) / static_cast<double>(pl.q_tiles);
+    }
+    // MMA: 2 n cycles per k block, at least 310 to issue its four instructions; fill: what a CTA loads per k block
+    // at 64 bytes a cycle
+    const double mma = std::max(2.0 * n, 310.0);
+    const double fill = (16384.0 + (pl.form == kRows ? q_tile_bytes(pl.bn / pl.pair, w_mn) : n * 128.0 / pl.pair)) / 64.0;
+    Estimate e;
+    e.tile = static_cast<double>(cdiv(kb, pl.split)) * std::max(mma, fill) + 400.0;
+    // the last epilogue of a CTA is not hidden, nor are the exchanges of a split tile
+    if (pl.split > 1)
+        e.tile += 1500.0 + n * 512.0 * (pl.split - 1) / pl.split / 18.0;
+    const int64_t at_once = h->max_clusters[pl.pair * pl.split];
+    e.work = static_cast<double>(items) * e.tile / static_cast<double>(at_once);
+    e.time = static_cast<double>(cdiv(items, at_once)) * e.tile + 12.0 * n;
+    return e;
+}
+
+// The variant of a rows product with the lowest estimate.  any: of all forms, else of the unsplit kRowsT ones on `pair`
+// CTAs.
+Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red, bool w_mn, bool any = true, int only_pair = 0)
+{
     const int64_t kb = cdiv(red, kKB);
-    Plan best{kRowsT, 1, 32, 1, 0, 0, 0, 0, 0, 1};
+    Plan best{kRowsT, only_pair ? only_pair : 1, 32, 1, 0, 0, 0, 0, 0, static_cast<int>(cdiv(rows, 32))};
     double best_t = 1e300;
-    for (int form = kRows; form <= kRowsT; ++form)
+    for (int form = any ? kRows : kRowsT; form <= kRowsT; ++form)
         for (int pair = 1; pair <= 2; ++pair)
             for (int bn = 32; bn <= 256; bn += 32)
-                for (int s = 1; s * pair <= 8 && s <= 4; ++s) {
-                    if ((form == kRows && bn < 128) || (pair == 2 && rows <= (form == kRows ? kPRows : 32)))
-                        continue;   // (a pair's second half would have no rows)
-                    const int64_t at_once = h->max_clusters[pair * s];
-                    if (at_once < 1 || (s > 1 && kb < 4 * s))
+                for (int s = 1; s * pair <= 8 && s <= (any ? 4 : 1); ++s) {
+                    if (only_pair && pair != only_pair)
                         continue;
-                    const int bm = kPRows * pair, u = 16 * pair;
-                    const int64_t least = form == kRowsT ? cdiv(rows, bn) : 1;
+                    if ((form == kRows && bn < 128) || (any && pair == 2 && rows <= (form == kRows ? kPRows : 32)))
+                        continue;   // (a pair's second half would have no rows)
+                    if (h->max_clusters[pair * s] < 1 || (s > 1 && kb < 4 * s))
+                        continue;
                     // tiles along the rows: as few as hold them, or up to two more for a fuller last round (never more
                     // than there are column steps: every tile gets at least one)
-                    const int64_t most = form == kRowsT && h->groups == 1 ? std::min<int64_t>(least + 2, cdiv(rows, u)) : least;
+                    const int64_t least = form == kRowsT ? cdiv(rows, bn) : 1;
+                    const int64_t most = form == kRowsT && h->groups == 1 ? std::min<int64_t>(least + 2, cdiv(rows, 16 * pair)) : least;
                     for (int64_t tq = least; tq <= most; ++tq) {
-                        // groups of ragged size: at least a tile each, and half a tile (a column step) too much
-                        int64_t items;
-                        double n = bn;
-                        if (form == kRows) {
-                            items = (h->groups > 1 ? std::max(groups, cdiv(rows, bm) + groups / 2) : cdiv(rows, bm)) * cdiv(out_cols, bn);
-                        } else if (h->groups > 1) {
-                            const int64_t tiles = std::max(groups, cdiv(rows, bn) + groups / 2);
-                            items = tiles * cdiv(out_cols, bm);
-                            n = std::min<double>(bn, static_cast<double>(rows) / static_cast<double>(tiles) + u / 2);
-                        } else {
-                            items = tq * cdiv(out_cols, bm);
-                            n = static_cast<double>(cdiv(rows, u) * u) / static_cast<double>(tq);
-                        }
-                        // MMA: 2 n cycles per k block, at least 310 to issue its four instructions; fill: what a CTA
-                        // loads per k block at 64 bytes a cycle
-                        const double mma = std::max(2.0 * n, 310.0);
-                        const double fill = (16384.0 + (form == kRows ? q_tile_bytes(bn / pair, w_mn) : n * 128.0 / pair)) / 64.0;
-                        const double step = std::max(mma, fill);
-                        const double waves = static_cast<double>(cdiv(items, at_once));
-                        // the last epilogue of a CTA is not hidden, nor are the exchanges of a split tile
-                        double t = waves * (static_cast<double>(cdiv(kb, s)) * step + 400.0) + 12.0 * n;
-                        if (s > 1)
-                            t += waves * (1500.0 + n * 512.0 * (s - 1) / s / 18.0);
+                        const Plan pl{form, pair, bn, s, 0, 0, 0, 0, 0, static_cast<int>(tq)};
+                        const double t = estimate_rows(h, pl, rows, out_cols, red, w_mn).time;
                         if (t < best_t) {
                             best_t = t;
-                            best = Plan{form, pair, bn, s, 0, 0, 0, 0, 0, static_cast<int>(tq)};
+                            best = pl;
                         }
                     }
                 }
@@ -172,6 +198,7 @@ Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red,
     return best;
 }
 
+// The weights' gradient: 256 x 256 tiles on pairs, or 128 x 128 ones where those would leave half of the SMs idle.
 Plan plan_reduce(const mlp_linear *h, int64_t p_ext, int64_t q_ext)
 {
     Plan pl{kReduce, 2, 256, 1, 0, 0, 0, 0, 0, 0};
@@ -181,7 +208,49 @@ Plan plan_reduce(const mlp_linear *h, int64_t p_ext, int64_t q_ext)
     return pl;
 }
 
-template <int kForm, int kPair>
+Estimate estimate_reduce(const mlp_linear *h, const Plan &pl, int64_t rows, int64_t p_ext, int64_t q_ext)
+{
+    const double kb = static_cast<double>(rows) / static_cast<double>(h->groups) / kKB + (h->groups > 1 ? 0.5 : 0.0);
+    const double items = static_cast<double>(h->groups * cdiv(p_ext, kPRows * pl.pair) * cdiv(q_ext, pl.bn));
+    Estimate e;
+    // k blocks as above; a tile's stores leave the SM at about 18 bytes a cycle
+    e.tile = std::max(kb * std::max(2.0 * pl.bn, 512.0), 128.0 * pl.bn * 2.0 / 18.0) + 400.0;
+    const double at_once = h->max_clusters[pl.pair];
+    e.work = items * e.tile / at_once;
+    e.time = std::ceil(items / at_once) * e.tile + 12.0 * pl.bn;
+    return e;
+}
+
+// The backward pass: variants of both gradients, and whether they share a launch when both are asked for.  That saves a
+// launch, a set-up and a last round that is partly idle: 29 rows of 3160 x 1024 23 us against 30, 3343 rows of 6624 x
+// 2336 154 against 166.  Not where few long tiles of the input's gradient would outlast everything else (a launch of two
+// splits no tile), and not past a few hundred microseconds, where two working sets in L2 cost more (2048 rows of 8192 x
+// 8192 338 us against 331).  The input's gradient takes the same variant either way, so its bits do not depend on what
+// else is asked for.
+struct GradPlan {
+    Plan x, w;
+    bool together;
+};
+
+GradPlan plan_grads(const mlp_linear *h, int64_t rows)
+{
+    const int64_t K = h->d.K, N = h->d.N;
+    const bool kn = h->d.weight_layout == 0;
+    const int64_t pe = kn ? K : N, qe = kn ? N : K;
+    GradPlan g;
+    g.w = plan_reduce(h, pe, qe);
+    g.x = plan_rows(h, rows, K, N, !kn);
+    const Plan x = plan_rows(h, rows, K, N, !kn, false, g.w.pair);
+    const Estimate ex = estimate_rows(h, x, rows, K, N, !kn), ew = estimate_reduce(h, g.w, rows, pe, qe);
+    const double both = std::max(ex.work + ew.work, std::max(ex.tile, ew.tile)) + 3000.0;
+    const double apart = estimate_rows(h, g.x, rows, K, N, !kn).time + ew.time + 6000.0;
+    g.together = both <= apart && both < 400e3;
+    if (g.together)
+        g.x = x;
+    return g;
+}
+
+template <int kForm, int kFormB, int kPair>
 bool launch_one(const LinearParams &p, int clusters, int cs, size_t smem, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg = {};
@@ -199,24 +268,28 @@ bool launch_one(const LinearParams &p, int clusters, int cs, size_t smem, cudaSt
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = cs > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, linear_kernel<kForm, kPair>, p) == cudaSuccess;
+    return cudaLaunchKernelEx(&cfg, linear_kernel<kForm, kFormB, kPair>, p) == cudaSuccess;
 }
 
-// items: the items of this launch, or an upper bound where the counts of groups are on the device.
-mlp_status launch(const mlp_linear *h, LinearParams &p, const Plan &pl, int64_t items, cudaStream_t st)
+// One product (w NULL), or a kRowsT one with the weights' gradient.  items: of the launch, or an upper bound where the
+// counts of groups are on the device.
+mlp_status launch(const mlp_linear *h, LinearParams &p, const Plan &pl, const Plan *w, int64_t items, cudaStream_t st)
 {
     p.groups = h->groups;
-    p.dense_items = static_cast<int32_t>(items);
-    p.bn = pl.bn;
+    for (int i = 0; i < 2; ++i)
+        p.pr[i].raster = 16 / pl.pair;
+    p.pr[0].bn = pl.bn;
+    if (w)
+        p.pr[1].bn = w->bn;
+    p.acc_cols = w ? std::max(pl.bn, w->bn) : pl.bn;
     p.split = pl.split;
-    p.raster = 16 / pl.pair;
-    p.num_pipe = pl.pipe;
-    p.slot_bytes = pl.slot;
+    p.slot_bytes = w ? std::max(pl.slot, w->slot) : pl.slot;
+    p.num_pipe = w ? std::min(pl.pipe, w->pipe) : pl.pipe;
     p.part_align = pl.part_align;
     p.recv_bufs = pl.recv_bufs;
     p.recv_bytes = pl.recv_bytes;
     // two accumulators; parts of a split tile that are no multiple of 32 columns are over-read
-    const uint32_t cols = 2u * static_cast<uint32_t>(pl.bn) + (pl.split > 1 && pl.part_align < 32 ? 32u : 0u);
+    const uint32_t cols = 2u * static_cast<uint32_t>(p.acc_cols) + (pl.split > 1 && pl.part_align < 32 ? 32u : 0u);
     p.tmem_cols = 32;
     while (p.tmem_cols < cols)
         p.tmem_cols *= 2;
@@ -224,46 +297,64 @@ mlp_status launch(const mlp_linear *h, LinearParams &p, const Plan &pl, int64_t 
     p.timeout_ns = static_cast<uint64_t>(h->d.timeout_us ? h->d.timeout_us : 2000000u) * 1000ull;
     const int cs = pl.pair * pl.split;
     const int clusters = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(items, h->max_clusters[cs])));
-    const size_t smem = linear_smem_bytes(pl.form == kRowsT, static_cast<uint32_t>(pl.pipe) * pl.slot,
+    const size_t smem = linear_smem_bytes(pl.form != kRows, static_cast<uint32_t>(p.num_pipe) * p.slot_bytes,
                                           static_cast<uint32_t>(pl.recv_bufs) * pl.recv_bytes, h->groups);
     bool ok = false;
-    if (pl.form == kRows)
-        ok = pl.pair == 2 ? launch_one<kRows, 2>(p, clusters, cs, smem, st) : launch_one<kRows, 1>(p, clusters, cs, smem, st);
+    const bool two = pl.pair == 2;
+    if (w)
+        ok = two ? launch_one<kRowsT, kReduce, 2>(p, clusters, cs, smem, st) : launch_one<kRowsT, kReduce, 1>(p, clusters, cs, smem, st);
+    else if (pl.form == kRows)
+        ok = two ? launch_one<kRows, -1, 2>(p, clusters, cs, smem, st) : launch_one<kRows, -1, 1>(p, clusters, cs, smem, st);
     else if (pl.form == kRowsT)
-        ok = pl.pair == 2 ? launch_one<kRowsT, 2>(p, clusters, cs, smem, st) : launch_one<kRowsT, 1>(p, clusters, cs, smem, st);
+        ok = two ? launch_one<kRowsT, -1, 2>(p, clusters, cs, smem, st) : launch_one<kRowsT, -1, 1>(p, clusters, cs, smem, st);
     else
-        ok = pl.pair == 2 ? launch_one<kReduce, 2>(p, clusters, cs, smem, st) : launch_one<kReduce, 1>(p, clusters, cs, smem, st);
+        ok = two ? launch_one<kReduce, -1, 2>(p, clusters, cs, smem, st) : launch_one<kReduce, -1, 1>(p, clusters, cs, smem, st);
     return ok ? MLP_OK : MLP_ERR_CUDA;
 }
 
-// out[rows, out_cols] = A[rows, red] * B, B stored out_cols-major (b_mn: red x out_cols) or red-major.
-mlp_status rows_product(const mlp_linear *h, LinearParams &p, int64_t rows, const void *A, int64_t lda, const void *B,
-                        int64_t out_cols, int64_t red, bool b_mn, cudaStream_t st)
+// out[rows, out_cols] = A[rows, red] * B, B stored out_cols-major (b_mn: red x out_cols) or red-major.  Returns the
+// product's items (at most), or 0 if a tensor map could not be made.
+int64_t describe_rows(const mlp_linear *h, Problem &q, const Plan &pl, int64_t rows, const void *A, int64_t lda, const void *B,
+                      int64_t out_cols, int64_t red, bool b_mn, bool offsets)
 {
-    const Plan pl = plan_rows(h, rows, out_cols, red, b_mn);
-    p.rows = static_cast<int32_t>(rows);
-    p.k_ext = static_cast<int32_t>(red);
+    q.k_ext = static_cast<int32_t>(red);
+    const int64_t b_in = b_mn ? out_cols : red, b_out = b_mn ? red : out_cols;
     int64_t items;
     if (pl.form == kRows) {
         // (a box never reaches past the last row of a short matrix: copies that are mostly out of range measured
         // several times slower than full ones)
         const int prows = static_cast<int>(std::min<int64_t>(kPRows, rows));
-        if (!operand(p, 0, false, A, red, rows, 1, lda, prows) ||
-            !operand(p, 1, b_mn, B, b_mn ? out_cols : red, b_mn ? red : out_cols, h->groups, b_mn ? out_cols : red, pl.bn / pl.pair))
-            return MLP_ERR_CUDA;
-        p.q_ext = static_cast<int32_t>(out_cols);
+        if (!operand(q, 0, false, A, red, rows, 1, lda, prows) || !operand(q, 1, b_mn, B, b_in, b_out, h->groups, b_in, pl.bn / pl.pair))
+            return 0;
+        q.q_ext = static_cast<int32_t>(out_cols);
         items = (cdiv(rows, kPRows * pl.pair) + h->groups - 1) * cdiv(out_cols, pl.bn);
     } else {
         const int qrows = static_cast<int>(std::min<int64_t>(pl.bn / pl.pair, rows));
-        if (!operand(p, 1, false, A, red, rows, 1, lda, qrows) ||
-            !operand(p, 0, b_mn, B, b_mn ? out_cols : red, b_mn ? red : out_cols, h->groups, b_mn ? out_cols : red, kPRows))
-            return MLP_ERR_CUDA;
-        p.p_ext = static_cast<int32_t>(out_cols);
-        if (h->groups == 1 && !p.offsets)
-            p.dense_q_tiles = pl.q_tiles;
-        items = (p.dense_q_tiles ? pl.q_tiles : cdiv(rows, pl.bn) + h->groups - 1) * cdiv(out_cols, kPRows * pl.pair);
+        if (!operand(q, 1, false, A, red, rows, 1, lda, qrows) || !operand(q, 0, b_mn, B, b_in, b_out, h->groups, b_in, kPRows))
+            return 0;
+        q.p_ext = static_cast<int32_t>(out_cols);
+        if (!offsets)
+            q.dense_q_tiles = pl.q_tiles;
+        items = (offsets ? cdiv(rows, pl.bn) + h->groups - 1 : pl.q_tiles) * cdiv(out_cols, kPRows * pl.pair);
     }
-    return launch(h, p, pl, items, st);
+    q.dense_items = static_cast<int32_t>(items);
+    return items;
+}
+
+// dW: P and Q have `rows` rows of pe and qe columns.
+int64_t describe_reduce(const mlp_linear *h, Problem &q, const Plan &pl, int64_t rows, const void *P, int64_t ldp, int64_t pe,
+                        const void *Q, int64_t ldq, int64_t qe, void *dW, bool f32)
+{
+    q.p_ext = static_cast<int32_t>(pe);
+    q.q_ext = static_cast<int32_t>(qe);
+    q.out = dW;
+    q.out_f32 = f32;
+    q.ld_out = qe;
+    if (!operand(q, 0, true, P, pe, rows, 1, ldp, kPRows) || !operand(q, 1, true, Q, qe, rows, 1, ldq, pl.bn / pl.pair))
+        return 0;
+    const int64_t items = h->groups * cdiv(pe, kPRows * pl.pair) * cdiv(qe, pl.bn);
+    q.dense_items = static_cast<int32_t>(items);
+    return items;
 }
 
 // ------------------------------------------------------- dZ = dY act'(Z) and the bias gradient --
@@ -466,12 +557,7 @@ extern "C" mlp_status mlp_linear_create(const mlp_linear_desc *d, mlp_linear_t *
     h->status = nullptr;
     mlp_status st = MLP_OK;
     if (cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, d->device) != cudaSuccess ||
-        cudaFuncSetAttribute(linear_kernel<kRows, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
-        cudaFuncSetAttribute(linear_kernel<kRows, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
-        cudaFuncSetAttribute(linear_kernel<kRowsT, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
-        cudaFuncSetAttribute(linear_kernel<kRowsT, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
-        cudaFuncSetAttribute(linear_kernel<kReduce, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
-        cudaFuncSetAttribute(linear_kernel<kReduce, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) {
+        !allow_smem<kRows, -1>() || !allow_smem<kRowsT, -1>() || !allow_smem<kReduce, -1>() || !allow_smem<kRowsT, kReduce>()) {
         st = MLP_ERR_CUDA;
     }
     for (int cs = 1; cs <= 8 && st == MLP_OK; ++cs) {
@@ -486,7 +572,7 @@ extern "C" mlp_status mlp_linear_create(const mlp_linear_desc *d, mlp_linear_t *
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<kRows, 1>, &cfg) != cudaSuccess || (n < 1 && cs <= 2))
+        if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<kRows, -1, 1>, &cfg) != cudaSuccess || (n < 1 && cs <= 2))
             st = MLP_ERR_CUDA;
         h->max_clusters[cs] = n;
     }
@@ -552,16 +638,21 @@ extern "C" mlp_status mlp_linear_forward(mlp_linear_t h, int64_t rows, const voi
     LinearParams p;
     std::memset(&p, 0, sizeof(p));
     p.offsets = offsets;
-    p.act = h->d.activation;
-    p.bias = bias;
-    p.bias_f32 = h->d.bias_dtype == MLP_DT_F32;
-    p.res = static_cast<const __nv_bfloat16 *>(residual);
-    p.ld_res = ldr;
-    p.z = static_cast<__nv_bfloat16 *>(Z);
-    p.ld_z = ldz;
-    p.out = Y;
-    p.ld_out = ldy;
-    return rows_product(h, p, rows, X, ldx, W, N, K, h->d.weight_layout == 0, static_cast<cudaStream_t>(stream));
+    p.rows = static_cast<int32_t>(rows);
+    Problem &q = p.pr[0];
+    q.act = h->d.activation;
+    q.bias = bias;
+    q.bias_f32 = h->d.bias_dtype == MLP_DT_F32;
+    q.res = static_cast<const __nv_bfloat16 *>(residual);
+    q.ld_res = ldr;
+    q.z = static_cast<__nv_bfloat16 *>(Z);
+    q.ld_z = ldz;
+    q.out = Y;
+    q.ld_out = ldy;
+    const bool kn = h->d.weight_layout == 0;
+    const Plan pl = plan_rows(h, rows, N, K, kn);
+    const int64_t items = describe_rows(h, q, pl, rows, X, ldx, W, N, K, kn, offsets != nullptr);
+    return items ? launch(h, p, pl, nullptr, items, static_cast<cudaStream_t>(stream)) : MLP_ERR_CUDA;
 }
 
 extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const void *dY, int64_t lddy, const void *X,
@@ -637,34 +728,39 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
                 return MLP_ERR_CUDA;
         }
     }
+    if (!dX && !dW)
+        return MLP_OK;
+    const bool kn = h->d.weight_layout == 0;
+    LinearParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.offsets = offsets;
+    p.rows = static_cast<int32_t>(rows);
+    // dX[m, k] = sum_n dZ[m, n] W(k, n): W stored K x N has the reduction inside
+    auto input_grad = [&](const Plan &pl) {
+        p.pr[0].out = dX;
+        p.pr[0].ld_out = lddx;
+        return describe_rows(h, p.pr[0], pl, rows, dz, ld_dz, W, K, N, !kn, offsets != nullptr);
+    };
+    const int64_t pe = kn ? K : N, qe = kn ? N : K;
+    auto weight_grad = [&](Problem &q, const Plan &pl) {
+        return describe_reduce(h, q, pl, rows, kn ? X : dz, kn ? ldx : ld_dz, pe, kn ? dz : X, kn ? ld_dz : ldx, qe, dW, dw_esz == 4);
+    };
+    const GradPlan plans = plan_grads(h, rows);
+    const Plan &px = plans.x, &pw = plans.w;
+    if (dX && dW && plans.together) {
+        const int64_t a = input_grad(px), b = weight_grad(p.pr[1], pw);
+        return a && b ? launch(h, p, px, &pw, a + b, st) : MLP_ERR_CUDA;
+    }
     if (dX) {
-        LinearParams p;
-        std::memset(&p, 0, sizeof(p));
-        p.offsets = offsets;
-        p.out = dX;
-        p.ld_out = lddx;
-        // dX[m, k] = sum_n dZ[m, n] W(k, n): W stored K x N has the reduction inside
-        const mlp_status r = rows_product(h, p, rows, dz, ld_dz, W, K, N, h->d.weight_layout == 1, st);
+        const int64_t items = input_grad(px);
+        const mlp_status r = items ? launch(h, p, px, nullptr, items, st) : MLP_ERR_CUDA;
         if (r != MLP_OK)
             return r;
     }
     if (dW) {
-        const bool kn = h->d.weight_layout == 0;
-        const int64_t pe = kn ? K : N, qe = kn ? N : K;
-        const Plan pl = plan_reduce(h, pe, qe);
-        LinearParams p;
-        std::memset(&p, 0, sizeof(p));
-        p.offsets = offsets;
-        p.rows = static_cast<int32_t>(rows);
-        p.p_ext = static_cast<int32_t>(pe);
-        p.q_ext = static_cast<int32_t>(qe);
-        p.out = dW;
-        p.out_f32 = dw_esz == 4;
-        p.ld_out = qe;
-        if (!operand(p, 0, true, kn ? X : dz, pe, rows, 1, kn ? ldx : ld_dz, kPRows) ||
-            !operand(p, 1, true, kn ? dz : X, qe, rows, 1, kn ? ld_dz : ldx, pl.bn / pl.pair))
-            return MLP_ERR_CUDA;
-        return launch(h, p, pl, h->groups * cdiv(pe, kPRows * pl.pair) * cdiv(qe, pl.bn), st);
+        std::memset(p.pr, 0, sizeof(p.pr));
+        const int64_t items = weight_grad(p.pr[0], pw);
+        return items ? launch(h, p, pw, nullptr, items, st) : MLP_ERR_CUDA;
     }
     return MLP_OK;
 }
@@ -687,10 +783,7 @@ extern "C" mlp_status mlp_linear_get_plan(mlp_linear_t h, int64_t rows, int32_t 
 {
     if (!h || !plan || rows < 1 || pass < 0 || pass > 2)
         return MLP_ERR_INVALID_ARG;
-    const bool kn = h->d.weight_layout == 0;
-    const Plan pl = pass == 0   ? plan_rows(h, rows, h->d.N, h->d.K, kn)
-                    : pass == 1 ? plan_rows(h, rows, h->d.K, h->d.N, !kn)
-                                : plan_reduce(h, kn ? h->d.K : h->d.N, kn ? h->d.N : h->d.K);
+    const Plan pl = pass == 0 ? plan_rows(h, rows, h->d.N, h->d.K, h->d.weight_layout == 0) : pass == 1 ? plan_grads(h, rows).x : plan_grads(h, rows).w;
     plan->form = pl.form;
     plan->cta_pair = pl.pair;
     plan->tile_cols = pl.bn;

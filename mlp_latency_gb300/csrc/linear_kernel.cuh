@@ -20,6 +20,9 @@
 // The accumulator is double buffered, so a tile's epilogue runs under the next tile's MMAs.  Tiles are dealt out
 // statically, in an order that lets the CTAs running at one time share operand panels in L2.
 //
+// kFormB >= 0: a launch of two products, kForm's and kFormB's, whose tiles every CTA takes in turn.  The backward pass
+// runs the input's and the weights' gradient this way.
+//
 // kPair = 2 runs 256-row tiles on CTA pairs (cta_group::2): each CTA loads its 128 rows of P and half
 // of Q's tile, a third less to fetch per SM and flop.  split > 1 shares one tile's reduction among the
 // CTAs (or pairs) of a cluster, each taking a range of k blocks; every CTA then finishes a range of the
@@ -53,25 +56,17 @@ __host__ __device__ inline uint32_t q_tile_bytes(int32_t cols, bool mn)
     return mn ? static_cast<uint32_t>((cols + 63) / 64) * kBoxBytes : static_cast<uint32_t>(cols) * 128u;
 }
 
-struct LinearParams {
+// One product of a launch.
+struct Problem {
     CUtensorMap map[2];             // P and Q: (inner, outer, group) views, or (64, outer, inner / 64, group)
     uint32_t copy_bytes[2];         // what one fill copies of each into a CTA
     int32_t boxed[2];               // the four-dimensional view: all boxes of an MN-major tile in one copy
     int32_t mn[2];                  // operand stored MN-major (else K-major)
-    const int32_t *offsets;         // device, groups + 1 entries, or null: one group of `rows` rows
-    int32_t groups, rows;
-    int32_t dense_items;            // items of a dense product (no offsets)
+    int32_t dense_items;            // items without offsets
     int32_t dense_q_tiles;          // kRowsT, dense: tiles along the rows, from rows / bn up to one per column step
     int32_t p_ext, q_ext, k_ext;    // extents of the dimensions that are not ragged
     int32_t bn;                     // columns of a tile (the pair's)
-    int32_t split;                  // CTAs, or pairs, sharing a tile's reduction
-    int32_t part_align;             // granularity of the column ranges that they finish: 8 or 32
-    int32_t recv_bufs;              // receive buffers for partial sums, of recv_bytes each; 0: the ring
-    uint32_t recv_bytes;            // serves as the one buffer and the next tile's copies wait for it
     int32_t raster;                 // row panels sharing a sweep over the column tiles
-    int32_t num_pipe;
-    uint32_t slot_bytes;
-    uint32_t tmem_cols;
     int32_t act;
     int32_t bias_f32, out_f32;
     const void *bias;               // groups x (output columns), or null
@@ -79,6 +74,20 @@ struct LinearParams {
     __nv_bfloat16 *z;               // pre-activation output, or null
     void *out;
     int64_t ld_out, ld_res, ld_z;   // row strides in elements
+};
+
+struct LinearParams {
+    Problem pr[2];
+    const int32_t *offsets;         // device, groups + 1 entries, or null: one group of `rows` rows
+    int32_t groups, rows;
+    int32_t acc_cols;               // TMEM columns of one accumulator
+    int32_t split;                  // CTAs, or pairs, sharing a tile's reduction
+    int32_t part_align;             // granularity of the column ranges that they finish: 8 or 32
+    int32_t recv_bufs;              // receive buffers for partial sums, of recv_bytes each; 0: the ring
+    uint32_t recv_bytes;            // serves as the one buffer and the next tile's copies wait for it
+    int32_t num_pipe;
+    uint32_t slot_bytes;
+    uint32_t tmem_cols;
     uint32_t *status;
     uint64_t timeout_ns;
 };
@@ -91,25 +100,25 @@ struct __align__(8) LCtrl {
     uint32_t tmem_base;
     volatile int32_t abort_flag;
     int32_t skip;
-    int32_t n_items;
+    int32_t n_items[2];
 };
 
-// Shared memory: ring (1024-byte aligned), receive buffers, staging per epilogue warp, bias tile (kRowsT: none),
-// control block, group tables.
+// Shared memory: ring (1024-byte aligned), receive buffers, staging per epilogue warp, a chunk's bias per epilogue warp
+// (kRows only), control block, group tables.
 struct SmemMap {
     uint32_t recv, stage, bias, ctrl, tab;
-    __host__ __device__ SmemMap(bool rows_t, uint32_t ring_bytes, uint32_t recv_total)
+    __host__ __device__ SmemMap(bool no_bias, uint32_t ring_bytes, uint32_t recv_total)
     {
         recv = ring_bytes;
         stage = recv + recv_total;
         bias = stage + kEpi * kStageWarpBytes;
-        ctrl = bias + (rows_t ? 0u : kEpi * 32u * 4u);
+        ctrl = bias + (no_bias ? 0u : kEpi * 32u * 4u);
         tab = ctrl + static_cast<uint32_t>((sizeof(LCtrl) + 15) / 16 * 16);
     }
 };
-__host__ inline size_t linear_smem_bytes(bool rows_t, uint32_t ring_bytes, uint32_t recv_total, int groups)
+__host__ inline size_t linear_smem_bytes(bool no_bias, uint32_t ring_bytes, uint32_t recv_total, int groups)
 {
-    return 1024 + SmemMap(rows_t, ring_bytes, recv_total).tab + (3 * static_cast<size_t>(groups) + 1) * 4;
+    return 1024 + SmemMap(no_bias, ring_bytes, recv_total).tab + (3 * static_cast<size_t>(groups) + 1) * 4;
 }
 
 __device__ __forceinline__ uint64_t policy_evict_normal()
@@ -223,6 +232,7 @@ struct GroupTab {
 };
 
 struct Tile {
+    int32_t which;       // product of the launch
     int32_t e, start, cnt;
     int32_t p0, q0;      // origin in the P and Q extents (inside the group's rows for a ragged one)
     int32_t n;           // MMA columns: bn, or what is left of the group's rows for kRowsT
@@ -230,70 +240,100 @@ struct Tile {
 };
 
 // kRowsT: tiles that a group's rows are dealt over.
-__device__ __forceinline__ int32_t q_tiles(const LinearParams &p, int32_t cnt)
+__device__ __forceinline__ int32_t q_tiles(const Problem &q, int32_t cnt)
 {
-    return p.dense_q_tiles ? p.dense_q_tiles : (cnt + p.bn - 1) / p.bn;
+    return q.dense_q_tiles ? q.dense_q_tiles : (cnt + q.bn - 1) / q.bn;
 }
 
 template <int kForm, int kPair>
-__device__ __forceinline__ int32_t items_of(const LinearParams &p, int32_t cnt)
+__device__ __forceinline__ int32_t items_of(const Problem &q, int32_t cnt)
 {
     constexpr int32_t bm = kPRows * kPair;
     if (kForm == kRows)
-        return (cnt + bm - 1) / bm * ((p.q_ext + p.bn - 1) / p.bn);
+        return (cnt + bm - 1) / bm * ((q.q_ext + q.bn - 1) / q.bn);
     if (kForm == kRowsT)
-        return q_tiles(p, cnt) * ((p.p_ext + bm - 1) / bm);
-    return (p.p_ext + bm - 1) / bm * ((p.q_ext + p.bn - 1) / p.bn);
+        return q_tiles(q, cnt) * ((q.p_ext + bm - 1) / bm);
+    return (q.p_ext + bm - 1) / bm * ((q.q_ext + q.bn - 1) / q.bn);
 }
 
-// One role's walk over its CTA's items: ids grow, so the group only ever advances.
-template <int kForm, int kPair>
+// One role's walk over its CTA's items: a product's ids grow, so the group only ever advances.
+template <int kForm, int kFormB, int kPair>
 struct Walk {
-    int32_t id, step, e, slice;
+    int32_t id, id_b, step, e, slice, turn;
     __device__ __forceinline__ Walk(const LinearParams &p)
         : id(static_cast<int32_t>(cluster_id_x())), step(static_cast<int32_t>(num_clusters_x())), e(0),
-          slice(p.split > 1 ? static_cast<int32_t>(cluster_ctarank()) / kPair : 0)
+          slice(p.split > 1 ? static_cast<int32_t>(cluster_ctarank()) / kPair : 0), turn(0)
     {
+        id_b = step - 1 - id;   // (dealt from the other end: a CTA with one tile more of one has fewer of the other)
     }
-    __device__ __forceinline__ bool next(const LinearParams &p, const GroupTab &g, int32_t n_items, Tile &t)
+    __device__ __forceinline__ bool next(const LinearParams &p, const GroupTab &g, int32_t n_items, int32_t n_items_b, Tile &t)
     {
-        if (id >= n_items)
-            return false;
-        constexpr int32_t bm = kPRows * kPair;
-        int32_t base = 0;
-        if (p.offsets) {
-            while (id >= g.base[e + 1])
-                ++e;
-            base = g.base[e];
-            t.start = g.start[e];
-            t.cnt = g.cnt[e];
-        } else {
-            t.start = 0;
-            t.cnt = p.rows;
+        if (kFormB < 0) {
+            if (id >= n_items)
+                return false;
+            t.which = 0;
+            place<kForm>(p, g, id, true, t);
+            id += step;
+            return true;
         }
-        t.e = e;
-        const int32_t i = id - base;
-        id += step;
-        const int32_t kext = kForm == kReduce ? t.cnt : p.k_ext;
+        const bool a = id < n_items, b = id_b < n_items_b;
+        if (!a && !b)
+            return false;
+        t.which = a && b ? turn : b;
+        turn ^= 1;
+        if (t.which == 0) {
+            place<kForm>(p, g, id, true, t);
+            id += step;
+        } else {
+            place<kFormB < 0 ? kForm : kFormB>(p, g, id_b, false, t);
+            id_b += step;
+        }
+        return true;
+    }
+    // tabled: the group tables count this product's items (else every group has the same number)
+    template <int kF>
+    __device__ __forceinline__ void place(const LinearParams &p, const GroupTab &g, int32_t item, bool tabled, Tile &t)
+    {
+        const Problem &q = p.pr[kFormB < 0 ? 0 : t.which];
+        constexpr int32_t bm = kPRows * kPair;
+        const int32_t tiles_q = (q.q_ext + q.bn - 1) / q.bn;   // (not for kRowsT)
+        int32_t i = item;
+        t.e = 0;
+        t.start = 0;
+        t.cnt = p.rows;
+        if (p.offsets) {
+            if (kF == kReduce) {
+                const int32_t each = (q.p_ext + bm - 1) / bm * tiles_q;
+                t.e = item / each;
+                i = item - t.e * each;
+            } else {
+                while (item >= g.base[e + 1])
+                    ++e;
+                t.e = e;
+                i = item - g.base[e];
+            }
+            t.start = g.start[t.e];
+            t.cnt = g.cnt[t.e];
+        }
+        const int32_t kext = kF == kReduce ? t.cnt : q.k_ext;
         const int32_t nkb = (kext + kKB - 1) / kKB;
-        if (kForm == kRowsT) {
+        if (kF == kRowsT) {
             // the group's rows in units of the MMA's column step, dealt evenly over the tiles
             constexpr int32_t u = 16 * kPair;
             const int32_t units = (t.cnt + u - 1) / u;
-            const int32_t tq = q_tiles(p, t.cnt);
+            const int32_t tq = q_tiles(q, t.cnt);
             const int32_t pi = i / tq, qi = i - pi * tq;
             const int32_t each = units / tq, more = units - each * tq;
             t.p0 = pi * bm;
             t.q0 = (qi * each + min(qi, more)) * u;
             t.n = (each + (qi < more ? 1 : 0)) * u;
         } else {
-            const int32_t tp = ((kForm == kRows ? t.cnt : p.p_ext) + bm - 1) / bm;
-            const int32_t tq = (p.q_ext + p.bn - 1) / p.bn;
-            const int32_t band = i / (p.raster * tq), first = band * p.raster;
-            const int32_t h = min(p.raster, tp - first), r = i - first * tq;
-            t.q0 = r / h * p.bn;
+            const int32_t tp = ((kF == kRows ? t.cnt : q.p_ext) + bm - 1) / bm;
+            const int32_t band = i / (q.raster * tiles_q), first = band * q.raster;
+            const int32_t h = min(q.raster, tp - first), r = i - first * tiles_q;
+            t.q0 = r / h * q.bn;
             t.p0 = (first + r % h) * bm;
-            t.n = p.bn;
+            t.n = q.bn;
         }
         if (p.split > 1) {
             const int32_t per = (nkb + p.split - 1) / p.split;
@@ -303,16 +343,26 @@ struct Walk {
             t.kb0 = 0;
             t.kb1 = nkb;
         }
-        return true;
     }
 };
 
+// The form of a tile's product: known at compile time in a launch of one.
+template <int kForm, int kFormB>
+__device__ __forceinline__ int form_of(const Tile &t)
+{
+    return kFormB < 0 ? kForm : t.which ? kFormB : kForm;
+}
+template <int kFormB>
+__device__ __forceinline__ const Problem &problem_of(const LinearParams &p, const Tile &t)
+{
+    return p.pr[kFormB < 0 ? 0 : t.which];
+}
+
 // A group's last k block holds rows of the next group when the reduction runs over a group's rows:
 // they are zeroed in shared memory.  (At the very end of the matrix the copy fills zeros itself.)
-template <int kForm>
-__device__ __forceinline__ int32_t masked_rows(const LinearParams &p, const Tile &t, int32_t kb)
+__device__ __forceinline__ int32_t masked_rows(int form, const LinearParams &p, const Tile &t, int32_t kb)
 {
-    if (kForm != kReduce)
+    if (form != kReduce)
         return 0;
     const int32_t have = t.cnt - kb * kKB;
     return have < kKB && t.start + t.cnt < p.rows ? kKB - have : 0;
@@ -320,10 +370,11 @@ __device__ __forceinline__ int32_t masked_rows(const LinearParams &p, const Tile
 
 // ------------------------------------------------------------------------------- TMA producers --
 // One of two threads, `which` = 0 or 1: the even or the odd fills of the ring.
-template <int kForm, int kPair>
+template <int kForm, int kFormB, int kPair>
 __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring, uint32_t which,
-                                           Walk<kForm, kPair> w, Tile t, bool have)
+                                           Walk<kForm, kFormB, kPair> w, Tile t, bool have)
 {
+    constexpr bool kMasks = kForm == kReduce || kFormB == kReduce;
     const uint32_t num_pipe = static_cast<uint32_t>(p.num_pipe);
     const uint32_t slot_bytes = p.slot_bytes;
     const uint32_t rank = cluster_ctarank();
@@ -331,17 +382,20 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
     const uint32_t full_lead0 = kPair == 2 ? map_to_rank(&c->full[0], rank & ~1u) : 0u;
     const uint32_t go_peer0 = kPair == 2 ? map_to_rank(&c->go[0], rank | 1u) : 0u;
     const uint32_t tail_own0 = kPair == 2 ? map_to_rank(&c->tail[0], rank) : 0u;
-    const bool p_mn = p.mn[0] != 0, q_mn = p.mn[1] != 0, p_boxed = p.boxed[0] != 0, q_boxed = p.boxed[1] != 0;
-    const uint32_t bytes = p.copy_bytes[0] + p.copy_bytes[1];
-    const int32_t q_boxes = static_cast<int32_t>(p.copy_bytes[1] / kBoxBytes);
     const bool shared_ring = p.split > 1 && p.recv_bufs == 0;
-    const int32_t n_items = c->n_items;
+    const int32_t n_items = c->n_items[0], n_items_b = c->n_items[1];
     const uint64_t pol = policy_evict_normal();
     uint32_t fills = 0, tail_ph = 0, tail_use = 0, item_ph = 0;
     uint32_t ps = 0, pph = 0;
     bool ok = true, first = true;
     griddep_wait();   // a programmatic launch: the kernel before this one is complete from here on
-    for (; ok && have; have = w.next(p, g, n_items, t)) {
+    for (; ok && have; have = w.next(p, g, n_items, n_items_b, t)) {
+        const int form = form_of<kForm, kFormB>(t);
+        const Problem &q = problem_of<kFormB>(p, t);
+        const bool p_mn = q.mn[0] != 0, q_mn = q.mn[1] != 0, p_boxed = q.boxed[0] != 0, q_boxed = q.boxed[1] != 0;
+        const uint32_t bytes = q.copy_bytes[0] + q.copy_bytes[1];
+        const int32_t q_boxes = static_cast<int32_t>(q.copy_bytes[1] / kBoxBytes);
+        const CUtensorMap *const map_p = &q.map[0], *const map_q = &q.map[1];
         if (shared_ring) {   // the ring was the exchange buffer of the previous item
             if (!first) {
                 if (!lwait(&c->ringfree, item_ph, c, p))
@@ -351,10 +405,10 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
             first = false;
         }
         // first row (column of an MN-major operand) of this CTA's share of each tile, and the group
-        const int32_t p_row = (kForm == kRows ? t.start : 0) + t.p0 + static_cast<int32_t>(half) * kPRows;
-        const int32_t q_row = (kForm == kRowsT ? t.start : 0) + t.q0 + static_cast<int32_t>(half) * (t.n / kPair);
-        const int32_t p_grp = kForm == kRowsT ? t.e : 0, q_grp = kForm == kRows ? t.e : 0;
-        int32_t k = (kForm == kReduce ? t.start : 0) + t.kb0 * kKB;
+        const int32_t p_row = (form == kRows ? t.start : 0) + t.p0 + static_cast<int32_t>(half) * kPRows;
+        const int32_t q_row = (form == kRowsT ? t.start : 0) + t.q0 + static_cast<int32_t>(half) * (t.n / kPair);
+        const int32_t p_grp = form == kRowsT ? t.e : 0, q_grp = form == kRows ? t.e : 0;
+        int32_t k = (form == kReduce ? t.start : 0) + t.kb0 * kKB;
         for (int32_t kb = t.kb0; kb < t.kb1; ++kb, k += kKB) {
             if ((fills & 1u) == which) {
                 if (kPair == 2 && half) {
@@ -366,14 +420,14 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
                     ok = false;
                     break;
                 }
-                const bool masked = masked_rows<kForm>(p, t, kb) != 0;
+                const bool masked = kMasks && masked_rows(form, p, t, kb) != 0;
                 if (masked) {
                     // completes on this CTA's own tail barrier; warp 2 zeroes the rows and completes `full`
                     mbar_arrive_expect_tx(&c->tail[ps], bytes);
                     tail_use |= 1u << ps;
                 } else if (!half) {
                     mbar_arrive_expect_tx(&c->full[ps], kPair * bytes);
-                    if (kForm == kReduce && kPair == 2)
+                    if (kMasks && kPair == 2)
                         mbar_arrive(&c->full[ps]);   // (the count is 2: one per CTA's warp 2 on a masked fill)
                 }
                 if (kPair == 2 && !half)
@@ -394,23 +448,23 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
                         tma_load_4d(dst, m, lb, 0, c1, c2, c3, pol);
                 };
                 if (!p_mn) {
-                    load3(a, &p.map[0], k, p_row, p_grp);
+                    load3(a, map_p, k, p_row, p_grp);
                 } else if (p_boxed) {
-                    load4(a, &p.map[0], k, p_row >> 6, p_grp);
+                    load4(a, map_p, k, p_row >> 6, p_grp);
                 } else {
-                    load3(a, &p.map[0], p_row, k, p_grp);
-                    load3(a + kBoxBytes, &p.map[0], p_row + 64, k, p_grp);
+                    load3(a, map_p, p_row, k, p_grp);
+                    load3(a + kBoxBytes, map_p, p_row + 64, k, p_grp);
                 }
                 if (!q_mn) {
-                    load3(b, &p.map[1], k, q_row, q_grp);
+                    load3(b, map_q, k, q_row, q_grp);
                 } else if (q_boxed) {
-                    load4(b, &p.map[1], k, q_row >> 6, q_grp);
+                    load4(b, map_q, k, q_row >> 6, q_grp);
                 } else {
                     for (int32_t j = 0; j < q_boxes; ++j)
-                        load3(b + j * kBoxBytes, &p.map[1], q_row + 64 * j, k, q_grp);
+                        load3(b + j * kBoxBytes, map_q, q_row + 64 * j, k, q_grp);
                 }
             }
-            if (kForm == kReduce && masked_rows<kForm>(p, t, kb) != 0)
+            if (kMasks && masked_rows(form, p, t, kb) != 0)
                 tail_ph ^= 1u << ps;   // (the other thread's too: the slot's tail barrier counts both)
             ++fills;
             if (++ps == num_pipe) {
@@ -436,36 +490,45 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
 }
 
 // ---------------------------------------------------------------------------------- MMA issuer --
-template <int kForm, int kPair>
+template <int kForm, int kFormB, int kPair>
 __device__ __forceinline__ void l_role_mma(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring,
                                            uint32_t tmem_base)
 {
     if (kPair == 2 && (cluster_ctarank() & 1u))
         return;   // the leader issues for both
     const int32_t num_pipe = p.num_pipe;
-    const uint32_t bn = static_cast<uint32_t>(p.bn);
+    const uint32_t acc_cols = static_cast<uint32_t>(p.acc_cols);
     const uint32_t tfull_peer0 = kPair == 2 ? map_to_rank(&c->tfull[0], cluster_ctarank() | 1u) : 0u;
-    const uint32_t idesc0 = idesc_bf16_f32(kPRows * kPair, 0, p.mn[1] ? 1u : 0u) | (p.mn[0] ? 1u << 15 : 0u);
     const uint32_t base = smem_u32(ring);
+    const uint64_t slot16 = p.slot_bytes >> 4;
+    const int32_t n_items = c->n_items[0], n_items_b = c->n_items[1];
     // K-major: 8-row groups 1024 bytes apart, a 16-deep k step 32 bytes along the row.  MN-major: 64
     // columns x 64 k per box, boxes kBoxBytes apart, a k step 16 rows of 128 bytes.  Slot offsets add to
     // the 14-bit address field in 16-byte units (shared memory is below 2^18 bytes: no carry).
-    const uint64_t pd = p.mn[0] ? smem_desc(base, kBoxBytes, 1024u, 2u) : smem_desc(base, 16u, 1024u, 2u);
-    const uint64_t qd = p.mn[1] ? smem_desc(base + kPBytes, kBoxBytes, 1024u, 2u) : smem_desc(base + kPBytes, 16u, 1024u, 2u);
-    const uint64_t pstep = p.mn[0] ? 128u : 2u, qstep = p.mn[1] ? 128u : 2u;
-    const uint64_t slot16 = p.slot_bytes >> 4;
-    const int32_t n_items = c->n_items;
+    uint32_t idesc0 = 0;
+    uint64_t pd = 0, qd = 0, pstep = 0, qstep = 0;
+    auto describe = [&](const Problem &q) {
+        idesc0 = idesc_bf16_f32(kPRows * kPair, 0, q.mn[1] ? 1u : 0u) | (q.mn[0] ? 1u << 15 : 0u);
+        pd = q.mn[0] ? smem_desc(base, kBoxBytes, 1024u, 2u) : smem_desc(base, 16u, 1024u, 2u);
+        qd = q.mn[1] ? smem_desc(base + kPBytes, kBoxBytes, 1024u, 2u) : smem_desc(base + kPBytes, 16u, 1024u, 2u);
+        pstep = q.mn[0] ? 128u : 2u;
+        qstep = q.mn[1] ? 128u : 2u;
+    };
+    if (kFormB < 0)
+        describe(p.pr[0]);
     int32_t ps = 0;
     uint32_t pph = 0, tiles = 0;
     bool issued = false, ok = true;
-    Walk<kForm, kPair> w(p);
+    Walk<kForm, kFormB, kPair> w(p);
     Tile t;
-    while (w.next(p, g, n_items, t)) {
+    while (w.next(p, g, n_items, n_items_b, t)) {
+        if (kFormB >= 0)
+            describe(problem_of<kFormB>(p, t));
         const uint32_t acc = tiles & 1u;
         if (!lwait(&c->tempty[acc], ((tiles >> 1) & 1u) ^ 1u, c, p, kPair == 2))
             break;
         tc_fence_after();
-        const uint32_t d = tmem_base + acc * bn;
+        const uint32_t d = tmem_base + acc * acc_cols;
         const uint32_t idesc = idesc0 | (static_cast<uint32_t>(t.n) >> 3) << 17;
         uint32_t accum = 0;
         for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
@@ -500,21 +563,21 @@ __device__ __forceinline__ void l_role_mma(const LinearParams &p, LCtrl *c, cons
 }
 
 // ---------------------------------------------------------------- ragged reduction tails (warp 2) --
-template <int kPair>
+template <int kForm, int kFormB, int kPair>
 __device__ __forceinline__ void l_role_mask(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring)
 {
     const int32_t lane = threadIdx.x & 31;
     const int32_t num_pipe = p.num_pipe;
-    const uint32_t boxes = (kPBytes + q_tile_bytes(p.bn / kPair, true)) / kBoxBytes;   // P's two, then Q's
+    const uint32_t boxes = (kPBytes + q_tile_bytes(p.pr[kFormB < 0 ? 0 : 1].bn / kPair, true)) / kBoxBytes;   // P's two, then Q's
     const uint32_t full_lead0 = kPair == 2 ? map_to_rank(&c->full[0], cluster_ctarank() & ~1u) : 0u;
-    const int32_t n_items = c->n_items;
+    const int32_t n_items = c->n_items[0], n_items_b = c->n_items[1];
     uint32_t fills = 0, tail_ph = 0;
-    Walk<kReduce, kPair> w(p);
+    Walk<kForm, kFormB, kPair> w(p);
     Tile t;
-    while (w.next(p, g, n_items, t)) {
+    while (w.next(p, g, n_items, n_items_b, t)) {
         if (t.kb1 <= t.kb0)
             continue;
-        const int32_t zero = masked_rows<kReduce>(p, t, t.kb1 - 1);
+        const int32_t zero = masked_rows(form_of<kForm, kFormB>(t), p, t, t.kb1 - 1);
         fills += static_cast<uint32_t>(t.kb1 - t.kb0);
         if (!zero)
             continue;
@@ -619,7 +682,7 @@ __device__ __forceinline__ void res_stage(const uint4 (&x)[4], uint8_t *stage, i
     __syncwarp();
 }
 
-__device__ __forceinline__ float load_bias(const LinearParams &p, int64_t i)
+__device__ __forceinline__ float load_bias(const Problem &p, int64_t i)
 {
     return p.bias_f32 ? static_cast<const float *>(p.bias)[i]
                       : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.bias)[i]);
@@ -647,7 +710,7 @@ __device__ __forceinline__ void put_bf16(const float (&v)[32], uint8_t *stage, i
 }
 
 template <int kAct, bool kLaneRow>
-__device__ __forceinline__ void finish_chunk(const LinearParams &p, float (&v)[32], uint8_t *stage, const Piece &out, const Piece &zp,
+__device__ __forceinline__ void finish_chunk(const Problem &p, float (&v)[32], uint8_t *stage, const Piece &out, const Piece &zp,
                                              const uint4 (&res)[4], int32_t row_lim, int32_t seg_lim, int32_t lane)
 {
     if (p.z) {
@@ -703,39 +766,38 @@ __device__ __forceinline__ void finish_f32(const float (&v)[32], uint8_t *stage,
     }
 }
 
+// What a warp of the epilogue carries from item to item.
+struct EpiState {
+    int32_t quarter, which, lane;   // TMEM lane quarter (= warp % 4); of its two warps the even or odd chunks
+    uint32_t rank, half;
+    uint8_t *stage, *recv_base;
+    float *bias_s;
+    uint32_t tmem_lanes;            // TMEM address of its lanes
+    uint32_t tempty_lead0;
+    uint32_t tiles;
+    int32_t buf;                    // receive buffer of this item, and how often it was used before (parity)
+    uint32_t buf_ph;
+};
+
+// One tile; false after an abort.
 template <int kForm, int kPair>
-__device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *recv_base,
-                                                uint8_t *stage_all, float *bias_all, uint32_t tmem_base)
+__device__ __forceinline__ bool epilogue_tile(const LinearParams &lp, const Problem &p, LCtrl *c, EpiState &st, const Tile &t)
 {
     constexpr bool kLaneRow = kForm != kRowsT;
-    const int32_t ew = static_cast<int32_t>(threadIdx.x / 32) - 4;
-    const int32_t quarter = ew & 3;            // = warp % 4: the TMEM lanes this warp can read
-    const int32_t which = ew >> 2;             // of the quarter's two warps: even or odd chunks
-    const int32_t lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
-    const uint32_t half = kPair == 2 ? (rank & 1u) : 0u;
-    uint8_t *stage = stage_all + ew * kStageWarpBytes;
-    float *bias_s = bias_all + ew * 32;
-    const int32_t bn = p.bn;
-    const int32_t n_items = c->n_items;
-    const bool splitk = p.split > 1;
-    const int32_t S = splitk ? p.split : 1;
-    const int32_t me = splitk ? static_cast<int32_t>(rank) / kPair : 0;
-    const int32_t nbuf = p.recv_bufs > 0 ? p.recv_bufs : 1;
+    const int32_t quarter = st.quarter, which = st.which, lane = st.lane, buf = st.buf;
+    const uint32_t half = st.half, tiles = st.tiles, buf_ph = st.buf_ph;
+    uint8_t *stage = st.stage;
+    float *bias_s = st.bias_s;
+    const bool splitk = lp.split > 1;
+    const int32_t S = splitk ? lp.split : 1;
+    const int32_t me = splitk ? static_cast<int32_t>(st.rank) / kPair : 0;
+    const int32_t nbuf = lp.recv_bufs > 0 ? lp.recv_bufs : 1;
     auto cta_of = [&](int32_t slice) { return static_cast<uint32_t>(slice * kPair) + half; };   // same half, other slice
-    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t tempty_lead0 = map_to_rank(&c->tempty[0], kPair == 2 ? rank & ~1u : rank);
-    griddep_wait();
-    uint32_t tiles = 0;
-    int32_t buf = 0;           // receive buffer of this item, and how often it was used before (parity)
-    uint32_t buf_ph = 0;
-    Walk<kForm, kPair> w(p);
-    Tile t;
-    while (w.next(p, g, n_items, t)) {
+    {
         const uint32_t acc = tiles & 1u;
         const uint32_t ph = (tiles >> 1) & 1u;
         // the columns of the tile that this CTA finishes
-        const int32_t part = splitk ? ((t.n + S - 1) / S + p.part_align - 1) / p.part_align * p.part_align : t.n;
+        const int32_t part = splitk ? ((t.n + S - 1) / S + lp.part_align - 1) / lp.part_align * lp.part_align : t.n;
         const int32_t c_lo = min(me * part, t.n), c_hi = min(c_lo + part, t.n);
         // This warp's chunks: accumulator columns col .. col + 31 of its lanes, for col = first, first + 64, ...
         const int32_t first = c_lo + 32 * which;
@@ -769,24 +831,24 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
         };
         request_bias(first);
         request_res(first);
-        if (!lwait_warp(&c->tfull[acc], ph, c, p, kPair == 2))
-            return;
+        if (!lwait_warp(&c->tfull[acc], ph, c, lp, kPair == 2))
+            return false;
         tc_fence_after();
-        const uint32_t d = tmem_base + acc * static_cast<uint32_t>(bn) + lane_base;
+        const uint32_t d = st.tmem_lanes + acc * static_cast<uint32_t>(lp.acc_cols);
         const bool have_k = t.kb1 > t.kb0;
-        uint8_t *recv = recv_base + static_cast<uint32_t>(buf) * p.recv_bytes;
+        uint8_t *recv = st.recv_base + static_cast<uint32_t>(buf) * lp.recv_bytes;
         if (splitk) {
             // Wait until the others can receive: with the ring as buffer, until every CTA's MMAs of this
             // item are done; with buffers of their own, until they have read this one's previous content.
-            if (p.recv_bufs == 0) {
+            if (lp.recv_bufs == 0) {
                 if (lane == 0)
                     for (int32_t r = 0; r < S; ++r)
                         mbar_arrive_relaxed_cluster(map_to_rank(&c->rdy[0], cta_of(r)), 1);   // publishes no data
-                if (!lwait_warp(&c->rdy[0], buf_ph, c, p, true))
-                    return;
+                if (!lwait_warp(&c->rdy[0], buf_ph, c, lp, true))
+                    return false;
             } else if (tiles >= static_cast<uint32_t>(nbuf)) {
-                if (!lwait_warp(&c->rdy[buf], buf_ph ^ 1u, c, p, true))
-                    return;
+                if (!lwait_warp(&c->rdy[buf], buf_ph ^ 1u, c, lp, true))
+                    return false;
             }
             // layout: [source][4-column block][128 lanes] float4
             for (int32_t o = 1; o < S; ++o) {
@@ -815,8 +877,8 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                 for (int32_t o = 1; o < S; ++o)
                     mbar_arrive_relaxed_cluster(map_to_rank(&c->got[buf], cta_of((me + o) % S)), 1);
             }
-            if (!lwait_warp(&c->got[buf], buf_ph, c, p, true))
-                return;
+            if (!lwait_warp(&c->got[buf], buf_ph, c, lp, true))
+                return false;
         }
         bool freed = false;
         for (int32_t col = first; col < c_hi; col += 64) {
@@ -841,7 +903,7 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_relaxed_cluster(tempty_lead0 + 8u * acc, 1);
+                    mbar_arrive_relaxed_cluster(st.tempty_lead0 + 8u * acc, 1);
             }
             if (splitk) {
                 const int32_t blocks = min(8, (c_hi - col + 3) / 4);
@@ -918,16 +980,16 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
             request_res(col + 64);
         }
         __syncwarp();
-        if (splitk && p.recv_bufs == 0) {
+        if (splitk && lp.recv_bufs == 0) {
             fence_proxy_async_shared();   // these reads of the ring before the producers' next copies
             __syncwarp();
         }
         if (lane == 0) {
             if (!freed) {
                 tc_fence_before();
-                mbar_arrive_relaxed_cluster(tempty_lead0 + 8u * acc, 1);
+                mbar_arrive_relaxed_cluster(st.tempty_lead0 + 8u * acc, 1);
             }
-            if (splitk && p.recv_bufs == 0) {
+            if (splitk && lp.recv_bufs == 0) {
                 mbar_arrive(&c->ringfree);
             } else if (splitk) {
                 fence_acq_rel_cluster();   // this warp's reads of the buffer before the others' next stores to it
@@ -935,22 +997,60 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
                     mbar_arrive_relaxed_cluster(map_to_rank(&c->rdy[buf], cta_of((me + o) % S)), 1);
             }
         }
-        ++tiles;
-        if (++buf == nbuf) {
-            buf = 0;
-            buf_ph ^= 1u;
+    }
+    ++st.tiles;
+    if (++st.buf == nbuf) {
+        st.buf = 0;
+        st.buf_ph ^= 1u;
+    }
+    return true;
+}
+
+template <int kForm, int kFormB, int kPair>
+__device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *recv_base,
+                                                uint8_t *stage_all, float *bias_all, uint32_t tmem_base)
+{
+    const int32_t ew = static_cast<int32_t>(threadIdx.x / 32) - 4;
+    EpiState st;
+    st.quarter = ew & 3;
+    st.which = ew >> 2;
+    st.lane = threadIdx.x & 31;
+    st.rank = cluster_ctarank();
+    st.half = kPair == 2 ? (st.rank & 1u) : 0u;
+    st.stage = stage_all + ew * kStageWarpBytes;
+    st.recv_base = recv_base;
+    st.bias_s = bias_all + ew * 32;
+    st.tmem_lanes = tmem_base + (static_cast<uint32_t>(st.quarter * 32) << 16);
+    st.tempty_lead0 = map_to_rank(&c->tempty[0], kPair == 2 ? st.rank & ~1u : st.rank);
+    st.tiles = 0;
+    st.buf = 0;
+    st.buf_ph = 0;
+    const int32_t n_items = c->n_items[0], n_items_b = c->n_items[1];
+    griddep_wait();
+    Walk<kForm, kFormB, kPair> w(p);
+    Tile t;
+    while (w.next(p, g, n_items, n_items_b, t)) {
+        if constexpr (kFormB < 0) {
+            if (!epilogue_tile<kForm, kPair>(p, p.pr[0], c, st, t))
+                return;
+        } else if (t.which == 0) {
+            if (!epilogue_tile<kForm, kPair>(p, p.pr[0], c, st, t))
+                return;
+        } else {
+            if (!epilogue_tile<kFormB, kPair>(p, p.pr[1], c, st, t))
+                return;
         }
     }
 }
 
 // --------------------------------------------------------------------------------------- kernel --
-template <int kForm, int kPair>
+template <int kForm, int kFormB, int kPair>
 __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_constant__ LinearParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + (((base + 1023u) & ~1023u) - base);
-    const SmemMap sm(kForm == kRowsT, static_cast<uint32_t>(p.num_pipe) * p.slot_bytes,
+    const SmemMap sm(kForm == kRowsT || kForm == kReduce, static_cast<uint32_t>(p.num_pipe) * p.slot_bytes,
                      static_cast<uint32_t>(p.recv_bufs) * p.recv_bytes);
     LCtrl *c = reinterpret_cast<LCtrl *>(ring + sm.ctrl);
     GroupTab g;
@@ -962,11 +1062,15 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
 
     if (warp == 0) {
         if (lane == 0) {
-            prefetch_tensormap(&p.map[0]);
-            prefetch_tensormap(&p.map[1]);
+            prefetch_tensormap(&p.pr[0].map[0]);
+            prefetch_tensormap(&p.pr[0].map[1]);
+            if (kFormB >= 0) {
+                prefetch_tensormap(&p.pr[1].map[0]);
+                prefetch_tensormap(&p.pr[1].map[1]);
+            }
         }
         for (int32_t i = lane; i < p.num_pipe; i += 32) {
-            mbar_init(&c->full[i], kForm == kReduce ? kPair : 1);
+            mbar_init(&c->full[i], kForm == kReduce || kFormB == kReduce ? kPair : 1);
             mbar_init(&c->empty[i], 1);
             mbar_init(&c->go[i], 1);
             mbar_init(&c->tail[i], 1);
@@ -984,15 +1088,19 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
             }
             mbar_init(&c->ringfree, kEpi);
             c->abort_flag = 0;
-            c->skip = ld_relaxed_gpu_u32(p.status) != 0;     // sticky error: do nothing
+            // a wait that ran out is sticky: do nothing.  (Bad offsets are not: a CTA of this very grid may have just
+            // reported them, and the CTAs of a cluster must agree.)
+            c->skip = ld_relaxed_gpu_u32(p.status) == kStTimeout;
         }
         fence_barrier_init();
     } else if (warp == 1) {
         tmem_alloc_g<kPair>(&c->tmem_base, p.tmem_cols);
         tmem_relinquish_g<kPair>();
     } else if (warp == 2 && !p.offsets) {
-        if (lane == 0)
-            c->n_items = p.dense_items;
+        if (lane == 0) {
+            c->n_items[0] = p.pr[0].dense_items;
+            c->n_items[1] = p.pr[1].dense_items;
+        }
     } else if (warp == 2) {
         griddep_wait();
         // Group tables.  Offsets come from device memory: anything out of order or out of range is
@@ -1008,7 +1116,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
                 bad |= lo != lo0 || hi != hi0;
                 g.start[e] = lo;
                 g.cnt[e] = hi - lo;
-                items = items_of<kForm, kPair>(p, hi - lo);
+                items = items_of<kForm, kPair>(p.pr[0], hi - lo);
             }
             int32_t sum = items;
 #pragma unroll
@@ -1023,17 +1131,18 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
         }
         if (lane == 0) {
             g.base[p.groups] = carry;
-            c->n_items = carry;
+            c->n_items[0] = carry;
+            c->n_items[1] = kFormB >= 0 ? p.groups * items_of<kFormB < 0 ? kForm : kFormB, kPair>(p.pr[1], 0) : 0;
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0)
             atomicCAS(p.status, 0u, kStBadOffsets);
     }
     // a dense product's first tile needs no tables: its coordinates are worked out before the barrier
-    Walk<kForm, kPair> w(p);
+    Walk<kForm, kFormB, kPair> w(p);
     Tile t;
     bool have = false;
     if (!p.offsets && (warp == 0 || warp == 3))
-        have = w.next(p, g, p.dense_items, t);
+        have = w.next(p, g, p.pr[0].dense_items, p.pr[1].dense_items, t);
     tc_fence_before();
     cluster_sync_all();   // barriers initialised before any remote arrival
     tc_fence_after();
@@ -1041,22 +1150,22 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
     if (!c->skip) {
         if (warp == 0) {
             if (p.offsets)
-                have = w.next(p, g, c->n_items, t);
+                have = w.next(p, g, c->n_items[0], c->n_items[1], t);
             if (elect_one())
-                l_role_tma<kForm, kPair>(p, c, g, ring, 0, w, t, have);
+                l_role_tma<kForm, kFormB, kPair>(p, c, g, ring, 0, w, t, have);
         } else if (warp == 1) {
             if (elect_one())
-                l_role_mma<kForm, kPair>(p, c, g, ring, tmem_base);
+                l_role_mma<kForm, kFormB, kPair>(p, c, g, ring, tmem_base);
         } else if (warp == 2) {
-            if (kForm == kReduce && p.offsets)
-                l_role_mask<kPair>(p, c, g, ring);
+            if ((kForm == kReduce || kFormB == kReduce) && p.offsets)
+                l_role_mask<kForm, kFormB, kPair>(p, c, g, ring);
         } else if (warp == 3) {
             if (p.offsets)
-                have = w.next(p, g, c->n_items, t);
+                have = w.next(p, g, c->n_items[0], c->n_items[1], t);
             if (elect_one())
-                l_role_tma<kForm, kPair>(p, c, g, ring, 1, w, t, have);
+                l_role_tma<kForm, kFormB, kPair>(p, c, g, ring, 1, w, t, have);
         } else {
-            l_role_epilogue<kForm, kPair>(p, c, g, ring + (p.recv_bufs ? sm.recv : 0u), ring + sm.stage,
+            l_role_epilogue<kForm, kFormB, kPair>(p, c, g, ring + (p.recv_bufs ? sm.recv : 0u), ring + sm.stage,
                                           reinterpret_cast<float *>(ring + sm.bias), tmem_base);
         }
     }
