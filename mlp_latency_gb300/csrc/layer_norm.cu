@@ -97,9 +97,9 @@ __device__ __forceinline__ void unpack(uint4 x, float (&f)[8])
     }
 }
 
-// Vectors at columns c, c + step, ... below cols.
-template <typename T, int V, int N>
-__device__ __forceinline__ void load_batch(const T *p, int64_t c, int64_t step, int64_t cols, Raw<T, V> (&r)[N])
+// Vectors at columns c, c + step, ... below cols.  (I: int where the width is known to fit.)
+template <typename T, int V, int N, typename I>
+__device__ __forceinline__ void load_batch(const T *p, I c, I step, I cols, Raw<T, V> (&r)[N])
 {
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -132,13 +132,13 @@ __device__ __forceinline__ void store(T *p, const float (&f)[V])
 // gamma or beta: N vectors of V columns at c, c + step, ... below cols (NULL: `none`).  kind: 0 bf16, 1 fp32; + 2:
 // aligned to V of them (at most 16 bytes), read in vectors.  Nothing that a kernel stores is read this way, so these
 // loads may move above stores.
-template <typename U, int V, int N>
-__device__ __forceinline__ void load_w_as(const U *w, int64_t c, int64_t step, int64_t cols, float (&f)[N][V])
+template <typename U, int V, int N, typename I>
+__device__ __forceinline__ void load_w_as(const U *w, I c, I step, I cols, float (&f)[N][V])
 {
     if constexpr (sizeof(U) * V > 16) {   // two loads of half the columns
         float lo[N][V / 2], hi[N][V / 2];
-        load_w_as<U, V / 2, N>(w, c, step, cols, lo);
-        load_w_as<U, V / 2, N>(w + V / 2, c, step, cols - V / 2, hi);
+        load_w_as<U, V / 2, N, I>(w, c, step, cols, lo);
+        load_w_as<U, V / 2, N, I>(w + V / 2, c, step, static_cast<I>(cols - V / 2), hi);
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -158,8 +158,8 @@ __device__ __forceinline__ void load_w_as(const U *w, int64_t c, int64_t step, i
     }
 }
 
-template <typename U, int V, int N>
-__device__ __forceinline__ void load_w_scalar(const U *w, int64_t c, int64_t step, int64_t cols, float (&f)[N][V])
+template <typename U, int V, int N, typename I>
+__device__ __forceinline__ void load_w_scalar(const U *w, I c, I step, I cols, float (&f)[N][V])
 {
     Raw<U, 1> r[N][V] = {};
 #pragma unroll
@@ -178,8 +178,8 @@ __device__ __forceinline__ void load_w_scalar(const U *w, int64_t c, int64_t ste
         }
 }
 
-template <int V, int N>
-__device__ __forceinline__ void load_w(const void *w, int kind, int64_t c, int64_t step, int64_t cols, float none, float (&f)[N][V])
+template <int V, int N, typename I>
+__device__ __forceinline__ void load_w(const void *w, int kind, I c, I step, I cols, float none, float (&f)[N][V])
 {
     if (!w) {
 #pragma unroll
@@ -188,13 +188,13 @@ __device__ __forceinline__ void load_w(const void *w, int kind, int64_t c, int64
             for (int j = 0; j < V; ++j)
                 f[i][j] = none;
     } else if (kind == 2) {
-        load_w_as<__nv_bfloat16, V, N>(static_cast<const __nv_bfloat16 *>(w), c, step, cols, f);
+        load_w_as<__nv_bfloat16, V, N, I>(static_cast<const __nv_bfloat16 *>(w), c, step, cols, f);
     } else if (kind == 3) {
-        load_w_as<float, V, N>(static_cast<const float *>(w), c, step, cols, f);
+        load_w_as<float, V, N, I>(static_cast<const float *>(w), c, step, cols, f);
     } else if (kind == 1) {
-        load_w_scalar<float, V, N>(static_cast<const float *>(w), c, step, cols, f);
+        load_w_scalar<float, V, N, I>(static_cast<const float *>(w), c, step, cols, f);
     } else {
-        load_w_scalar<__nv_bfloat16, V, N>(static_cast<const __nv_bfloat16 *>(w), c, step, cols, f);
+        load_w_scalar<__nv_bfloat16, V, N, I>(static_cast<const __nv_bfloat16 *>(w), c, step, cols, f);
     }
 }
 
@@ -202,7 +202,7 @@ __device__ __forceinline__ void load_w(const void *w, int kind, int64_t c, int64
 template <int V>
 __device__ __forceinline__ void load_w(const void *w, int kind, int64_t c, float none, float (&f)[V])
 {
-    load_w<V, 1>(w, kind, c, 0, c + 1, none, *reinterpret_cast<float(*)[1][V]>(&f));
+    load_w<V, 1, int64_t>(w, kind, c, 0, c + 1, none, *reinterpret_cast<float(*)[1][V]>(&f));
 }
 
 __device__ __forceinline__ float warp_sum(float v)
@@ -843,7 +843,7 @@ __global__ void __launch_bounds__(512) norm_backward_staged_kernel(const NormPar
 {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float scratch[2 * R][16];
-    constexpr int kBatch = R == 1 ? 8 / V : 4 / V;
+    constexpr int kBatch = R == 1 ? 4 : 4 / V;
     const int cols = static_cast<int>(p.cols), c0 = static_cast<int>(threadIdx.x) * V, cstep = static_cast<int>(blockDim.x) * V;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, warps = blockDim.x / 32;
     float *ag = reinterpret_cast<float *>(smem), *ab = ag + cols;   // (a thread touches only its own columns)
