@@ -381,8 +381,8 @@ struct Sum {
     __device__ __forceinline__ float total() const { return kW == 2 ? w[0] + w[kW - 1] : w[0]; }
 };
 
-// ---- sums over a block of at most 512 threads, once per row of a loop.  The scratch (32 floats, zero where a warp
-// is absent) alternates between two halves, so one barrier suffices: no thread can be two rows ahead of another.
+// ---- sums over a block, once per row of a loop.  The scratch (32 floats, zero where a warp is absent) alternates between
+// two halves, so one barrier suffices: no thread can be two rows ahead of another.
 __device__ __forceinline__ void block_sum_init(float (*scratch)[32])
 {
     if (threadIdx.x < 32)
@@ -396,14 +396,10 @@ __device__ __forceinline__ float block_sum(float v, float (*scratch)[32], int pa
     if (lane == 0)
         scratch[parity][warp] = v;
     __syncthreads();
-    v = scratch[parity][lane & 15];
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    return warp_sum(scratch[parity][lane]);
 }
 
-// Two sums at once: after the first exchange the lower half of a warp carries one value and the upper half the
+// Two sums at once, blocks of at most 512 threads: after the first exchange the lower half of a warp carries one value and the upper half the
 // other, so both take one chain of shuffles.
 __device__ __forceinline__ void block_sum2(float &a, float &b, float (*scratch)[32], int parity)
 {
@@ -774,7 +770,7 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormParams
 
 // Forward: the row waits in shared memory in fp32 between its three passes.
 template <typename T, int V>
-__global__ void __launch_bounds__(512) norm_forward_staged_kernel(const NormParams p)
+__global__ void __launch_bounds__(1024) norm_forward_staged_kernel(const NormParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s1[2][32], s2[2][32];
@@ -837,148 +833,165 @@ __global__ void __launch_bounds__(512) norm_forward_staged_kernel(const NormPara
 }
 
 // Backward, R rows at a time: a column's R contributions to dgamma and dbeta are added in registers and then to the
-// block's running sums in shared memory; dx reads its rows a second time (from L2).
+// block's running sums in shared memory; dx reads its rows a second time (from L1 or L2).  Fewer rows than R at the end
+// go one by one.
+struct StagedSums {
+    float *ag, *ab;      // running sums of the block (a thread touches only its own columns) ...
+    float *pg, *pb;      // ... or, with one round per block, the partial row itself
+    bool want, once;
+};
+
+template <typename T, int V, int R>
+__device__ __forceinline__ void backward_rows(const NormParams &p, int64_t row, const StagedSums &q, float (*scratch)[16])
+{
+    constexpr int kBatch = R == 1 ? 4 : 2;
+    const int cols = static_cast<int>(p.cols), c0 = static_cast<int>(threadIdx.x) * V, cstep = static_cast<int>(blockDim.x) * V;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    const T *x[R], *dy[R];
+    float mean[R], rstd[R], s0[R], s1[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        x[r] = static_cast<const T *>(p.x) + (row + r) * p.ldx;
+        dy[r] = static_cast<const T *>(p.dy) + (row + r) * p.lddy;
+        mean[r] = p.mean_in[row + r];
+        rstd[r] = p.rstd_in[row + r];
+        s0[r] = s1[r] = 0.0f;
+    }
+    for (int c = c0; c < cols; c += kBatch * cstep) {
+        Raw<T, V> ra[R][kBatch], rd[R][kBatch];
+        float g[kBatch][V];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            load_batch<T, V, kBatch>(x[r], c, cstep, cols, ra[r]);
+            load_batch<T, V, kBatch>(dy[r], c, cstep, cols, rd[r]);
+        }
+        load_w<V, kBatch>(p.gamma, p.w_kind, c, cstep, cols, 1.0f, g);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (c + i * cstep < cols) {
+                float dg[V], db[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    dg[j] = db[j] = 0.0f;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float a[V], d[V];
+                    unpack<T>(ra[r][i], a);
+                    unpack<T>(rd[r][i], d);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float xh = (a[j] - mean[r]) * rstd[r], gd = g[i][j] * d[j];
+                        db[j] += d[j];
+                        dg[j] = fmaf(d[j], xh, dg[j]);
+                        s0[r] += gd;
+                        s1[r] = fmaf(gd, xh, s1[r]);
+                    }
+                }
+                if (q.want) {
+                    const int k = c + i * cstep;
+                    if (q.once)
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            q.pg[k + j] = dg[j];
+                            q.pb[k + j] = db[j];
+                        }
+                    else
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            q.ag[k + j] += dg[j];
+                            q.ab[k + j] += db[j];
+                        }
+                }
+            }
+    }
+    if (!p.dx)
+        return;
+    __syncthreads();   // the sums of the rows before have been read
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        s0[r] = warp_sum(s0[r]);
+        s1[r] = warp_sum(s1[r]);
+        if (lane == 0) {
+            scratch[2 * r][warp] = s0[r];
+            scratch[2 * r + 1][warp] = s1[r];
+        }
+    }
+    __syncthreads();
+    float m0[R], m1[R];   // dx = rstd g + (m0 + m1 xh)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float u = (lane & 15) < warps ? scratch[2 * r][lane & 15] : 0.0f, w = (lane & 15) < warps ? scratch[2 * r + 1][lane & 15] : 0.0f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            u += __shfl_xor_sync(0xffffffffu, u, o);
+            w += __shfl_xor_sync(0xffffffffu, w, o);
+        }
+        m0[r] = -rstd[r] * p.inv_cols * u;
+        m1[r] = -rstd[r] * p.inv_cols * w;
+    }
+    for (int c = c0; c < cols; c += kBatch * cstep) {
+        Raw<T, V> ra[R][kBatch], rd[R][kBatch], rq[R][kBatch];
+        float g[kBatch][V];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            load_batch<T, V, kBatch>(x[r], c, cstep, cols, ra[r]);
+            load_batch<T, V, kBatch>(dy[r], c, cstep, cols, rd[r]);
+            if (p.add)
+                load_batch<T, V, kBatch>(static_cast<const T *>(p.add) + (row + r) * p.ldadd, c, cstep, cols, rq[r]);
+        }
+        load_w<V, kBatch>(p.gamma, p.w_kind, c, cstep, cols, 1.0f, g);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (c + i * cstep < cols)
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float o[V], a[V], d[V], e[V];
+                    unpack<T>(ra[r][i], a);
+                    unpack<T>(rd[r][i], d);
+                    unpack<T>(rq[r][i], e);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        o[j] = fmaf(g[i][j] * d[j], rstd[r], fmaf((a[j] - mean[r]) * rstd[r], m1[r], m0[r]));
+                        if (p.add)
+                            o[j] += e[j];
+                    }
+                    store<T, V>(static_cast<T *>(p.dx) + (row + r) * p.lddx + c + i * cstep, o);
+                }
+    }
+}
+
 template <typename T, int V, int R>
 __global__ void __launch_bounds__(512) norm_backward_staged_kernel(const NormParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float scratch[2 * R][16];
-    constexpr int kBatch = R == 1 ? 4 : 4 / V;
     const int cols = static_cast<int>(p.cols), c0 = static_cast<int>(threadIdx.x) * V, cstep = static_cast<int>(blockDim.x) * V;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, warps = blockDim.x / 32;
-    float *ag = reinterpret_cast<float *>(smem), *ab = ag + cols;   // (a thread touches only its own columns)
-    const bool sums = p.part != nullptr;
-    const bool once = static_cast<int64_t>(gridDim.x) * R >= p.rows;   // one round per block: no running sums
-    float *pg = p.part + static_cast<int64_t>(blockIdx.x) * 2 * cols, *pb = pg + cols;
+    StagedSums q;
+    q.want = p.part != nullptr;
+    q.once = static_cast<int64_t>(gridDim.x) * R >= p.rows && p.rows % R == 0;
+    q.ag = reinterpret_cast<float *>(smem);
+    q.ab = q.ag + cols;
+    q.pg = p.part + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+    q.pb = q.pg + cols;
     griddep_launch_dependents();   // the finishing kernel waits for this grid by itself
-    if (sums && !once)
+    if (q.want && !q.once)
         for (int c = c0; c < cols; c += cstep)
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                ag[c + j] = ab[c + j] = 0.0f;
+                q.ag[c + j] = q.ab[c + j] = 0.0f;
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * R; row < p.rows; row += static_cast<int64_t>(gridDim.x) * R) {
-        const int n = static_cast<int>(min(p.rows - row, static_cast<int64_t>(R)));
-        const T *x = static_cast<const T *>(p.x) + row * p.ldx, *dy = static_cast<const T *>(p.dy) + row * p.lddy;
-        float mean[R], rstd[R], s0[R], s1[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            mean[r] = p.mean_in[row + min(r, n - 1)];
-            rstd[r] = p.rstd_in[row + min(r, n - 1)];
-            s0[r] = s1[r] = 0.0f;
-        }
-        for (int c = c0; c < cols; c += kBatch * cstep) {
-            Raw<T, V> ra[R][kBatch], rd[R][kBatch];
-            float g[kBatch][V];
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r < n) {
-                    load_batch<T, V, kBatch>(x + r * p.ldx, c, cstep, cols, ra[r]);
-                    load_batch<T, V, kBatch>(dy + r * p.lddy, c, cstep, cols, rd[r]);
-                }
-            load_w<V, kBatch>(p.gamma, p.w_kind, c, cstep, cols, 1.0f, g);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (c + i * cstep < cols) {
-                    float dg[V], db[V];
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        dg[j] = db[j] = 0.0f;
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        if (r < n) {
-                            float a[V], d[V];
-                            unpack<T>(ra[r][i], a);
-                            unpack<T>(rd[r][i], d);
-#pragma unroll
-                            for (int j = 0; j < V; ++j) {
-                                const float xh = (a[j] - mean[r]) * rstd[r], gd = g[i][j] * d[j];
-                                db[j] += d[j];
-                                dg[j] = fmaf(d[j], xh, dg[j]);
-                                s0[r] += gd;
-                                s1[r] = fmaf(gd, xh, s1[r]);
-                            }
-                        }
-                    if (sums) {
-                        if (once)
-#pragma unroll
-                            for (int j = 0; j < V; ++j) {
-                                pg[c + i * cstep + j] = dg[j];
-                                pb[c + i * cstep + j] = db[j];
-                            }
-                        else
-#pragma unroll
-                            for (int j = 0; j < V; ++j) {
-                                ag[c + i * cstep + j] += dg[j];
-                                ab[c + i * cstep + j] += db[j];
-                            }
-                    }
-                }
-        }
-        if (!p.dx)
-            continue;
-        __syncthreads();   // the sums of the rows before have been read
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            s0[r] = warp_sum(s0[r]);
-            s1[r] = warp_sum(s1[r]);
-            if (lane == 0) {
-                scratch[2 * r][warp] = s0[r];
-                scratch[2 * r + 1][warp] = s1[r];
-            }
-        }
-        __syncthreads();
-        float m0[R], m1[R];   // dx = rstd g + (m0 + m1 xh)
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float u = (lane & 15) < warps ? scratch[2 * r][lane & 15] : 0.0f, w = (lane & 15) < warps ? scratch[2 * r + 1][lane & 15] : 0.0f;
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) {
-                u += __shfl_xor_sync(0xffffffffu, u, o);
-                w += __shfl_xor_sync(0xffffffffu, w, o);
-            }
-            m0[r] = -rstd[r] * p.inv_cols * u;
-            m1[r] = -rstd[r] * p.inv_cols * w;
-        }
-        T *dx = static_cast<T *>(p.dx) + row * p.lddx;
-        const T *add = p.add ? static_cast<const T *>(p.add) + row * p.ldadd : nullptr;
-        for (int c = c0; c < cols; c += kBatch * cstep) {
-            Raw<T, V> ra[R][kBatch], rd[R][kBatch], rq[R][kBatch];
-            float g[kBatch][V];
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r < n) {
-                    load_batch<T, V, kBatch>(x + r * p.ldx, c, cstep, cols, ra[r]);
-                    load_batch<T, V, kBatch>(dy + r * p.lddy, c, cstep, cols, rd[r]);
-                    if (add)
-                        load_batch<T, V, kBatch>(add + r * p.ldadd, c, cstep, cols, rq[r]);
-                }
-            load_w<V, kBatch>(p.gamma, p.w_kind, c, cstep, cols, 1.0f, g);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (c + i * cstep < cols)
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        if (r < n) {
-                            float o[V], a[V], d[V], q[V];
-                            unpack<T>(ra[r][i], a);
-                            unpack<T>(rd[r][i], d);
-                            unpack<T>(rq[r][i], q);
-#pragma unroll
-                            for (int j = 0; j < V; ++j) {
-                                o[j] = fmaf(g[i][j] * d[j], rstd[r], fmaf((a[j] - mean[r]) * rstd[r], m1[r], m0[r]));
-                                if (add)
-                                    o[j] += q[j];
-                            }
-                            store<T, V>(dx + r * p.lddx + c + i * cstep, o);
-                        }
-        }
+        if (R == 1 || row + R <= p.rows)
+            backward_rows<T, V, R>(p, row, q, scratch);
+        else
+            for (int64_t r = row; r < p.rows; ++r)
+                backward_rows<T, V, 1>(p, r, q, scratch);
     }
-    if (sums && !once)
+    if (q.want && !q.once)
         for (int c = c0; c < cols; c += cstep)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                pg[c + j] = ag[c + j];
-                pb[c + j] = ab[c + j];
+                q.pg[c + j] = q.ag[c + j];
+                q.pb[c + j] = q.ab[c + j];
             }
 }
 
@@ -1157,10 +1170,12 @@ int ring_items(int64_t nvec, int v)
 
 int ring_threads(int64_t nvec, int items) { return static_cast<int>(cdiv(cdiv(nvec, items), 32) * 32); }
 
-// Threads of the kernels that loop over columns, about `each` vectors apiece.
-int loop_threads(int64_t nvec, int each)
+// Threads of the kernels that loop over columns in rounds of `batch` vectors: as few rounds as `most` threads need, and no
+// more threads than fill those (a round that is mostly past the row's end costs as much as a full one).
+int loop_threads(int64_t nvec, int batch, int most)
 {
-    return static_cast<int>(std::min<int64_t>(512, std::max<int64_t>(64, cdiv(cdiv(nvec, each), 32) * 32)));
+    const int64_t rounds = cdiv(nvec, static_cast<int64_t>(batch) * most);
+    return static_cast<int>(std::max<int64_t>(64, cdiv(cdiv(nvec, rounds * batch), 32) * 32));
 }
 
 // Blocks per SM of the fused backward kernels: small blocks share an SM, wide rows take one each.
@@ -1177,7 +1192,7 @@ int64_t most_fused_blocks(int64_t cols)
     for (int v = 1; v <= 8; v *= 2) {
         const int64_t nvec = cdiv(cols, v);
         if (v <= 2)
-            per_sm = std::max(per_sm, staged_per_sm(loop_threads(nvec, 4), static_cast<size_t>(cols) * 8, 1));
+            per_sm = std::max(per_sm, staged_per_sm(loop_threads(nvec, 4, 512), static_cast<size_t>(cols) * 8, 1));
         else if (const int items = ring_items(nvec, v))
             per_sm = std::max(per_sm, ring_per_sm(ring_threads(nvec, items)));
     }
@@ -1241,12 +1256,12 @@ bool launch_forward_ring(const NormParams &p, int64_t nvec, cudaStream_t st)
 template <typename T, int V>
 bool launch_forward_staged(const NormParams &p, cudaStream_t st)
 {
-    const int threads = loop_threads(cdiv(p.cols, V), 8);
+    const int threads = loop_threads(cdiv(p.cols, V), 8, 1024);
     const size_t smem = static_cast<size_t>(p.cols) * 4;
     auto kernel = norm_forward_staged_kernel<T, V>;
     if (smem > kRingLimit || !allow_smem(kernel, smem))
         return false;
-    const int per_sm = std::max(1, std::min({16, 2048 / threads, static_cast<int>(kRingLimit / smem)}));
+    const int per_sm = std::max(1, std::min({16, 1024 / threads, static_cast<int>(kRingLimit / smem)}));
     kernel<<<static_cast<unsigned>(std::min<int64_t>(p.rows, static_cast<int64_t>(per_sm) * kSms)), threads, smem, st>>>(p);
     return true;
 }
@@ -1318,7 +1333,7 @@ bool backward_staged_r(NormParams &p, int threads, size_t smem, cudaStream_t st)
 template <typename T, int V>
 bool backward_staged(NormParams &p, cudaStream_t st)
 {
-    const int threads = loop_threads(cdiv(p.cols, V), 4);
+    const int threads = loop_threads(cdiv(p.cols, V), 4, 512);
     const size_t smem = p.part ? static_cast<size_t>(p.cols) * 8 : 0;
     if (smem > kRingLimit)
         return false;
