@@ -155,12 +155,13 @@ Estimate estimate_rows(const mlp_linear *h, const Plan &pl, int64_t rows, int64_
     const double fill = (16384.0 + (pl.form == kRows ? q_tile_bytes(pl.bn / pl.pair, w_mn) : n * 128.0 / pl.pair)) / 64.0;
     Estimate e;
     e.tile = static_cast<double>(cdiv(kb, pl.split)) * std::max(mma, fill) + 400.0;
-    // the last epilogue of a CTA is not hidden, nor are the exchanges of a split tile
+    // the last epilogue of a CTA is not hidden, nor are the exchanges of a split tile; clusters start later
     if (pl.split > 1)
-        e.tile += 1500.0 + n * 512.0 * (pl.split - 1) / pl.split / 18.0;
-    const int64_t at_once = h->max_clusters[pl.pair * pl.split];
-    e.work = static_cast<double>(items) * e.tile / static_cast<double>(at_once);
-    e.time = static_cast<double>(cdiv(items, at_once)) * e.tile + 12.0 * n;
+        e.tile += 2500.0 + n * 512.0 * (pl.split - 1) / pl.split / 18.0;
+    const double rounds = static_cast<double>(items) / h->max_clusters[pl.pair * pl.split];
+    e.work = rounds * e.tile;
+    // (tiles of ragged groups differ, so their last round is rarely a full one)
+    e.time = (h->groups > 1 ? std::max(1.0, rounds + 0.3) : std::ceil(rounds)) * e.tile + 12.0 * n + (pl.pair > 1 ? 800.0 : 0.0);
     return e;
 }
 

@@ -396,7 +396,9 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
         const uint32_t bytes = q.copy_bytes[0] + q.copy_bytes[1];
         const int32_t q_boxes = static_cast<int32_t>(q.copy_bytes[1] / kBoxBytes);
         const CUtensorMap *const map_p = &q.map[0], *const map_q = &q.map[1];
-        if (shared_ring) {   // the ring was the exchange buffer of the previous item
+        // The ring was the exchange buffer of the previous item.  (One thread makes all copies then: a thread without a
+        // copy in some item could fall a phase of this barrier behind.)
+        if (shared_ring && which == 0) {
             if (!first) {
                 if (!lwait(&c->ringfree, item_ph, c, p))
                     break;
@@ -410,7 +412,7 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
         const int32_t p_grp = form == kRowsT ? t.e : 0, q_grp = form == kRows ? t.e : 0;
         int32_t k = (form == kReduce ? t.start : 0) + t.kb0 * kKB;
         for (int32_t kb = t.kb0; kb < t.kb1; ++kb, k += kKB) {
-            if ((fills & 1u) == which) {
+            if (shared_ring ? which == 0 : (fills & 1u) == which) {
                 if (kPair == 2 && half) {
                     if (!lwait(&c->go[ps], pph, c, p, true)) {   // the leader armed this fill
                         ok = false;
@@ -479,7 +481,7 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
         // until the final cluster barrier); masked fills complete on each CTA's own.
         for (uint32_t f = fills > num_pipe ? fills - num_pipe : 0u; f < fills; ++f) {
             const uint32_t slot = f % num_pipe;
-            if ((f & 1u) != which)
+            if (shared_ring ? which != 0 : (f & 1u) != which)
                 continue;
             if (tail_use >> slot & 1u)
                 lwait(&c->tail[slot], (tail_ph >> slot & 1u) ^ 1u, c, p, false, true);
@@ -1177,6 +1179,8 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
         tc_fence_after();
         tmem_dealloc_g<kPair>(tmem_base, p.tmem_cols);
     }
+    if (kPair == 2)
+        cluster_sync_all();   // a pair's CTAs free their TMEM together
 }
 
 }  // namespace mlpl
