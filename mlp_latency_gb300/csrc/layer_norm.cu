@@ -764,17 +764,110 @@ __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormParams
 }
 
 // ------------------------------------------------------------------------ rows without 16-byte alignment --
-// Any width and stride, V elements (1, or 2 where rows are in 4-byte units) at a time, in loops over the columns.
-// Each round first requests the loads of kBatch vectors and then works on them: a loop that uses a value where it
-// loads it waits for memory once per vector (one row of 14876 columns took 28 us that way).
+// Any width and stride, in loops over the columns.  Forward, a thread works on two neighbouring bf16 columns or one fp32
+// column at a time (bf16 pairs of a row that starts between two 4-byte words are loaded and stored as halves).  Each
+// round first requests the loads of kBatch vectors and then works on them: a loop that uses a value where it loads it waits for
+// memory once per vector (one row of 14876 columns took 28 us that way).
+template <typename T>
+constexpr int kLoopV = sizeof(T) == 2 ? 2 : 1;
+
+template <typename T>
+__device__ __forceinline__ bool between_words(const void *row) { return sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(row) & 2) != 0; }
+
+// Vectors of a row at columns c, c + step, ... below cols, as they were loaded: a value or a word of two, or the two halves
+// of a pair between words (nothing here uses a loaded value, so all loads go out before any is waited for).  The half of a
+// pair past the row's end is zero.
+struct Loaded {
+    uint32_t a, b;
+};
+
+template <typename T, int N>
+__device__ __forceinline__ void load_row(const T *p, bool split, int c, int step, int cols, Loaded (&r)[N])
+{
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (c + i * step < cols)
+                r[i].a = *reinterpret_cast<const uint32_t *>(p + c + i * step);
+    } else {
+        const unsigned short *h = reinterpret_cast<const unsigned short *>(p);
+        if (!split) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int k = c + i * step;
+                if (k + 1 < cols)
+                    r[i].a = *reinterpret_cast<const uint32_t *>(h + k);
+                else if (k < cols)
+                    r[i].a = h[k];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int k = c + i * step;
+                r[i].b = 0;
+                if (k < cols)
+                    r[i].a = h[k];
+                if (k + 1 < cols)
+                    r[i].b = h[k + 1];
+            }
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack_row(bool split, const Loaded &r, float (&f)[kLoopV<T>])
+{
+    if constexpr (sizeof(T) == 4) {
+        f[0] = __uint_as_float(r.a);
+    } else {
+        f[0] = bf16_lo(r.a);
+        f[1] = split ? bf16_lo(r.b) : bf16_hi(r.a);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_row(T *p, bool split, int k, int cols, const float (&f)[kLoopV<T>])
+{
+    if constexpr (sizeof(T) == 4) {
+        p[k] = f[0];
+    } else {
+        const uint32_t w = pack_bf16(f[0], f[1]);
+        unsigned short *h = reinterpret_cast<unsigned short *>(p);
+        if (!split && k + 1 < cols) {
+            *reinterpret_cast<uint32_t *>(h + k) = w;
+        } else {
+            h[k] = static_cast<unsigned short>(w);
+            if (k + 1 < cols)
+                h[k + 1] = static_cast<unsigned short>(w >> 16);
+        }
+    }
+}
+
+// gamma or beta at those columns.
+template <int V, int N>
+__device__ __forceinline__ void load_w_row(const void *w, int kind, int c, int step, int cols, float none, float (&f)[N][V])
+{
+    if constexpr (V == 1) {
+        load_w<1, N>(w, kind, c, step, cols, none, f);
+    } else {
+        const int pairs = cols & ~1;   // a last single column is read by itself
+        load_w<2, N>(w, kind, c, step, pairs, none, f);
+        if (w && (cols & 1))
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (c + i * step == cols - 1)
+                    f[i][0] = kind & 1 ? __ldg(static_cast<const float *>(w) + cols - 1)
+                                       : __bfloat162float(__ldg(static_cast<const __nv_bfloat16 *>(w) + cols - 1));
+    }
+}
 
 // Forward: the row waits in shared memory in fp32 between its three passes.
-template <typename T, int V>
+template <typename T>
 __global__ void __launch_bounds__(1024) norm_forward_staged_kernel(const NormParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s1[2][32], s2[2][32];
-    constexpr int kBatch = 8;
+    constexpr int kBatch = 8, V = kLoopV<T>;
     float *buf = reinterpret_cast<float *>(smem);
     const int cols = static_cast<int>(p.cols), c0 = static_cast<int>(threadIdx.x) * V, cstep = static_cast<int>(blockDim.x) * V;
     block_sum_init(s1);
@@ -784,31 +877,38 @@ __global__ void __launch_bounds__(1024) norm_forward_staged_kernel(const NormPar
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
         const T *x = static_cast<const T *>(p.x) + row * p.ldx;
         T *y = static_cast<T *>(p.y) + row * p.ldy;
+        const bool sx = between_words<T>(x), sy = between_words<T>(y);
         float s = 0.0f;
         for (int c = c0; c < cols; c += kBatch * cstep) {   // (each thread reads back only what it wrote: no barrier)
-            Raw<T, V> raw[kBatch];
-            load_batch<T, V, kBatch>(x, c, cstep, cols, raw);
+            Loaded raw[kBatch];
+            load_row<T, kBatch>(x, sx, c, cstep, cols, raw);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
                 if (c + i * cstep < cols) {
                     float v[V];
-                    unpack<T>(raw[i], v);
+                    unpack_row<T>(sx, raw[i], v);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
+                    for (int j = 0; j < V; ++j)
                         s += v[j];
-                        buf[c + i * cstep + j] = v[j];
-                    }
+                    if constexpr (V == 2)
+                        *reinterpret_cast<float2 *>(buf + c + i * cstep) = make_float2(v[0], v[1]);
+                    else
+                        buf[c + i * cstep] = v[0];
                 }
         }
         const float mean = __fdiv_rn(block_sum(s, s1, parity), static_cast<float>(cols));
         s = 0.0f;
-#pragma unroll 8
-        for (int c = c0; c < cols; c += cstep)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float d = buf[c + j] - mean;
+#pragma unroll 4
+        for (int c = c0; c < cols; c += cstep) {
+            if constexpr (V == 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(buf + c);
+                const float d = v.x - mean, e = c + 1 < cols ? v.y - mean : 0.0f;
+                s = fmaf(d, d, fmaf(e, e, s));
+            } else {
+                const float d = buf[c] - mean;
                 s = fmaf(d, d, s);
             }
+        }
         const float rstd = rsqrtf(fmaf(block_sum(s, s2, parity), p.inv_cols, p.eps));
         if (threadIdx.x == 0) {
             if (p.mean)
@@ -818,19 +918,22 @@ __global__ void __launch_bounds__(1024) norm_forward_staged_kernel(const NormPar
         }
         for (int c = c0; c < cols; c += kBatch * cstep) {
             float g[kBatch][V], b[kBatch][V], o[V];
-            load_w<V, kBatch>(p.gamma, p.w_kind, c, cstep, cols, 1.0f, g);
-            load_w<V, kBatch>(p.beta, p.w_kind, c, cstep, cols, 0.0f, b);
+            load_w_row<V, kBatch>(p.gamma, p.w_kind, c, cstep, cols, 1.0f, g);
+            load_w_row<V, kBatch>(p.beta, p.w_kind, c, cstep, cols, 0.0f, b);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
                 if (c + i * cstep < cols) {
 #pragma unroll
                     for (int j = 0; j < V; ++j)
                         o[j] = fmaf((buf[c + i * cstep + j] - mean) * rstd, g[i][j], b[i][j]);
-                    store<T, V>(y + c + i * cstep, o);
+                    store_row<T>(y, sy, c + i * cstep, cols, o);
                 }
         }
     }
 }
+
+// (The backward kernels take bf16 in pairs only where rows are in 4-byte units: with pairs between words their loops
+// took twice as long as with single columns.)
 
 // Backward, R rows at a time: a column's R contributions to dgamma and dbeta are added in registers and then to the
 // block's running sums in shared memory; dx reads its rows a second time (from L1 or L2).  Fewer rows than R at the end
@@ -1253,12 +1356,12 @@ bool launch_forward_ring(const NormParams &p, int64_t nvec, cudaStream_t st)
     return true;
 }
 
-template <typename T, int V>
+template <typename T>
 bool launch_forward_staged(const NormParams &p, cudaStream_t st)
 {
-    const int threads = loop_threads(cdiv(p.cols, V), 8, 1024);
-    const size_t smem = static_cast<size_t>(p.cols) * 4;
-    auto kernel = norm_forward_staged_kernel<T, V>;
+    const int threads = loop_threads(cdiv(p.cols, kLoopV<T>), 8, 1024);
+    const size_t smem = static_cast<size_t>((p.cols + 1) & ~int64_t{1}) * 4;
+    auto kernel = norm_forward_staged_kernel<T>;
     if (smem > kRingLimit || !allow_smem(kernel, smem))
         return false;
     const int per_sm = std::max(1, std::min({16, 1024 / threads, static_cast<int>(kRingLimit / smem)}));
@@ -1291,7 +1394,7 @@ void forward_v(const NormParams &p, cudaStream_t st)
             return launch_forward<T, V, 1, 1024>(p, nvec, st);
         if (nvec <= 128)
             return launch_forward<T, V, 4, 512>(p, nvec, st);
-        if (launch_forward_staged<T, V>(p, st))
+        if (launch_forward_staged<T>(p, st))
             return;
     }
     norm_forward_wide_kernel<T><<<static_cast<unsigned>(p.rows), kMaxThreads, 0, st>>>(p);
