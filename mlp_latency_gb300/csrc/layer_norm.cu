@@ -198,6 +198,61 @@ __device__ __forceinline__ void load_w(const void *w, int kind, I c, I step, I c
     }
 }
 
+// The same for columns at any place in a 16-byte word, zero where a column is outside [0, cols): whole words, shifted in
+// registers (single columns took 10 us of a kernel's start).  Vectors whose words are not all inside are read by columns.
+template <typename U, int V, int N>
+__device__ __forceinline__ void load_w_shifted(const U *w, int c, int step, int cols, float (&f)[N][V])
+{
+    constexpr int kOut = V * static_cast<int>(sizeof(U)) / 4, kIn = (kOut + 3) / 4 + 1;   // 4-byte words of a vector; 16-byte words it touches
+    uint4 raw[N][kIn];
+    bool whole[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(w + c + i * step) & ~uintptr_t{15};
+        whole[i] = at >= reinterpret_cast<uintptr_t>(w) && at + 16 * kIn <= reinterpret_cast<uintptr_t>(w + cols);
+#pragma unroll
+        for (int k = 0; k < kIn; ++k)
+            raw[i][k] = whole[i] ? __ldg(reinterpret_cast<const uint4 *>(at) + k) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(w + c + i * step)) & 15;
+        uint32_t q[4 * kIn];
+#pragma unroll
+        for (int k = 0; k < kIn; ++k) {
+            q[4 * k] = raw[i][k].x;
+            q[4 * k + 1] = raw[i][k].y;
+            q[4 * k + 2] = raw[i][k].z;
+            q[4 * k + 3] = raw[i][k].w;
+        }
+#pragma unroll
+        for (int k = 0; k + 2 < 4 * kIn; ++k)
+            q[k] = shift & 8 ? q[k + 2] : q[k];
+#pragma unroll
+        for (int k = 0; k + 1 < 4 * kIn; ++k)
+            q[k] = shift & 4 ? q[k + 1] : q[k];
+#pragma unroll
+        for (int k = 0; k < kOut; ++k) {
+            const uint32_t v = __funnelshift_r(q[k], q[k + 1], (shift & 2) * 8);
+            if constexpr (sizeof(U) == 2) {
+                f[i][2 * k] = bf16_lo(v);
+                f[i][2 * k + 1] = bf16_hi(v);
+            } else {
+                f[i][k] = __uint_as_float(v);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (!whole[i])
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int k = c + i * step + j;
+                if (k >= 0 && k < cols)
+                    f[i][j] = to_f32<U>(__ldg(w + k));
+            }
+}
+
 // One vector.
 template <int V>
 __device__ __forceinline__ void load_w(const void *w, int kind, int64_t c, float none, float (&f)[V])
@@ -244,8 +299,10 @@ struct NormParams {
     float eps, inv_cols;
     int32_t w_f32, w_kind;         // dtype of the weights; how load_w reads them
     float *part;                   // column sums: blocks x 2 x cols
+    int64_t part_ld;               // its row pitch
     int64_t block_rows;
     int32_t blocks;
+    int32_t part_step, part_mask;  // block b's row begins at element (b part_step) & part_mask
 };
 
 // ---- element-wise arithmetic on a vector of V columns: pairs through the two-wide fp32 instructions of
@@ -429,6 +486,12 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// `bytes` of them, and zeros for the rest
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kPending>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory"); }
@@ -436,24 +499,75 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Rows that start or end inside a 16-byte word (kOdd) are handled on the words of memory all the same: the first and the
+// last word of a row are partly another's, are read as zeros there and stored element by element.  The place `o` of a row's
+// first column in its word repeats after at most V rows, and the grid is a multiple of V, so it is the same for all rows of
+// a block and a thread still keeps its columns from row to row.  All arrays share it (their base addresses are multiples of
+// 16 bytes and their row strides are equal modulo V).  The elements before a row that are read lie in the same array: row 0
+// has o = 0.
+
 // kStages slots of `bufs` rows, kItems vectors of V elements (16 bytes) per thread and row.
-template <typename T, int V, int kItems, int kStages>
+template <typename T, int V, int kItems, int kStages, bool kOdd>
 struct RowRing {
     static constexpr int kBytes = 16;
-    static_assert(V * sizeof(T) == 16, "rows in 16-byte units");
+    static_assert(V * sizeof(T) == 16, "words of 16 bytes");
     uint32_t first, last;        // this thread's place in the first and last slot
     uint32_t rd, wr;             // ... in the slot to read and to fill next
     uint32_t item, row, slot;    // strides of vectors, rows and slots
-    int cols, c0, cstep;         // this thread's first column, and the step to its next vector
-    __device__ __forceinline__ RowRing(const void *smem, int bufs, int n_cols) : cols(n_cols)
+    int cols, c0, cstep;         // this thread's first column (-o for thread 0), and the step to its next vector
+    int o;
+    __device__ __forceinline__ RowRing(const void *smem, int bufs, int n_cols, int64_t ld) : cols(n_cols)
     {
+        o = kOdd ? static_cast<int>(blockIdx.x * ld) & (V - 1) : 0;
         item = blockDim.x * kBytes;
         row = item * kItems;
         slot = row * static_cast<uint32_t>(bufs);
         first = rd = wr = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * kBytes;
         last = first + slot * (kStages - 1);
-        c0 = static_cast<int>(threadIdx.x) * V;
+        c0 = static_cast<int>(threadIdx.x) * V - o;
         cstep = static_cast<int>(blockDim.x) * V;
+    }
+    // vector i is partly outside the row / its element j is outside
+    __device__ __forceinline__ bool edge(int i) const { return kOdd && (c0 + i * cstep < 0 || c0 + i * cstep + V > cols); }
+    __device__ __forceinline__ bool outside(int i, int j) const { return static_cast<unsigned>(c0 + i * cstep + j) >= static_cast<unsigned>(cols); }
+    __device__ __forceinline__ void clear_outside(int i, float (&f)[V]) const
+    {
+        if (edge(i))
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (outside(i, j))
+                    f[j] = 0.0f;
+    }
+    // vector i of the row of which p is this thread's first column
+    __device__ __forceinline__ void write(T *p, int i, const float (&f)[V]) const
+    {
+        if (edge(i)) {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (!outside(i, j))
+                    p[i * cstep + j] = from_f32<T>(f[j]);
+        } else {
+            store<T, V>(p + i * cstep, f);
+        }
+    }
+    // gamma or beta at this thread's columns, zero outside the row
+    __device__ __forceinline__ void weights(const void *w, int kind, float none, float (&f)[kItems][V]) const
+    {
+        if constexpr (!kOdd) {
+            load_w<V, kItems>(w, kind, c0, cstep, cols, none, f);
+        } else {
+            if (!w) {
+#pragma unroll
+                for (int i = 0; i < kItems; ++i)
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        f[i][j] = none;
+            } else if (kind & 1) {
+                load_w_shifted<float, V, kItems>(static_cast<const float *>(w), c0, cstep, cols, f);
+            } else {
+                load_w_shifted<__nv_bfloat16, V, kItems>(static_cast<const __nv_bfloat16 *>(w), c0, cstep, cols, f);
+            }
+        }
     }
     __device__ __forceinline__ bool has(int i) const { return c0 + i * cstep < cols; }
     __device__ __forceinline__ void advance(uint32_t &at) const { at = at == last ? first : at + slot; }
@@ -463,8 +577,12 @@ struct RowRing {
         src += c0;
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
-            if (has(i))
-                copy_async(wr + buf * row + i * item, src + i * cstep);
+            if (has(i)) {
+                if constexpr (kOdd)
+                    copy_async(wr + buf * row + i * item, src + i * cstep, min(V, cols - c0 - i * cstep) * static_cast<uint32_t>(sizeof(T)));
+                else
+                    copy_async(wr + buf * row + i * item, src + i * cstep);
+            }
     }
     // vector i of buffer `buf` of the slot to read
     __device__ __forceinline__ void read(int buf, int i, float (&f)[V]) const
@@ -483,16 +601,17 @@ struct RowRing {
                 f[j] = __uint_as_float(w[j]);
             }
         }
+        clear_outside(i, f);
     }
 };
 
 // Forward over many rows.  A thread keeps its columns from row to row, so gamma and beta stay in registers.
-template <typename T, int V, int kItems, int kStages>
+template <typename T, int V, int kItems, int kStages, bool kOdd>
 __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s1[2][32], s2[2][32];
-    RowRing<T, V, kItems, kStages> ring(smem, 1, static_cast<int>(p.cols));
+    RowRing<T, V, kItems, kStages, kOdd> ring(smem, 1, static_cast<int>(p.cols), p.ldx);
     const int64_t step = gridDim.x;
     const T *ahead = static_cast<const T *>(p.x) + blockIdx.x * p.ldx;   // next row to fetch
     T *y = static_cast<T *>(p.y) + blockIdx.x * p.ldy + ring.c0;
@@ -511,8 +630,8 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams
     block_sum_init(s1);
     block_sum_init(s2);
     float g[kItems][V], b[kItems][V];
-    load_w<V, kItems>(p.gamma, p.w_kind, ring.c0, ring.cstep, ring.cols, 1.0f, g);
-    load_w<V, kItems>(p.beta, p.w_kind, ring.c0, ring.cstep, ring.cols, 0.0f, b);
+    ring.weights(p.gamma, p.w_kind, 1.0f, g);
+    ring.weights(p.beta, p.w_kind, 0.0f, b);
     __syncthreads();
     int parity = 0;
     for (int64_t row = blockIdx.x; left > 0; --left, row += step, parity ^= 1) {
@@ -532,6 +651,7 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams
         for (int i = 0; i < kItems; ++i)
             if (ring.has(i)) {
                 fma_s<V>(v[i], v[i], 1.0f, -mean);
+                ring.clear_outside(i, v[i]);
                 sq.fma(v[i], v[i]);
             }
         const float rstd = rsqrtf(fmaf(block_sum(sq.total(), s2, parity), p.inv_cols, p.eps));
@@ -546,7 +666,7 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams
             if (ring.has(i)) {
                 mul_s<V>(v[i], v[i], rstd);
                 fma_v<V>(v[i], v[i], g[i], b[i]);
-                store<T, V>(y + i * ring.cstep, v[i]);
+                ring.write(y, i, v[i]);
             }
         y += step * p.ldy;
     }
@@ -557,14 +677,14 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams
 // keep gamma and, over the row's reduction, g and xh; more columns are read and computed again.  (x rstd -
 // mean rstd would save an instruction, but leaves rounding errors where x = mean.)  The sums of the blocks are added
 // by norm_colsum_finish_kernel.
-template <typename T, int V, int kItems, int kStages>
+template <typename T, int V, int kItems, int kStages, bool kOdd>
 __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float scratch[2][32];
     constexpr bool kKeep = V * kItems <= 16;
     constexpr int kK = kKeep ? kItems : 1;
-    RowRing<T, V, kItems, kStages> ring(smem, p.add ? 3 : 2, static_cast<int>(p.cols));
+    RowRing<T, V, kItems, kStages, kOdd> ring(smem, p.add ? 3 : 2, static_cast<int>(p.cols), p.ldx);
     const int64_t step = gridDim.x;
     const int cols = ring.cols;
     const int64_t r0 = blockIdx.x;
@@ -600,8 +720,20 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
         for (int j = 0; j < V; ++j)
             ag[i][j] = ab[i][j] = 0.0f;
     }
-    if constexpr (kKeep)
-        load_w<V, kItems>(p.gamma, p.w_kind, ring.c0, ring.cstep, cols, 1.0f, gk);
+    // (gamma of more columns: from global memory in vectors; where the columns are shifted, from shared memory behind
+    // the ring, in which each thread lays out its own)
+    float4 *gs = reinterpret_cast<float4 *>(smem + kStages * ring.slot) + threadIdx.x;
+    if constexpr (kKeep) {
+        ring.weights(p.gamma, p.w_kind, 1.0f, gk);
+    } else if constexpr (kOdd) {
+        float w[kItems][V];
+        ring.weights(p.gamma, p.w_kind, 1.0f, w);
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+#pragma unroll
+            for (int j = 0; j < V; j += 4)
+                gs[(i * V + j) / 4 * blockDim.x] = make_float4(w[i][j], w[i][j + 1], w[i][j + 2], w[i][j + 3]);
+    }
     // mean and rstd of 32 rows at a time, a row a lane, the next 32 on their way: one row ahead is not enough for
     // memory under load
     const int lane = static_cast<int>(threadIdx.x & 31);
@@ -636,7 +768,18 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
                 mul_v<V>(go, gk[kKeep ? i : 0], d);
             } else {
                 float w[V];
-                load_w<V>(p.gamma, p.w_kind, ring.c0 + i * ring.cstep, 1.0f, w);
+                if constexpr (kOdd) {
+#pragma unroll
+                    for (int j = 0; j < V; j += 4) {
+                        const float4 q = gs[(i * V + j) / 4 * blockDim.x];
+                        w[j] = q.x;
+                        w[j + 1] = q.y;
+                        w[j + 2] = q.z;
+                        w[j + 3] = q.w;
+                    }
+                } else {
+                    load_w<V>(p.gamma, p.w_kind, ring.c0 + i * ring.cstep, 1.0f, w);
+                }
                 mul_v<V>(go, w, d);
             }
         };
@@ -670,22 +813,22 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
                         ring.read(2, i, r);
                         add_v<V>(o, o, r);
                     }
-                    store<T, V>(dx + i * ring.cstep, o);
+                    ring.write(dx, i, o);
                 }
             dx += step * p.lddx;
         }
         ring.advance(ring.rd);
     }
     if (p.part) {
-        float *out = p.part + r0 * 2 * cols;
+        float *out = p.part + r0 * 2 * p.part_ld;   // (with kOdd its first column is column -o)
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-            const int c = ring.c0 + i * ring.cstep;
+            const int c = ring.c0 + ring.o + i * ring.cstep;
             if (ring.has(i)) {
 #pragma unroll
                 for (int j = 0; j < V; j += 4) {
                     *reinterpret_cast<float4 *>(out + c + j) = make_float4(ag[i][j], ag[i][j + 1], ag[i][j + 2], ag[i][j + 3]);
-                    *reinterpret_cast<float4 *>(out + cols + c + j) = make_float4(ab[i][j], ab[i][j + 1], ab[i][j + 2], ab[i][j + 3]);
+                    *reinterpret_cast<float4 *>(out + p.part_ld + c + j) = make_float4(ab[i][j], ab[i][j + 1], ab[i][j + 2], ab[i][j + 3]);
                 }
             }
         }
@@ -1238,7 +1381,7 @@ __global__ void __launch_bounds__(1024) norm_colsum_finish_kernel(const NormPara
     if (c < p.cols)
 #pragma unroll 8
         for (int b = set; b < p.blocks; b += 32)
-            s += p.part[(static_cast<int64_t>(b) * 2 + w) * p.cols + c];
+            s += p.part[(static_cast<int64_t>(b) * 2 + w) * p.part_ld + c + ((b * p.part_step) & p.part_mask)];
     red[set][lane] = s;
     __syncthreads();
     if (set == 0 && c < p.cols) {
@@ -1257,6 +1400,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int kSms = 152;
 constexpr int kColsumBlocks = 64;     // row blocks of the two-kernel backward pass, at most
+constexpr int64_t kOddLeast = 32;     // words
 constexpr size_t kRingLimit = 200 * 1024;
 constexpr int64_t kFusedCols = kRingLimit / 8;   // its widest rows
 
@@ -1288,17 +1432,20 @@ int staged_per_sm(int threads, size_t smem, int at_a_time)
     return std::max(1, std::min({8, (at_a_time == 1 ? 1536 : 1024) / threads, static_cast<int>(kRingLimit / smem)}));
 }
 
+// Words that a row of `cols` columns touches at most, from the place in its first word on.
+int64_t odd_words(int64_t cols, int v) { return cdiv(cols + v - 1, v); }
+
 // The most blocks that a fused backward kernel uses at this width, over the kinds of alignment.
 int64_t most_fused_blocks(int64_t cols)
 {
     int per_sm = 1;
-    for (int v = 1; v <= 8; v *= 2) {
-        const int64_t nvec = cdiv(cols, v);
-        if (v <= 2)
-            per_sm = std::max(per_sm, staged_per_sm(loop_threads(nvec, 4, 512), static_cast<size_t>(cols) * 8, 1));
-        else if (const int items = ring_items(nvec, v))
-            per_sm = std::max(per_sm, ring_per_sm(ring_threads(nvec, items)));
-    }
+    for (int v = 1; v <= 8; v *= 2)
+        for (const int64_t nvec : {cdiv(cols, v), odd_words(cols, v)}) {
+            if (v <= 2)
+                per_sm = std::max(per_sm, staged_per_sm(loop_threads(nvec, 4, 512), static_cast<size_t>(cols) * 8, 1));
+            else if (const int items = ring_items(nvec, v))
+                per_sm = std::max(per_sm, ring_per_sm(ring_threads(nvec, items)));
+        }
     return static_cast<int64_t>(per_sm) * kSms;
 }
 
@@ -1333,7 +1480,7 @@ void launch_forward(const NormParams &p, int64_t nvec, cudaStream_t st)
     }
 }
 
-template <typename T, int V, int kItems>
+template <typename T, int V, int kItems, bool kOdd>
 bool launch_forward_ring(const NormParams &p, int64_t nvec, cudaStream_t st)
 {
     constexpr int kStages = 3;   // (4 and 5 slots measured no faster at 2048 x 8192)
@@ -1348,7 +1495,8 @@ bool launch_forward_ring(const NormParams &p, int64_t nvec, cudaStream_t st)
     for (int n = most; n >= std::max(1, most / 2); --n)
         if (cdiv(p.rows, static_cast<int64_t>(n) * kSms) * n < cdiv(p.rows, static_cast<int64_t>(per_sm) * kSms) * per_sm)
             per_sm = n;
-    auto kernel = norm_forward_ring_kernel<T, V, kItems, kStages>;
+    static_assert(kSms % V == 0, "rows of a block start at the same place in a word");
+    auto kernel = norm_forward_ring_kernel<T, V, kItems, kStages, kOdd>;
     if (!allow_smem(kernel, smem))
         return false;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.rows, static_cast<int64_t>(per_sm) * kSms));
@@ -1369,6 +1517,19 @@ bool launch_forward_staged(const NormParams &p, cudaStream_t st)
     return true;
 }
 
+// Rows of any width and stride on the words of memory; false where they are too wide (or, many of them, too narrow to fill
+// a block).
+template <typename T>
+bool forward_odd(const NormParams &p, cudaStream_t st)
+{
+    constexpr int V = 16 / sizeof(T), kMost = 32 / V;
+    const int64_t nvec = odd_words(p.cols, V);
+    if (nvec <= kOddLeast)
+        return false;
+    return nvec <= 256 ? launch_forward_ring<T, V, 1, true>(p, nvec, st)
+                       : nvec <= 512 * kMost && launch_forward_ring<T, V, kMost, true>(p, nvec, st);
+}
+
 // Rows in 16-byte units.  Few rows: one vector per thread and one row per block, so that a row's loads go out at once
 // from as many threads as there are.  Many rows: narrow ones a warp each, wide ones through the ring.  Other rows:
 // narrow ones a warp each, wide ones staged.  What fits none of these takes three passes over the row.
@@ -1380,8 +1541,8 @@ void forward_v(const NormParams &p, cudaStream_t st)
     if constexpr (V * sizeof(T) == 16) {
         constexpr int kMost = 32 / V;   // 32 columns a thread
         if (many && nvec > 128 &&
-            ((nvec <= 256 && launch_forward_ring<T, V, 1>(p, nvec, st)) ||
-             (nvec > 256 && nvec <= 512 * kMost && launch_forward_ring<T, V, kMost>(p, nvec, st))))
+            ((nvec <= 256 && launch_forward_ring<T, V, 1, false>(p, nvec, st)) ||
+             (nvec > 256 && nvec <= 512 * kMost && launch_forward_ring<T, V, kMost, false>(p, nvec, st))))
             return;
         if (nvec <= (many ? 32 : 1024))
             return launch_forward<T, V, 1, 1024>(p, nvec, st);
@@ -1400,26 +1561,38 @@ void forward_v(const NormParams &p, cudaStream_t st)
     norm_forward_wide_kernel<T><<<static_cast<unsigned>(p.rows), kMaxThreads, 0, st>>>(p);
 }
 
-template <typename T, int V, int kItems, int kStages>
+template <typename T, int V, int kItems, int kStages, bool kOdd>
 bool launch_backward(const NormParams &p, int threads, size_t smem, cudaStream_t st)
 {
-    auto kernel = norm_backward_kernel<T, V, kItems, kStages>;
+    auto kernel = norm_backward_kernel<T, V, kItems, kStages, kOdd>;
     if (!allow_smem(kernel, smem))
         return false;
     kernel<<<static_cast<unsigned>(p.blocks), threads, smem, st>>>(p);
     return true;
 }
 
-// Rows in 16-byte units through a ring of 4 slots, or 2 where the rows are wide; false where they are too wide.
-template <typename T, int V, int kItems>
+// Through a ring of 4 slots, or 2 where the rows are wide; false where they are too wide.
+template <typename T, int V, int kItems, bool kOdd>
 bool backward_ring(NormParams &p, int64_t nvec, cudaStream_t st)
 {
     const int threads = ring_threads(nvec, kItems);
     p.blocks = static_cast<int32_t>(std::min<int64_t>(p.rows, static_cast<int64_t>(ring_per_sm(threads)) * kSms));
     const size_t slot = static_cast<size_t>(p.add ? 3 : 2) * kItems * threads * 16;
-    if (4 * slot * cdiv(p.blocks, kSms) <= kRingLimit)
-        return launch_backward<T, V, kItems, 4>(p, threads, 4 * slot, st);
-    return 2 * slot <= kRingLimit && launch_backward<T, V, kItems, 2>(p, threads, 2 * slot, st);
+    const size_t more = kOdd && V * kItems > 16 ? static_cast<size_t>(kItems) * threads * V * 4 : 0;   // gamma
+    if ((4 * slot + more) * cdiv(p.blocks, kSms) <= kRingLimit)
+        return launch_backward<T, V, kItems, 4, kOdd>(p, threads, 4 * slot + more, st);
+    return 2 * slot + more <= kRingLimit && launch_backward<T, V, kItems, 2, kOdd>(p, threads, 2 * slot + more, st);
+}
+
+template <typename T, int V, bool kOdd>
+bool backward_rings(NormParams &p, int64_t nvec, cudaStream_t st)
+{
+    const int items = ring_items(nvec, V);
+    if constexpr (V == 4)
+        if (items == 8)
+            return backward_ring<T, V, 8, kOdd>(p, nvec, st);
+    return (items == 1 && backward_ring<T, V, 1, kOdd>(p, nvec, st)) || (items == 2 && backward_ring<T, V, 2, kOdd>(p, nvec, st)) ||
+           (items == 4 && backward_ring<T, V, 4, kOdd>(p, nvec, st));
 }
 
 template <typename T, int V, int R>
@@ -1446,20 +1619,27 @@ bool backward_staged(NormParams &p, cudaStream_t st)
     return four ? backward_staged_r<T, V, 4>(p, threads, smem, st) : backward_staged_r<T, V, 1>(p, threads, smem, st);
 }
 
+template <typename T>
+bool backward_odd(NormParams &p, int64_t ld, cudaStream_t st)
+{
+    constexpr int V = 16 / sizeof(T);
+    const NormParams keep = p;
+    p.part_ld = odd_words(p.cols, V) * V;
+    p.part_step = static_cast<int32_t>(ld & (V - 1));
+    p.part_mask = V - 1;
+    if (odd_words(p.cols, V) > kOddLeast && backward_rings<T, V, true>(p, odd_words(p.cols, V), st))
+        return true;
+    p = keep;
+    return false;
+}
+
 // One kernel for all gradients; false where the rows are too wide for it.
 template <typename T, int V>
 bool backward_v(NormParams &p, cudaStream_t st)
 {
-    if constexpr (V * sizeof(T) == 16) {
-        const int64_t nvec = cdiv(p.cols, V);
-        const int items = ring_items(nvec, V);
-        if constexpr (V == 4)
-            if (items == 8 && backward_ring<T, V, 8>(p, nvec, st))
-                return true;
-        if ((items == 1 && backward_ring<T, V, 1>(p, nvec, st)) || (items == 2 && backward_ring<T, V, 2>(p, nvec, st)) ||
-            (items == 4 && backward_ring<T, V, 4>(p, nvec, st)))
+    if constexpr (V * sizeof(T) == 16)
+        if (backward_rings<T, V, false>(p, cdiv(p.cols, V), st))
             return true;
-    }
     return backward_staged<T, V * sizeof(T) == 16 ? (sizeof(T) == 2 ? 2 : 1) : V>(p, st);
 }
 
@@ -1510,16 +1690,20 @@ extern "C" mlp_status mlp_layernorm_forward(int64_t rows, int64_t cols, const vo
     auto wide = [&](size_t bytes) {
         return static_cast<size_t>(cols) * esz % bytes == 0 && aligned(x, ldx, esz, bytes) && aligned(y, ldy, esz, bytes);
     };
+    const int64_t mod = 16 / static_cast<int64_t>(esz);
+    const bool odd = aligned(x, 0, esz, 16) && aligned(y, 0, esz, 16) && ldx % mod == ldy % mod;
     if (dtype == MLP_DT_BF16) {
         if (wide(16))
             forward_v<__nv_bfloat16, 8>(p, st);
+        else if (odd && forward_odd<__nv_bfloat16>(p, st))
+            ;
         else if (wide(4))
             forward_v<__nv_bfloat16, 2>(p, st);
         else
             forward_v<__nv_bfloat16, 1>(p, st);
     } else if (wide(16)) {
         forward_v<float, 4>(p, st);
-    } else {
+    } else if (!(odd && forward_odd<float>(p, st))) {
         forward_v<float, 1>(p, st);
     }
     return cudaGetLastError() == cudaSuccess ? MLP_OK : MLP_ERR_CUDA;
@@ -1531,7 +1715,7 @@ extern "C" mlp_status mlp_layernorm_workspace_size(int64_t rows, int64_t cols, s
         return MLP_ERR_INVALID_ARG;
     const int64_t blocks = cols <= kFusedCols ? std::min<int64_t>(std::max<int64_t>(rows, kColsumBlocks), std::max<int64_t>(most_fused_blocks(cols), kColsumBlocks))
                                               : kColsumBlocks;
-    *bytes = static_cast<size_t>(blocks) * 2 * static_cast<size_t>(cols) * 4;
+    *bytes = static_cast<size_t>(blocks) * 2 * static_cast<size_t>(cols + 14) * 4;   // (row pitch: at most 14 more)
     return MLP_OK;
 }
 
@@ -1578,11 +1762,18 @@ extern "C" mlp_status mlp_layernorm_backward(int64_t rows, int64_t cols, const v
     p.w_f32 = w_dtype == MLP_DT_F32;
     p.w_kind = p.w_f32 + (aligned(gamma, 0, wsz, 16) ? 2 : 0);
     p.part = want_w ? static_cast<float *>(workspace) : nullptr;
+    p.part_ld = cols;
     auto wide = [&](size_t bytes) {
         return static_cast<size_t>(cols) * esz % bytes == 0 && aligned(x, ldx, esz, bytes) && aligned(dy, lddy, esz, bytes) &&
                aligned(dx, lddx, esz, bytes) && aligned(dx_add, ldadd, esz, bytes);
     };
-    if (dtype == MLP_DT_BF16) {
+    const int64_t mod = 16 / static_cast<int64_t>(esz);
+    const bool odd = !wide(16) && aligned(x, 0, esz, 16) && aligned(dy, 0, esz, 16) && aligned(dx, 0, esz, 16) &&
+                     aligned(dx_add, 0, esz, 16) && ldx % mod == lddy % mod && (!dx || ldx % mod == lddx % mod) &&
+                     (!dx_add || ldx % mod == ldadd % mod);
+    if (odd && (dtype == MLP_DT_BF16 ? backward_odd<__nv_bfloat16>(p, ldx, st) : backward_odd<float>(p, ldx, st))) {
+        // launched
+    } else if (dtype == MLP_DT_BF16) {
         if (!(wide(16) ? backward_v<__nv_bfloat16, 8>(p, st) : wide(4) ? backward_v<__nv_bfloat16, 2>(p, st)
                                                                        : backward_v<__nv_bfloat16, 1>(p, st)))
             wide(16) ? backward_wide<__nv_bfloat16, 8>(p, st) : backward_wide<__nv_bfloat16, 1>(p, st);

@@ -228,3 +228,61 @@ def test_refusals_of_tensors(mc):
         mc.layer_norm_backward(x, x, g, t(4), t(4), y, dgamma=g, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError):
         mc.layer_norm_backward(x, x, g, None, t(4), y)
+
+
+ODD_ROWS = [(700, 300, 300), (1400, 1357, 1357), (400, 5111, 5120), (400, 5111, 5111), (333, 8189, 8195), (310, 11249, 11249),
+            (310, 12001, 12003), (17, 16383, 16383), (9, 16378, 16378), (2, 517, 523)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("R,C,ld", ODD_ROWS)
+@pytest.mark.parametrize("add", [False, True])
+def test_rows_that_start_inside_a_word(mc, R, C, ld, dtype, add):
+    """Many rows whose ends lie inside 16-byte words.  NaN between the rows is neither used nor overwritten, and neither is
+    the row before or after."""
+    x, dy, r_ = draw((R, C), 1, dtype, 2.0, 0.5), draw((R, C), 4, dtype), draw((R, C), 5, dtype)
+    gamma, beta = draw((C,), 2, F32, 0.3, 1.0), draw((C,), 3, F32, 0.3)
+    nan = torch.full((R, C), float("nan"), dtype=dtype)
+    xd, dyd = place(x, ld - C, 0), place(dy, ld - C, 0)
+    y, dx = place(nan, ld - C, 0), place(nan, ld - C, 0)
+    mean, rstd = torch.empty(R, device=DEV), torch.empty(R, device=DEV)
+    mc.layer_norm_forward(xd, gamma.to(DEV), beta.to(DEV), y, mean=mean, rstd=rstd, eps=EPS)
+    want, m, r = ref.norm(f64(x), f64(gamma), f64(beta), EPS)
+    n, rnd = terms(C), 2.0 ** -8 if dtype is BF else 0.0
+    mag = np.abs(f64(x)).mean(1)
+    close(mean, m, n * 2.0 ** -24 * mag + 1e-30, "mean")
+    close(rstd, r, n * 2.0 ** -23 * r * (1 + mag * r), "rstd")
+    err = n * 2.0 ** -23 * (np.abs(want) + np.abs(f64(gamma)) * (1 + mag * r)[:, None] + np.abs(f64(beta)))
+    close(y, want, err * (1 + np.abs(want)) + rnd * np.abs(want), "y")
+    dg, db = torch.empty(C, device=DEV), torch.empty(C, device=DEV)
+    ws = torch.full((mc.layer_norm_workspace_size(R, C),), 0xff, dtype=torch.uint8, device=DEV)
+    mc.layer_norm_backward(dyd, xd, gamma.to(DEV), mean, rstd, dx, dgamma=dg, dbeta=db,
+                           dx_add=place(r_, ld - C, 0) if add else None, workspace=ws)
+    m32, r32 = f64(mean), f64(rstd)
+    want, wg, wb = ref.norm_grad(f64(dy), f64(x), f64(gamma), m32, r32, f64(r_) if add else None)
+    xh = np.abs((f64(x) - m32[:, None]) * r32[:, None])
+    g = np.abs(f64(dy) * f64(gamma))
+    scale = r32[:, None] * (g + g.mean(1, keepdims=True) + (xh + 1) * (g * (xh + 1)).mean(1, keepdims=True))
+    close(dx, want, n * 2.0 ** -23 * (scale + np.abs(want)) + rnd * np.abs(want), "dx")
+    rel = (R + 8) * 2.0 ** -24
+    close(dg, wg, rel * (np.abs(f64(dy)) * (xh + 1)).sum(0), "dgamma")
+    close(db, wb, rel * np.abs(f64(dy)).sum(0), "dbeta")
+    for out in (y, dx):
+        gaps = torch.as_strided(out, (R, ld - C), (ld, 1), C)
+        assert torch.isnan(gaps).all()
+
+
+@pytest.mark.parametrize("R,C", [(700, 1357), (400, 5111), (310, 11249)])
+def test_in_place_rows_that_start_inside_a_word(mc, R, C):
+    """dx over dy, and y over x, where a word holds the end of one row and the start of the next: the same bits as elsewhere."""
+    x, dy = draw((R, C), 1, BF, 2.0, 0.5).to(DEV), draw((R, C), 4, BF).to(DEV)
+    gamma, beta = draw((C,), 2, F32, 0.3, 1.0).to(DEV), draw((C,), 3, F32, 0.3).to(DEV)
+    mean, rstd, y, dx = torch.empty(R, device=DEV), torch.empty(R, device=DEV), torch.empty_like(x), torch.empty_like(x)
+    mc.layer_norm_forward(x, gamma, beta, y, mean=mean, rstd=rstd, eps=EPS)
+    mc.layer_norm_backward(dy, x, gamma, mean, rstd, dx)
+    over = dy.clone()
+    mc.layer_norm_backward(over, x, gamma, mean, rstd, over)
+    assert torch.equal(over, dx)
+    over = x.clone()
+    mc.layer_norm_forward(over, gamma, beta, over, eps=EPS)
+    assert torch.equal(over, y)
