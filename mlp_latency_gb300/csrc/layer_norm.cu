@@ -1400,7 +1400,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int kSms = 152;
 constexpr int kColsumBlocks = 64;     // row blocks of the two-kernel backward pass, at most
-constexpr int64_t kOddLeast = 32;     // words
+constexpr int64_t kOddLeast = 16;     // words
 constexpr size_t kRingLimit = 200 * 1024;
 constexpr int64_t kFusedCols = kRingLimit / 8;   // its widest rows
 
@@ -1425,8 +1425,12 @@ int loop_threads(int64_t nvec, int batch, int most)
     return static_cast<int>(std::max<int64_t>(64, cdiv(cdiv(nvec, rounds * batch), 32) * 32));
 }
 
-// Blocks per SM of the fused backward kernels: small blocks share an SM, wide rows take one each.
-int ring_per_sm(int threads) { return std::max(1, std::min(8, 768 / threads)); }
+// Blocks per SM of the fused backward kernels: as many as its 65536 registers hold (64, 96 or 128 a thread for 4, 8 or
+// more columns).
+int ring_per_sm(int threads, int columns)
+{
+    return std::max(1, std::min(8, 65536 / ((columns <= 4 ? 64 : columns <= 8 ? 96 : 128) * threads)));
+}
 int staged_per_sm(int threads, size_t smem, int at_a_time)
 {
     return std::max(1, std::min({8, (at_a_time == 1 ? 1536 : 1024) / threads, static_cast<int>(kRingLimit / smem)}));
@@ -1444,7 +1448,7 @@ int64_t most_fused_blocks(int64_t cols)
             if (v <= 2)
                 per_sm = std::max(per_sm, staged_per_sm(loop_threads(nvec, 4, 512), static_cast<size_t>(cols) * 8, 1));
             else if (const int items = ring_items(nvec, v))
-                per_sm = std::max(per_sm, ring_per_sm(ring_threads(nvec, items)));
+                per_sm = std::max(per_sm, ring_per_sm(ring_threads(nvec, items), items * v));
         }
     return static_cast<int64_t>(per_sm) * kSms;
 }
@@ -1488,9 +1492,9 @@ bool launch_forward_ring(const NormParams &p, int64_t nvec, cudaStream_t st)
     const size_t smem = static_cast<size_t>(kStages) * kItems * threads * V * sizeof(T);
     if (smem > kRingLimit)
         return false;
-    // Blocks per SM: as many as fit registers (128 a thread) and rings, unless fewer leave the last round fuller
+    // Blocks per SM: as many as fit registers (40, 64 or 128 a thread for 4, 8 or 32 columns) and rings, unless fewer leave the last round fuller
     // (the blocks of an SM share its throughput, so a round of n rows per SM costs n).
-    const int most = std::max(1, std::min({8, 512 / threads, static_cast<int>(kRingLimit / smem)}));
+    const int most = std::max(1, std::min({12, (V * kItems <= 4 ? 1536 : V * kItems <= 8 ? 1024 : 512) / threads, static_cast<int>(kRingLimit / smem)}));
     int per_sm = most;
     for (int n = most; n >= std::max(1, most / 2); --n)
         if (cdiv(p.rows, static_cast<int64_t>(n) * kSms) * n < cdiv(p.rows, static_cast<int64_t>(per_sm) * kSms) * per_sm)
@@ -1576,7 +1580,7 @@ template <typename T, int V, int kItems, bool kOdd>
 bool backward_ring(NormParams &p, int64_t nvec, cudaStream_t st)
 {
     const int threads = ring_threads(nvec, kItems);
-    p.blocks = static_cast<int32_t>(std::min<int64_t>(p.rows, static_cast<int64_t>(ring_per_sm(threads)) * kSms));
+    p.blocks = static_cast<int32_t>(std::min<int64_t>(p.rows, static_cast<int64_t>(ring_per_sm(threads, kItems * V)) * kSms));
     const size_t slot = static_cast<size_t>(p.add ? 3 : 2) * kItems * threads * 16;
     const size_t more = kOdd && V * kItems > 16 ? static_cast<size_t>(kItems) * threads * V * 4 : 0;   // gamma
     if ((4 * slot + more) * cdiv(p.blocks, kSms) <= kRingLimit)
