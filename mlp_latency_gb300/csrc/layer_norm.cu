@@ -302,6 +302,7 @@ struct NormParams {
     int64_t part_ld;               // its row pitch
     int64_t block_rows;
     int32_t blocks;
+    int32_t gamma_smem;            // the backward ring kernel holds it in shared memory
     int32_t part_step, part_mask;  // block b's row begins at element (b part_step) & part_mask
 };
 
@@ -528,7 +529,7 @@ struct RowRing {
         cstep = static_cast<int>(blockDim.x) * V;
     }
     // vector i is partly outside the row / its element j is outside
-    __device__ __forceinline__ bool edge(int i) const { return kOdd && (c0 + i * cstep < 0 || c0 + i * cstep + V > cols); }
+    __device__ __forceinline__ bool edge(int i) const { return kOdd && ((i == 0 && c0 < 0) || c0 + i * cstep + V > cols); }
     __device__ __forceinline__ bool outside(int i, int j) const { return static_cast<unsigned>(c0 + i * cstep + j) >= static_cast<unsigned>(cols); }
     __device__ __forceinline__ void clear_outside(int i, float (&f)[V]) const
     {
@@ -601,7 +602,11 @@ struct RowRing {
                 f[j] = __uint_as_float(w[j]);
             }
         }
-        clear_outside(i, f);
+        if constexpr (kOdd)
+            if (i == 0)   // (the copies put zeros behind the row's end)
+#pragma unroll
+                for (int j = 0; j < V - 1; ++j)
+                    f[j] = c0 + j < 0 ? 0.0f : f[j];
     }
 };
 
@@ -720,12 +725,12 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
         for (int j = 0; j < V; ++j)
             ag[i][j] = ab[i][j] = 0.0f;
     }
-    // (gamma of more columns: from global memory in vectors; where the columns are shifted, from shared memory behind
-    // the ring, in which each thread lays out its own)
+    // gamma of more columns: behind the ring in fp32, where each thread lays out its own (1898 x 11248 58 -> 48 us), or,
+    // without room there, from global memory
     float4 *gs = reinterpret_cast<float4 *>(smem + kStages * ring.slot) + threadIdx.x;
     if constexpr (kKeep) {
         ring.weights(p.gamma, p.w_kind, 1.0f, gk);
-    } else if constexpr (kOdd) {
+    } else if (kOdd || p.gamma_smem) {
         float w[kItems][V];
         ring.weights(p.gamma, p.w_kind, 1.0f, w);
 #pragma unroll
@@ -768,7 +773,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
                 mul_v<V>(go, gk[kKeep ? i : 0], d);
             } else {
                 float w[V];
-                if constexpr (kOdd) {
+                if (kOdd || p.gamma_smem) {
 #pragma unroll
                     for (int j = 0; j < V; j += 4) {
                         const float4 q = gs[(i * V + j) / 4 * blockDim.x];
@@ -1492,9 +1497,10 @@ bool launch_forward_ring(const NormParams &p, int64_t nvec, cudaStream_t st)
     const size_t smem = static_cast<size_t>(kStages) * kItems * threads * V * sizeof(T);
     if (smem > kRingLimit)
         return false;
-    // Blocks per SM: as many as fit registers (40, 64 or 128 a thread for 4, 8 or 32 columns) and rings, unless fewer leave the last round fuller
-    // (the blocks of an SM share its throughput, so a round of n rows per SM costs n).
-    const int most = std::max(1, std::min({12, (V * kItems <= 4 ? 1536 : V * kItems <= 8 ? 1024 : 512) / threads, static_cast<int>(kRingLimit / smem)}));
+    // Blocks per SM: as many as fit registers (40, 64 or 128 a thread for 4, 8 or 32 columns) and rings, unless fewer leave
+    // the last round fuller (the blocks of an SM share its throughput, so a round of n rows per SM costs n).
+    const int most = std::max(1, std::min({12, (V * kItems <= 4 ? 1536 : V * kItems <= 8 ? 1024 : 512) / threads,
+                                            static_cast<int>(kRingLimit / smem)}));
     int per_sm = most;
     for (int n = most; n >= std::max(1, most / 2); --n)
         if (cdiv(p.rows, static_cast<int64_t>(n) * kSms) * n < cdiv(p.rows, static_cast<int64_t>(per_sm) * kSms) * per_sm)
@@ -1530,6 +1536,9 @@ bool forward_odd(const NormParams &p, cudaStream_t st)
     const int64_t nvec = odd_words(p.cols, V);
     if (nvec <= kOddLeast)
         return false;
+    if constexpr (V == 4)   // (8 vectors a thread: 4000 x 2001 22.6 us, 2: 18.4; in bf16 2 instead of 4 gained as often as it lost)
+        if (nvec > 256 && nvec <= 512)
+            return launch_forward_ring<T, V, 2, true>(p, nvec, st);
     return nvec <= 256 ? launch_forward_ring<T, V, 1, true>(p, nvec, st)
                        : nvec <= 512 * kMost && launch_forward_ring<T, V, kMost, true>(p, nvec, st);
 }
@@ -1582,7 +1591,10 @@ bool backward_ring(NormParams &p, int64_t nvec, cudaStream_t st)
     const int threads = ring_threads(nvec, kItems);
     p.blocks = static_cast<int32_t>(std::min<int64_t>(p.rows, static_cast<int64_t>(ring_per_sm(threads, kItems * V)) * kSms));
     const size_t slot = static_cast<size_t>(p.add ? 3 : 2) * kItems * threads * 16;
-    const size_t more = kOdd && V * kItems > 16 ? static_cast<size_t>(kItems) * threads * V * 4 : 0;   // gamma
+    const size_t more = V * kItems > 16 ? static_cast<size_t>(kItems) * threads * V * 4 : 0;   // gamma
+    p.gamma_smem = 2 * slot + more <= kRingLimit;
+    if (!kOdd && !p.gamma_smem)
+        return 2 * slot <= kRingLimit && launch_backward<T, V, kItems, 2, kOdd>(p, threads, 2 * slot, st);
     if ((4 * slot + more) * cdiv(p.blocks, kSms) <= kRingLimit)
         return launch_backward<T, V, kItems, 4, kOdd>(p, threads, 4 * slot + more, st);
     return 2 * slot + more <= kRingLimit && launch_backward<T, V, kItems, 2, kOdd>(p, threads, 2 * slot + more, st);
