@@ -1407,6 +1407,7 @@ constexpr int kSms = 152;
 constexpr int kColsumBlocks = 64;     // row blocks of the two-kernel backward pass, at most
 constexpr int64_t kOddLeast = 16;     // words
 constexpr size_t kRingLimit = 200 * 1024;
+constexpr size_t kAloneLimit = 226 * 1024;       // of a block that has an SM to itself
 constexpr int64_t kFusedCols = kRingLimit / 8;   // its widest rows
 
 // Vectors per thread of the backward ring kernel, for at most 512 threads and 32 columns a thread.  0: too wide.
@@ -1592,12 +1593,13 @@ bool backward_ring(NormParams &p, int64_t nvec, cudaStream_t st)
     p.blocks = static_cast<int32_t>(std::min<int64_t>(p.rows, static_cast<int64_t>(ring_per_sm(threads, kItems * V)) * kSms));
     const size_t slot = static_cast<size_t>(p.add ? 3 : 2) * kItems * threads * 16;
     const size_t more = V * kItems > 16 ? static_cast<size_t>(kItems) * threads * V * 4 : 0;   // gamma
-    p.gamma_smem = 2 * slot + more <= kRingLimit;
+    const size_t limit = p.blocks <= kSms ? kAloneLimit : kRingLimit;
+    p.gamma_smem = 2 * slot + more <= limit;
     if (!kOdd && !p.gamma_smem)
         return 2 * slot <= kRingLimit && launch_backward<T, V, kItems, 2, kOdd>(p, threads, 2 * slot, st);
-    if ((4 * slot + more) * cdiv(p.blocks, kSms) <= kRingLimit)
+    if ((4 * slot + more) * cdiv(p.blocks, kSms) <= limit)
         return launch_backward<T, V, kItems, 4, kOdd>(p, threads, 4 * slot + more, st);
-    return 2 * slot + more <= kRingLimit && launch_backward<T, V, kItems, 2, kOdd>(p, threads, 2 * slot + more, st);
+    return p.gamma_smem && launch_backward<T, V, kItems, 2, kOdd>(p, threads, 2 * slot + more, st);
 }
 
 template <typename T, int V, bool kOdd>
