@@ -1,4 +1,5 @@
-"""Build and load libmlp_chain.so (the CUDA library behind include/mlp_chain.h and mlp_block.h).
+"""Build and load libmlp_chain.so (the CUDA library behind include/mlp_chain.h and mlp_block.h), and
+_marshal.so (the argument checks of block.py, compiled against torch's headers).
 
 The library is compiled in-tree with nvcc for sm_103a only. Loading it never falls back to
 anything else: if the shared object is missing, ``load()`` raises.
@@ -6,9 +7,11 @@ anything else: if the shared object is missing, ``load()`` raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 import tempfile
 import threading
 
@@ -17,6 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libmlp_chain.so")
+MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
+MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("mlp_chain.cu", "host_protocol.cpp", "linear.cu", "layer_norm.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("chain_kernel.cuh", "ptx.cuh", "protocol.h", "dep_groups.h",
                                                      "linear_kernel.cuh")] + [
@@ -29,13 +34,21 @@ NVCC_FLAGS = [
 
 _lock = threading.Lock()
 _lib = None
+_marshal = None
+
+
+def _older(path: str, sources) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(f) > os.path.getmtime(path) for f in sources)
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
-        return True
-    t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(f) > t for f in DEPENDS)
+    return _older(LIB_PATH, DEPENDS) or _older(MARSHAL_PATH, [MARSHAL_SOURCE, os.path.join(INCLUDE, "mlp_block.h")])
+
+
+def _marshal_flags():
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    return (["-I", os.path.join(torch_dir, "include"), "-I", sysconfig.get_paths()["include"]],
+            ["-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -48,6 +61,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             objs = [os.path.join(work, os.path.basename(f) + ".o") for f in SOURCES]
             cmds = [[nvcc, *NVCC_FLAGS, "-I", INCLUDE, "-c", "-o", o, f] for f, o in zip(SOURCES, objs)]
             link = [nvcc, *NVCC_FLAGS, "-shared", "-o", tmp, *objs]
+            compile_flags, link_flags = _marshal_flags()
+            cmds.append([nvcc, *NVCC_FLAGS, *compile_flags, "-shared", "-o", tmp + ".marshal", MARSHAL_SOURCE, *link_flags])
             if verbose:
                 print("\n".join(" ".join(c) for c in cmds + [link]))
             procs = [subprocess.Popen(c) for c in cmds]
@@ -55,6 +70,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 if rc:
                     raise subprocess.CalledProcessError(rc, c)
             subprocess.run(link, check=True)
+            os.replace(tmp + ".marshal", MARSHAL_PATH)
             os.replace(tmp, LIB_PATH)
         finally:
             shutil.rmtree(work, ignore_errors=True)
@@ -159,3 +175,22 @@ def load():
                 fn.argtypes = args
             _lib = lib
     return _lib
+
+
+def load_marshal():
+    """The argument checks of block.py, bound to the loaded library."""
+    global _marshal
+    lib = load()
+    with _lock:
+        if _marshal is None:
+            import torch  # noqa: F401  (the module's symbols are torch's)
+            if not os.path.exists(MARSHAL_PATH):
+                raise RuntimeError(f"{MARSHAL_PATH} is missing: call mlp_latency_gb300.build() first")
+            spec = importlib.util.spec_from_file_location("mlp_latency_gb300._marshal", MARSHAL_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+                "mlp_layernorm_forward", "mlp_layernorm_backward", "mlp_layernorm_workspace_size", "mlp_linear_workspace_size",
+                "mlp_linear_forward", "mlp_linear_backward")))
+            _marshal = module
+    return _marshal

@@ -7,6 +7,7 @@ import subprocess
 
 import numpy as np
 import pytest
+import torch
 
 import block_reference as ref
 import mlp_latency_gb300 as mc
@@ -158,3 +159,19 @@ def test_reference_norm_gradients_against_differences():
         up[i], dn[i] = a[i] + h * U, a[i] - h * U
         num = ((ref.norm(*up, 1e-5)[0] - ref.norm(*dn, 1e-5)[0]) * G).sum() / (2 * h)
         assert abs(num - (got * U).sum()) < 1e-6 * (1 + abs(num))
+
+
+def test_layer_norm_refuses_tensors_before_any_launch(lib):
+    x, w = torch.zeros(2, 8), torch.zeros(8)
+    v = torch.zeros(2)
+    for call, what in ((lambda: mc.layer_norm_forward(x, w, w, x), "x: expected a CUDA tensor"),
+                       (lambda: mc.layer_norm_forward(None, w, w, x), "x is missing"),
+                       (lambda: mc.layer_norm_forward([1.0], w, w, x), "x: expected a tensor"),
+                       (lambda: mc.layer_norm_forward(w, w, w, x), "layer norm takes matrices"),
+                       (lambda: mc.layer_norm_forward(x.int(), w, w, x), "layer norm takes matrices"),
+                       (lambda: mc.layer_norm_forward(x, w.half(), None, x), "layer norm weights are"),
+                       (lambda: mc.layer_norm_backward(None, x, w, v, v, x), "dy is missing")):
+        with pytest.raises(ValueError, match=what):
+            call()
+    with pytest.raises(TypeError):
+        mc.layer_norm_forward(x, w, w)
