@@ -268,6 +268,15 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// First statement of every kernel here: the next launch on the stream may come onto the SMs while this one runs, and
+// this one waits for the one before (which waited for those before it).  A launch then costs its own work and not the
+// start and end of a grid as well.
+__device__ __forceinline__ void take_turn()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Sums of N values over the threads of a row's team (a warp, or the whole block), in a fixed order.
 template <int N, bool kWarpTeam>
 __device__ __forceinline__ void team_sum(float (&v)[N], float *scratch)
@@ -497,8 +506,6 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int kPending>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory"); }
 
-__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Rows that start or end inside a 16-byte word (kOdd) are handled on the words of memory all the same: the first and the
 // last word of a row are partly another's, are read as zeros there and stored element by element.  The place `o` of a row's
@@ -614,6 +621,7 @@ struct RowRing {
 template <typename T, int V, int kItems, int kStages, bool kOdd>
 __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams p)
 {
+    take_turn();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s1[2][32], s2[2][32];
     RowRing<T, V, kItems, kStages, kOdd> ring(smem, 1, static_cast<int>(p.cols), p.ldx);
@@ -685,6 +693,7 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams
 template <typename T, int V, int kItems, int kStages, bool kOdd>
 __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
 {
+    take_turn();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float scratch[2][32];
     constexpr bool kKeep = V * kItems <= 16;
@@ -698,7 +707,6 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
     T *dx = p.dx ? static_cast<T *>(p.dx) + r0 * p.lddx + ring.c0 : nullptr;
     const int mine = static_cast<int>((p.rows - r0 + step - 1) / step);   // rows of this block
     int to_fetch = mine;
-    griddep_launch_dependents();   // the finishing kernel waits for this grid by itself
     // x, dy and add run ahead: they point to the next row to fetch
     auto fetch = [&] {
         if (to_fetch > 0) {
@@ -844,6 +852,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
 template <typename T, int V, int kItems, bool kWarpTeam, int kThreads>
 __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormParams p)
 {
+    take_turn();
     __shared__ float scratch[32];
     const int team = kWarpTeam ? 32 : static_cast<int>(blockDim.x);
     const int t = kWarpTeam ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
@@ -1013,6 +1022,7 @@ __device__ __forceinline__ void load_w_row(const void *w, int kind, int c, int s
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_forward_staged_kernel(const NormParams p)
 {
+    take_turn();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s1[2][32], s2[2][32];
     constexpr int kBatch = 8, V = kLoopV<T>;
@@ -1214,6 +1224,7 @@ __device__ __forceinline__ void backward_rows(const NormParams &p, int64_t row, 
 template <typename T, int V, int R>
 __global__ void __launch_bounds__(512) norm_backward_staged_kernel(const NormParams p)
 {
+    take_turn();
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float scratch[2 * R][16];
     const int cols = static_cast<int>(p.cols), c0 = static_cast<int>(threadIdx.x) * V, cstep = static_cast<int>(blockDim.x) * V;
@@ -1224,7 +1235,6 @@ __global__ void __launch_bounds__(512) norm_backward_staged_kernel(const NormPar
     q.ab = q.ag + cols;
     q.pg = p.part + static_cast<int64_t>(blockIdx.x) * 2 * cols;
     q.pb = q.pg + cols;
-    griddep_launch_dependents();   // the finishing kernel waits for this grid by itself
     if (q.want && !q.once)
         for (int c = c0; c < cols; c += cstep)
 #pragma unroll
@@ -1250,6 +1260,7 @@ __global__ void __launch_bounds__(512) norm_backward_staged_kernel(const NormPar
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads) norm_forward_wide_kernel(const NormParams p)
 {
+    take_turn();
     __shared__ float scratch[32];
     const int64_t row = blockIdx.x;
     const T *x = static_cast<const T *>(p.x) + row * p.ldx;
@@ -1285,6 +1296,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_forward_wide_kernel(const No
 template <typename T, int V>
 __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormParams p)
 {
+    take_turn();
     __shared__ float scratch[64];
     const int64_t row = blockIdx.x;
     const T *x = static_cast<const T *>(p.x) + row * p.ldx;
@@ -1330,6 +1342,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormParams p
 template <typename T, int V>
 __global__ void __launch_bounds__(256) norm_colsum_kernel(const NormParams p)
 {
+    take_turn();
     __shared__ float red[2][8][32 * V];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * V;
@@ -1374,11 +1387,11 @@ __global__ void __launch_bounds__(256) norm_colsum_kernel(const NormParams p)
 // loads are few and go out together), added in a fixed order.
 __global__ void __launch_bounds__(1024) norm_colsum_finish_kernel(const NormParams p, void *dgamma, void *dbeta)
 {
+    take_turn();
     __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, set = threadIdx.x / 32;
     const int w = blockIdx.y;
     void *out = w ? dbeta : dgamma;
-    griddep_wait();
     if (!out)
         return;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
@@ -1478,15 +1491,32 @@ bool bad_rows(const void *p, int64_t ld, int64_t cols, size_t esz)
     return !p || reinterpret_cast<uintptr_t>(p) % esz != 0 || ld < cols;
 }
 
+// (see take_turn)
+template <typename... A, typename... B>
+void launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, B... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, A(args)...);
+}
+
 template <typename T, int V, int kItems, int kThreads>
 void launch_forward(const NormParams &p, int64_t nvec, cudaStream_t st)
 {
     if (nvec <= 32 * kItems) {
         const int teams = 4;
-        norm_forward_kernel<T, V, kItems, true, 128><<<static_cast<unsigned>(cdiv(p.rows, teams)), 32 * teams, 0, st>>>(p);
+        launch(norm_forward_kernel<T, V, kItems, true, 128>, static_cast<unsigned>(cdiv(p.rows, teams)), 32 * teams, 0, st, p);
     } else {
         const int threads = static_cast<int>(cdiv(cdiv(nvec, kItems), 32) * 32);
-        norm_forward_kernel<T, V, kItems, false, kThreads><<<static_cast<unsigned>(p.rows), threads, 0, st>>>(p);
+        launch(norm_forward_kernel<T, V, kItems, false, kThreads>, static_cast<unsigned>(p.rows), threads, 0, st, p);
     }
 }
 
@@ -1511,7 +1541,7 @@ bool launch_forward_ring(const NormParams &p, int64_t nvec, cudaStream_t st)
     if (!allow_smem(kernel, smem))
         return false;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.rows, static_cast<int64_t>(per_sm) * kSms));
-    kernel<<<grid, threads, smem, st>>>(p);
+    launch(kernel, grid, threads, smem, st, p);
     return true;
 }
 
@@ -1524,7 +1554,7 @@ bool launch_forward_staged(const NormParams &p, cudaStream_t st)
     if (smem > kRingLimit || !allow_smem(kernel, smem))
         return false;
     const int per_sm = std::max(1, std::min({16, 1024 / threads, static_cast<int>(kRingLimit / smem)}));
-    kernel<<<static_cast<unsigned>(std::min<int64_t>(p.rows, static_cast<int64_t>(per_sm) * kSms)), threads, smem, st>>>(p);
+    launch(kernel, static_cast<unsigned>(std::min<int64_t>(p.rows, static_cast<int64_t>(per_sm) * kSms)), threads, smem, st, p);
     return true;
 }
 
@@ -1572,7 +1602,7 @@ void forward_v(const NormParams &p, cudaStream_t st)
         if (launch_forward_staged<T>(p, st))
             return;
     }
-    norm_forward_wide_kernel<T><<<static_cast<unsigned>(p.rows), kMaxThreads, 0, st>>>(p);
+    launch(norm_forward_wide_kernel<T>, static_cast<unsigned>(p.rows), kMaxThreads, 0, st, p);
 }
 
 template <typename T, int V, int kItems, int kStages, bool kOdd>
@@ -1581,7 +1611,7 @@ bool launch_backward(const NormParams &p, int threads, size_t smem, cudaStream_t
     auto kernel = norm_backward_kernel<T, V, kItems, kStages, kOdd>;
     if (!allow_smem(kernel, smem))
         return false;
-    kernel<<<static_cast<unsigned>(p.blocks), threads, smem, st>>>(p);
+    launch(kernel, static_cast<unsigned>(p.blocks), threads, smem, st, p);
     return true;
 }
 
@@ -1619,7 +1649,7 @@ bool backward_staged_r(NormParams &p, int threads, size_t smem, cudaStream_t st)
     auto kernel = norm_backward_staged_kernel<T, V, R>;
     if (!allow_smem(kernel, smem))
         return false;
-    kernel<<<static_cast<unsigned>(p.blocks), threads, smem, st>>>(p);
+    launch(kernel, static_cast<unsigned>(p.blocks), threads, smem, st, p);
     return true;
 }
 
@@ -1668,9 +1698,9 @@ void backward_wide(NormParams &p, cudaStream_t st)
     p.block_rows = std::max<int64_t>(cdiv(p.rows, kColsumBlocks), 8);
     p.blocks = static_cast<int32_t>(cdiv(p.rows, p.block_rows));
     if (p.part)
-        norm_colsum_kernel<T, V><<<dim3(static_cast<unsigned>(cdiv(p.cols, 32 * V)), static_cast<unsigned>(p.blocks)), 256, 0, st>>>(p);
+        launch(norm_colsum_kernel<T, V>, dim3(static_cast<unsigned>(cdiv(p.cols, 32 * V)), static_cast<unsigned>(p.blocks)), 256, 0, st, p);
     if (p.dx)
-        norm_dx_kernel<T, V><<<static_cast<unsigned>(p.rows), kMaxThreads, 0, st>>>(p);
+        launch(norm_dx_kernel<T, V>, static_cast<unsigned>(p.rows), kMaxThreads, 0, st, p);
 }
 
 }  // namespace
@@ -1799,17 +1829,7 @@ extern "C" mlp_status mlp_layernorm_backward(int64_t rows, int64_t cols, const v
         wide(16) ? backward_wide<float, 4>(p, st) : backward_wide<float, 1>(p, st);
     }
     if (want_w && cudaPeekAtLastError() == cudaSuccess) {
-        // launched while the kernel before it still runs; it waits for that one's results by itself
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.gridDim = dim3(static_cast<unsigned>(cdiv(cols, 32)), 2);
-        cfg.blockDim = dim3(1024);
-        cfg.stream = st;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        cudaLaunchKernelEx(&cfg, norm_colsum_finish_kernel, p, dgamma, dbeta);
+        launch(norm_colsum_finish_kernel, dim3(static_cast<unsigned>(cdiv(cols, 32)), 2), 1024, 0, st, p, dgamma, dbeta);
     }
     return cudaGetLastError() == cudaSuccess ? MLP_OK : MLP_ERR_CUDA;
 }
