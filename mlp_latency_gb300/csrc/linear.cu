@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const GradParams p)
 {
     __shared__ float red[8][kStrip];
     griddep_launch_dependents();
+    griddep_wait();   // launched while the kernel before it runs, as all kernels here are
     const int32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int32_t col = blockIdx.x * kStrip + lane * 8;
     const bool col_ok = col < p.N;
@@ -706,28 +707,22 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         g.part = dbias ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part) : nullptr;
         g.dbias = dbias;
         g.bias_f32 = bias_esz == 4;
-        const dim3 grid(static_cast<unsigned>(cdiv(N, kStrip)), static_cast<unsigned>(g.blocks));
-        switch (h->d.activation) {
-        case MLP_ACT_RELU: act_grad_kernel<kActRelu><<<grid, 256, 0, st>>>(g); break;
-        case MLP_ACT_GELU_TANH: act_grad_kernel<kActGelu><<<grid, 256, 0, st>>>(g); break;
-        case MLP_ACT_SILU: act_grad_kernel<kActSilu><<<grid, 256, 0, st>>>(g); break;
-        default: act_grad_kernel<kActNone><<<grid, 256, 0, st>>>(g); break;
-        }
-        if (cudaGetLastError() != cudaSuccess)
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(cdiv(N, kStrip)), static_cast<unsigned>(g.blocks));
+        cfg.blockDim = dim3(256);
+        cfg.stream = st;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        void (*const kernels[])(GradParams) = {act_grad_kernel<kActNone>, act_grad_kernel<kActRelu>, act_grad_kernel<kActGelu>,
+                                               act_grad_kernel<kActSilu>};
+        if (cudaLaunchKernelEx(&cfg, kernels[h->d.activation], g) != cudaSuccess)
             return MLP_ERR_CUDA;
-        if (dbias) {
-            cudaLaunchConfig_t cfg = {};
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-            attr[0].val.programmaticStreamSerializationAllowed = 1;
-            cfg.gridDim = dim3(static_cast<unsigned>(cdiv(N, 256)), static_cast<unsigned>(h->groups));
-            cfg.blockDim = dim3(256);
-            cfg.stream = st;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            if (cudaLaunchKernelEx(&cfg, bias_grad_kernel, g) != cudaSuccess)
-                return MLP_ERR_CUDA;
-        }
+        cfg.gridDim = dim3(static_cast<unsigned>(cdiv(N, 256)), static_cast<unsigned>(h->groups));
+        if (dbias && cudaLaunchKernelEx(&cfg, bias_grad_kernel, g) != cudaSuccess)
+            return MLP_ERR_CUDA;
     }
     if (!dX && !dW)
         return MLP_OK;
