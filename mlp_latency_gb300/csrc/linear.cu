@@ -391,66 +391,92 @@ struct GradParams {
     int32_t rows, N, groups, block_rows, blocks;
     const int32_t *offsets;
     float *part;                // (blocks + groups) x N column sums, or null
-    void *dbias;
-    int32_t bias_f32;
 };
 
-__device__ __forceinline__ void group_range(const GradParams &p, int32_t e, int32_t &lo, int32_t &hi)
+// Rows of group e of the offsets `off` (device or shared memory; null: one group), clamped to the matrix.
+__device__ __forceinline__ void group_range(const int32_t *off, int32_t rows, int32_t e, int32_t &lo, int32_t &hi)
 {
-    lo = p.offsets ? min(max(p.offsets[e], 0), p.rows) : 0;
-    hi = p.offsets ? min(max(p.offsets[e + 1], lo), p.rows) : p.rows;
+    lo = off ? min(max(off[e], 0), rows) : 0;
+    hi = off ? min(max(off[e + 1], lo), rows) : rows;
 }
 
 // One CTA: a block of rows x 256 columns.  Memory-bound: reads dY and Z once, writes dZ once; the column
 // sums stay in registers and leave as one fp32 row per (block, group) pair.  Blocks and groups are both
-// ascending ranges, so block + group numbers those pairs without collisions.
+// ascending ranges, so block + group numbers those pairs without collisions.  Rows are requested 32 at a time whatever
+// groups they belong to (a group at a time, 25 rows of 7 groups took 5 us longer).
 template <int kAct>
 __global__ void __launch_bounds__(256) act_grad_kernel(const GradParams p)
 {
     __shared__ float red[8][kStrip];
+    __shared__ int32_t off_s[MLP_MAX_EXPERTS + 1];
     griddep_launch_dependents();
     griddep_wait();   // launched while the kernel before it runs, as all kernels here are
     const int32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int32_t col = blockIdx.x * kStrip + lane * 8;
     const bool col_ok = col < p.N;
     const int32_t b_lo = blockIdx.y * p.block_rows, b_hi = min(b_lo + p.block_rows, p.rows);
+    const int32_t *off = nullptr;
     int32_t e = 0;
     if (p.offsets) {   // first group that ends past the block's start
+        for (int32_t i = threadIdx.x; i <= p.groups; i += 256)
+            off_s[i] = p.offsets[i];
+        __syncthreads();
+        off = off_s;
         int32_t lo = 0, hi = p.groups;
         while (lo < hi) {
             const int32_t mid = (lo + hi) / 2;
-            if (p.offsets[mid + 1] > b_lo)
+            if (off[mid + 1] > b_lo)
                 hi = mid;
             else
                 lo = mid + 1;
         }
         e = lo;
     }
-    for (; e < p.groups; ++e) {
-        int32_t g_lo, g_hi;
-        group_range(p, e, g_lo, g_hi);
-        if (g_lo >= b_hi)
-            break;
-        const int32_t lo = max(g_lo, b_lo), hi = min(g_hi, b_hi);
-        if (lo >= hi)
-            continue;
-        float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    auto flush = [&] {   // the sums of group e over this block's rows
+        if (p.part) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                red[warp][lane * 8 + j] = acc[j];
+            __syncthreads();
+            const int32_t c = blockIdx.x * kStrip + threadIdx.x;
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+                s += red[w][threadIdx.x];
+            if (c < p.N)
+                p.part[static_cast<int64_t>(blockIdx.y + e) * p.N + c] = s;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            acc[j] = 0.0f;
+    };
+    int32_t g_lo = 0, g_hi = 0;
+    for (int32_t r0 = b_lo; r0 < b_hi && e < p.groups; r0 += 32) {
+        const int32_t end = min(r0 + 32, b_hi);
+        // all loads before any store: the stores of one row could be the loads of the next for all the compiler knows
+        uint4 dyv[4], zv[4];
         if (col_ok) {
-            // four rows a round, all of their loads first: the stores of one could be the loads of the next for all
-            // the compiler knows
-            for (int32_t r = lo + warp; r < hi; r += 32) {
-                uint4 dyv[4], zv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int32_t q = min(r0 + warp + 8 * i, end - 1);
+                dyv[i] = __ldg(reinterpret_cast<const uint4 *>(p.dy + q * p.ld_dy + col));
+                if (kAct != kActNone)
+                    zv[i] = __ldg(reinterpret_cast<const uint4 *>(p.z + q * p.ld_z + col));
+            }
+        }
+        for (; e < p.groups; ++e) {
+            group_range(off, p.rows, e, g_lo, g_hi);
+            if (g_lo >= end)
+                break;
+            if (col_ok) {
+                const int32_t lo = max(g_lo, r0), hi = min(g_hi, end);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int32_t q = min(r + 8 * i, hi - 1);
-                    dyv[i] = __ldg(reinterpret_cast<const uint4 *>(p.dy + q * p.ld_dy + col));
-                    if (kAct != kActNone)
-                        zv[i] = __ldg(reinterpret_cast<const uint4 *>(p.z + q * p.ld_z + col));
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (r + 8 * i >= hi)
-                        break;
+                    const int32_t r = r0 + warp + 8 * i;
+                    if (r < lo || r >= hi)
+                        continue;
                     const uint32_t dw[4] = {dyv[i].x, dyv[i].y, dyv[i].z, dyv[i].w};
                     uint32_t zw[4] = {0u, 0u, 0u, 0u};
                     if (kAct != kActNone) {
@@ -469,49 +495,27 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const GradParams p)
                         ow[j] = pack2(g0, g1);
                     }
                     if (kAct != kActNone && p.dz)
-                        *reinterpret_cast<uint4 *>(p.dz + static_cast<int64_t>(r + 8 * i) * p.N + col) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+                        *reinterpret_cast<uint4 *>(p.dz + static_cast<int64_t>(r) * p.N + col) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
                 }
             }
-        }
-        if (p.part) {
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                red[warp][lane * 8 + j] = acc[j];
-            __syncthreads();
-            const int32_t c = blockIdx.x * kStrip + threadIdx.x;
-            float s = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w)
-                s += red[w][threadIdx.x];
-            if (c < p.N)
-                p.part[static_cast<int64_t>(blockIdx.y + e) * p.N + c] = s;
+            if (g_hi > end)
+                break;   // it goes on
+            if (g_hi > max(g_lo, b_lo))
+                flush();
         }
     }
+    if (e < p.groups && g_lo < b_hi && g_hi > b_hi)
+        flush();   // it goes on in the next block
 }
 
-// dbias[e, :]: the partial rows of the blocks that hold rows of group e, in block order.
-__global__ void __launch_bounds__(256) bias_grad_kernel(const GradParams p)
+// dbias where no product is asked for that would add the sums on its way.
+__global__ void __launch_bounds__(256) bias_grad_kernel(const BiasSums q, const int32_t *offsets, int32_t rows)
 {
-    const int32_t c = blockIdx.x * 256 + threadIdx.x, e = blockIdx.y;
-    griddep_wait();   // launched while act_grad_kernel runs
     griddep_launch_dependents();
-    if (c >= p.N)
-        return;
+    griddep_wait();
     int32_t lo, hi;
-    group_range(p, e, lo, hi);
-    float s = 0.0f;
-    if (hi > lo) {
-        const int32_t b1 = (hi - 1) / p.block_rows;
-#pragma unroll 8
-        for (int32_t b = lo / p.block_rows; b <= b1; ++b)
-            s += p.part[static_cast<int64_t>(b + e) * p.N + c];
-    }
-    const int64_t o = static_cast<int64_t>(e) * p.N + c;
-    if (p.bias_f32)
-        static_cast<float *>(p.dbias)[o] = s;
-    else
-        static_cast<__nv_bfloat16 *>(p.dbias)[o] = __float2bfloat16_rn(s);
+    group_range(offsets, rows, blockIdx.y, lo, hi);
+    add_bias_sums(q, blockIdx.y, blockIdx.x * 256 + threadIdx.x, lo, hi);
 }
 
 // Rows per block: about four CTAs per SM, at least 16 rows (two per warp).
@@ -684,6 +688,7 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         return MLP_ERR_CUDA;
     const void *dz = dY;
     int64_t ld_dz = lddy;
+    BiasSums bias = {};
     if ((act && (dX || dW)) || dbias) {
         size_t part, total;
         workspace_layout(h, rows, &part, &total);
@@ -705,8 +710,7 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         g.blocks = static_cast<int32_t>(cdiv(rows, g.block_rows));
         g.offsets = offsets;
         g.part = dbias ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part) : nullptr;
-        g.dbias = dbias;
-        g.bias_f32 = bias_esz == 4;
+        bias = BiasSums{g.part, dbias, g.N, g.block_rows, bias_esz == 4};
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -721,7 +725,7 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         if (cudaLaunchKernelEx(&cfg, kernels[h->d.activation], g) != cudaSuccess)
             return MLP_ERR_CUDA;
         cfg.gridDim = dim3(static_cast<unsigned>(cdiv(N, 256)), static_cast<unsigned>(h->groups));
-        if (dbias && cudaLaunchKernelEx(&cfg, bias_grad_kernel, g) != cudaSuccess)
+        if (dbias && !dX && !dW && cudaLaunchKernelEx(&cfg, bias_grad_kernel, bias, offsets, g.rows) != cudaSuccess)
             return MLP_ERR_CUDA;
     }
     if (!dX && !dW)
@@ -731,6 +735,7 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
     std::memset(&p, 0, sizeof(p));
     p.offsets = offsets;
     p.rows = static_cast<int32_t>(rows);
+    p.bias = bias;
     // dX[m, k] = sum_n dZ[m, n] W(k, n): W stored K x N has the reduction inside
     auto input_grad = [&](const Plan &pl) {
         p.pr[0].out = dX;
@@ -752,6 +757,7 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         const mlp_status r = items ? launch(h, p, px, nullptr, items, st) : MLP_ERR_CUDA;
         if (r != MLP_OK)
             return r;
+        p.bias.out = nullptr;   // done
     }
     if (dW) {
         std::memset(p.pr, 0, sizeof(p.pr));

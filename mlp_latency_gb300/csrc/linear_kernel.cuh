@@ -76,8 +76,16 @@ struct Problem {
     int64_t ld_out, ld_res, ld_z;   // row strides in elements
 };
 
+// The bias gradient: partial rows of column sums, one per (block of rows, group) pair at block + group, to be added.
+struct BiasSums {
+    const float *part;
+    void *out;                      // groups x N, or null
+    int32_t N, block_rows, f32;
+};
+
 struct LinearParams {
     Problem pr[2];
+    BiasSums bias;                  // added by the epilogue warps before their first tile
     const int32_t *offsets;         // device, groups + 1 entries, or null: one group of `rows` rows
     int32_t groups, rows;
     int32_t acc_cols;               // TMEM columns of one accumulator
@@ -1008,6 +1016,25 @@ __device__ __forceinline__ bool epilogue_tile(const LinearParams &lp, const Prob
     return true;
 }
 
+// out[e, c]: the partial rows of the blocks that hold rows lo .. hi - 1 (those of group e), in block order.
+__device__ __forceinline__ void add_bias_sums(const BiasSums &q, int32_t e, int32_t c, int32_t lo, int32_t hi)
+{
+    if (c >= q.N)
+        return;
+    float s = 0.0f;
+    if (hi > lo) {
+        const int32_t b1 = (hi - 1) / q.block_rows;
+#pragma unroll 8
+        for (int32_t b = lo / q.block_rows; b <= b1; ++b)
+            s += q.part[static_cast<int64_t>(b + e) * q.N + c];
+    }
+    const int64_t o = static_cast<int64_t>(e) * q.N + c;
+    if (q.f32)
+        static_cast<float *>(q.out)[o] = s;
+    else
+        static_cast<__nv_bfloat16 *>(q.out)[o] = __float2bfloat16_rn(s);
+}
+
 template <int kForm, int kFormB, int kPair>
 __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *recv_base,
                                                 uint8_t *stage_all, float *bias_all, uint32_t tmem_base)
@@ -1029,6 +1056,13 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
     st.buf_ph = 0;
     const int32_t n_items = c->n_items[0], n_items_b = c->n_items[1];
     griddep_wait();
+    if (p.bias.out) {   // (while the first tile's products run: a launch of its own took 3 us)
+        const int32_t strips = (p.bias.N + kEpi * 32 - 1) / (kEpi * 32), todo = strips * p.groups;
+        for (int32_t i = static_cast<int32_t>(blockIdx.x); i < todo; i += static_cast<int32_t>(gridDim.x)) {
+            const int32_t e = i / strips, lo = p.offsets ? g.start[e] : 0;
+            add_bias_sums(p.bias, e, (i - e * strips) * kEpi * 32 + ew * 32 + st.lane, lo, p.offsets ? lo + g.cnt[e] : p.rows);
+        }
+    }
     Walk<kForm, kFormB, kPair> w(p);
     Tile t;
     while (w.next(p, g, n_items, n_items_b, t)) {
