@@ -386,8 +386,8 @@ constexpr int kStrip = 256;    // columns per CTA: 32 lanes x 8
 
 struct GradParams {
     const __nv_bfloat16 *dy, *z;
-    __nv_bfloat16 *dz;          // rows x N contiguous, or null
-    int64_t ld_dy, ld_z;
+    __nv_bfloat16 *dz;          // or null
+    int64_t ld_dy, ld_z, ld_dz;
     int32_t rows, N, groups, block_rows, blocks;
     const int32_t *offsets;
     float *part;                // (blocks + groups) x N column sums, or null
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const GradParams p)
                         ow[j] = pack2(g0, g1);
                     }
                     if (kAct != kActNone && p.dz)
-                        *reinterpret_cast<uint4 *>(p.dz + static_cast<int64_t>(r) * p.N + col) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+                        *reinterpret_cast<uint4 *>(p.dz + r * p.ld_dz + col) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
                 }
             }
             if (g_hi > end)
@@ -525,6 +525,9 @@ int32_t grad_block_rows(const mlp_linear *h, int64_t rows)
     const int64_t blocks = std::max<int64_t>(1, cdiv(4 * h->num_sms, strips));
     return static_cast<int32_t>(std::max<int64_t>(16, cdiv(cdiv(rows, blocks), 8) * 8));
 }
+
+// Row pitch of dZ: its rows start on 128-byte lines, without which every copy of 64 columns takes two requests to L2.
+int64_t dz_pitch(int64_t N) { return (N + 63) & ~int64_t{63}; }
 
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
@@ -612,7 +615,7 @@ extern "C" mlp_status mlp_linear_destroy(mlp_linear_t h)
 // dZ, then the partial column sums.
 static void workspace_layout(const mlp_linear *h, int64_t rows, size_t *part, size_t *total)
 {
-    const size_t dz = h->d.activation == MLP_ACT_NONE ? 0 : align256(static_cast<size_t>(rows) * h->d.N * 2);
+    const size_t dz = h->d.activation == MLP_ACT_NONE ? 0 : align256(static_cast<size_t>(rows) * dz_pitch(h->d.N) * 2);
     const int64_t blocks = cdiv(rows, grad_block_rows(h, rows));
     *part = dz;
     *total = dz + align256(static_cast<size_t>(blocks + h->groups) * h->d.N * 4);
@@ -701,7 +704,7 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         if (act && (dX || dW)) {
             g.dz = static_cast<__nv_bfloat16 *>(workspace);
             dz = workspace;
-            ld_dz = N;
+            ld_dz = g.ld_dz = dz_pitch(N);
         }
         g.rows = static_cast<int32_t>(rows);
         g.N = static_cast<int32_t>(N);
