@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const GradParams p)
                         acc[2 * j + 1] += g1;
                         ow[j] = pack2(g0, g1);
                     }
-                    if (kAct != kActNone && p.dz)
+                    if (p.dz)
                         *reinterpret_cast<uint4 *>(p.dz + r * p.ld_dz + col) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
                 }
             }
@@ -528,6 +528,10 @@ int32_t grad_block_rows(const mlp_linear *h, int64_t rows)
 
 // Row pitch of dZ: its rows start on 128-byte lines, without which every copy of 64 columns takes two requests to L2.
 int64_t dz_pitch(int64_t N) { return (N + 63) & ~int64_t{63}; }
+
+// Without an activation dZ is dY.  Where the bias gradient reads dY anyway, a copy of it whose rows start on those lines
+// pays for itself in the products of many rows.
+bool copies_dy(const mlp_linear *h, int64_t rows) { return h->d.activation == MLP_ACT_NONE && h->d.N % 64 != 0 && rows >= 256; }
 
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
@@ -615,7 +619,7 @@ extern "C" mlp_status mlp_linear_destroy(mlp_linear_t h)
 // dZ, then the partial column sums.
 static void workspace_layout(const mlp_linear *h, int64_t rows, size_t *part, size_t *total)
 {
-    const size_t dz = h->d.activation == MLP_ACT_NONE ? 0 : align256(static_cast<size_t>(rows) * dz_pitch(h->d.N) * 2);
+    const size_t dz = h->d.activation == MLP_ACT_NONE && !copies_dy(h, rows) ? 0 : align256(static_cast<size_t>(rows) * dz_pitch(h->d.N) * 2);
     const int64_t blocks = cdiv(rows, grad_block_rows(h, rows));
     *part = dz;
     *total = dz + align256(static_cast<size_t>(blocks + h->groups) * h->d.N * 4);
@@ -701,7 +705,7 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         g.ld_dy = lddy;
         g.z = static_cast<const __nv_bfloat16 *>(Z);
         g.ld_z = ldz;
-        if (act && (dX || dW)) {
+        if ((act || copies_dy(h, rows)) && (dX || dW)) {
             g.dz = static_cast<__nv_bfloat16 *>(workspace);
             dz = workspace;
             ld_dz = g.ld_dz = dz_pitch(N);
