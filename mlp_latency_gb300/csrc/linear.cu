@@ -405,7 +405,7 @@ __device__ __forceinline__ void group_range(const int32_t *off, int32_t rows, in
 // ascending ranges, so block + group numbers those pairs without collisions.  Rows are requested 32 at a time whatever
 // groups they belong to (a group at a time, 25 rows of 7 groups took 5 us longer).
 template <int kAct>
-__global__ void __launch_bounds__(256) act_grad_kernel(const GradParams p)
+__global__ void __launch_bounds__(256, 4) act_grad_kernel(const GradParams p)
 {
     __shared__ float red[8][kStrip];
     __shared__ int32_t off_s[MLP_MAX_EXPERTS + 1];
