@@ -1383,34 +1383,65 @@ __global__ void __launch_bounds__(256) norm_colsum_kernel(const NormParams p)
     }
 }
 
-// dgamma and dbeta: the blocks' partial rows.  32 columns per block, 32 interleaved sets of rows (a column's
-// loads are few and go out together), added in a fixed order.
-__global__ void __launch_bounds__(1024) norm_colsum_finish_kernel(const NormParams p, void *dgamma, void *dbeta)
+// dgamma and dbeta: the blocks' partial rows, added in a fixed order.  Latency is all there is to it (10 MB from L2 for
+// 152 rows of 8192), so L = 8 threads of a warp take a row (32 where the rows are few and blocks would be many), a block
+// 256 / L interleaved sets of rows, and a thread requests 8 rows at once: V = 4 columns each where the rows are in 16-byte
+// units, else one.  (One thread a column and 32 rows a block of 1024 threads: 3 us longer at 152 x 8192.)
+template <int V, int L>
+__global__ void __launch_bounds__(256) norm_colsum_finish_kernel(const NormParams p, void *dgamma, void *dbeta)
 {
+    __shared__ float red[8][L * V];
     take_turn();
-    __shared__ float red[32][33];
-    const int lane = threadIdx.x & 31, set = threadIdx.x / 32;
+    constexpr int kBatch = 8, kSets = 256 / L;
+    const int lane = threadIdx.x & (L - 1), set = threadIdx.x / L;
     const int w = blockIdx.y;
     void *out = w ? dbeta : dgamma;
     if (!out)
         return;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-    float s = 0.0f;
-    if (c < p.cols)
-#pragma unroll 8
-        for (int b = set; b < p.blocks; b += 32)
-            s += p.part[(static_cast<int64_t>(b) * 2 + w) * p.part_ld + c + ((b * p.part_step) & p.part_mask)];
-    red[set][lane] = s;
-    __syncthreads();
-    if (set == 0 && c < p.cols) {
-        s = 0.0f;
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) * L + lane) * V;
+    float s[V];
 #pragma unroll
-        for (int q = 0; q < 32; ++q)
-            s += red[q][lane];
+    for (int j = 0; j < V; ++j)
+        s[j] = 0.0f;
+    if (c < p.cols)
+        for (int b0 = set; b0 < p.blocks; b0 += kSets * kBatch) {
+            Raw<float, V> r[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int b = b0 + kSets * i;
+                if (b < p.blocks)
+                    r[i] = *reinterpret_cast<const Raw<float, V> *>(p.part + (static_cast<int64_t>(b) * 2 + w) * p.part_ld + c +
+                                                                    ((b * p.part_step) & p.part_mask));
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (b0 + kSets * i < p.blocks) {
+                    float x[V];
+                    unpack<float>(r[i], x);
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        s[j] += x[j];
+                }
+        }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+        for (int o = L; o < 32; o *= 2)
+            s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+        if ((threadIdx.x & 31) < L)
+            red[threadIdx.x / 32][lane * V + j] = s[j];
+    }
+    __syncthreads();
+    const int64_t k = static_cast<int64_t>(blockIdx.x) * L * V + threadIdx.x;
+    if (threadIdx.x < L * V && k < p.cols) {
+        float t = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            t += red[q][threadIdx.x];
         if (p.w_f32)
-            static_cast<float *>(out)[c] = s;
+            static_cast<float *>(out)[k] = t;
         else
-            static_cast<__nv_bfloat16 *>(out)[c] = __float2bfloat16_rn(s);
+            static_cast<__nv_bfloat16 *>(out)[k] = __float2bfloat16_rn(t);
     }
 }
 
@@ -1829,7 +1860,12 @@ extern "C" mlp_status mlp_layernorm_backward(int64_t rows, int64_t cols, const v
         wide(16) ? backward_wide<float, 4>(p, st) : backward_wide<float, 1>(p, st);
     }
     if (want_w && cudaPeekAtLastError() == cudaSuccess) {
-        launch(norm_colsum_finish_kernel, dim3(static_cast<unsigned>(cdiv(cols, 32)), 2), 1024, 0, st, p, dgamma, dbeta);
+        if (cols % 4 == 0 && p.part_ld % 4 == 0 && p.part_step == 0)
+            launch(norm_colsum_finish_kernel<4, 8>, dim3(static_cast<unsigned>(cdiv(cols, 32)), 2), 256, 0, st, p, dgamma, dbeta);
+        else if (p.blocks <= 64)
+            launch(norm_colsum_finish_kernel<1, 32>, dim3(static_cast<unsigned>(cdiv(cols, 32)), 2), 256, 0, st, p, dgamma, dbeta);
+        else
+            launch(norm_colsum_finish_kernel<1, 8>, dim3(static_cast<unsigned>(cdiv(cols, 8)), 2), 256, 0, st, p, dgamma, dbeta);
     }
     return cudaGetLastError() == cudaSuccess ? MLP_OK : MLP_ERR_CUDA;
 }
