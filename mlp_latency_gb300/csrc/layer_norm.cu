@@ -199,7 +199,7 @@ __device__ __forceinline__ void load_w(const void *w, int kind, I c, I step, I c
 }
 
 // The same for columns at any place in a 16-byte word, zero where a column is outside [0, cols): whole words, shifted in
-// registers (single columns took 10 us of a kernel's start).  Vectors whose words are not all inside are read by columns.
+// registers (read by single columns, 2000 x 5111 took 4 us longer).  Vectors whose words are not all inside are read by columns.
 template <typename U, int V, int N>
 __device__ __forceinline__ void load_w_shifted(const U *w, int c, int step, int cols, float (&f)[N][V])
 {
@@ -618,6 +618,8 @@ struct RowRing {
 };
 
 // Forward over many rows.  A thread keeps its columns from row to row, so gamma and beta stay in registers.
+// 2048 x 8192 bf16: 14.1 us, 4.8 TB/s of read and written bytes; its first loads and last stores bound so short a kernel.
+// Rows inside words: 2000 x 5111 15.7 us.
 template <typename T, int V, int kItems, int kStages, bool kOdd>
 __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams p)
 {
@@ -689,7 +691,8 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams
 // columns from row to row), so x and dy are read once for all three gradients.  Up to 16 columns a thread also
 // keep gamma and, over the row's reduction, g and xh; more columns are read and computed again.  (x rstd -
 // mean rstd would save an instruction, but leaves rounding errors where x = mean.)  The sums of the blocks are added
-// by norm_colsum_finish_kernel.
+// by norm_colsum_finish_kernel.  4096 x 8192 bf16 with dx_add: 43 us, 6.2 TB/s, of 48 with the finish; the issue of
+// instructions (53 % of cycles) and memory come close to each other.
 template <typename T, int V, int kItems, int kStages, bool kOdd>
 __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
 {
@@ -733,7 +736,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
         for (int j = 0; j < V; ++j)
             ag[i][j] = ab[i][j] = 0.0f;
     }
-    // gamma of more columns: behind the ring in fp32, where each thread lays out its own (1898 x 11248 58 -> 48 us), or,
+    // gamma of more columns: behind the ring in fp32, where each thread lays out its own (1898 x 11248 58 -> 45 us), or,
     // without room there, from global memory
     float4 *gs = reinterpret_cast<float4 *>(smem + kStages * ring.slot) + threadIdx.x;
     if constexpr (kKeep) {
@@ -848,7 +851,8 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
     }
 }
 
-// One row per team, the row in registers (kItems vectors of V per thread): moments, then the output.
+// One row per team, the row in registers (kItems vectors of V per thread): moments, then the output.  For few rows
+// or narrow ones: latency (one row of 4096 4.2 us, back to back 2.2 by the host).
 template <typename T, int V, int kItems, bool kWarpTeam, int kThreads>
 __global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormParams p)
 {
@@ -1018,7 +1022,8 @@ __device__ __forceinline__ void load_w_row(const void *w, int kind, int c, int s
     }
 }
 
-// Forward: the row waits in shared memory in fp32 between its three passes.
+// Forward: the row waits in shared memory in fp32 between its three passes.  For arrays whose rows start at different
+// places in their words: 2000 x 5111 30.5 us, bound by the issue of narrow loads and stores.
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_forward_staged_kernel(const NormParams p)
 {
@@ -1095,7 +1100,7 @@ __global__ void __launch_bounds__(1024) norm_forward_staged_kernel(const NormPar
 
 // Backward, R rows at a time: a column's R contributions to dgamma and dbeta are added in registers and then to the
 // block's running sums in shared memory; dx reads its rows a second time (from L1 or L2).  Fewer rows than R at the end
-// go one by one.
+// go one by one.  2000 x 5111 47 us, bound by the issue of loads of single columns.
 struct StagedSums {
     float *ag, *ab;      // running sums of the block (a thread touches only its own columns) ...
     float *pg, *pb;      // ... or, with one round per block, the partial row itself
@@ -1256,7 +1261,8 @@ __global__ void __launch_bounds__(512) norm_backward_staged_kernel(const NormPar
             }
 }
 
-// Rows too wide for registers and shared memory: three passes over the row (the later ones come from L2).
+// Rows too wide for registers and shared memory: three passes over the row (the later ones come from L2).  256 x 40000
+// bf16: 49 us, bound by its narrow loads; such rows are here to be right.
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads) norm_forward_wide_kernel(const NormParams p)
 {
@@ -1292,7 +1298,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_forward_wide_kernel(const No
 }
 
 // dx of one row per block: two sums over the row, then the output; the row is read twice (the second
-// time from L1 or L2), so any width fits.
+// time from L1 or L2), so any width fits.  256 x 40000 bf16: 16 us.
 template <typename T, int V>
 __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormParams p)
 {
@@ -1338,7 +1344,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_dx_kernel(const NormParams p
     }
 }
 
-// Column sums of dy xh and dy over one block of rows: 32 lanes x V columns, 8 warps over the rows.
+// Column sums of dy xh and dy over one block of rows: 32 lanes x V columns, 8 warps over the rows.  256 x 40000 bf16:
+// 27 us, bound by the latency of few rows a thread.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) norm_colsum_kernel(const NormParams p)
 {
@@ -1449,7 +1456,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int kSms = 152;
 constexpr int kColsumBlocks = 64;     // row blocks of the two-kernel backward pass, at most
-constexpr int64_t kOddLeast = 16;     // words
+constexpr int64_t kOddLeast = 16;     // words a row (forward_odd)
 constexpr size_t kRingLimit = 200 * 1024;
 constexpr size_t kAloneLimit = 226 * 1024;       // of a block that has an SM to itself
 constexpr int64_t kFusedCols = kRingLimit / 8;   // its widest rows
@@ -1589,8 +1596,8 @@ bool launch_forward_staged(const NormParams &p, cudaStream_t st)
     return true;
 }
 
-// Rows of any width and stride on the words of memory; false where they are too wide (or, many of them, too narrow to fill
-// a block).
+// Rows of any width and stride on the words of memory (2000 x 5111 18 us, staged 31); false where they are too wide, or
+// too narrow: up to 16 words a row the kernels for other rows are as fast (8000 x 71 8 us, through the ring 14).
 template <typename T>
 bool forward_odd(const NormParams &p, cudaStream_t st)
 {
@@ -1606,8 +1613,8 @@ bool forward_odd(const NormParams &p, cudaStream_t st)
 }
 
 // Rows in 16-byte units.  Few rows: one vector per thread and one row per block, so that a row's loads go out at once
-// from as many threads as there are.  Many rows: narrow ones a warp each, wide ones through the ring.  Other rows:
-// narrow ones a warp each, wide ones staged.  What fits none of these takes three passes over the row.
+// from as many threads as there are.  Many rows: narrow ones a warp each, wide ones through the ring.  Other rows
+// (those that forward_odd leaves): narrow ones a warp each, wide ones staged.  What fits none of these takes three passes over the row.
 template <typename T, int V>
 void forward_v(const NormParams &p, cudaStream_t st)
 {

@@ -403,7 +403,8 @@ __device__ __forceinline__ void group_range(const int32_t *off, int32_t rows, in
 // One CTA: a block of rows x 256 columns.  Memory-bound: reads dY and Z once, writes dZ once; the column
 // sums stay in registers and leave as one fp32 row per (block, group) pair.  Blocks and groups are both
 // ascending ranges, so block + group numbers those pairs without collisions.  Rows are requested 32 at a time whatever
-// groups they belong to (a group at a time, 25 rows of 7 groups took 5 us longer).
+// groups they belong to (a group at a time, 25 rows of 7 groups took 5 us longer).  4000 x 4096 gelu, 32 groups: 24.6 us,
+// 4.0 TB/s; the exponentials and divisions take two thirds of the issue slots.
 template <int kAct>
 __global__ void __launch_bounds__(256, 4) act_grad_kernel(const GradParams p)
 {

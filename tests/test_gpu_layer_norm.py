@@ -286,3 +286,33 @@ def test_in_place_rows_that_start_inside_a_word(mc, R, C):
     over = x.clone()
     mc.layer_norm_forward(over, gamma, beta, over, eps=EPS)
     assert torch.equal(over, y)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("R,C", [(5, 300), (400, 1357), (320, 5111), (3, 16379)])
+def test_arrays_whose_rows_start_at_different_places(mc, R, C, dtype):
+    """The same results, up to rounding, as for arrays of equal strides."""
+    x, dy, r_ = draw((R, C), 1, dtype, 2.0, 0.5), draw((R, C), 4, dtype), draw((R, C), 5, dtype)
+    gamma, beta = draw((C,), 2, BF, 0.3, 1.0), draw((C,), 3, BF, 0.3)
+    nan = torch.full((R, C), float("nan"), dtype=dtype)
+    y, dx = place(nan, 3, 0), place(nan, 2, 1)
+    mean, rstd = torch.empty(R, device=DEV), torch.empty(R, device=DEV)
+    mc.layer_norm_forward(place(x, 0, 0), gamma.to(DEV), beta.to(DEV), y, mean=mean, rstd=rstd, eps=EPS)
+    want, m, r = ref.norm(f64(x), f64(gamma), f64(beta), EPS)
+    n, rnd = terms(C), 2.0 ** -8 if dtype is BF else 0.0
+    mag = np.abs(f64(x)).mean(1)
+    err = n * 2.0 ** -23 * (np.abs(want) + np.abs(f64(gamma)) * (1 + mag * r)[:, None] + np.abs(f64(beta)))
+    close(y, want, err * (1 + np.abs(want)) + rnd * np.abs(want), "y")
+    dg, db = torch.empty(C, dtype=BF, device=DEV), torch.empty(C, dtype=BF, device=DEV)
+    ws = torch.full((mc.layer_norm_workspace_size(R, C),), 0xff, dtype=torch.uint8, device=DEV)
+    mc.layer_norm_backward(place(dy, 1, 0), place(x, 0, 0), gamma.to(DEV), mean, rstd, dx, dgamma=dg, dbeta=db,
+                           dx_add=place(r_, 5, 0), workspace=ws)
+    m32, r32 = f64(mean), f64(rstd)
+    want, wg, wb = ref.norm_grad(f64(dy), f64(x), f64(gamma), m32, r32, f64(r_))
+    xh = np.abs((f64(x) - m32[:, None]) * r32[:, None])
+    g = np.abs(f64(dy) * f64(gamma))
+    scale = r32[:, None] * (g + g.mean(1, keepdims=True) + (xh + 1) * (g * (xh + 1)).mean(1, keepdims=True))
+    close(dx, want, n * 2.0 ** -23 * (scale + np.abs(want)) + rnd * np.abs(want), "dx")
+    rel = (R + 8) * 2.0 ** -24
+    close(dg, wg, rel * (np.abs(f64(dy)) * (xh + 1)).sum(0) + 2.0 ** -8 * np.abs(wg), "dgamma")
+    close(db, wb, rel * np.abs(f64(dy)).sum(0) + 2.0 ** -8 * np.abs(wb), "dbeta")
