@@ -13,7 +13,7 @@
 // In MMA terms every form is D[p, q] = sum_k P[p, k] Q[q, k] with operands that are K-major or
 // MN-major in memory (the descriptors' and the TMA boxes' business only).
 //
-// Roles (384 threads): warps 0 and 3 copy P and Q tiles into a ring (one thread each, taking fills in turn: a thread
+// Roles (384 threads): warps 0 and 3 copy P and Q tiles into a ring (one thread each, taking slots in turn: a thread
 // issues one 16 KB copy per ~400 cycles, longer than a fill's MMAs), warp 1 issues MMAs and owns TMEM, warp 2 builds
 // the group tables and masks ragged reduction tails, warps 4-11 run the epilogue (two per TMEM lane quarter, on
 // alternating column chunks).
@@ -386,7 +386,9 @@ __device__ __forceinline__ int32_t masked_rows(int form, const LinearParams &p, 
 }
 
 // ------------------------------------------------------------------------------- TMA producers --
-// One of two threads, `which` = 0 or 1: the even or the odd fills of the ring.
+// One of two threads, `which` = 0 or 1: the fills of the ring's even or odd slots.  (A slot always has the same thread: with
+// fills in turn and an odd number of slots, a pair's second CTA could take the barrier by which its leader armed one fill of a
+// slot for that of the fill after next, when the leader's other thread lagged.)
 template <int kForm, int kFormB, int kPair>
 __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring, uint32_t which,
                                            Walk<kForm, kFormB, kPair> w, Tile t, bool have)
@@ -429,7 +431,7 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
         const int32_t p_grp = form == kRowsT ? t.e : 0, q_grp = form == kRows ? t.e : 0;
         int32_t k = (form == kReduce ? t.start : 0) + t.kb0 * kKB;
         for (int32_t kb = t.kb0; kb < t.kb1; ++kb, k += kKB) {
-            if (shared_ring ? which == 0 : (fills & 1u) == which) {
+            if (shared_ring ? which == 0 : (ps & 1u) == which) {
                 if (kPair == 2 && half) {
                     if (!lwait(&c->go[ps], pph, c, p, true)) {   // the leader armed this fill
                         ok = false;
@@ -498,7 +500,7 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
         // until the final cluster barrier); masked fills complete on each CTA's own.
         for (uint32_t f = fills > num_pipe ? fills - num_pipe : 0u; f < fills; ++f) {
             const uint32_t slot = f % num_pipe;
-            if (shared_ring ? which != 0 : (f & 1u) != which)
+            if (shared_ring ? which != 0 : (slot & 1u) != which)
                 continue;
             if (tail_use >> slot & 1u)
                 lwait(&c->tail[slot], (tail_ph >> slot & 1u) ^ 1u, c, p, false, true);

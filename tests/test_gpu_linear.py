@@ -363,3 +363,28 @@ def test_refusals_of_tensors(mc):
             lin.forward(X, t(4, K, N), Y)
         with pytest.raises(ValueError):
             lin.forward(X, t(4, K, N), Y, offsets=t(4, d=torch.int32))
+
+
+def test_pairs_with_an_odd_ring_keep_their_fills_apart(mc):
+    """Products split over CTA pairs whose ring has an odd number of slots, many launches back to back: each has the first
+    one's bits and none runs into a bounded wait."""
+    found = 0
+    for rows, K, N, E in ((384, 4096, 4096, 0), (380, 1544, 9224, 0), (430, 4104, 4096, 0), (200, 5896, 2056, 5), (700, 5896, 1032, 6),
+                          (1000, 8200, 520, 7)):
+        with mc.Linear(K, N, experts=E) as lin:
+            p = lin.plan(rows)
+            if p["cta_pair"] != 2 or p["pipe_stages"] % 2 == 0:
+                continue
+            found += p["k_split"] > 1
+            X, W = draw((rows, K), 1.0, 80).to(DEV), draw(((E, K, N) if E else (K, N)), K ** -0.5, 81).to(DEV)
+            off = torch.tensor([rows * i // E for i in range(E + 1)], dtype=torch.int32, device=DEV) if E else None
+            first = blank(rows, N, 0)
+            lin.forward(X, W, first, offsets=off)
+            outs = [blank(rows, N, 0) for _ in range(4)]
+            for i in range(60):
+                lin.forward(X, W, outs[i % 4], offsets=off)
+            assert lin.check() == 0, p
+            assert all(torch.equal(first, o) for o in outs), p
+            want = torch.cat([X[rows * i // E:rows * (i + 1) // E].float() @ W[i].float() for i in range(E)]) if E else X.float() @ W.float()
+            assert float((first.float() - want).abs().max()) <= 2.0 ** -7 * float(want.abs().max())
+    assert found
