@@ -56,8 +56,12 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 template <int kForm, int kFormB>
 bool allow_smem()
 {
-    return cudaFuncSetAttribute(linear_kernel<kForm, kFormB, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess &&
-           cudaFuncSetAttribute(linear_kernel<kForm, kFormB, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess;
+    constexpr bool kWide = kForm == kRowsT && kFormB < 0;
+    auto allow = [](void (*kernel)(LinearParams)) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess;
+    };
+    return allow(linear_kernel<kForm, kFormB, 1, false>) && allow(linear_kernel<kForm, kFormB, 2, false>) &&
+           (!kWide || allow(linear_kernel<kForm, kFormB, 2, kWide>));
 }
 
 bool encode_boxed(CUtensorMap *map, const void *ptr, int64_t inner, int64_t outer, int64_t groups, int64_t ld, int boxes)
@@ -110,13 +114,15 @@ struct mlp_linear {
 
 namespace {
 
+int accumulators(int bn) { return bn <= 256 ? 2 : 1; }
+
 // Ring depth and exchange buffers of a chosen variant.
 void finish_plan(const mlp_linear *h, Plan &pl, bool q_mn)
 {
     const bool rows_t = pl.form == kRowsT;
     pl.slot = kPBytes + q_tile_bytes(pl.bn / pl.pair, q_mn);
     // an accumulator next to another one of full width leaves no columns to over-read
-    pl.part_align = 2 * pl.bn + 32 <= 512 && rows_t ? 8 : 32;
+    pl.part_align = accumulators(pl.bn) * pl.bn + 32 <= 512 && rows_t ? 8 : 32;
     const int part = static_cast<int>(cdiv(cdiv(pl.bn, pl.split), pl.part_align)) * pl.part_align;
     pl.recv_bytes = static_cast<uint32_t>((pl.split - 1) * part) * kPRows * 4;
     pl.recv_bufs = pl.split > 1 && rows_t ? (pl.recv_bytes <= 24 * 1024 ? 2 : pl.recv_bytes <= 64 * 1024 ? 1 : 0) : 0;
@@ -130,9 +136,17 @@ struct Estimate {
     double time, tile, work;
 };
 
+// Row pitch of dZ: its rows start on 128-byte lines, without which every copy of 64 columns takes two requests to L2.
+int64_t dz_pitch(int64_t N) { return (N + 63) & ~int64_t{63}; }
+
+// Requests to L2 for rows of this pitch (elements), copied in pieces of 128 bytes: a piece that does not start on a line of
+// 128 bytes takes two, and one that does not start on a sector of 32 a sector more.  (Measured as bytes a cycle: 9700 on
+// lines, about 6000 on sectors, 3900 on neither.)
+double l2_cost(int64_t pitch) { return pitch % 64 == 0 ? 1.0 : pitch % 16 == 0 ? 1.6 : 2.5; }
+
 // A rows product.  rows: of the whole call; out_cols, red: output columns and reduction extent; w_mn: the weights' tile
-// is MN-major.
-Estimate estimate_rows(const mlp_linear *h, const Plan &pl, int64_t rows, int64_t out_cols, int64_t red, bool w_mn)
+// is MN-major; a_pitch: of the activations' rows.
+Estimate estimate_rows(const mlp_linear *h, const Plan &pl, int64_t rows, int64_t out_cols, int64_t red, bool w_mn, int64_t a_pitch)
 {
     const int64_t groups = std::min<int64_t>(h->groups, rows), kb = cdiv(red, kKB);
     const int bm = kPRows * pl.pair, u = 16 * pl.pair;
@@ -150,31 +164,42 @@ Estimate estimate_rows(const mlp_linear *h, const Plan &pl, int64_t rows, int64_
         n = static_cast<double>(cdiv(rows, u) * u) / static_cast<double>(pl.q_tiles);
     }
     // MMA: 2 n cycles per k block, at least 310 to issue its four instructions; fill: what a CTA loads per k block
-    // at 64 bytes a cycle
-    const double mma = std::max(2.0 * n, 310.0);
-    const double fill = (16384.0 + (pl.form == kRows ? q_tile_bytes(pl.bn / pl.pair, w_mn) : n * 128.0 / pl.pair)) / 64.0;
+    // at 64 bytes a cycle.  (Wide tiles do not hide all of one behind the other.)
+    const double act = pl.form == kRows ? 16384.0 : (h->groups > 1 ? pl.bn : n) * 128.0 / pl.pair;
+    const double wgt = pl.form == kRows ? q_tile_bytes(pl.bn / pl.pair, w_mn) : 16384.0;
+    const double mma = std::max(2.0 * n, 310.0), fill = (act + wgt) / 64.0;
+    const double step = n < 160.0 ? std::max(mma, fill) : std::pow(std::pow(mma, 4.0) + std::pow(fill, 4.0), 0.25);
     Estimate e;
-    e.tile = static_cast<double>(cdiv(kb, pl.split)) * std::max(mma, fill) + 400.0;
+    e.tile = static_cast<double>(cdiv(kb, pl.split)) * step + 400.0;
+    // one accumulator: no epilogue is hidden (with an activation, Z and a residual)
+    if (accumulators(pl.bn) == 1)
+        e.tile += 40.0 * n;
     // the last epilogue of a CTA is not hidden, nor are the exchanges of a split tile; clusters start later
     if (pl.split > 1)
         e.tile += 2500.0 + n * 512.0 * (pl.split - 1) / pl.split / 18.0;
-    const double rounds = static_cast<double>(items) / h->max_clusters[pl.pair * pl.split];
-    e.work = rounds * e.tile;
+    const double at_once = h->max_clusters[pl.pair * pl.split], rounds = static_cast<double>(items) / at_once;
+    // What L2 needs for a tile: it serves all SMs together with 9700 bytes a cycle
+    const double l2 = static_cast<double>(kb) * pl.pair * (act * l2_cost(a_pitch) + wgt * l2_cost(w_mn ? out_cols : red)) / 9700.0;
     // (tiles of ragged groups differ, so their last round is rarely a full one)
-    e.time = (h->groups > 1 ? std::max(1.0, rounds + 0.3) : std::ceil(rounds)) * e.tile + 12.0 * n + (pl.pair > 1 ? 800.0 : 0.0);
+    const double full = std::floor(rounds), rest = (rounds - full) * at_once, round = std::max(e.tile, at_once * l2);
+    e.work = rounds * round;
+    e.time = h->groups > 1 ? std::max(std::max(1.0, rounds + 0.3) * e.tile, static_cast<double>(items) * l2)
+                           : full * round + (rest > 0.0 ? std::max(e.tile, rest * l2) : 0.0);
+    e.time += (accumulators(pl.bn) == 1 ? 0.0 : 12.0 * n) + (pl.pair > 1 ? 1500.0 : 0.0);
     return e;
 }
 
 // The variant of a rows product with the lowest estimate.  any: of all forms, else of the unsplit kRowsT ones on `pair`
 // CTAs.
-Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red, bool w_mn, bool any = true, int only_pair = 0)
+Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red, bool w_mn, int64_t a_pitch, bool any = true,
+               int only_pair = 0)
 {
     const int64_t kb = cdiv(red, kKB);
     Plan best{kRowsT, only_pair ? only_pair : 1, 32, 1, 0, 0, 0, 0, 0, static_cast<int>(cdiv(rows, 32))};
     double best_t = 1e300;
     for (int form = any ? kRows : kRowsT; form <= kRowsT; ++form)
         for (int pair = 1; pair <= 2; ++pair)
-            for (int bn = 32; bn <= 256; bn += 32)
+            for (int bn = 32; bn <= (any && pair == 2 && form == kRowsT ? 512 : 256); bn += bn < 256 ? 32 : 64)
                 for (int s = 1; s * pair <= 8 && s <= (any ? 4 : 1); ++s) {
                     if (only_pair && pair != only_pair)
                         continue;
@@ -186,9 +211,11 @@ Plan plan_rows(const mlp_linear *h, int64_t rows, int64_t out_cols, int64_t red,
                     // than there are column steps: every tile gets at least one)
                     const int64_t least = form == kRowsT ? cdiv(rows, bn) : 1;
                     const int64_t most = form == kRowsT && h->groups == 1 ? std::min<int64_t>(least + 2, cdiv(rows, 16 * pair)) : least;
+                    if (bn > 256 && (s > 1 || rows <= 256))
+                        continue;   // (the exchange of such tiles took longer than it saved)
                     for (int64_t tq = least; tq <= most; ++tq) {
                         const Plan pl{form, pair, bn, s, 0, 0, 0, 0, 0, static_cast<int>(tq)};
-                        const double t = estimate_rows(h, pl, rows, out_cols, red, w_mn).time;
+                        const double t = estimate_rows(h, pl, rows, out_cols, red, w_mn, a_pitch).time;
                         if (t < best_t) {
                             best_t = t;
                             best = pl;
@@ -240,18 +267,19 @@ GradPlan plan_grads(const mlp_linear *h, int64_t rows)
     const int64_t pe = kn ? K : N, qe = kn ? N : K;
     GradPlan g;
     g.w = plan_reduce(h, pe, qe);
-    g.x = plan_rows(h, rows, K, N, !kn);
-    const Plan x = plan_rows(h, rows, K, N, !kn, false, g.w.pair);
-    const Estimate ex = estimate_rows(h, x, rows, K, N, !kn), ew = estimate_reduce(h, g.w, rows, pe, qe);
+    const int64_t pitch = h->d.activation != MLP_ACT_NONE ? dz_pitch(N) : N;
+    g.x = plan_rows(h, rows, K, N, !kn, pitch);
+    const Plan x = plan_rows(h, rows, K, N, !kn, pitch, false, g.w.pair);
+    const Estimate ex = estimate_rows(h, x, rows, K, N, !kn, pitch), ew = estimate_reduce(h, g.w, rows, pe, qe);
     const double both = std::max(ex.work + ew.work, std::max(ex.tile, ew.tile)) + 3000.0;
-    const double apart = estimate_rows(h, g.x, rows, K, N, !kn).time + ew.time + 6000.0;
+    const double apart = estimate_rows(h, g.x, rows, K, N, !kn, pitch).time + ew.time + 6000.0;
     g.together = both <= apart && both < 400e3;
     if (g.together)
         g.x = x;
     return g;
 }
 
-template <int kForm, int kFormB, int kPair>
+template <int kForm, int kFormB, int kPair, bool kWide = false>
 bool launch_one(const LinearParams &p, int clusters, int cs, size_t smem, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg = {};
@@ -269,7 +297,7 @@ bool launch_one(const LinearParams &p, int clusters, int cs, size_t smem, cudaSt
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = cs > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, linear_kernel<kForm, kFormB, kPair>, p) == cudaSuccess;
+    return cudaLaunchKernelEx(&cfg, linear_kernel<kForm, kFormB, kPair, kWide>, p) == cudaSuccess;
 }
 
 // One product (w NULL), or a kRowsT one with the weights' gradient.  items: of the launch, or an upper bound where the
@@ -289,8 +317,8 @@ mlp_status launch(const mlp_linear *h, LinearParams &p, const Plan &pl, const Pl
     p.part_align = pl.part_align;
     p.recv_bufs = pl.recv_bufs;
     p.recv_bytes = pl.recv_bytes;
-    // two accumulators; parts of a split tile that are no multiple of 32 columns are over-read
-    const uint32_t cols = 2u * static_cast<uint32_t>(p.acc_cols) + (pl.split > 1 && pl.part_align < 32 ? 32u : 0u);
+    // parts of a split tile that are no multiple of 32 columns are over-read
+    const uint32_t cols = static_cast<uint32_t>(accumulators(p.acc_cols) * p.acc_cols) + (pl.split > 1 && pl.part_align < 32 ? 32u : 0u);
     p.tmem_cols = 32;
     while (p.tmem_cols < cols)
         p.tmem_cols *= 2;
@@ -306,6 +334,8 @@ mlp_status launch(const mlp_linear *h, LinearParams &p, const Plan &pl, const Pl
         ok = two ? launch_one<kRowsT, kReduce, 2>(p, clusters, cs, smem, st) : launch_one<kRowsT, kReduce, 1>(p, clusters, cs, smem, st);
     else if (pl.form == kRows)
         ok = two ? launch_one<kRows, -1, 2>(p, clusters, cs, smem, st) : launch_one<kRows, -1, 1>(p, clusters, cs, smem, st);
+    else if (pl.bn > 256)
+        ok = launch_one<kRowsT, -1, 2, true>(p, clusters, cs, smem, st);
     else if (pl.form == kRowsT)
         ok = two ? launch_one<kRowsT, -1, 2>(p, clusters, cs, smem, st) : launch_one<kRowsT, -1, 1>(p, clusters, cs, smem, st);
     else
@@ -331,7 +361,17 @@ int64_t describe_rows(const mlp_linear *h, Problem &q, const Plan &pl, int64_t r
         items = (cdiv(rows, kPRows * pl.pair) + h->groups - 1) * cdiv(out_cols, pl.bn);
     } else {
         const int qrows = static_cast<int>(std::min<int64_t>(pl.bn / pl.pair, rows));
-        if (!operand(q, 1, false, A, red, rows, 1, lda, qrows) || !operand(q, 0, b_mn, B, b_in, b_out, h->groups, b_in, kPRows))
+        if (pl.bn > 256) {   // two halves, each a copy and an MMA of its own
+            q.wide = static_cast<uint32_t>(pl.bn / 2 / pl.pair) * 128u;
+            if (!operand(q, 1, false, A, red, rows, 1, lda, std::min(pl.bn / 2 / pl.pair, qrows)))
+                return 0;
+            if (q.copy_bytes[1] != q.wide)
+                return 0;
+            q.copy_bytes[1] *= 2;
+        } else if (!operand(q, 1, false, A, red, rows, 1, lda, qrows)) {
+            return 0;
+        }
+        if (!operand(q, 0, b_mn, B, b_in, b_out, h->groups, b_in, kPRows))
             return 0;
         q.p_ext = static_cast<int32_t>(out_cols);
         if (!offsets)
@@ -590,9 +630,6 @@ int32_t grad_block_rows(const mlp_linear *h, int64_t rows)
     return static_cast<int32_t>(std::max<int64_t>(16, cdiv(cdiv(rows, blocks), 8) * 8));
 }
 
-// Row pitch of dZ: its rows start on 128-byte lines, without which every copy of 64 columns takes two requests to L2.
-int64_t dz_pitch(int64_t N) { return (N + 63) & ~int64_t{63}; }
-
 // Without an activation dZ is dY.  Where the bias gradient reads dY anyway, a copy of it whose rows start on those lines
 // pays for itself in the products of many rows.
 bool copies_dy(const mlp_linear *h, int64_t rows) { return h->d.activation == MLP_ACT_NONE && h->d.N % 64 != 0 && rows >= 256; }
@@ -649,7 +686,7 @@ extern "C" mlp_status mlp_linear_create(const mlp_linear_desc *d, mlp_linear_t *
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<kRows, -1, 1>, &cfg) != cudaSuccess || (n < 1 && cs <= 2))
+        if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<kRows, -1, 1, false>, &cfg) != cudaSuccess || (n < 1 && cs <= 2))
             st = MLP_ERR_CUDA;
         h->max_clusters[cs] = n;
     }
@@ -727,7 +764,7 @@ extern "C" mlp_status mlp_linear_forward(mlp_linear_t h, int64_t rows, const voi
     q.out = Y;
     q.ld_out = ldy;
     const bool kn = h->d.weight_layout == 0;
-    const Plan pl = plan_rows(h, rows, N, K, kn);
+    const Plan pl = plan_rows(h, rows, N, K, kn, K);
     const int64_t items = describe_rows(h, q, pl, rows, X, ldx, W, N, K, kn, offsets != nullptr);
     return items ? launch(h, p, pl, nullptr, items, static_cast<cudaStream_t>(stream)) : MLP_ERR_CUDA;
 }
@@ -856,7 +893,8 @@ extern "C" mlp_status mlp_linear_get_plan(mlp_linear_t h, int64_t rows, int32_t 
 {
     if (!h || !plan || rows < 1 || pass < 0 || pass > 2)
         return MLP_ERR_INVALID_ARG;
-    const Plan pl = pass == 0 ? plan_rows(h, rows, h->d.N, h->d.K, h->d.weight_layout == 0) : pass == 1 ? plan_grads(h, rows).x : plan_grads(h, rows).w;
+    const Plan pl = pass == 0 ? plan_rows(h, rows, h->d.N, h->d.K, h->d.weight_layout == 0, h->d.K)
+                              : pass == 1 ? plan_grads(h, rows).x : plan_grads(h, rows).w;
     plan->form = pl.form;
     plan->cta_pair = pl.pair;
     plan->tile_cols = pl.bn;

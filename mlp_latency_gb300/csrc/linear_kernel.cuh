@@ -20,6 +20,9 @@
 // The accumulator is double buffered, so a tile's epilogue runs under the next tile's MMAs.  Tiles are dealt out
 // statically, in an order that lets the CTAs running at one time share operand panels in L2.
 //
+// kWide (kRowsT on pairs): tiles of 257 to 512 activation rows, each k block two MMAs that share the weights' tile, in one
+// accumulator, whose epilogue then runs under no MMA.  (As a flag at run time it cost the other tiles 10 %.)
+//
 // kFormB >= 0: a launch of two products, kForm's and kFormB's, whose tiles every CTA takes in turn.  The backward pass
 // runs the input's and the weights' gradient this way.
 //
@@ -69,6 +72,7 @@ __host__ __device__ inline uint32_t q_tile_bytes(int32_t cols, bool mn)
 struct Problem {
     CUtensorMap map[2];             // P and Q: (inner, outer, group) views, or (64, outer, inner / 64, group)
     uint32_t copy_bytes[2];         // what one fill copies of each into a CTA
+    uint32_t wide;                  // kRowsT on pairs, tiles of more than 256 columns: bytes of one of Q's two halves
     int32_t boxed[2];               // the four-dimensional view: all boxes of an MN-major tile in one copy
     int32_t mn[2];                  // operand stored MN-major (else K-major)
     int32_t dense_items;            // items without offsets
@@ -204,6 +208,20 @@ __device__ __forceinline__ bool lwait(uint64_t *bar, uint32_t parity, LCtrl *c, 
             return false;
         }
     }
+}
+
+// Accumulator of an item, and the parity of its uses.  Wide tiles have one: two are more than TMEM holds.
+template <bool kWide>
+__device__ __forceinline__ uint32_t acc_of(uint32_t tiles) { return kWide ? 0u : tiles & 1u; }
+template <bool kWide>
+__device__ __forceinline__ uint32_t acc_parity(uint32_t tiles) { return (kWide ? tiles : tiles >> 1) & 1u; }
+
+// Columns of the first of a wide tile's two MMAs.
+template <int kPair>
+__device__ __forceinline__ int32_t first_half(int32_t n)
+{
+    constexpr int32_t u = 16 * kPair;
+    return (n / u + 1) / 2 * u;
 }
 
 // Lane 0 waits, then every lane acquires the completed phase itself.
@@ -389,7 +407,7 @@ __device__ __forceinline__ int32_t masked_rows(int form, const LinearParams &p, 
 // One of two threads, `which` = 0 or 1: the fills of the ring's even or odd slots.  (A slot always has the same thread: with
 // fills in turn and an odd number of slots, a pair's second CTA could take the barrier by which its leader armed one fill of a
 // slot for that of the fill after next, when the leader's other thread lagged.)
-template <int kForm, int kFormB, int kPair>
+template <int kForm, int kFormB, int kPair, bool kWide>
 __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring, uint32_t which,
                                            Walk<kForm, kFormB, kPair> w, Tile t, bool have)
 {
@@ -427,7 +445,9 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
         }
         // first row (column of an MN-major operand) of this CTA's share of each tile, and the group
         const int32_t p_row = (form == kRows ? t.start : 0) + t.p0 + static_cast<int32_t>(half) * kPRows;
-        const int32_t q_row = (form == kRowsT ? t.start : 0) + t.q0 + static_cast<int32_t>(half) * (t.n / kPair);
+        const int32_t n1 = kWide ? first_half<kPair>(t.n) : t.n;
+        const int32_t q_row = (form == kRowsT ? t.start : 0) + t.q0 + static_cast<int32_t>(half) * (n1 / kPair);
+        const int32_t q_row2 = t.start + t.q0 + n1 + static_cast<int32_t>(half) * ((t.n - n1) / kPair);
         const int32_t p_grp = form == kRowsT ? t.e : 0, q_grp = form == kRows ? t.e : 0;
         int32_t k = (form == kReduce ? t.start : 0) + t.kb0 * kKB;
         for (int32_t kb = t.kb0; kb < t.kb1; ++kb, k += kKB) {
@@ -478,6 +498,8 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
                 }
                 if (!q_mn) {
                     load3(b, map_q, k, q_row, q_grp);
+                    if (kWide)
+                        load3(b + q.wide, map_q, k, q_row2, q_grp);
                 } else if (q_boxed) {
                     load4(b, map_q, k, q_row >> 6, q_grp);
                 } else {
@@ -511,7 +533,7 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
 }
 
 // ---------------------------------------------------------------------------------- MMA issuer --
-template <int kForm, int kFormB, int kPair>
+template <int kForm, int kFormB, int kPair, bool kWide>
 __device__ __forceinline__ void l_role_mma(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring,
                                            uint32_t tmem_base)
 {
@@ -545,12 +567,14 @@ __device__ __forceinline__ void l_role_mma(const LinearParams &p, LCtrl *c, cons
     while (w.next(p, g, n_items, n_items_b, t)) {
         if (kFormB >= 0)
             describe(problem_of<kFormB>(p, t));
-        const uint32_t acc = tiles & 1u;
-        if (!lwait(&c->tempty[acc], ((tiles >> 1) & 1u) ^ 1u, c, p, kPair == 2))
+        const uint32_t acc = acc_of<kWide>(tiles);
+        if (!lwait(&c->tempty[acc], acc_parity<kWide>(tiles) ^ 1u, c, p, kPair == 2))
             break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * acc_cols;
-        const uint32_t idesc = idesc0 | (static_cast<uint32_t>(t.n) >> 3) << 17;
+        const uint32_t n1 = static_cast<uint32_t>(kWide ? first_half<kPair>(t.n) : t.n), n2 = static_cast<uint32_t>(t.n) - n1;
+        const uint32_t idesc = idesc0 | (n1 >> 3) << 17, idesc2 = idesc0 | (n2 >> 3) << 17;
+        const uint64_t wide16 = p.pr[0].wide >> 4;
         uint32_t accum = 0;
         for (int32_t kb = t.kb0; kb < t.kb1; ++kb) {
             if (!lwait(&c->full[ps], pph, c, p, kPair == 2)) {
@@ -561,6 +585,8 @@ __device__ __forceinline__ void l_role_mma(const LinearParams &p, LCtrl *c, cons
 #pragma unroll
             for (uint32_t kk = 0; kk < kKB / 16; ++kk) {
                 mma_bf16_ss_g<kPair>(d, pd + off + pstep * kk, qd + off + qstep * kk, idesc, accum);
+                if (kWide && n2 != 0)   // (an MMA has at most 256 columns)
+                    mma_bf16_ss_g<kPair>(d + n1, pd + off + pstep * kk, qd + off + wide16 + qstep * kk, idesc2, accum);
                 accum = 1u;
             }
             issued = true;
@@ -801,7 +827,7 @@ struct EpiState {
 };
 
 // One tile; false after an abort.
-template <int kForm, int kPair>
+template <int kForm, int kPair, bool kWide>
 __device__ __forceinline__ bool epilogue_tile(const LinearParams &lp, const Problem &p, LCtrl *c, EpiState &st, const Tile &t)
 {
     constexpr bool kLaneRow = kForm != kRowsT;
@@ -815,8 +841,8 @@ __device__ __forceinline__ bool epilogue_tile(const LinearParams &lp, const Prob
     const int32_t nbuf = lp.recv_bufs > 0 ? lp.recv_bufs : 1;
     auto cta_of = [&](int32_t slice) { return static_cast<uint32_t>(slice * kPair) + half; };   // same half, other slice
     {
-        const uint32_t acc = tiles & 1u;
-        const uint32_t ph = (tiles >> 1) & 1u;
+        const uint32_t acc = acc_of<kWide>(tiles);
+        const uint32_t ph = acc_parity<kWide>(tiles);
         // the columns of the tile that this CTA finishes
         const int32_t part = splitk ? ((t.n + S - 1) / S + lp.part_align - 1) / lp.part_align * lp.part_align : t.n;
         const int32_t c_lo = min(me * part, t.n), c_hi = min(c_lo + part, t.n);
@@ -1046,7 +1072,7 @@ __device__ __forceinline__ void add_bias_sums(const BiasSums &q, int32_t e, int3
         static_cast<__nv_bfloat16 *>(q.out)[o] = __float2bfloat16_rn(s);
 }
 
-template <int kForm, int kFormB, int kPair>
+template <int kForm, int kFormB, int kPair, bool kWide>
 __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *recv_base,
                                                 uint8_t *stage_all, float *bias_all, uint32_t tmem_base)
 {
@@ -1078,20 +1104,20 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
     Tile t;
     while (w.next(p, g, n_items, n_items_b, t)) {
         if constexpr (kFormB < 0) {
-            if (!epilogue_tile<kForm, kPair>(p, p.pr[0], c, st, t))
+            if (!epilogue_tile<kForm, kPair, kWide>(p, p.pr[0], c, st, t))
                 return;
         } else if (t.which == 0) {
-            if (!epilogue_tile<kForm, kPair>(p, p.pr[0], c, st, t))
+            if (!epilogue_tile<kForm, kPair, kWide>(p, p.pr[0], c, st, t))
                 return;
         } else {
-            if (!epilogue_tile<kFormB, kPair>(p, p.pr[1], c, st, t))
+            if (!epilogue_tile<kFormB, kPair, kWide>(p, p.pr[1], c, st, t))
                 return;
         }
     }
 }
 
 // --------------------------------------------------------------------------------------- kernel --
-template <int kForm, int kFormB, int kPair>
+template <int kForm, int kFormB, int kPair, bool kWide>
 __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_constant__ LinearParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1199,10 +1225,10 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
             if (p.offsets)
                 have = w.next(p, g, c->n_items[0], c->n_items[1], t);
             if (elect_one())
-                l_role_tma<kForm, kFormB, kPair>(p, c, g, ring, 0, w, t, have);
+                l_role_tma<kForm, kFormB, kPair, kWide>(p, c, g, ring, 0, w, t, have);
         } else if (warp == 1) {
             if (elect_one())
-                l_role_mma<kForm, kFormB, kPair>(p, c, g, ring, tmem_base);
+                l_role_mma<kForm, kFormB, kPair, kWide>(p, c, g, ring, tmem_base);
         } else if (warp == 2) {
             if ((kForm == kReduce || kFormB == kReduce) && p.offsets)
                 l_role_mask<kForm, kFormB, kPair>(p, c, g, ring);
@@ -1210,9 +1236,9 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
             if (p.offsets)
                 have = w.next(p, g, c->n_items[0], c->n_items[1], t);
             if (elect_one())
-                l_role_tma<kForm, kFormB, kPair>(p, c, g, ring, 1, w, t, have);
+                l_role_tma<kForm, kFormB, kPair, kWide>(p, c, g, ring, 1, w, t, have);
         } else {
-            l_role_epilogue<kForm, kFormB, kPair>(p, c, g, ring + (p.recv_bufs ? sm.recv : 0u), ring + sm.stage,
+            l_role_epilogue<kForm, kFormB, kPair, kWide>(p, c, g, ring + (p.recv_bufs ? sm.recv : 0u), ring + sm.stage,
                                           reinterpret_cast<float *>(ring + sm.bias), tmem_base);
         }
     }

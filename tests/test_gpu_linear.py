@@ -388,3 +388,25 @@ def test_pairs_with_an_odd_ring_keep_their_fills_apart(mc):
             want = torch.cat([X[rows * i // E:rows * (i + 1) // E].float() @ W[i].float() for i in range(E)]) if E else X.float() @ W.float()
             assert float((first.float() - want).abs().max()) <= 2.0 ** -7 * float(want.abs().max())
     assert found
+
+
+WIDE = [(979, 2056, 5912, None), (394, 1544, 13208, None), (845, 1032, 9992, None), (1579, 2056, 2056, None), (301, 4104, 19000, None),
+        (1800, 2056, 3448, [300, 0, 511, 513, 33, 443]), (2300, 1928, 3080, [1, 1200, 600, 499])]
+
+
+def test_some_products_take_tiles_of_more_than_256_columns(mc):
+    n = 0
+    for rows, K, N, counts in WIDE:
+        with mc.Linear(K, N, activation="gelu", experts=len(counts or ())) as lin:
+            n += lin.plan(rows)["tile_cols"] > 256
+    assert n >= 3
+
+
+@pytest.mark.parametrize("rows,K,N,counts", WIDE)
+def test_forward_tiles_of_more_than_256_columns(mc, rows, K, N, counts):
+    run_forward(mc, rows, K, N, "gelu", "kn", counts=counts, extra=8 if rows % 2 else 0, seed=rows)
+
+
+@pytest.mark.parametrize("rows,K,N,counts", [(979, 5912, 520, None), (1800, 3448, 264, [300, 0, 511, 513, 33, 443])])
+def test_backward_tiles_of_more_than_256_columns(mc, rows, K, N, counts):
+    run_backward(mc, rows, K, N, "gelu", "nk", counts=counts, seed=rows)
