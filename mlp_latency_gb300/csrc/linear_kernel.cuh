@@ -39,7 +39,7 @@
 //   2048 x 8192 x 8192          184 us    1.5 PFLOP/s at the power cap, 3.8 rounds of 4
 //   4000 rows, 32 experts of 2048 x 4096, both gradients  245 us   writing dW (write-only traffic reaches 3.9 TB/s)
 // Tiles of 256 columns on pairs need the whole of that intake (32 KB per 512 cycles), which is why narrower ones do not get
-// faster in proportion and wider ones would not fit TMEM twice.
+// faster in proportion.
 #pragma once
 #include <cuda_bf16.h>
 
