@@ -168,7 +168,8 @@ Estimate estimate_rows(const mlp_linear *h, const Plan &pl, int64_t rows, int64_
     const double act = pl.form == kRows ? 16384.0 : (h->groups > 1 ? pl.bn : n) * 128.0 / pl.pair;
     const double wgt = pl.form == kRows ? q_tile_bytes(pl.bn / pl.pair, w_mn) : 16384.0;
     const double mma = std::max(2.0 * n, 310.0), fill = (act + wgt) / 64.0;
-    const double step = n < 160.0 ? std::max(mma, fill) : std::pow(std::pow(mma, 4.0) + std::pow(fill, 4.0), 0.25);
+    const double m2 = mma * mma, f2 = fill * fill;
+    const double step = n < 160.0 ? std::max(mma, fill) : std::sqrt(std::sqrt(m2 * m2 + f2 * f2));
     Estimate e;
     e.tile = static_cast<double>(cdiv(kb, pl.split)) * step + 400.0;
     // one accumulator: no epilogue is hidden (with an activation, Z and a residual)
