@@ -253,11 +253,11 @@ __device__ __forceinline__ void load_w_shifted(const U *w, int c, int step, int 
             }
 }
 
-// One vector.
+// One vector, which is inside the row.  (The bound is the vector's end: where it is read in two halves, each is checked.)
 template <int V>
 __device__ __forceinline__ void load_w(const void *w, int kind, int64_t c, float none, float (&f)[V])
 {
-    load_w<V, 1, int64_t>(w, kind, c, 0, c + 1, none, *reinterpret_cast<float(*)[1][V]>(&f));
+    load_w<V, 1, int64_t>(w, kind, c, 0, c + V, none, *reinterpret_cast<float(*)[1][V]>(&f));
 }
 
 __device__ __forceinline__ float warp_sum(float v)
