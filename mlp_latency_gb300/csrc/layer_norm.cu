@@ -1510,11 +1510,13 @@ int64_t most_fused_blocks(int64_t cols)
     return static_cast<int64_t>(per_sm) * kSms;
 }
 
+// A kernel's limit is raised to the same value whatever a launch takes: the limit belongs to the kernel, and another thread may
+// be about to launch it with more.
 template <typename K>
 bool allow_smem(K *kernel, size_t bytes)
 {
     return bytes <= 47 * 1024 ||   // (the blocks also hold up to 1 KB of static shared memory)
-           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess;
+           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kAloneLimit)) == cudaSuccess;
 }
 
 bool aligned(const void *p, int64_t ld, size_t esz, size_t bytes)
