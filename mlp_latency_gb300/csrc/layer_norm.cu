@@ -1510,13 +1510,27 @@ int64_t most_fused_blocks(int64_t cols)
     return static_cast<int64_t>(per_sm) * kSms;
 }
 
+// An error is reported by the call that had it, and not left with the runtime for a later one.
+bool succeeded(cudaError_t e)
+{
+    if (e != cudaSuccess)
+        cudaGetLastError();
+    return e == cudaSuccess;
+}
+
+// A call's launches: none after one that failed.
+struct Stream {
+    cudaStream_t stream;
+    bool failed = false;
+};
+
 // A kernel's limit is raised to the same value whatever a launch takes: the limit belongs to the kernel, and another thread may
 // be about to launch it with more.
 template <typename K>
 bool allow_smem(K *kernel, size_t bytes)
 {
     return bytes <= 47 * 1024 ||   // (the blocks also hold up to 1 KB of static shared memory)
-           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kAloneLimit)) == cudaSuccess;
+           succeeded(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kAloneLimit)));
 }
 
 bool aligned(const void *p, int64_t ld, size_t esz, size_t bytes)
@@ -1533,8 +1547,10 @@ bool bad_rows(const void *p, int64_t ld, int64_t cols, size_t esz)
 
 // (see take_turn)
 template <typename... A, typename... B>
-void launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, B... args)
+void launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, Stream &st, B... args)
 {
+    if (st.failed)
+        return;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1542,14 +1558,14 @@ void launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStrea
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
+    cfg.stream = st.stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, kernel, A(args)...);
+    st.failed = !succeeded(cudaLaunchKernelEx(&cfg, kernel, A(args)...));
 }
 
 template <typename T, int V, int kItems, int kThreads>
-void launch_forward(const NormParams &p, int64_t nvec, cudaStream_t st)
+void launch_forward(const NormParams &p, int64_t nvec, Stream &st)
 {
     if (nvec <= 32 * kItems) {
         const int teams = 4;
@@ -1561,7 +1577,7 @@ void launch_forward(const NormParams &p, int64_t nvec, cudaStream_t st)
 }
 
 template <typename T, int V, int kItems, bool kOdd>
-bool launch_forward_ring(const NormParams &p, int64_t nvec, cudaStream_t st)
+bool launch_forward_ring(const NormParams &p, int64_t nvec, Stream &st)
 {
     constexpr int kStages = 3;   // (4 and 5 slots measured no faster at 2048 x 8192)
     const int threads = static_cast<int>(cdiv(cdiv(nvec, kItems), 32) * 32);
@@ -1586,7 +1602,7 @@ bool launch_forward_ring(const NormParams &p, int64_t nvec, cudaStream_t st)
 }
 
 template <typename T>
-bool launch_forward_staged(const NormParams &p, cudaStream_t st)
+bool launch_forward_staged(const NormParams &p, Stream &st)
 {
     const int threads = loop_threads(cdiv(p.cols, kLoopV<T>), 8, 1024);
     const size_t smem = static_cast<size_t>((p.cols + 1) & ~int64_t{1}) * 4;
@@ -1601,7 +1617,7 @@ bool launch_forward_staged(const NormParams &p, cudaStream_t st)
 // Rows of any width and stride on the words of memory (2000 x 5111 18 us, staged 31); false where they are too wide, or
 // too narrow: up to 16 words a row the kernels for other rows are as fast (8000 x 71 8 us, through the ring 14).
 template <typename T>
-bool forward_odd(const NormParams &p, cudaStream_t st)
+bool forward_odd(const NormParams &p, Stream &st)
 {
     constexpr int V = 16 / sizeof(T), kMost = 32 / V;
     const int64_t nvec = odd_words(p.cols, V);
@@ -1618,7 +1634,7 @@ bool forward_odd(const NormParams &p, cudaStream_t st)
 // from as many threads as there are.  Many rows: narrow ones a warp each, wide ones through the ring.  Other rows
 // (those that forward_odd leaves): narrow ones a warp each, wide ones staged.  What fits none of these takes three passes over the row.
 template <typename T, int V>
-void forward_v(const NormParams &p, cudaStream_t st)
+void forward_v(const NormParams &p, Stream &st)
 {
     const int64_t nvec = cdiv(p.cols, V);
     const bool many = p.rows > 2 * kSms;
@@ -1646,7 +1662,7 @@ void forward_v(const NormParams &p, cudaStream_t st)
 }
 
 template <typename T, int V, int kItems, int kStages, bool kOdd>
-bool launch_backward(const NormParams &p, int threads, size_t smem, cudaStream_t st)
+bool launch_backward(const NormParams &p, int threads, size_t smem, Stream &st)
 {
     auto kernel = norm_backward_kernel<T, V, kItems, kStages, kOdd>;
     if (!allow_smem(kernel, smem))
@@ -1657,7 +1673,7 @@ bool launch_backward(const NormParams &p, int threads, size_t smem, cudaStream_t
 
 // Through a ring of 4 slots, or 2 where the rows are wide; false where they are too wide.
 template <typename T, int V, int kItems, bool kOdd>
-bool backward_ring(NormParams &p, int64_t nvec, cudaStream_t st)
+bool backward_ring(NormParams &p, int64_t nvec, Stream &st)
 {
     const int threads = ring_threads(nvec, kItems);
     p.blocks = static_cast<int32_t>(std::min<int64_t>(p.rows, static_cast<int64_t>(ring_per_sm(threads, kItems * V)) * kSms));
@@ -1673,7 +1689,7 @@ bool backward_ring(NormParams &p, int64_t nvec, cudaStream_t st)
 }
 
 template <typename T, int V, bool kOdd>
-bool backward_rings(NormParams &p, int64_t nvec, cudaStream_t st)
+bool backward_rings(NormParams &p, int64_t nvec, Stream &st)
 {
     const int items = ring_items(nvec, V);
     if constexpr (V == 4)
@@ -1684,7 +1700,7 @@ bool backward_rings(NormParams &p, int64_t nvec, cudaStream_t st)
 }
 
 template <typename T, int V, int R>
-bool backward_staged_r(NormParams &p, int threads, size_t smem, cudaStream_t st)
+bool backward_staged_r(NormParams &p, int threads, size_t smem, Stream &st)
 {
     auto kernel = norm_backward_staged_kernel<T, V, R>;
     if (!allow_smem(kernel, smem))
@@ -1695,7 +1711,7 @@ bool backward_staged_r(NormParams &p, int threads, size_t smem, cudaStream_t st)
 
 // Other rows, four at a time where there are enough to keep every SM busy.
 template <typename T, int V>
-bool backward_staged(NormParams &p, cudaStream_t st)
+bool backward_staged(NormParams &p, Stream &st)
 {
     const int threads = loop_threads(cdiv(p.cols, V), 4, 512);
     const size_t smem = p.part ? static_cast<size_t>(p.cols) * 8 : 0;
@@ -1708,7 +1724,7 @@ bool backward_staged(NormParams &p, cudaStream_t st)
 }
 
 template <typename T>
-bool backward_odd(NormParams &p, int64_t ld, cudaStream_t st)
+bool backward_odd(NormParams &p, int64_t ld, Stream &st)
 {
     constexpr int V = 16 / sizeof(T);
     const NormParams keep = p;
@@ -1723,7 +1739,7 @@ bool backward_odd(NormParams &p, int64_t ld, cudaStream_t st)
 
 // One kernel for all gradients; false where the rows are too wide for it.
 template <typename T, int V>
-bool backward_v(NormParams &p, cudaStream_t st)
+bool backward_v(NormParams &p, Stream &st)
 {
     if constexpr (V * sizeof(T) == 16)
         if (backward_rings<T, V, false>(p, cdiv(p.cols, V), st))
@@ -1733,7 +1749,7 @@ bool backward_v(NormParams &p, cudaStream_t st)
 
 // Rows wider than a block's registers: the column sums first (dx may overwrite what they read), then dx.
 template <typename T, int V>
-void backward_wide(NormParams &p, cudaStream_t st)
+void backward_wide(NormParams &p, Stream &st)
 {
     p.block_rows = std::max<int64_t>(cdiv(p.rows, kColsumBlocks), 8);
     p.blocks = static_cast<int32_t>(cdiv(p.rows, p.block_rows));
@@ -1773,7 +1789,7 @@ extern "C" mlp_status mlp_layernorm_forward(int64_t rows, int64_t cols, const vo
     p.eps = eps;
     p.inv_cols = 1.0f / static_cast<float>(cols);
     p.w_f32 = w_dtype == MLP_DT_F32;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    Stream st{static_cast<cudaStream_t>(stream)};
     p.w_kind = p.w_f32 + (aligned(gamma, 0, wsz, 16) && aligned(beta, 0, wsz, 16) ? 2 : 0);
     auto wide = [&](size_t bytes) {
         return static_cast<size_t>(cols) * esz % bytes == 0 && aligned(x, ldx, esz, bytes) && aligned(y, ldy, esz, bytes);
@@ -1794,7 +1810,7 @@ extern "C" mlp_status mlp_layernorm_forward(int64_t rows, int64_t cols, const vo
     } else if (!(odd && forward_odd<float>(p, st))) {
         forward_v<float, 1>(p, st);
     }
-    return cudaGetLastError() == cudaSuccess ? MLP_OK : MLP_ERR_CUDA;
+    return st.failed ? MLP_ERR_CUDA : MLP_OK;
 }
 
 extern "C" mlp_status mlp_layernorm_workspace_size(int64_t rows, int64_t cols, size_t *bytes)
@@ -1818,13 +1834,13 @@ extern "C" mlp_status mlp_layernorm_backward(int64_t rows, int64_t cols, const v
     if (bad_dtype(dtype) || bad_dtype(w_dtype))
         return MLP_ERR_UNSUPPORTED;
     const size_t esz = dtype == MLP_DT_BF16 ? 2 : 4, wsz = w_dtype == MLP_DT_BF16 ? 2 : 4;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    Stream st{static_cast<cudaStream_t>(stream)};
     if (!aligned(dgamma, 0, wsz, wsz) || !aligned(dbeta, 0, wsz, wsz) || !aligned(gamma, 0, wsz, wsz))
         return MLP_ERR_INVALID_ARG;
     const bool want_w = dgamma || dbeta;
     if (rows == 0) {
-        if ((dgamma && cudaMemsetAsync(dgamma, 0, static_cast<size_t>(cols) * wsz, st) != cudaSuccess) ||
-            (dbeta && cudaMemsetAsync(dbeta, 0, static_cast<size_t>(cols) * wsz, st) != cudaSuccess))
+        if ((dgamma && !succeeded(cudaMemsetAsync(dgamma, 0, static_cast<size_t>(cols) * wsz, st.stream))) ||
+            (dbeta && !succeeded(cudaMemsetAsync(dbeta, 0, static_cast<size_t>(cols) * wsz, st.stream))))
             return MLP_ERR_CUDA;
         return MLP_OK;
     }
@@ -1868,7 +1884,7 @@ extern "C" mlp_status mlp_layernorm_backward(int64_t rows, int64_t cols, const v
     } else if (!(wide(16) ? backward_v<float, 4>(p, st) : backward_v<float, 1>(p, st))) {
         wide(16) ? backward_wide<float, 4>(p, st) : backward_wide<float, 1>(p, st);
     }
-    if (want_w && cudaPeekAtLastError() == cudaSuccess) {
+    if (want_w) {
         if (cols % 4 == 0 && p.part_ld % 4 == 0 && p.part_step == 0)
             launch(norm_colsum_finish_kernel<4, 8>, dim3(static_cast<unsigned>(cdiv(cols, 32)), 2), 256, 0, st, p, dgamma, dbeta);
         else if (p.blocks <= 64)
@@ -1876,5 +1892,5 @@ extern "C" mlp_status mlp_layernorm_backward(int64_t rows, int64_t cols, const v
         else
             launch(norm_colsum_finish_kernel<1, 8>, dim3(static_cast<unsigned>(cdiv(cols, 8)), 2), 256, 0, st, p, dgamma, dbeta);
     }
-    return cudaGetLastError() == cudaSuccess ? MLP_OK : MLP_ERR_CUDA;
+    return st.failed ? MLP_ERR_CUDA : MLP_OK;
 }
