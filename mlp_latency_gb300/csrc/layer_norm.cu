@@ -12,6 +12,9 @@
 #include <cstdint>
 
 #include "../../include/mlp_block.h"
+#include "cuda_call.h"
+
+using mlpc::succeeded;
 
 namespace {
 
@@ -1508,14 +1511,6 @@ int64_t most_fused_blocks(int64_t cols)
                 per_sm = std::max(per_sm, ring_per_sm(ring_threads(nvec, items), items * v));
         }
     return static_cast<int64_t>(per_sm) * kSms;
-}
-
-// An error is reported by the call that had it, and not left with the runtime for a later one.
-bool succeeded(cudaError_t e)
-{
-    if (e != cudaSuccess)
-        cudaGetLastError();
-    return e == cudaSuccess;
 }
 
 // A call's launches: none after one that failed.

@@ -9,6 +9,7 @@
 #include <new>
 
 #include "../../include/mlp_block.h"
+#include "cuda_call.h"
 #include "linear_kernel.cuh"
 
 using namespace mlpl;
@@ -24,7 +25,7 @@ EncodeFn encoder()
     static const EncodeFn fn = [] {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        if (!succeeded(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q)) ||
             q != cudaDriverEntryPointSuccess)
             p = nullptr;
         return reinterpret_cast<EncodeFn>(p);
@@ -58,7 +59,7 @@ bool allow_smem()
 {
     constexpr bool kWide = kForm == kRowsT && kFormB < 0;
     auto allow = [](void (*kernel)(LinearParams)) {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess;
+        return succeeded(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit));
     };
     return allow(linear_kernel<kForm, kFormB, 1, false>) && allow(linear_kernel<kForm, kFormB, 2, false>) &&
            (!kWide || allow(linear_kernel<kForm, kFormB, 2, kWide>));
@@ -298,7 +299,7 @@ bool launch_one(const LinearParams &p, int clusters, int cs, size_t smem, cudaSt
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = cs > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, linear_kernel<kForm, kFormB, kPair, kWide>, p) == cudaSuccess;
+    return succeeded(cudaLaunchKernelEx(&cfg, linear_kernel<kForm, kFormB, kPair, kWide>, p));
 }
 
 // One product (w NULL), or a kRowsT one with the weights' gradient.  items: of the launch, or an upper bound where the
@@ -662,7 +663,7 @@ extern "C" mlp_status mlp_linear_create(const mlp_linear_desc *d, mlp_linear_t *
         (d->bias_dtype != MLP_DT_BF16 && d->bias_dtype != MLP_DT_F32) ||
         (d->dw_dtype != MLP_DT_BF16 && d->dw_dtype != MLP_DT_F32))
         return MLP_ERR_UNSUPPORTED;
-    if (cudaSetDevice(d->device) != cudaSuccess)
+    if (!succeeded(cudaSetDevice(d->device)))
         return MLP_ERR_CUDA;
     mlp_linear *h = new (std::nothrow) mlp_linear();
     if (!h)
@@ -671,7 +672,7 @@ extern "C" mlp_status mlp_linear_create(const mlp_linear_desc *d, mlp_linear_t *
     h->groups = d->experts ? d->experts : 1;
     h->status = nullptr;
     mlp_status st = MLP_OK;
-    if (cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, d->device) != cudaSuccess ||
+    if (!succeeded(cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, d->device)) ||
         !allow_smem<kRows, -1>() || !allow_smem<kRowsT, -1>() || !allow_smem<kReduce, -1>() || !allow_smem<kRowsT, kReduce>()) {
         st = MLP_ERR_CUDA;
     }
@@ -687,18 +688,17 @@ extern "C" mlp_status mlp_linear_create(const mlp_linear_desc *d, mlp_linear_t *
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, linear_kernel<kRows, -1, 1, false>, &cfg) != cudaSuccess || (n < 1 && cs <= 2))
+        if (!succeeded(cudaOccupancyMaxActiveClusters(&n, linear_kernel<kRows, -1, 1, false>, &cfg)) || (n < 1 && cs <= 2))
             st = MLP_ERR_CUDA;
         h->max_clusters[cs] = n;
     }
-    if (st == MLP_OK && cudaMalloc(&h->status, 256) != cudaSuccess) {
+    if (st == MLP_OK && !succeeded(cudaMalloc(&h->status, 256))) {
         h->status = nullptr;
         st = MLP_ERR_OOM;
     }
-    if (st == MLP_OK && cudaMemset(h->status, 0, 256) != cudaSuccess)
+    if (st == MLP_OK && !succeeded(cudaMemset(h->status, 0, 256)))
         st = MLP_ERR_CUDA;
     if (st != MLP_OK) {
-        cudaGetLastError();
         if (h->status)
             cudaFree(h->status);
         delete h;
@@ -748,7 +748,7 @@ extern "C" mlp_status mlp_linear_forward(mlp_linear_t h, int64_t rows, const voi
     if (bad_matrix(X, ldx, K) || bad_matrix(Y, ldy, N) || !W || misaligned(W) || (residual && bad_matrix(residual, ldr, N)) ||
         (Z && bad_matrix(Z, ldz, N)) || (bias && misaligned(bias, h->d.bias_dtype == MLP_DT_F32 ? 4 : 2)))
         return MLP_ERR_INVALID_ARG;
-    if (cudaSetDevice(h->d.device) != cudaSuccess)
+    if (!succeeded(cudaSetDevice(h->d.device)))
         return MLP_ERR_CUDA;
     LinearParams p;
     std::memset(&p, 0, sizeof(p));
@@ -783,9 +783,9 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         return MLP_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (rows == 0) {
-        if (cudaSetDevice(h->d.device) != cudaSuccess ||
-            (dW && cudaMemsetAsync(dW, 0, static_cast<size_t>(h->groups) * K * N * dw_esz, st) != cudaSuccess) ||
-            (dbias && cudaMemsetAsync(dbias, 0, static_cast<size_t>(h->groups) * N * bias_esz, st) != cudaSuccess))
+        if (!succeeded(cudaSetDevice(h->d.device)) ||
+            (dW && !succeeded(cudaMemsetAsync(dW, 0, static_cast<size_t>(h->groups) * K * N * dw_esz, st))) ||
+            (dbias && !succeeded(cudaMemsetAsync(dbias, 0, static_cast<size_t>(h->groups) * N * bias_esz, st))))
             return MLP_ERR_CUDA;
         return MLP_OK;
     }
@@ -793,7 +793,7 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         (dX && (bad_matrix(dX, lddx, K) || !W || misaligned(W))) ||
         (((act && (dX || dW)) || dbias) && (!workspace || misaligned(workspace, 256))))
         return MLP_ERR_INVALID_ARG;
-    if (cudaSetDevice(h->d.device) != cudaSuccess)
+    if (!succeeded(cudaSetDevice(h->d.device)))
         return MLP_ERR_CUDA;
     const void *dz = dY;
     int64_t ld_dz = lddy;
@@ -831,10 +831,10 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         cfg.numAttrs = 1;
         void (*const kernels[])(GradParams) = {act_grad_kernel<kActNone>, act_grad_kernel<kActRelu>, act_grad_kernel<kActGelu>,
                                                act_grad_kernel<kActSilu>};
-        if (cudaLaunchKernelEx(&cfg, kernels[h->d.activation], g) != cudaSuccess)
+        if (!succeeded(cudaLaunchKernelEx(&cfg, kernels[h->d.activation], g)))
             return MLP_ERR_CUDA;
         cfg.gridDim = dim3(static_cast<unsigned>(cdiv(N, 256)), static_cast<unsigned>(h->groups));
-        if (dbias && !dX && !dW && cudaLaunchKernelEx(&cfg, bias_grad_kernel, bias, offsets, g.rows) != cudaSuccess)
+        if (dbias && !dX && !dW && !succeeded(cudaLaunchKernelEx(&cfg, bias_grad_kernel, bias, offsets, g.rows)))
             return MLP_ERR_CUDA;
     }
     if (!dX && !dW)
@@ -882,10 +882,10 @@ extern "C" mlp_status mlp_linear_check(mlp_linear_t h, void *stream)
         return MLP_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint32_t v = 0;
-    if (cudaSetDevice(h->d.device) != cudaSuccess ||
-        cudaMemcpyAsync(&v, h->status, 4, cudaMemcpyDeviceToHost, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
+    if (!succeeded(cudaSetDevice(h->d.device)) ||
+        !succeeded(cudaMemcpyAsync(&v, h->status, 4, cudaMemcpyDeviceToHost, st)) || !succeeded(cudaStreamSynchronize(st)))
         return MLP_ERR_CUDA;
-    if (v && (cudaMemsetAsync(h->status, 0, 4, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess))
+    if (v && (!succeeded(cudaMemsetAsync(h->status, 0, 4, st)) || !succeeded(cudaStreamSynchronize(st))))
         return MLP_ERR_CUDA;
     return static_cast<mlp_status>(v);
 }
