@@ -3,8 +3,9 @@
 // Per row of C columns: mean = sum x / C, var = sum (x - mean)^2 / C, rstd = 1 / sqrt(var + eps),
 // xh = (x - mean) rstd, y = xh gamma + beta.  Backward, with g = dy gamma:
 // dx = rstd (g - mean(g) - xh mean(g xh)), dgamma = sum_rows dy xh, dbeta = sum_rows dy.
-// A handful of operations per element: the memory system is the bound, so every kernel reads its rows
-// once, in the widest loads that the addresses allow, and keeps them in registers between the passes.
+// A handful of operations per element: the memory system is the bound, so rows that fit registers or shared memory are read
+// once, in the widest loads that the addresses allow, and kept there between the passes.  Wider ones, and gradients of
+// arrays whose rows start at different places, are read again for each pass.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -1463,6 +1464,7 @@ constexpr int64_t kOddLeast = 16;     // words a row (forward_odd)
 constexpr size_t kRingLimit = 200 * 1024;
 constexpr size_t kAloneLimit = 226 * 1024;       // of a block that has an SM to itself
 constexpr int64_t kFusedCols = kRingLimit / 8;   // its widest rows
+constexpr int64_t kLoopCols = int64_t{1} << 30;  // the widest rows of kernels that count columns in int
 
 // Vectors per thread of the backward ring kernel, for at most 512 threads and 32 columns a thread.  0: too wide.
 int ring_items(int64_t nvec, int v)
@@ -1709,10 +1711,10 @@ template <typename T, int V>
 bool backward_staged(NormParams &p, Stream &st)
 {
     const int threads = loop_threads(cdiv(p.cols, V), 4, 512);
-    const size_t smem = p.part ? static_cast<size_t>(p.cols) * 8 : 0;
-    if (smem > kRingLimit)
+    if (p.cols > (p.part ? kFusedCols : kLoopCols))
         return false;
-    auto most = [&](int r) { return static_cast<int64_t>(staged_per_sm(threads, static_cast<size_t>(p.cols) * 8, r)) * kSms; };
+    const size_t sums = static_cast<size_t>(p.cols) * 8, smem = p.part ? sums : 0;
+    auto most = [&](int r) { return static_cast<int64_t>(staged_per_sm(threads, sums, r)) * kSms; };
     const bool four = p.rows >= 2 * most(4);
     p.blocks = static_cast<int32_t>(four ? std::min(cdiv(p.rows, 4), most(4)) : std::min(p.rows, most(1)));
     return four ? backward_staged_r<T, V, 4>(p, threads, smem, st) : backward_staged_r<T, V, 1>(p, threads, smem, st);
@@ -1732,13 +1734,18 @@ bool backward_odd(NormParams &p, int64_t ld, Stream &st)
     return false;
 }
 
-// One kernel for all gradients; false where the rows are too wide for it.
+// One kernel for all gradients; false where the rows are too wide for it.  dx alone needs no room for the sums, so any width
+// would fit the staged kernel; but rows in 16-byte units are read faster by norm_dx_kernel (256 x 40000 bf16 21 us, staged 40).
+// Others stay here (4000 x 30002 263 us, there 504).
 template <typename T, int V>
 bool backward_v(NormParams &p, Stream &st)
 {
-    if constexpr (V * sizeof(T) == 16)
+    if constexpr (V * sizeof(T) == 16) {
         if (backward_rings<T, V, false>(p, cdiv(p.cols, V), st))
             return true;
+        if (p.cols > kFusedCols)
+            return false;
+    }
     return backward_staged<T, V * sizeof(T) == 16 ? (sizeof(T) == 2 ? 2 : 1) : V>(p, st);
 }
 
