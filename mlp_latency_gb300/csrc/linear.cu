@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(256, 4) act_grad_kernel(const GradParams p)
     const int32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int32_t col = blockIdx.x * kStrip + lane * 8;
     const bool col_ok = col < p.N;
-    const int32_t b_lo = blockIdx.y * p.block_rows, b_hi = min(b_lo + p.block_rows, p.rows);
+    const int32_t b_lo = blockIdx.y * p.block_rows, b_hi = b_lo + min(p.block_rows, p.rows - b_lo);   // (a sum past the rows could wrap)
     const int32_t *off = nullptr;
     int32_t e = 0;
     if (p.offsets) {   // first group that ends past the block's start
