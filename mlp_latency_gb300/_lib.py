@@ -24,7 +24,7 @@ MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
 MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("mlp_chain.cu", "host_protocol.cpp", "linear.cu", "layer_norm.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("chain_kernel.cuh", "ptx.cuh", "protocol.h", "dep_groups.h",
-                                                     "linear_kernel.cuh", "cuda_call.h")] + [
+                                                     "linear_kernel.cuh", "cuda_call.h", "row_blocks.h")] + [
     os.path.join(INCLUDE, f) for f in ("mlp_chain.h", "mlp_block.h")]
 
 NVCC_FLAGS = [

@@ -11,6 +11,7 @@
 #include "../../include/mlp_block.h"
 #include "cuda_call.h"
 #include "linear_kernel.cuh"
+#include "row_blocks.h"
 
 using namespace mlpl;
 
@@ -488,8 +489,6 @@ __device__ __forceinline__ uint64_t act_grad(float2 dy, float2 z)
     return mul2(two(dy.x, dy.y), fma2(w, s, s));
 }
 
-constexpr int kStrip = 256;    // columns per CTA: 32 lanes x 8
-
 struct GradParams {
     const __nv_bfloat16 *dy, *z;
     __nv_bfloat16 *dz;          // or null
@@ -521,7 +520,7 @@ __global__ void __launch_bounds__(256, 4) act_grad_kernel(const GradParams p)
     const int32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int32_t col = blockIdx.x * kStrip + lane * 8;
     const bool col_ok = col < p.N;
-    const int32_t b_lo = blockIdx.y * p.block_rows, b_hi = b_lo + min(p.block_rows, p.rows - b_lo);   // (a sum past the rows could wrap)
+    const int32_t b_lo = blockIdx.y * p.block_rows, b_hi = block_end(b_lo, p.block_rows, p.rows);
     const int32_t *off = nullptr;
     int32_t e = 0;
     if (p.offsets) {   // first group that ends past the block's start
@@ -624,14 +623,6 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const BiasSums q, const 
     add_bias_sums(q, blockIdx.y, blockIdx.x * 256 + threadIdx.x, lo, hi);
 }
 
-// Rows per block: about four CTAs per SM, at least 16 rows (two per warp).
-int32_t grad_block_rows(const mlp_linear *h, int64_t rows)
-{
-    const int64_t strips = cdiv(h->d.N, kStrip);
-    const int64_t blocks = std::max<int64_t>(1, cdiv(4 * h->num_sms, strips));
-    return static_cast<int32_t>(std::max<int64_t>(16, cdiv(cdiv(rows, blocks), 8) * 8));
-}
-
 // Without an activation dZ is dY.  Where the bias gradient reads dY anyway, a copy of it whose rows start on those lines
 // pays for itself in the products of many rows.
 bool copies_dy(const mlp_linear *h, int64_t rows) { return h->d.activation == MLP_ACT_NONE && h->d.N % 64 != 0 && rows >= 256; }
@@ -722,7 +713,7 @@ extern "C" mlp_status mlp_linear_destroy(mlp_linear_t h)
 static void workspace_layout(const mlp_linear *h, int64_t rows, size_t *part, size_t *total)
 {
     const size_t dz = h->d.activation == MLP_ACT_NONE && !copies_dy(h, rows) ? 0 : align256(static_cast<size_t>(rows) * dz_pitch(h->d.N) * 2);
-    const int64_t blocks = cdiv(rows, grad_block_rows(h, rows));
+    const int64_t blocks = cdiv(rows, grad_block_rows(h->d.N, h->num_sms, rows));
     *part = dz;
     *total = dz + align256(static_cast<size_t>(blocks + h->groups) * h->d.N * 4);
 }
@@ -815,7 +806,7 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         g.rows = static_cast<int32_t>(rows);
         g.N = static_cast<int32_t>(N);
         g.groups = h->groups;
-        g.block_rows = grad_block_rows(h, rows);
+        g.block_rows = grad_block_rows(h->d.N, h->num_sms, rows);
         g.blocks = static_cast<int32_t>(cdiv(rows, g.block_rows));
         g.offsets = offsets;
         g.part = dbias ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part) : nullptr;
