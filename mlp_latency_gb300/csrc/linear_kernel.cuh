@@ -187,8 +187,8 @@ __device__ __forceinline__ bool elect_one()
 __device__ __forceinline__ void fence_proxy_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ------------------------------------------------------------------------------ bounded waits --
-// On expiry: first error wins in the status word, the CTA's abort flag stops the other roles.  Drain
-// waits (own copies and MMAs in flight after an abort) ignore the flag and use a short limit.
+// On expiry: first error wins in the status word, the CTA's abort flag stops the other roles.  Draining waits (for own
+// copies and MMAs in flight after an abort) ignore the flag and use a short limit.
 __device__ __forceinline__ bool lwait(uint64_t *bar, uint32_t parity, LCtrl *c, const LinearParams &p,
                                       bool cluster = false, bool draining = false)
 {
@@ -208,6 +208,13 @@ __device__ __forceinline__ bool lwait(uint64_t *bar, uint32_t parity, LCtrl *c, 
             return false;
         }
     }
+}
+
+// The wait that ends a role, for what it has in flight: the CTA's shared memory and TMEM go away after the roles.  In every
+// run, since another role's wait may run out at any later time; where none does, the other roles wait for the same.
+__device__ __forceinline__ bool settle(uint64_t *bar, uint32_t parity, LCtrl *c, const LinearParams &p)
+{
+    return lwait(bar, parity, c, p) || lwait(bar, parity, c, p, false, true);
 }
 
 // Accumulator of an item, and the parity of its uses.  Wide tiles have one: two are more than TMEM holds.
@@ -422,7 +429,7 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
     const bool shared_ring = p.split > 1 && p.recv_bufs == 0;
     const int32_t n_items = c->n_items[0], n_items_b = c->n_items[1];
     const uint64_t pol = policy_evict_normal();
-    uint32_t fills = 0, tail_ph = 0, tail_use = 0, item_ph = 0;
+    uint32_t fills = 0, tail_ph = 0, tail_last = 0, item_ph = 0;   // (tail_last: slots whose last fill was masked)
     uint32_t ps = 0, pph = 0;
     bool ok = true, first = true;
     griddep_wait();   // a programmatic launch: the kernel before this one is complete from here on
@@ -465,7 +472,6 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
                 if (masked) {
                     // completes on this CTA's own tail barrier; warp 2 zeroes the rows and completes `full`
                     mbar_arrive_expect_tx(&c->tail[ps], bytes);
-                    tail_use |= 1u << ps;
                 } else if (!half) {
                     mbar_arrive_expect_tx(&c->full[ps], kPair * bytes);
                     if (kMasks && kPair == 2)
@@ -507,8 +513,11 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
                         load3(b + j * kBoxBytes, map_q, q_row + 64 * j, k, q_grp);
                 }
             }
-            if (kMasks && masked_rows(form, p, t, kb) != 0)
-                tail_ph ^= 1u << ps;   // (the other thread's too: the slot's tail barrier counts both)
+            if (kMasks) {   // (the other thread's too: the slot's tail barrier counts both)
+                const uint32_t bit = masked_rows(form, p, t, kb) != 0 ? 1u << ps : 0u;
+                tail_ph ^= bit;
+                tail_last = (tail_last & ~(1u << ps)) | bit;
+            }
             ++fills;
             if (++ps == num_pipe) {
                 ps = 0;
@@ -516,18 +525,18 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
             }
         }
     }
-    if (c->abort_flag) {
-        // Let this thread's copies land before the shared memory goes away.  Unmasked fills of a pair complete on
-        // the leader's barriers (the peer fills only what the leader armed, and keeps its shared memory
-        // until the final cluster barrier); masked fills complete on each CTA's own.
-        for (uint32_t f = fills > num_pipe ? fills - num_pipe : 0u; f < fills; ++f) {
-            const uint32_t slot = f % num_pipe;
-            if (shared_ring ? which != 0 : (slot & 1u) != which)
-                continue;
-            if (tail_use >> slot & 1u)
-                lwait(&c->tail[slot], (tail_ph >> slot & 1u) ^ 1u, c, p, false, true);
-            if (!half)
-                lwait(&c->full[slot], (f / num_pipe) & 1u, c, p, false, true);
+    // This thread's copies land: each on its slot's last barrier phase.  Unmasked fills of a pair complete on the leader's
+    // barriers (the peer fills only what the leader armed, and keeps its shared memory until the cluster barriers at the
+    // end); masked fills complete on each CTA's own.  A wait that ran out was long enough for the rest.
+    for (uint32_t f = fills > num_pipe ? fills - num_pipe : 0u; f < fills; ++f) {
+        const uint32_t slot = f % num_pipe;
+        if (shared_ring ? which != 0 : (slot & 1u) != which)
+            continue;
+        if (tail_last >> slot & 1u) {
+            if (!settle(&c->tail[slot], (tail_ph >> slot & 1u) ^ 1u, c, p))
+                break;
+        } else if (!half && !settle(&c->full[slot], (f / num_pipe) & 1u, c, p)) {
+            break;
         }
     }
 }
@@ -603,9 +612,9 @@ __device__ __forceinline__ void l_role_mma(const LinearParams &p, LCtrl *c, cons
             mma_commit_g<kPair>(tfull_peer0 + acc * 8u);
         ++tiles;
     }
-    if (c->abort_flag && issued) {
+    if (issued) {
         mma_commit_g<kPair>(smem_u32(&c->drain));
-        lwait(&c->drain, 0, c, p, false, true);
+        settle(&c->drain, 0, c, p);
     }
 }
 
