@@ -100,8 +100,8 @@ mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const void *dY, int
                                void *dX, int64_t lddx, void *dW, void *dbias, void *workspace, void *stream);
 
 /* Synchronise `stream`, read the handle's device status word and clear it: OK, TIMEOUT, or INVALID_ARG
- * (bad offsets), the first that occurred.  After a TIMEOUT further calls of the handle do nothing until this
- * is called. */
+ * (bad offsets), the first that occurred.  After a TIMEOUT further calls of the handle store no output until this
+ * is called (but for the zeros of a gradient without rows). */
 mlp_status mlp_linear_check(mlp_linear_t h, void *stream);
 
 /* The variant a product of this handle runs with for `rows` rows: pass 0 = Y, 1 = dX, 2 = dW. */

@@ -614,10 +614,12 @@ __global__ void __launch_bounds__(256, 4) act_grad_kernel(const GradParams p)
 }
 
 // dbias where no product is asked for that would add the sums on its way.
-__global__ void __launch_bounds__(256) bias_grad_kernel(const BiasSums q, const int32_t *offsets, int32_t rows)
+__global__ void __launch_bounds__(256) bias_grad_kernel(const BiasSums q, const int32_t *offsets, int32_t rows, uint32_t *status)
 {
     griddep_launch_dependents();
     griddep_wait();
+    if (ld_relaxed_gpu_u32(status) == kStTimeout)
+        return;
     int32_t lo, hi;
     group_range(offsets, rows, blockIdx.y, lo, hi);
     add_bias_sums(q, blockIdx.y, blockIdx.x * 256 + threadIdx.x, lo, hi);
@@ -825,7 +827,7 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         if (!succeeded(cudaLaunchKernelEx(&cfg, kernels[h->d.activation], g)))
             return MLP_ERR_CUDA;
         cfg.gridDim = dim3(static_cast<unsigned>(cdiv(N, 256)), static_cast<unsigned>(h->groups));
-        if (dbias && !dX && !dW && !succeeded(cudaLaunchKernelEx(&cfg, bias_grad_kernel, bias, offsets, g.rows)))
+        if (dbias && !dX && !dW && !succeeded(cudaLaunchKernelEx(&cfg, bias_grad_kernel, bias, offsets, g.rows, h->status)))
             return MLP_ERR_CUDA;
     }
     if (!dX && !dW)

@@ -833,6 +833,7 @@ struct EpiState {
     uint32_t tiles;
     int32_t buf;                    // receive buffer of this item, and how often it was used before (parity)
     uint32_t buf_ph;
+    int32_t keep;                   // -1, or 0: the launch before ended in a wait that ran out, and this one stores nothing
 };
 
 // One tile; false after an abort.
@@ -938,7 +939,7 @@ __device__ __forceinline__ bool epilogue_tile(const LinearParams &lp, const Prob
         }
         bool freed = false;
         for (int32_t col = first; col < c_hi; col += 64) {
-            const int32_t row_lim = row_lim_of(col), seg_lim = seg_lim_of(col);
+            const int32_t row_lim = row_lim_of(col) & st.keep, seg_lim = seg_lim_of(col);
             // accumulator columns [col, col + 32) of this lane, partial sums of all slices in slice order
             float v[32];
             {
@@ -1102,7 +1103,9 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
     st.buf_ph = 0;
     const int32_t n_items = c->n_items[0], n_items_b = c->n_items[1];
     griddep_wait();
-    if (p.bias.out) {   // (while the first tile's products run: a launch of its own took 3 us)
+    // (from here on only this launch or another stream's can report a wait that ran out)
+    st.keep = ld_relaxed_gpu_u32(p.status) == kStTimeout ? 0 : -1;
+    if (p.bias.out && st.keep) {   // (while the first tile's products run: a launch of its own took 3 us)
         const int32_t strips = (p.bias.N + kEpi * 32 - 1) / (kEpi * 32), todo = strips * p.groups;
         for (int32_t i = static_cast<int32_t>(blockIdx.x); i < todo; i += static_cast<int32_t>(gridDim.x)) {
             const int32_t e = i / strips, lo = p.offsets ? g.start[e] : 0;
@@ -1171,7 +1174,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
             mbar_init(&c->ringfree, kEpi);
             c->abort_flag = 0;
             // a wait that ran out is sticky: do nothing.  (Bad offsets are not: a CTA of this very grid may have just
-            // reported them, and the CTAs of a cluster must agree.)
+            // reported them.)  The launch before may still be running and report one: see EpiState::keep.
             c->skip = ld_relaxed_gpu_u32(p.status) == kStTimeout;
         }
         fence_barrier_init();
@@ -1229,7 +1232,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
     cluster_sync_all();   // barriers initialised before any remote arrival
     tc_fence_after();
     const uint32_t tmem_base = c->tmem_base;
-    if (!c->skip) {
+    if (!ld_cluster_s32(map_to_rank(&c->skip, 0))) {   // the CTAs of a cluster agree: they wait for one another
         if (warp == 0) {
             if (p.offsets)
                 have = w.next(p, g, c->n_items[0], c->n_items[1], t);

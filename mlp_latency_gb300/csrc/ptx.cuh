@@ -100,6 +100,13 @@ __device__ __forceinline__ void st_cluster_s32(uint32_t cluster_addr, int32_t v)
     asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ int32_t ld_cluster_s32(uint32_t cluster_addr)
+{
+    int32_t v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
 // Arrive once on an mbarrier of any CTA in the cluster, releasing this thread's prior writes at
 // cluster scope.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)

@@ -64,3 +64,33 @@ def test_both_gradients_in_one_launch_end_too(mc):  # noqa: F811
             assert lin.check() == status
             outs.append((dX, dW, db))
     assert all(torch.equal(a, b) for a, b in zip(outs[0], outs[2]))
+
+
+def test_the_calls_after_it_store_nothing_until_it_is_read(mc):  # noqa: F811
+    """Also those whose launch came onto the SMs before the wait ran out: the long product here has 4 tiles, beside which the next
+    launch starts at once."""
+    rows, K, N = 262144, 256, 256
+    X, dY, W, b = draw((rows, K), 1.0, 1).to(DEV), draw((rows, N), 1.0, 2).to(DEV), draw((K, N), 0.1, 3).to(DEV), draw((N,), 1.0, 4).to(DEV)
+    few = slice(0, 512)
+    dW, Y, Z, dX = torch.empty_like(W), blank(512, N, 0), blank(512, N, 0), blank(512, K, 0)
+    db, db2 = (torch.full((N,), float("nan"), dtype=BF, device=DEV) for _ in range(2))
+    with mc.Linear(K, N, timeout_us=LIMIT_US) as lin:
+        ws = torch.empty(lin.workspace_size(512), dtype=torch.uint8, device=DEV)
+
+        def later():
+            lin.forward(X[few], W, Y, bias=b, Z=Z)
+            lin.backward(dY[few], None, W, dX=dX, dbias=db, workspace=ws)
+            lin.backward(dY[few], None, None, dbias=db2, workspace=ws)
+
+        for _ in range(5):
+            lin.backward(dY, X, None, dW=dW)
+            later()
+            later()
+            assert lin.check() == mc.ERR_TIMEOUT
+            for t in (Y, Z, dX, db, db2):
+                assert bool(torch.isnan(t.float()).all())
+        later()
+        assert lin.check() == 0
+    for t in (Y, Z, dX, db, db2):
+        assert bool(torch.isfinite(t.float()).all())
+    assert torch.equal(db, db2)
