@@ -66,7 +66,8 @@ typedef struct {
     mlp_dtype bias_dtype;     /* BF16 or F32: bias and its gradient                                     */
     mlp_dtype dw_dtype;       /* BF16 or F32: the weights' gradient                                     */
     int32_t device;
-    uint32_t timeout_us;      /* bounded device waits; 0 = 2 000 000                                    */
+    uint32_t timeout_us;      /* limit of every device wait, the longest of which is for the reduction of a
+                                 tile; work before the call on its stream does not count; 0 = 2 000 000  */
 } mlp_linear_desc;
 
 typedef struct mlp_linear *mlp_linear_t;

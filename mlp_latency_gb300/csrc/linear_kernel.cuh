@@ -573,6 +573,7 @@ __device__ __forceinline__ void l_role_mma(const LinearParams &p, LCtrl *c, cons
     bool issued = false, ok = true;
     Walk<kForm, kFormB, kPair> w(p);
     Tile t;
+    griddep_wait();   // as the copying threads do: what is left of the kernel before counts against no wait's limit
     while (w.next(p, g, n_items, n_items_b, t)) {
         if (kFormB >= 0)
             describe(problem_of<kFormB>(p, t));

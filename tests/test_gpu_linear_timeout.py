@@ -94,3 +94,19 @@ def test_the_calls_after_it_store_nothing_until_it_is_read(mc):  # noqa: F811
     for t in (Y, Z, dX, db, db2):
         assert bool(torch.isfinite(t.float()).all())
     assert torch.equal(db, db2)
+
+
+@pytest.mark.parametrize("experts", [0, 2])
+def test_the_launch_before_does_not_count(mc, experts):  # noqa: F811
+    """A short product behind one of a millisecond, which leaves most SMs free: its launch starts beside it and waits for its end."""
+    rows, K, N, n = 262144, 256, 256, 64
+    lead = (experts,) if experts else ()
+    X, dY, W = draw((rows, K), 1.0, 1).to(DEV), draw((rows, N), 1.0, 2).to(DEV), draw(lead + (K, N), 0.1, 3).to(DEV)
+    off = torch.tensor([0, 20, n], dtype=torch.int32, device=DEV) if experts else None
+    dW, Y = torch.empty(K, N, dtype=BF, device=DEV), blank(n, N, 0)
+    with mc.Linear(K, N) as slow, mc.Linear(K, N, experts=experts, timeout_us=200) as lin:
+        for _ in range(5):
+            slow.backward(dY, X, None, dW=dW)
+            lin.forward(X[:n], W, Y, offsets=off)
+            assert lin.check() == 0 and slow.check() == 0
+    assert bool(torch.isfinite(Y.float()).all())
