@@ -95,7 +95,7 @@ mlp_status mlp_linear_forward(mlp_linear_t h, int64_t rows, const void *X, int64
  * dZ is rounded to bf16 for the two products (the tensor cores' operand type); db sums it unrounded.
  * Any of dX, dW, dbias may be NULL (not computed); Z may be NULL without an activation; X may be NULL
  * without dW, W without dX.  The gradients of an expert without rows are zero.  dX rows outside every
- * expert's range are not written.  workspace: >= mlp_linear_workspace_size bytes, 256-byte aligned. */
+ * expert's range are not written.  Bad offsets are clamped and reported as above.  workspace: >= mlp_linear_workspace_size bytes, 256-byte aligned. */
 mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const void *dY, int64_t lddy, const void *X,
                                int64_t ldx, const void *W, const void *Z, int64_t ldz, const int32_t *offsets,
                                void *dX, int64_t lddx, void *dW, void *dbias, void *workspace, void *stream);

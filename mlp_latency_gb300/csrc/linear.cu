@@ -620,9 +620,12 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const BiasSums q, const 
     griddep_wait();
     if (ld_relaxed_gpu_u32(status) == kStTimeout)
         return;
+    const int32_t e = static_cast<int32_t>(blockIdx.y);
     int32_t lo, hi;
-    group_range(offsets, rows, blockIdx.y, lo, hi);
-    add_bias_sums(q, blockIdx.y, blockIdx.x * 256 + threadIdx.x, lo, hi);
+    group_range(offsets, rows, e, lo, hi);
+    if (offsets && threadIdx.x == 0 && (lo != offsets[e] || hi != offsets[e + 1]))
+        atomicCAS(status, 0u, kStBadOffsets);
+    add_bias_sums(q, e, blockIdx.x * 256 + threadIdx.x, lo, hi);
 }
 
 // Without an activation dZ is dY.  Where the bias gradient reads dY anyway, a copy of it whose rows start on those lines
