@@ -67,7 +67,8 @@ typedef struct {
     mlp_dtype dw_dtype;       /* BF16 or F32: the weights' gradient                                     */
     int32_t device;
     uint32_t timeout_us;      /* limit of every device wait, the longest of which is for the reduction of a
-                                 tile; work before the call on its stream does not count; 0 = 2 000 000  */
+                                 tile; work before the call on its stream does not count; 0 = 2 000 000 and
+                                 one more for every 64 terms of the longest reduction                  */
 } mlp_linear_desc;
 
 typedef struct mlp_linear *mlp_linear_t;
@@ -95,7 +96,8 @@ mlp_status mlp_linear_forward(mlp_linear_t h, int64_t rows, const void *X, int64
  * dZ is rounded to bf16 for the two products (the tensor cores' operand type); db sums it unrounded.
  * Any of dX, dW, dbias may be NULL (not computed); Z may be NULL without an activation; X may be NULL
  * without dW, W without dX.  The gradients of an expert without rows are zero.  dX rows outside every
- * expert's range are not written.  Bad offsets are clamped and reported as above.  workspace: >= mlp_linear_workspace_size bytes, 256-byte aligned. */
+ * expert's range are not written.  Bad offsets are clamped and reported as above.  workspace: >=
+ * mlp_linear_workspace_size bytes, 256-byte aligned. */
 mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const void *dY, int64_t lddy, const void *X,
                                int64_t ldx, const void *W, const void *Z, int64_t ldz, const int32_t *offsets,
                                void *dX, int64_t lddx, void *dW, void *dbias, void *workspace, void *stream);

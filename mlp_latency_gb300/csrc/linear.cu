@@ -326,7 +326,10 @@ mlp_status launch(const mlp_linear *h, LinearParams &p, const Plan &pl, const Pl
     while (p.tmem_cols < cols)
         p.tmem_cols *= 2;
     p.status = h->status;
-    p.timeout_ns = static_cast<uint64_t>(h->d.timeout_us ? h->d.timeout_us : 2000000u) * 1000ull;
+    // By default two seconds and a microsecond for each k block of the longest reduction, which takes 0.2 to 0.3 (600 million
+    // rows of 8 x 8: 2.5 s for the one tile)
+    const int64_t kb = cdiv(std::max({p.pr[0].k_ext, p.pr[1].k_ext, w || pl.form == kReduce ? p.rows : 0}), kKB);
+    p.timeout_ns = h->d.timeout_us ? h->d.timeout_us * 1000ull : 2000000000ull + static_cast<uint64_t>(kb) * 1000ull;
     const int cs = pl.pair * pl.split;
     const int clusters = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(items, h->max_clusters[cs])));
     const size_t smem = linear_smem_bytes(pl.form != kRows, static_cast<uint32_t>(p.num_pipe) * p.slot_bytes,

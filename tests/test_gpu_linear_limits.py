@@ -19,3 +19,16 @@ def test_bad_offsets_of_a_gradient_are_reported(mc, offsets, what):  # noqa: F81
         for off, status in ((offsets, mc.ERR_INVALID_ARG), ([0, 60, 100], 0)):
             lin.backward(dY, X, W, offsets=torch.tensor(off, dtype=torch.int32, device=DEV), workspace=ws, **asked)
             assert lin.check() == status
+
+
+def test_a_reduction_over_very_many_rows_is_within_the_default_limit(mc):  # noqa: F811
+    """600 million rows, of which only the last are not zero: exact."""
+    rows, n, last = 600_000_000, 8, 5
+    X, dY = (torch.zeros(rows, n, dtype=BF, device=DEV) for _ in range(2))
+    X[-last:] = torch.arange(last * n, device=DEV).view(last, n).to(BF)
+    dY[-last:] = torch.arange(last * n, device=DEV).view(last, n).flip(0).to(BF)
+    dW = torch.full((n, n), float("nan"), device=DEV)
+    with mc.Linear(n, n, dw_dtype=torch.float32) as lin:
+        lin.backward(dY, X, None, dW=dW)
+        assert lin.check() == 0
+    assert torch.equal(dW.cpu().double(), X[-last:].cpu().double().t() @ dY[-last:].cpu().double())
