@@ -2,9 +2,10 @@
 residual in its epilogue, dense or grouped by expert, forward and backward.
 
 Argument checks and marshalling only, compiled (csrc/marshal.cpp) because a call takes a few microseconds: every
-tensor is a CUDA tensor of the caller's, outputs and workspaces included, and a call enqueues work on ``stream``
-(default: torch's current stream) without synchronising.  A wrong dtype, shape or stride raises ValueError, an error of
-the library MlpChainError.
+tensor is a CUDA tensor of the caller's, outputs and workspaces included, all of a call on one device (x's for layer
+norm, the handle's for Linear), and a call enqueues work on ``stream`` (default: torch's current stream of that device)
+without synchronising.  A wrong dtype, shape, device or order of elements raises ValueError, an error of the library
+(strides and alignments that it does not take, for instance) MlpChainError.
 """
 from __future__ import annotations
 

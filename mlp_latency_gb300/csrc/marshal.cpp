@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -43,11 +44,16 @@ const at::Tensor &tensor(PyObject *o, const char *name)
     return THPVariable_Unpack(o);
 }
 
-[[noreturn]] void refuse(const at::Tensor &t, const char *name, const char *kind, at::ScalarType dtype, at::IntArrayRef shape)
+// All tensors of a call are on one device: a kernel runs on one, with addresses that mean something there.
+bool elsewhere(const at::Tensor &t, int device) { return !t.is_cuda() || t.get_device() != device; }
+
+[[noreturn]] void refuse(const at::Tensor &t, const char *name, const char *kind, at::ScalarType dtype, at::IntArrayRef shape, int device)
 {
     std::ostringstream s;
-    s << name << ": expected a " << kind << "CUDA tensor " << c10::toString(dtype) << ' ' << shape << ", got "
-      << c10::toString(t.scalar_type()) << ' ' << t.sizes() << " on " << t.device();
+    s << name << ": expected a " << kind << "CUDA tensor " << c10::toString(dtype) << ' ' << shape;
+    if (device >= 0)
+        s << " on cuda:" << device;
+    s << ", got " << c10::toString(t.scalar_type()) << ' ' << t.sizes() << " on " << t.device();
     throw Refused(s.str());
 }
 
@@ -56,44 +62,50 @@ struct Matrix {
     int64_t ld = 0;
 };
 
-// A matrix whose rows are contiguous.
-Matrix matrix(PyObject *o, const char *name, int64_t rows, int64_t cols, at::ScalarType dtype)
-{
-    const at::Tensor &t = tensor(o, name);
-    if (t.scalar_type() != dtype || t.dim() != 2 || t.size(0) != rows || t.size(1) != cols || !t.is_cuda())
-        refuse(t, name, "", dtype, {rows, cols});
-    if (t.stride(1) != 1 && cols > 1)
-        throw Refused(std::string(name) + ": rows must be contiguous");
-    return {t.data_ptr(), rows > 1 ? t.stride(0) : (cols + 7) & ~int64_t{7}};   // (one row: any stride will do)
-}
+// What the tensors of a call have to be.
+struct Tensors {
+    int device;
 
-Matrix matrix_or_none(PyObject *o, const char *name, int64_t rows, int64_t cols, at::ScalarType dtype)
-{
-    return absent(o) ? Matrix() : matrix(o, name, rows, cols, dtype);
-}
+    // A matrix whose rows are contiguous.
+    Matrix matrix(PyObject *o, const char *name, int64_t rows, int64_t cols, at::ScalarType dtype) const
+    {
+        const at::Tensor &t = tensor(o, name);
+        if (t.scalar_type() != dtype || t.dim() != 2 || t.size(0) != rows || t.size(1) != cols || elsewhere(t, device))
+            refuse(t, name, "", dtype, {rows, cols}, device);
+        if (t.stride(1) != 1 && cols > 1)
+            throw Refused(std::string(name) + ": rows must be contiguous");
+        return {t.data_ptr(), rows > 1 ? t.stride(0) : (cols + 7) & ~int64_t{7}};   // (one row: any stride will do)
+    }
 
-void *dense(PyObject *o, const char *name, at::IntArrayRef shape, at::ScalarType dtype)
-{
-    const at::Tensor &t = tensor(o, name);
-    if (t.scalar_type() != dtype || t.sizes() != shape || !t.is_cuda() || !t.is_contiguous())
-        refuse(t, name, "contiguous ", dtype, shape);
-    return t.data_ptr();
-}
+    Matrix matrix_or_none(PyObject *o, const char *name, int64_t rows, int64_t cols, at::ScalarType dtype) const
+    {
+        return absent(o) ? Matrix() : matrix(o, name, rows, cols, dtype);
+    }
 
-void *dense_or_none(PyObject *o, const char *name, at::IntArrayRef shape, at::ScalarType dtype)
-{
-    return absent(o) ? nullptr : dense(o, name, shape, dtype);
-}
+    void *dense(PyObject *o, const char *name, at::IntArrayRef shape, at::ScalarType dtype) const
+    {
+        const at::Tensor &t = tensor(o, name);
+        if (t.scalar_type() != dtype || t.sizes() != shape || elsewhere(t, device) || !t.is_contiguous())
+            refuse(t, name, "contiguous ", dtype, shape, device);
+        return t.data_ptr();
+    }
 
-void *workspace(PyObject *o, size_t need)
-{
-    if (absent(o))
-        return nullptr;
-    const at::Tensor &t = tensor(o, "workspace");
-    if (!t.is_cuda() || !t.is_contiguous() || t.nbytes() < need)
-        throw Refused("workspace: expected a contiguous CUDA tensor of at least " + std::to_string(need) + " bytes");
-    return t.data_ptr();
-}
+    void *dense_or_none(PyObject *o, const char *name, at::IntArrayRef shape, at::ScalarType dtype) const
+    {
+        return absent(o) ? nullptr : dense(o, name, shape, dtype);
+    }
+
+    void *workspace(PyObject *o, size_t need) const
+    {
+        if (absent(o))
+            return nullptr;
+        const at::Tensor &t = tensor(o, "workspace");
+        if (elsewhere(t, device) || !t.is_contiguous() || t.nbytes() < need)
+            throw Refused("workspace: expected a contiguous CUDA tensor of at least " + std::to_string(need) + " bytes on cuda:" +
+                          std::to_string(device));
+        return t.data_ptr();
+    }
+};
 
 // None: torch's current stream of the device; an address; or an object with one in cuda_stream.
 void *stream_of(PyObject *o, int device)
@@ -181,14 +193,16 @@ PyObject *norm_forward(PyObject *, PyObject *const *a, Py_ssize_t n)
         const at::Tensor &t = norm_input(a[0]);
         const at::ScalarType dt = t.scalar_type(), wd = weight_type({a[1], a[2]});
         const int64_t R = t.size(0), C = t.size(1);
-        const Matrix x = matrix(a[0], "x", R, C, dt), y = matrix(a[3], "y", R, C, dt);
-        const void *gamma = dense_or_none(a[1], "gamma", {C}, wd), *beta = dense_or_none(a[2], "beta", {C}, wd);
-        float *mean = static_cast<float *>(dense_or_none(a[4], "mean", {R}, kF32));
-        float *rstd = static_cast<float *>(dense_or_none(a[5], "rstd", {R}, kF32));
+        const Tensors on{static_cast<int>(t.get_device())};
+        const Matrix x = on.matrix(a[0], "x", R, C, dt), y = on.matrix(a[3], "y", R, C, dt);
+        const void *gamma = on.dense_or_none(a[1], "gamma", {C}, wd), *beta = on.dense_or_none(a[2], "beta", {C}, wd);
+        float *mean = static_cast<float *>(on.dense_or_none(a[4], "mean", {R}, kF32));
+        float *rstd = static_cast<float *>(on.dense_or_none(a[5], "rstd", {R}, kF32));
         const float eps = static_cast<float>(PyFloat_AsDouble(a[6]));
         void *st = stream_of(a[7], t.get_device());
         if (PyErr_Occurred())
             return 0;
+        const c10::cuda::CUDAGuard guard(t.device());   // (a layer norm launches on the current device)
         return unlocked([&] { return norm_forward_fn(R, C, x.p, x.ld, code(dt), gamma, beta, code(wd), eps, y.p, y.ld, mean, rstd, st); });
     });
 }
@@ -200,18 +214,20 @@ PyObject *norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
         const at::Tensor &t = norm_input(a[1]);
         const at::ScalarType dt = t.scalar_type(), wd = weight_type({a[2], a[6], a[7]});
         const int64_t R = t.size(0), C = t.size(1);
-        const Matrix dy = matrix(a[0], "dy", R, C, dt), x = matrix(a[1], "x", R, C, dt);
-        const Matrix add = matrix_or_none(a[8], "dx_add", R, C, dt), dx = matrix_or_none(a[5], "dx", R, C, dt);
-        const void *gamma = dense_or_none(a[2], "gamma", {C}, wd);
-        const float *mean = static_cast<float *>(dense(a[3], "mean", {R}, kF32)), *rstd = static_cast<float *>(dense(a[4], "rstd", {R}, kF32));
-        void *dgamma = dense_or_none(a[6], "dgamma", {C}, wd), *dbeta = dense_or_none(a[7], "dbeta", {C}, wd);
+        const Tensors on{static_cast<int>(t.get_device())};
+        const Matrix dy = on.matrix(a[0], "dy", R, C, dt), x = on.matrix(a[1], "x", R, C, dt);
+        const Matrix add = on.matrix_or_none(a[8], "dx_add", R, C, dt), dx = on.matrix_or_none(a[5], "dx", R, C, dt);
+        const void *gamma = on.dense_or_none(a[2], "gamma", {C}, wd);
+        const float *mean = static_cast<float *>(on.dense(a[3], "mean", {R}, kF32)), *rstd = static_cast<float *>(on.dense(a[4], "rstd", {R}, kF32));
+        void *dgamma = on.dense_or_none(a[6], "dgamma", {C}, wd), *dbeta = on.dense_or_none(a[7], "dbeta", {C}, wd);
         size_t need = 0;
         if (dgamma || dbeta)
             if (const mlp_status s = norm_workspace_fn(R, C, &need))
                 return static_cast<int>(s);
-        void *ws = workspace(a[9], need), *st = stream_of(a[10], t.get_device());
+        void *ws = on.workspace(a[9], need), *st = stream_of(a[10], t.get_device());
         if (PyErr_Occurred())
             return 0;
+        const c10::cuda::CUDAGuard guard(t.device());
         return unlocked([&] {
             return norm_backward_fn(R, C, dy.p, dy.ld, x.p, x.ld, code(dt), gamma, code(wd), mean, rstd, add.p, add.ld, dx.p, dx.ld,
                                     dgamma, dbeta, ws, st);
@@ -285,7 +301,7 @@ int64_t rows_of(PyObject *o, const char *name)
 const int32_t *offsets_of(const LinearArgs &l, PyObject *o)
 {
     if (l.experts)
-        return static_cast<const int32_t *>(dense(o, "offsets", {l.experts + int64_t{1}}, at::ScalarType::Int));
+        return static_cast<const int32_t *>(Tensors{l.device}.dense(o, "offsets", {l.experts + int64_t{1}}, at::ScalarType::Int));
     if (!absent(o))
         throw Refused("offsets: this handle has no experts");
     return nullptr;
@@ -299,9 +315,10 @@ PyObject *linear_forward(PyObject *, PyObject *const *a, Py_ssize_t n)
             return static_cast<int>(MLP_ERR_INVALID_ARG);
         const LinearArgs &l = args_of(a[0]);
         const int64_t R = rows_of(a[1], "X");
-        const Matrix x = matrix(a[1], "X", R, l.K, kBf16), y = matrix(a[3], "Y", R, l.N, kBf16);
-        const Matrix r = matrix_or_none(a[5], "residual", R, l.N, kBf16), z = matrix_or_none(a[6], "Z", R, l.N, kBf16);
-        const void *w = dense(a[2], "W", l.weight_shape, kBf16), *bias = dense_or_none(a[4], "bias", l.bias_shape, l.bias);
+        const Tensors on{l.device};
+        const Matrix x = on.matrix(a[1], "X", R, l.K, kBf16), y = on.matrix(a[3], "Y", R, l.N, kBf16);
+        const Matrix r = on.matrix_or_none(a[5], "residual", R, l.N, kBf16), z = on.matrix_or_none(a[6], "Z", R, l.N, kBf16);
+        const void *w = on.dense(a[2], "W", l.weight_shape, kBf16), *bias = on.dense_or_none(a[4], "bias", l.bias_shape, l.bias);
         const int32_t *off = offsets_of(l, a[7]);
         void *st = stream_of(a[8], l.device);
         if (PyErr_Occurred())
@@ -318,18 +335,19 @@ PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
             return static_cast<int>(MLP_ERR_INVALID_ARG);
         const LinearArgs &l = args_of(a[0]);
         const int64_t R = rows_of(a[1], "dY");
-        const Matrix dy = matrix(a[1], "dY", R, l.N, kBf16);
-        const Matrix x = absent(a[6]) ? matrix_or_none(a[2], "X", R, l.K, kBf16) : matrix(a[2], "X", R, l.K, kBf16);
-        const Matrix z = l.act ? matrix(a[4], "Z", R, l.N, kBf16) : matrix_or_none(a[4], "Z", R, l.N, kBf16);
-        const Matrix dx = matrix_or_none(a[5], "dX", R, l.K, kBf16);
-        const void *w = absent(a[5]) ? dense_or_none(a[3], "W", l.weight_shape, kBf16) : dense(a[3], "W", l.weight_shape, kBf16);
-        void *dw = dense_or_none(a[6], "dW", l.weight_shape, l.dw), *db = dense_or_none(a[7], "dbias", l.bias_shape, l.bias);
+        const Tensors on{l.device};
+        const Matrix dy = on.matrix(a[1], "dY", R, l.N, kBf16);
+        const Matrix x = absent(a[6]) ? on.matrix_or_none(a[2], "X", R, l.K, kBf16) : on.matrix(a[2], "X", R, l.K, kBf16);
+        const Matrix z = l.act ? on.matrix(a[4], "Z", R, l.N, kBf16) : on.matrix_or_none(a[4], "Z", R, l.N, kBf16);
+        const Matrix dx = on.matrix_or_none(a[5], "dX", R, l.K, kBf16);
+        const void *w = absent(a[5]) ? on.dense_or_none(a[3], "W", l.weight_shape, kBf16) : on.dense(a[3], "W", l.weight_shape, kBf16);
+        void *dw = on.dense_or_none(a[6], "dW", l.weight_shape, l.dw), *db = on.dense_or_none(a[7], "dbias", l.bias_shape, l.bias);
         const int32_t *off = offsets_of(l, a[8]);
         size_t need = 0;
         if (l.act || db)
             if (const mlp_status s = linear_workspace_fn(l.h, R, &need))
                 return static_cast<int>(s);
-        void *ws = workspace(a[9], need), *st = stream_of(a[10], l.device);
+        void *ws = on.workspace(a[9], need), *st = stream_of(a[10], l.device);
         if (PyErr_Occurred())
             return 0;
         return unlocked([&] { return linear_backward_fn(l.h, R, dy.p, dy.ld, x.p, x.ld, w, z.p, z.ld, off, dx.p, dx.ld, dw, db, ws, st); });
