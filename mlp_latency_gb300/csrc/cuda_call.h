@@ -12,4 +12,22 @@ inline bool succeeded(cudaError_t e)
     return e == cudaSuccess;
 }
 
+// A handle's device, for the length of a call: the caller's current device is the same afterwards.
+class OnDevice {
+public:
+    explicit OnDevice(int device) : ok_(succeeded(cudaGetDevice(&before_)) && succeeded(cudaSetDevice(device))), changed_(ok_ && device != before_) {}
+    ~OnDevice()
+    {
+        if (changed_)
+            succeeded(cudaSetDevice(before_));
+    }
+    OnDevice(const OnDevice &) = delete;
+    OnDevice &operator=(const OnDevice &) = delete;
+    explicit operator bool() const { return ok_; }
+
+private:
+    int before_ = 0;
+    bool ok_, changed_;
+};
+
 }  // namespace mlpc

@@ -662,7 +662,8 @@ extern "C" mlp_status mlp_linear_create(const mlp_linear_desc *d, mlp_linear_t *
         (d->bias_dtype != MLP_DT_BF16 && d->bias_dtype != MLP_DT_F32) ||
         (d->dw_dtype != MLP_DT_BF16 && d->dw_dtype != MLP_DT_F32))
         return MLP_ERR_UNSUPPORTED;
-    if (!succeeded(cudaSetDevice(d->device)))
+    const OnDevice on(d->device);
+    if (!on)
         return MLP_ERR_CUDA;
     mlp_linear *h = new (std::nothrow) mlp_linear();
     if (!h)
@@ -711,8 +712,8 @@ extern "C" mlp_status mlp_linear_destroy(mlp_linear_t h)
 {
     if (!h)
         return MLP_ERR_INVALID_ARG;
-    cudaSetDevice(h->d.device);
-    cudaFree(h->status);
+    const OnDevice on(h->d.device);
+    succeeded(cudaFree(h->status));
     delete h;
     return MLP_OK;
 }
@@ -747,7 +748,8 @@ extern "C" mlp_status mlp_linear_forward(mlp_linear_t h, int64_t rows, const voi
     if (bad_matrix(X, ldx, K) || bad_matrix(Y, ldy, N) || !W || misaligned(W) || (residual && bad_matrix(residual, ldr, N)) ||
         (Z && bad_matrix(Z, ldz, N)) || (bias && misaligned(bias, h->d.bias_dtype == MLP_DT_F32 ? 4 : 2)))
         return MLP_ERR_INVALID_ARG;
-    if (!succeeded(cudaSetDevice(h->d.device)))
+    const OnDevice on(h->d.device);
+    if (!on)
         return MLP_ERR_CUDA;
     LinearParams p;
     std::memset(&p, 0, sizeof(p));
@@ -782,8 +784,8 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         return MLP_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (rows == 0) {
-        if (!succeeded(cudaSetDevice(h->d.device)) ||
-            (dW && !succeeded(cudaMemsetAsync(dW, 0, static_cast<size_t>(h->groups) * K * N * dw_esz, st))) ||
+        const OnDevice on(h->d.device);
+        if (!on || (dW && !succeeded(cudaMemsetAsync(dW, 0, static_cast<size_t>(h->groups) * K * N * dw_esz, st))) ||
             (dbias && !succeeded(cudaMemsetAsync(dbias, 0, static_cast<size_t>(h->groups) * N * bias_esz, st))))
             return MLP_ERR_CUDA;
         return MLP_OK;
@@ -792,7 +794,8 @@ extern "C" mlp_status mlp_linear_backward(mlp_linear_t h, int64_t rows, const vo
         (dX && (bad_matrix(dX, lddx, K) || !W || misaligned(W))) ||
         (((act && (dX || dW)) || dbias) && (!workspace || misaligned(workspace, 256))))
         return MLP_ERR_INVALID_ARG;
-    if (!succeeded(cudaSetDevice(h->d.device)))
+    const OnDevice on(h->d.device);
+    if (!on)
         return MLP_ERR_CUDA;
     const void *dz = dY;
     int64_t ld_dz = lddy;
@@ -881,8 +884,8 @@ extern "C" mlp_status mlp_linear_check(mlp_linear_t h, void *stream)
         return MLP_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint32_t v = 0;
-    if (!succeeded(cudaSetDevice(h->d.device)) ||
-        !succeeded(cudaMemcpyAsync(&v, h->status, 4, cudaMemcpyDeviceToHost, st)) || !succeeded(cudaStreamSynchronize(st)))
+    const OnDevice on(h->d.device);
+    if (!on || !succeeded(cudaMemcpyAsync(&v, h->status, 4, cudaMemcpyDeviceToHost, st)) || !succeeded(cudaStreamSynchronize(st)))
         return MLP_ERR_CUDA;
     if (v && (!succeeded(cudaMemsetAsync(h->status, 0, 4, st)) || !succeeded(cudaStreamSynchronize(st))))
         return MLP_ERR_CUDA;
