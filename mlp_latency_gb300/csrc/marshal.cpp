@@ -120,6 +120,16 @@ void *stream_of(PyObject *o, int device)
     return p;
 }
 
+// A layer norm launches on the current device.  (A guard that sets it whether or not it is another one took 0.2 us.)
+struct CurrentDevice {
+    c10::cuda::OptionalCUDAGuard guard;
+    explicit CurrentDevice(int device)
+    {
+        if (c10::cuda::current_device() != device)
+            guard.set_index(static_cast<c10::DeviceIndex>(device));
+    }
+};
+
 // Runs `call` (which ends in a call of the library) and turns what goes wrong on the way into Python's exceptions.
 template <typename F>
 PyObject *guarded(Py_ssize_t got, Py_ssize_t wanted, F call)
@@ -202,7 +212,7 @@ PyObject *norm_forward(PyObject *, PyObject *const *a, Py_ssize_t n)
         void *st = stream_of(a[7], t.get_device());
         if (PyErr_Occurred())
             return 0;
-        const c10::cuda::CUDAGuard guard(t.device());   // (a layer norm launches on the current device)
+        const CurrentDevice current(on.device);
         return unlocked([&] { return norm_forward_fn(R, C, x.p, x.ld, code(dt), gamma, beta, code(wd), eps, y.p, y.ld, mean, rstd, st); });
     });
 }
@@ -227,7 +237,7 @@ PyObject *norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
         void *ws = on.workspace(a[9], need), *st = stream_of(a[10], t.get_device());
         if (PyErr_Occurred())
             return 0;
-        const c10::cuda::CUDAGuard guard(t.device());
+        const CurrentDevice current(on.device);
         return unlocked([&] {
             return norm_backward_fn(R, C, dy.p, dy.ld, x.p, x.ld, code(dt), gamma, code(wd), mean, rstd, add.p, add.ld, dx.p, dx.ld,
                                     dgamma, dbeta, ws, st);
