@@ -1,16 +1,20 @@
 """Build and load libmlp_chain.so (the CUDA library behind include/mlp_chain.h and mlp_block.h), and
-_marshal.so (the argument checks of block.py, compiled against torch's headers).
+_marshal (the argument checks of block.py, compiled against torch's headers).
 
 The library is compiled in-tree with nvcc for sm_103a only. Loading it never falls back to
-anything else: if the shared object is missing, ``load()`` raises.
+anything else: if the shared object is missing, ``load()`` raises.  _marshal needs torch to be
+compiled and to be used, the library does not.
 """
 from __future__ import annotations
 
 import ctypes
+import glob
 import importlib.util
 import os
+import runpy
 import shutil
 import subprocess
+import sys
 import sysconfig
 import tempfile
 import threading
@@ -20,7 +24,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libmlp_chain.so")
-MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
 MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("mlp_chain.cu", "host_protocol.cpp", "linear.cu", "layer_norm.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("chain_kernel.cuh", "ptx.cuh", "protocol.h", "dep_groups.h",
@@ -41,39 +44,67 @@ def _older(path: str, sources) -> bool:
     return not os.path.exists(path) or any(os.path.getmtime(f) > os.path.getmtime(path) for f in sources)
 
 
-def _stale() -> bool:
-    return _older(LIB_PATH, DEPENDS) or _older(MARSHAL_PATH, [MARSHAL_SOURCE, os.path.join(INCLUDE, "mlp_block.h")])
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
 
 
-def _marshal_flags():
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+def marshal_path(torch_dir: str) -> str:
+    """Where _marshal is for this Python and this torch: compiled against another one's headers it is another module."""
+    version = runpy.run_path(os.path.join(torch_dir, "version.py"))["__version__"]
+    return os.path.join(PKG, f"_marshal.{sys.implementation.cache_tag}-torch-{version}.so")
+
+
+def _marshal_flags(torch_dir: str):
     return (["-I", os.path.join(torch_dir, "include"), "-I", sysconfig.get_paths()["include"]],
             ["-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library with nvcc (cross-compiles without a GPU). Returns its path."""
-    if force or _stale():
-        nvcc = os.environ.get("NVCC", "nvcc")
-        tmp = LIB_PATH + f".tmp{os.getpid()}"
-        work = tempfile.mkdtemp(prefix="mlp_chain_build")
-        try:   # one compiler per source, side by side
+    """Compile what is older than its sources, with nvcc (cross-compiles without a GPU): the library, and _marshal where torch
+    is installed. Returns the library's path."""
+    nvcc = os.environ.get("NVCC", "nvcc")
+    torch_dir = _torch_dir()
+    marshal = torch_dir and marshal_path(torch_dir)
+    work = tempfile.mkdtemp(prefix="mlp_chain_build")
+    tmp = f".tmp{os.getpid()}"
+    procs = []
+
+    def start(cmd):
+        if verbose:
+            print(" ".join(cmd))
+        procs.append(subprocess.Popen(cmd))
+        return procs[-1]
+
+    def finish(proc):
+        if proc.wait():
+            raise subprocess.CalledProcessError(proc.returncode, proc.args)
+
+    try:   # one compiler per source, side by side
+        checks, objs, parts = None, [], []
+        if marshal and (force or _older(marshal, [MARSHAL_SOURCE, os.path.join(INCLUDE, "mlp_block.h")])):
+            compile_flags, link_flags = _marshal_flags(torch_dir)
+            checks = start([nvcc, *NVCC_FLAGS, *compile_flags, "-shared", "-o", marshal + tmp, MARSHAL_SOURCE, *link_flags])
+        if force or _older(LIB_PATH, DEPENDS):
             objs = [os.path.join(work, os.path.basename(f) + ".o") for f in SOURCES]
-            cmds = [[nvcc, *NVCC_FLAGS, "-I", INCLUDE, "-c", "-o", o, f] for f, o in zip(SOURCES, objs)]
-            link = [nvcc, *NVCC_FLAGS, "-shared", "-o", tmp, *objs]
-            compile_flags, link_flags = _marshal_flags()
-            cmds.append([nvcc, *NVCC_FLAGS, *compile_flags, "-shared", "-o", tmp + ".marshal", MARSHAL_SOURCE, *link_flags])
-            if verbose:
-                print("\n".join(" ".join(c) for c in cmds + [link]))
-            procs = [subprocess.Popen(c) for c in cmds]
-            for rc, c in zip([p.wait() for p in procs], cmds):
-                if rc:
-                    raise subprocess.CalledProcessError(rc, c)
-            subprocess.run(link, check=True)
-            os.replace(tmp + ".marshal", MARSHAL_PATH)
-            os.replace(tmp, LIB_PATH)
-        finally:
-            shutil.rmtree(work, ignore_errors=True)
+            parts = [start([nvcc, *NVCC_FLAGS, "-I", INCLUDE, "-c", "-o", o, f]) for f, o in zip(SOURCES, objs)]
+        for p in parts:
+            finish(p)
+        if parts:
+            finish(start([nvcc, *NVCC_FLAGS, "-shared", "-o", LIB_PATH + tmp, *objs]))
+            os.replace(LIB_PATH + tmp, LIB_PATH)
+        if checks:   # (after the library, which does not need it)
+            finish(checks)
+            for f in glob.glob(os.path.join(glob.escape(PKG), "_marshal*.so")):   # for other versions
+                os.remove(f)
+            os.replace(marshal + tmp, marshal)
+    finally:
+        for p in procs:
+            p.wait()
+        for f in (LIB_PATH + tmp, (marshal or "") + tmp):
+            if os.path.exists(f):
+                os.remove(f)
+        shutil.rmtree(work, ignore_errors=True)
     return LIB_PATH
 
 
@@ -184,9 +215,10 @@ def load_marshal():
     with _lock:
         if _marshal is None:
             import torch  # noqa: F401  (the module's symbols are torch's)
-            if not os.path.exists(MARSHAL_PATH):
-                raise RuntimeError(f"{MARSHAL_PATH} is missing: call mlp_latency_gb300.build() first")
-            spec = importlib.util.spec_from_file_location("mlp_latency_gb300._marshal", MARSHAL_PATH)
+            path = marshal_path(os.path.dirname(torch.__file__))
+            if not os.path.exists(path):
+                raise RuntimeError(f"{path} is missing: call mlp_latency_gb300.build() first")
+            spec = importlib.util.spec_from_file_location("mlp_latency_gb300._marshal", path)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
             module.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
