@@ -83,7 +83,7 @@ class Linear:
                        _DTYPES[dw_dtype], device, timeout_us)
         h = ctypes.c_void_p()
         _check(lib.mlp_linear_create(ctypes.byref(d), ctypes.byref(h)), "mlp_linear_create")
-        self._lib, self._h, self._ws_sizes = lib, h, {}
+        self._lib, self._h = lib, h
         self._args = marshal.linear(h.value, int(K), int(N), int(experts), d.weight_layout, d.activation, d.bias_dtype,
                                     d.dw_dtype, int(device))
         self.K, self.N, self.experts, self.activation = int(K), int(N), int(experts), activation
@@ -111,12 +111,9 @@ class Linear:
 
     def workspace_size(self, rows: int) -> int:
         """Bytes of workspace backward() needs for this many rows (forward() needs none)."""
-        need = self._ws_sizes.get(rows)
-        if need is None:
-            n = ctypes.c_size_t()
-            _check(self._lib.mlp_linear_workspace_size(self._h, rows, ctypes.byref(n)), "mlp_linear_workspace_size")
-            need = self._ws_sizes[rows] = n.value
-        return need
+        n = ctypes.c_size_t()
+        _check(self._lib.mlp_linear_workspace_size(self._h, rows, ctypes.byref(n)), "mlp_linear_workspace_size")
+        return n.value
 
     def forward(self, X, W, Y, *, bias=None, residual=None, Z=None, offsets=None, workspace=None, stream=None):
         """Y = act(X W + bias) + residual; Z (optional) receives the pre-activation X W + bias.  workspace is

@@ -69,3 +69,16 @@ def test_layer_norm_arguments_of_another_device_are_refused(mc):  # noqa: F811
             a[name] = a[name].cpu()
             with pytest.raises(ValueError, match=": expected a .*CUDA tensor"):
                 call(**a)
+
+
+def test_a_handle_does_not_grow_with_its_calls(mc):  # noqa: F811
+    """A served batch has another number of rows from call to call."""
+    import sys
+    with mc.Linear(64, 64, activation="gelu") as lin:
+        def size():
+            return sum(sys.getsizeof(v) for v in vars(lin).values())
+        lin.workspace_size(1)
+        before = size()
+        for rows in range(1, 3000):
+            assert lin.workspace_size(rows) >= rows * 64 * 2
+        assert size() == before
