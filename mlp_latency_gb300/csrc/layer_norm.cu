@@ -623,7 +623,7 @@ struct RowRing {
 
 // Forward over many rows.  A thread keeps its columns from row to row, so gamma and beta stay in registers.
 // 2048 x 8192 bf16: 14.1 us, 4.8 TB/s of read and written bytes; its first loads and last stores bound so short a kernel.
-// Rows inside words: 2000 x 5111 15.7 us.
+// Rows inside words: 2000 x 5111 16.6 us.  fp32: 2048 x 8192 22.3 us, 4096 x 4096 23.7 (6.0 and 5.7 TB/s).
 template <typename T, int V, int kItems, int kStages, bool kOdd>
 __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams p)
 {
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(512) norm_forward_ring_kernel(const NormParams
 // columns from row to row), so x and dy are read once for all three gradients.  Up to 16 columns a thread also
 // keep gamma and, over the row's reduction, g and xh; more columns are read and computed again.  (x rstd -
 // mean rstd would save an instruction, but leaves rounding errors where x = mean.)  The sums of the blocks are added
-// by norm_colsum_finish_kernel.  4096 x 8192 bf16 with dx_add: 43 us, 6.2 TB/s, of 48 with the finish; the issue of
+// by norm_colsum_finish_kernel.  4096 x 8192 bf16 with dx_add: 43.4 us, 6.2 TB/s, of 49 with the finish; the issue of
 // instructions (53 % of cycles) and memory come close to each other.
 template <typename T, int V, int kItems, int kStages, bool kOdd>
 __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p)
@@ -1611,7 +1611,7 @@ bool launch_forward_staged(const NormParams &p, Stream &st)
     return true;
 }
 
-// Rows of any width and stride on the words of memory (2000 x 5111 18 us, staged 31); false where they are too wide, or
+// Rows of any width and stride on the words of memory (2000 x 5111 16.6 us, staged 30.5); false where they are too wide, or
 // too narrow: up to 16 words a row the kernels for other rows are as fast (8000 x 71 8 us, through the ring 14).
 template <typename T>
 bool forward_odd(const NormParams &p, Stream &st)
@@ -1735,8 +1735,8 @@ bool backward_odd(NormParams &p, int64_t ld, Stream &st)
 }
 
 // One kernel for all gradients; false where the rows are too wide for it.  dx alone needs no room for the sums, so any width
-// would fit the staged kernel; but rows in 16-byte units are read faster by norm_dx_kernel (256 x 40000 bf16 21 us, staged 40).
-// Others stay here (4000 x 30002 263 us, there 504).
+// would fit the staged kernel; but rows in 16-byte units are read faster by norm_dx_kernel (256 x 40000 bf16, from cold caches, 21 us,
+// staged 40).  Others stay here (4000 x 30002 263 us, there 504).
 template <typename T, int V>
 bool backward_v(NormParams &p, Stream &st)
 {

@@ -13,8 +13,8 @@
 // In MMA terms every form is D[p, q] = sum_k P[p, k] Q[q, k] with operands that are K-major or
 // MN-major in memory (the descriptors' and the TMA boxes' business only).
 //
-// Roles (384 threads): warps 0 and 3 copy P and Q tiles into a ring (one thread each, taking slots in turn: a thread
-// issues one 16 KB copy per ~400 cycles, longer than a fill's MMAs), warp 1 issues MMAs and owns TMEM, warp 2 builds
+// Roles (384 threads): warps 0 and 3 copy P and Q tiles into a ring (one thread each, for its even and its odd slots: a
+// thread issues one 16 KB copy per ~400 cycles, longer than a fill's MMAs), warp 1 issues MMAs and owns TMEM, warp 2 builds
 // the group tables and masks ragged reduction tails, warps 4-11 run the epilogue (two per TMEM lane quarter, on
 // alternating column chunks).
 // The accumulator is double buffered, so a tile's epilogue runs under the next tile's MMAs.  Tiles are dealt out
@@ -33,11 +33,11 @@
 // adds them in slice order, so the result does not depend on timing.
 //
 // What bounds it, measured alone (bf16):
-//   1 x 4096 x 14336            20.7 us   memory: 5.7 TB/s of weights, set-up and the last epilogue
-//   128 x 4096 x 4096, split 4  13.6 us   set-up, exchange and epilogue; the k loop is a third
-//   301 x 14336 x 4096          37.7 us   an SM's intake (64 bytes a cycle), 128 of 152 SMs at work
-//   2048 x 8192 x 8192          184 us    1.5 PFLOP/s at the power cap, 3.8 rounds of 4
-//   4000 rows, 32 experts of 2048 x 4096, both gradients  245 us   writing dW (write-only traffic reaches 3.9 TB/s)
+//   1 x 4096 x 14336            21.0 us   memory: 5.6 TB/s of weights, set-up and the last epilogue
+//   128 x 4096 x 4096, split 4  13.8 us   set-up, exchange and epilogue; the k loop is a third
+//   301 x 14336 x 4096          38.0 us   an SM's intake (64 bytes a cycle), 128 of 152 SMs at work
+//   2048 x 8192 x 8192          185 us    1.5 PFLOP/s at the power cap (the first 60 launches after a pause 168), 3.8 rounds of 4
+//   4000 rows, 32 experts of 2048 x 4096, both gradients  245 us   the order of the tiles (Walk::next)
 // Tiles of 256 columns on pairs need the whole of that intake (32 KB per 512 cycles), which is why narrower ones do not get
 // faster in proportion.
 #pragma once
@@ -250,7 +250,7 @@ __device__ __forceinline__ bool lwait_warp(uint64_t *bar, uint32_t parity, LCtrl
 
 // ---------------------------------------------------------------------------------- activations --
 // x sigmoid(t) as x / (1 + e^-t): relative accuracy for every sign of t (a tanh form cancels for
-// t << 0); e^-t overflowing to infinity gives the limit 0.
+// t << 0) down to t = -87, where the result is below 2^-119; from there on the quotient is the limit 0.
 __device__ __forceinline__ float x_sigmoid(float x, float t) { return __fdividef(x, 1.0f + __expf(-t)); }
 
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
@@ -321,6 +321,9 @@ struct Walk {
         const bool a = id < n_items, b = id_b < n_items_b;
         if (!a && !b)
             return false;
+        // (One to one while both have tiles left.  Where one product has many more, as the weights' gradient of many small
+        // experts has, the other's come all at the start: the input's gradient reads the weights first, and what is left
+        // only writes, at the 3.9 TB/s of write-only traffic instead of the 6.8 of a copy.)
         t.which = a && b ? turn : b;
         turn ^= 1;
         if (t.which == 0) {
