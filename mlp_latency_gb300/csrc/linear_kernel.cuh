@@ -118,6 +118,10 @@ struct __align__(8) LCtrl {
     uint64_t go[kMaxRing];   // leader to peer: the fill is armed
     uint64_t tfull[2], tempty[2];
     uint64_t drain, rdy[2], got[2], ringfree;
+    uint64_t left;           // the copying threads and the MMA thread are through, and have noted what they leave in flight:
+    uint32_t fills[2], tail_ph[2];   // of each copying thread
+    uint32_t masked[kMaxRing];       // a slot's last masked fill
+    uint32_t issued;
     uint32_t tmem_base;
     volatile int32_t abort_flag;
     int32_t skip;
@@ -210,11 +214,35 @@ __device__ __forceinline__ bool lwait(uint64_t *bar, uint32_t parity, LCtrl *c, 
     }
 }
 
-// The wait that ends a role, for what it has in flight: the CTA's shared memory and TMEM go away after the roles.  In every
-// run, since another role's wait may run out at any later time; where none does, the other roles wait for the same.
-__device__ __forceinline__ bool settle(uint64_t *bar, uint32_t parity, LCtrl *c, const LinearParams &p)
+// After an abort, before the CTA's shared memory and TMEM go away: waits for all copies and MMAs in flight.  By a thread of the
+// first epilogue warp, since that one knows: if it saw all its tiles' accumulators, every MMA is over and every copy was
+// read by one.  (The copying and MMA threads do not: another role's wait can run out after they are through.  Waits of
+// their own at the end of every run cost 0.6 us of 13.4 where tiles have one k block.)
+template <int kPair>
+__device__ __noinline__ void land(LCtrl *c, const LinearParams &p)
 {
-    return lwait(bar, parity, c, p) || lwait(bar, parity, c, p, false, true);
+    if (!lwait(&c->left, 0, c, p, false, true))
+        return;
+    const bool half = kPair == 2 && (cluster_ctarank() & 1u) != 0;
+    if (c->issued && !lwait(&c->drain, 0, c, p, false, true))
+        return;
+    // Each copy on its slot's last barrier phase.  Unmasked fills of a pair complete on the leader's barriers (the peer fills
+    // only what the leader armed, and keeps its shared memory until the cluster barriers at the end); masked fills complete
+    // on each CTA's own.  A wait that ran out was long enough for the rest.
+    const bool shared_ring = p.split > 1 && p.recv_bufs == 0;
+    const uint32_t num_pipe = static_cast<uint32_t>(p.num_pipe);
+    for (uint32_t which = 0; which < (shared_ring ? 1u : 2u); ++which)
+        for (uint32_t fills = c->fills[which], f = fills > num_pipe ? fills - num_pipe : 0u; f < fills; ++f) {
+            const uint32_t slot = f % num_pipe;
+            if (!shared_ring && (slot & 1u) != which)
+                continue;
+            if (c->masked[slot] == f) {
+                if (!lwait(&c->tail[slot], (c->tail_ph[which] >> slot & 1u) ^ 1u, c, p, false, true))
+                    return;
+            } else if (!half && !lwait(&c->full[slot], (f / num_pipe) & 1u, c, p, false, true)) {
+                return;
+            }
+        }
 }
 
 // Accumulator of an item, and the parity of its uses.  Wide tiles have one: two are more than TMEM holds.
@@ -432,7 +460,7 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
     const bool shared_ring = p.split > 1 && p.recv_bufs == 0;
     const int32_t n_items = c->n_items[0], n_items_b = c->n_items[1];
     const uint64_t pol = policy_evict_normal();
-    uint32_t fills = 0, tail_ph = 0, tail_last = 0, item_ph = 0;   // (tail_last: slots whose last fill was masked)
+    uint32_t fills = 0, tail_ph = 0, item_ph = 0;
     uint32_t ps = 0, pph = 0;
     bool ok = true, first = true;
     griddep_wait();   // a programmatic launch: the kernel before this one is complete from here on
@@ -475,6 +503,7 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
                 if (masked) {
                     // completes on this CTA's own tail barrier; warp 2 zeroes the rows and completes `full`
                     mbar_arrive_expect_tx(&c->tail[ps], bytes);
+                    c->masked[ps] = fills;
                 } else if (!half) {
                     mbar_arrive_expect_tx(&c->full[ps], kPair * bytes);
                     if (kMasks && kPair == 2)
@@ -516,11 +545,8 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
                         load3(b + j * kBoxBytes, map_q, q_row + 64 * j, k, q_grp);
                 }
             }
-            if (kMasks) {   // (the other thread's too: the slot's tail barrier counts both)
-                const uint32_t bit = masked_rows(form, p, t, kb) != 0 ? 1u << ps : 0u;
-                tail_ph ^= bit;
-                tail_last = (tail_last & ~(1u << ps)) | bit;
-            }
+            if (kMasks && masked_rows(form, p, t, kb) != 0)
+                tail_ph ^= 1u << ps;   // (the other thread's too: the slot's tail barrier counts both)
             ++fills;
             if (++ps == num_pipe) {
                 ps = 0;
@@ -528,20 +554,9 @@ __device__ __forceinline__ void l_role_tma(const LinearParams &p, LCtrl *c, cons
             }
         }
     }
-    // This thread's copies land: each on its slot's last barrier phase.  Unmasked fills of a pair complete on the leader's
-    // barriers (the peer fills only what the leader armed, and keeps its shared memory until the cluster barriers at the
-    // end); masked fills complete on each CTA's own.  A wait that ran out was long enough for the rest.
-    for (uint32_t f = fills > num_pipe ? fills - num_pipe : 0u; f < fills; ++f) {
-        const uint32_t slot = f % num_pipe;
-        if (shared_ring ? which != 0 : (slot & 1u) != which)
-            continue;
-        if (tail_last >> slot & 1u) {
-            if (!settle(&c->tail[slot], (tail_ph >> slot & 1u) ^ 1u, c, p))
-                break;
-        } else if (!half && !settle(&c->full[slot], (f / num_pipe) & 1u, c, p)) {
-            break;
-        }
-    }
+    c->fills[which] = fills;
+    c->tail_ph[which] = tail_ph;
+    mbar_arrive(&c->left);
 }
 
 // ---------------------------------------------------------------------------------- MMA issuer --
@@ -549,8 +564,11 @@ template <int kForm, int kFormB, int kPair, bool kWide>
 __device__ __forceinline__ void l_role_mma(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *ring,
                                            uint32_t tmem_base)
 {
-    if (kPair == 2 && (cluster_ctarank() & 1u))
-        return;   // the leader issues for both
+    if (kPair == 2 && (cluster_ctarank() & 1u)) {   // the leader issues for both
+        c->issued = 0;
+        mbar_arrive(&c->left);
+        return;
+    }
     const int32_t num_pipe = p.num_pipe;
     const uint32_t acc_cols = static_cast<uint32_t>(p.acc_cols);
     const uint32_t tfull_peer0 = kPair == 2 ? map_to_rank(&c->tfull[0], cluster_ctarank() | 1u) : 0u;
@@ -616,10 +634,10 @@ __device__ __forceinline__ void l_role_mma(const LinearParams &p, LCtrl *c, cons
             mma_commit_g<kPair>(tfull_peer0 + acc * 8u);
         ++tiles;
     }
-    if (issued) {
+    if (issued)
         mma_commit_g<kPair>(smem_u32(&c->drain));
-        settle(&c->drain, 0, c, p);
-    }
+    c->issued = issued;
+    mbar_arrive(&c->left);
 }
 
 // ---------------------------------------------------------------- ragged reduction tails (warp 2) --
@@ -1118,18 +1136,17 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
     }
     Walk<kForm, kFormB, kPair> w(p);
     Tile t;
-    while (w.next(p, g, n_items, n_items_b, t)) {
-        if constexpr (kFormB < 0) {
-            if (!epilogue_tile<kForm, kPair, kWide>(p, p.pr[0], c, st, t))
-                return;
-        } else if (t.which == 0) {
-            if (!epilogue_tile<kForm, kPair, kWide>(p, p.pr[0], c, st, t))
-                return;
-        } else {
-            if (!epilogue_tile<kFormB, kPair, kWide>(p, p.pr[1], c, st, t))
-                return;
-        }
+    bool ok = true;
+    while (ok && w.next(p, g, n_items, n_items_b, t)) {
+        if constexpr (kFormB < 0)
+            ok = epilogue_tile<kForm, kPair, kWide>(p, p.pr[0], c, st, t);
+        else if (t.which == 0)
+            ok = epilogue_tile<kForm, kPair, kWide>(p, p.pr[0], c, st, t);
+        else
+            ok = epilogue_tile<kFormB, kPair, kWide>(p, p.pr[1], c, st, t);
     }
+    if (!ok && ew == 0 && st.lane == 0)
+        land<kPair>(c, p);
 }
 
 // --------------------------------------------------------------------------------------- kernel --
@@ -1163,6 +1180,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
             mbar_init(&c->empty[i], 1);
             mbar_init(&c->go[i], 1);
             mbar_init(&c->tail[i], 1);
+            c->masked[i] = 0xffffffffu;
         }
         if (lane < 2) {
             mbar_init(&c->tfull[lane], 1);
@@ -1171,6 +1189,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
         if (lane == 0) {
             const int32_t S = p.split > 1 ? p.split : 1;
             mbar_init(&c->drain, 1);
+            mbar_init(&c->left, 3);
             for (int b = 0; b < 2; ++b) {   // epilogue warps of the other CTAs (and, sharing the ring, of this one)
                 mbar_init(&c->rdy[b], p.recv_bufs == 0 ? kEpi * S : S > 1 ? kEpi * (S - 1) : 1);
                 mbar_init(&c->got[b], S > 1 ? kEpi * (S - 1) : 1);
