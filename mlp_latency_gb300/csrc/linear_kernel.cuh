@@ -1107,8 +1107,9 @@ __device__ __forceinline__ void add_bias_sums(const BiasSums &q, int32_t e, int3
         static_cast<__nv_bfloat16 *>(q.out)[o] = __float2bfloat16_rn(s);
 }
 
+// False after an abort.
 template <int kForm, int kFormB, int kPair, bool kWide>
-__device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *recv_base,
+__device__ __forceinline__ bool l_role_epilogue(const LinearParams &p, LCtrl *c, const GroupTab g, uint8_t *recv_base,
                                                 uint8_t *stage_all, float *bias_all, uint32_t tmem_base)
 {
     const int32_t ew = static_cast<int32_t>(threadIdx.x / 32) - 4;
@@ -1139,17 +1140,19 @@ __device__ __forceinline__ void l_role_epilogue(const LinearParams &p, LCtrl *c,
     }
     Walk<kForm, kFormB, kPair> w(p);
     Tile t;
-    bool ok = true;
-    while (ok && w.next(p, g, n_items, n_items_b, t)) {
-        if constexpr (kFormB < 0)
-            ok = epilogue_tile<kForm, kPair, kWide>(p, p.pr[0], c, st, t);
-        else if (t.which == 0)
-            ok = epilogue_tile<kForm, kPair, kWide>(p, p.pr[0], c, st, t);
-        else
-            ok = epilogue_tile<kFormB, kPair, kWide>(p, p.pr[1], c, st, t);
+    while (w.next(p, g, n_items, n_items_b, t)) {
+        if constexpr (kFormB < 0) {
+            if (!epilogue_tile<kForm, kPair, kWide>(p, p.pr[0], c, st, t))
+                return false;
+        } else if (t.which == 0) {
+            if (!epilogue_tile<kForm, kPair, kWide>(p, p.pr[0], c, st, t))
+                return false;
+        } else {
+            if (!epilogue_tile<kFormB, kPair, kWide>(p, p.pr[1], c, st, t))
+                return false;
+        }
     }
-    if (!ok && ew == 0 && st.lane == 0)
-        land<kPair>(c, p);
+    return true;
 }
 
 // --------------------------------------------------------------------------------------- kernel --
@@ -1276,8 +1279,10 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_kernel(const __grid_const
             if (elect_one())
                 l_role_tma<kForm, kFormB, kPair, kWide>(p, c, g, ring, 1, w, t, have);
         } else {
-            l_role_epilogue<kForm, kFormB, kPair, kWide>(p, c, g, ring + (p.recv_bufs ? sm.recv : 0u), ring + sm.stage,
-                                          reinterpret_cast<float *>(ring + sm.bias), tmem_base);
+            const bool ok = l_role_epilogue<kForm, kFormB, kPair, kWide>(p, c, g, ring + (p.recv_bufs ? sm.recv : 0u), ring + sm.stage,
+                                                                         reinterpret_cast<float *>(ring + sm.bias), tmem_base);
+            if (!ok && warp == 4 && lane == 0)
+                land<kPair>(c, p);
         }
     }
     __syncwarp();
