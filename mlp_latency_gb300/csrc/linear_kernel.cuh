@@ -34,7 +34,7 @@
 //
 // What bounds it, measured alone (bf16):
 //   1 x 4096 x 14336            21.0 us   memory: 5.6 TB/s of weights, set-up and the last epilogue
-//   128 x 4096 x 4096, split 4  13.8 us   set-up, exchange and epilogue; the k loop is a third
+//   128 x 4096 x 4096, split 4  13.6 us   set-up, exchange and epilogue; the k loop is a third
 //   301 x 14336 x 4096          38.0 us   an SM's intake (64 bytes a cycle), 128 of 152 SMs at work
 //   2048 x 8192 x 8192          185 us    1.5 PFLOP/s at the power cap (the first 60 launches after a pause 168), 3.8 rounds of 4
 //   4000 rows, 32 experts of 2048 x 4096, both gradients  245 us   the order of the tiles (Walk::next)
