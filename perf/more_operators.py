@@ -58,7 +58,7 @@ def _log_int(rng, lo, hi):
 def draw(rng):
     op = rng.choice(["route", "route", "route_grad", "dispatch", "dispatch_grad", "combine", "combine_grad", "clip", "clip"])
     if op == "clip":
-        case = {"op": op, "blocks": _log_int(rng, 1, 9), "width": _log_int(rng, 64, 4096), "hidden": _log_int(rng, 64, 8192),
+        case = {"op": op, "blocks": _log_int(rng, 1, 24), "width": _log_int(rng, 64, 4096), "hidden": _log_int(rng, 64, 8192),
                 "experts": rng.choice([0, 0, rng.randrange(2, 17)]), "dtype": rng.choice(["bf16", "f32", "mixed"]),
                 "limit": rng.choice([0.3, 0.3, 4.0])}
         while case["blocks"] * max(case["experts"], 1) * case["width"] * case["hidden"] > 4096 * 8192:
