@@ -79,13 +79,14 @@ __device__ __forceinline__ int part_of(const List<N> &l, uint32_t piece, int lo)
     return lo;
 }
 
-// A sum of squares that keeps the exponent's range: values whose squares would leave fp32's are summed apart, scaled by
-// powers of two (big: 2^-72, so 2^128 squares to 2^112; small: 2^84, so 2^-149 squares to 2^-130).  A sum in between is at most
-// 2^90, so 2^37 of them, 32 values each, stay in range.
+// A sum of squares that keeps the exponent's range: a group of words, 16 or 32 values, whose squares would leave fp32's is summed apart,
+// scaled by a power of two.  Groups above 2^90 (big) by 2^-96: a value of 2^128 adds 2^64, the largest of such a group 2^-107 at least.
+// Groups below 2^-80 (small) by 2^84: a value of 2^-149 adds 2^-130, a group at most 2^88.  A call takes fewer than 2^40 values, in 2^36
+// groups, so no sum leaves the range: big 2^104, in between 2^126, small 2^124.
 struct Squares {
     float big = 0.0f, mid = 0.0f, small = 0.0f;
 };
-constexpr float kBig = 0x1p-72f, kSmall = 0x1p84f;
+constexpr float kBig = 0x1p-96f, kSmall = 0x1p84f;
 
 __device__ __forceinline__ float squares(uint4 w, bool f32, float scale, float s)
 {
@@ -260,7 +261,7 @@ __device__ __forceinline__ double total_norm(const Partial &p)
     }
     if (v[0] == 0.0f && v[2] == 0.0f)
         return sqrtf(v[1]);
-    return sqrt(static_cast<double>(v[0]) * 0x1p144 + static_cast<double>(v[1]) + static_cast<double>(v[2]) * 0x1p-168);
+    return sqrt(static_cast<double>(v[0]) * 0x1p192 + static_cast<double>(v[1]) + static_cast<double>(v[2]) * 0x1p-168);
 }
 
 __global__ void __launch_bounds__(kThreads) finish_kernel(Partial partial, float *norm)

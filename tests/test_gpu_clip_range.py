@@ -1,0 +1,81 @@
+"""GPU tests of clipping at the ends of fp32's range, of lists that are clipped partly in place, and of long sums, against 64 bits.
+
+Units are 2^-24, relative, counted from the kernels as they are.  A thread adds the squares of its 4 words of a piece (16384 bytes), 8 or
+4 a word: one rounding each, the product's among them, and for values in fp32's middle range two more for the words and one for the piece.
+Then 5 shuffles and 8 warps; of the partial sums 5 a round, 5 shuffles and 8 warps.  The root halves the error and has one of its own.  A
+clipped value has the norm's error, the factor's two roundings, its own product's and half a step of its type; below 2^-126, where fp32 holds
+multiples of 2^-149 and bf16 those of 2^-133, half such a step for each of two products and for the type."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV, BF, F32 = "cuda", torch.bfloat16, torch.float32
+U = 2.0 ** -24
+HALF = {BF: 2.0 ** -8, F32: U}
+LEAST = {BF: 2.0 ** -134 + 2.0 ** -149, F32: 2.0 ** -149}
+INF = float("inf")
+BLOCKS, WORDS = 1216, 1024      # of a launch; of a piece
+
+
+@pytest.fixture(scope="module")
+def mc():
+    import mlp_latency_gb300
+    mlp_latency_gb300.build()
+    return mlp_latency_gb300
+
+
+def units(tensors):
+    """Of the norm."""
+    pieces = sum(max(1, -(-t.numel() * t.element_size() // (16 * WORDS))) for t in tensors)
+    per = max(16 // t.element_size() for t in tensors)
+    return ((4 * per + 3) * -(-pieces // BLOCKS) + 5 + 8 + 5 + 5 + 8) / 2 + 1
+
+
+def clip(mc, tensors, max_norm, eps=0.0, shift=0, out_shift=None):
+    """The norm, and the clipped values (in place where out_shift is None) of tensors that begin `shift` elements after a 16-byte word."""
+    def placed(t, by):
+        buf = torch.empty(t.numel() + by, dtype=t.dtype, device=DEV)
+        buf[by:].copy_(t.reshape(-1))
+        return buf[by:]
+
+    src = [placed(t, shift) for t in tensors]
+    out = None if out_shift is None else [placed(torch.zeros_like(t), out_shift) for t in tensors]
+    norm = torch.empty(1, device=DEV)
+    ws = torch.empty(mc.clip_workspace_size(len(tensors)), dtype=torch.uint8, device=DEV)
+    mc.clip_gradients(src, max_norm, norm, out=out, eps=eps, workspace=ws)
+    return float(norm), src if out is None else out
+
+
+def expect(tensors, got, max_norm, eps=0.0):
+    """Compares a clip's result with the definition in 64 bits."""
+    norm, out = got
+    n = float(torch.stack([t.double().square().sum() for t in tensors]).sum().sqrt())
+    max_norm, eps = float(np.float32(max_norm)), float(np.float32(eps))
+    c = 1.0 if n == 0 or max_norm >= n + eps else max_norm / (n + eps)
+    e = units(tensors)
+    if n < 2.0 ** 128 * (1 - e * U):
+        assert abs(norm - n) <= e * U * n + 2.0 ** -150, (norm, n)
+    elif n > 2.0 ** 128 * (1 + e * U):
+        assert norm == INF
+    for t, o in zip(tensors, out):
+        want = t.reshape(-1).to(DEV).double() * c
+        tol = (((e + 3) * U + HALF[t.dtype]) * want.abs() * (1 + 2.0 ** -7) + LEAST[t.dtype]) if c < 1 else 0 * want
+        assert bool(((o.double() - want).abs() <= tol).all()), float(((o.double() - want).abs() - tol).max())
+
+
+PLACES = [dict(), dict(shift=1), dict(out_shift=0), dict(shift=3, out_shift=2)]
+
+
+def normal(n, dtype, scale, seed=1):
+    t = torch.randn(n, generator=torch.Generator().manual_seed(seed)).clamp(-3, 3)
+    return (t.double() * scale).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [50_000, 200_000, 3_000_000])
+def test_many_values_near_the_largest(mc, n, dtype):
+    """The sum of their squares is past 2^270; the factor is an ordinary number."""
+    t = torch.full((n,), 3e38).to(dtype)
+    for place in PLACES:
+        expect([t], clip(mc, [t], 1e5, **place), 1e5)
