@@ -33,7 +33,7 @@ mlp_status mlp_gradient_norm(int64_t tensors, const mlp_tensor *list, float *nor
 /* The same, and out = c * data with c = max_norm / (norm + eps), 1 where that is larger (also for a norm of 0), rounded once.
  * Tensors that are clipped in place (out = data) are not written when c = 1.  max_norm >= 0 (infinity: c = 1), eps >= 0.
  * A norm of NaN makes c NaN, an infinite element makes c 0; finite elements whose norm is past fp32's largest value are scaled by
- * the norm itself.
+ * the norm itself.  c has fp32's 24 bits however small it is.
  * An out overlaps no other tensor's data or out; it is its own data, or does not overlap it. */
 mlp_status mlp_clip_gradients(int64_t tensors, const mlp_tensor *list, float max_norm, float eps, float *norm,
                               void *workspace, void *stream);

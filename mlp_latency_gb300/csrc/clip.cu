@@ -128,18 +128,41 @@ __device__ __forceinline__ void store_with(void *p, uint4 v, uint64_t policy)
     asm volatile("st.global.L2::cache_hint.v4.b32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "l"(policy) : "memory");
 }
 
-template <typename T>
-__device__ __forceinline__ uint4 times(uint4 w, float c);
-template <>
-__device__ __forceinline__ uint4 times<float>(uint4 w, float c)
+// What values are multiplied by: c, then a power of two, which is 1 unless max_norm / norm is below fp32's normal numbers.
+struct Factor {
+    float c, power;
+
+    __device__ __forceinline__ float of(float x) const { return x * c * power; }
+};
+
+// min(1, max_norm / (norm + eps)).  Where fp32 has few bits or none for the quotient, or none for the sum (a norm or norm + eps past its
+// range), it is found in 64 bits; c is then between 1/2 and 1, so that its product with a value of any size keeps its bits until the power is
+// applied.  (The least power there is, 2^-149, goes with a smaller c; below 2^-275 c is subnormal too, and so is all that is left.)
+__device__ __forceinline__ Factor factor_of(double exact, float max_norm, float eps)
 {
-    return make_uint4(__float_as_uint(__uint_as_float(w.x) * c), __float_as_uint(__uint_as_float(w.y) * c),
-                      __float_as_uint(__uint_as_float(w.z) * c), __float_as_uint(__uint_as_float(w.w) * c));
+    const float norm = static_cast<float>(exact), sum = norm + eps;
+    if (norm == 0.0f || max_norm >= sum)
+        return {1.0f, 1.0f};
+    const float c = max_norm / sum;   // (a NaN stays one)
+    if (!(c < 0x1p-126f) || isinf(exact))
+        return {c, 1.0f};
+    int e;
+    const double f = static_cast<double>(max_norm) / (exact + static_cast<double>(eps)), half = frexp(f, &e);
+    return {static_cast<float>(ldexp(half, min(e + 149, 0))), ldexpf(1.0f, max(e, -149))};
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 times(uint4 w, Factor f);
+template <>
+__device__ __forceinline__ uint4 times<float>(uint4 w, Factor f)
+{
+    return make_uint4(__float_as_uint(f.of(__uint_as_float(w.x))), __float_as_uint(f.of(__uint_as_float(w.y))),
+                      __float_as_uint(f.of(__uint_as_float(w.z))), __float_as_uint(f.of(__uint_as_float(w.w))));
 }
 template <>
-__device__ __forceinline__ uint4 times<__nv_bfloat16>(uint4 w, float c)
+__device__ __forceinline__ uint4 times<__nv_bfloat16>(uint4 w, Factor f)
 {
-    auto two = [c](uint32_t v) { return pack_bf16(bf16_lo(v) * c, bf16_hi(v) * c); };
+    auto two = [f](uint32_t v) { return pack_bf16(f.of(bf16_lo(v)), f.of(bf16_hi(v))); };
     return make_uint4(two(w.x), two(w.y), two(w.z), two(w.w));
 }
 
@@ -278,20 +301,18 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, 4) scale_kernel(const __grid_constant__ List<N> l, uint32_t pieces, Partial partial, bool in_place,
                                                            float max_norm, float eps, float *norm)
 {
-    __shared__ float factor;
+    __shared__ Factor factor;
     take_turn();
     const double exact = total_norm(partial);
     if (threadIdx.x == 0) {
-        const float v = static_cast<float>(exact);
         if (norm && blockIdx.x == 0)
-            *norm = v;
-        factor = v == 0.0f || max_norm >= v + eps ? 1.0f : max_norm / (v + eps);   // (a NaN stays one)
-        if (isinf(v) && !isinf(exact) && !isinf(max_norm))
-            factor = static_cast<float>(max_norm / (exact + eps));   // finite values whose norm is past fp32's range
+            *norm = static_cast<float>(exact);
+        factor = factor_of(exact, max_norm, eps);
     }
     __syncthreads();
-    const float c = factor;
-    if (c == 1.0f && in_place)
+    const Factor f = factor;
+    const bool whole = f.c * f.power == 1.0f;
+    if (whole && in_place)
         return;
     const uint64_t policy = passing();
     int k = l.parts - 1;
@@ -299,13 +320,13 @@ __global__ void __launch_bounds__(kThreads, 4) scale_kernel(const __grid_constan
         const uint32_t piece = pieces - 1 - turn;
         k = part_of(l, piece, k);
         const Part &t = l.part[k];
-        if (c == 1.0f && t.out == t.data)
+        if (whole && t.out == t.data)
             continue;
         const int64_t w0 = static_cast<int64_t>(piece - (k ? l.part[k - 1].last : 0)) * kPiece;
         const bool f32 = t.f32;
         if (t.by_element) {
             for (int64_t i = w0 + threadIdx.x; i < min(w0 + kPiece, t.words); i += kThreads)
-                put_element(t.out, f32, i, c * element(t.data, f32, i));
+                put_element(t.out, f32, i, f.of(element(t.data, f32, i)));
             continue;
         }
         const int64_t head = static_cast<int>(t.head) * (f32 ? 4 : 2);
@@ -320,11 +341,11 @@ __global__ void __launch_bounds__(kThreads, 4) scale_kernel(const __grid_constan
         for (int i = 0; i < kWords; ++i) {
             const int64_t at = w0 + i * kThreads + threadIdx.x;
             if (at < t.words)
-                store_with(t.out + head + at * 16, f32 ? times<float>(w[i], c) : times<__nv_bfloat16>(w[i], c), policy);
+                store_with(t.out + head + at * 16, f32 ? times<float>(w[i], f) : times<__nv_bfloat16>(w[i], f), policy);
         }
         if (w0 == 0 && threadIdx.x < t.head + t.tail) {
             const int64_t at = threadIdx.x < t.head ? threadIdx.x : t.words * (f32 ? 4 : 8) + threadIdx.x;
-            put_element(t.out, f32, at, c * element(t.data, f32, at));
+            put_element(t.out, f32, at, f.of(element(t.data, f32, at)));
         }
     }
 }

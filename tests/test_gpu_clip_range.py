@@ -79,3 +79,26 @@ def test_many_values_near_the_largest(mc, n, dtype):
     t = torch.full((n,), 3e38).to(dtype)
     for place in PLACES:
         expect([t], clip(mc, [t], 1e5, **place), 1e5)
+
+
+FACTORS = [(1e38, 10000, 1e-3), (1e38, 10000, 1e-6), (1e38, 10000, 1e-20), (1e38, 10000, 1e-38), (1e38, 10, 2.0 ** -149), (3e38, 200_000, 1.0),
+           (1e30, 1000, 1e-20), (1e20, 1000, 1e-30), (1.0, 1000, 1e-40), (1e-10, 1000, 1e-45), (1e38, 300_000, 0.0)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale,n,limit", FACTORS)
+def test_a_factor_below_the_least_normal_number(mc, scale, n, limit, dtype):
+    """limit / norm is below 2^-126, down to 2^-297; what it leaves of a value is not."""
+    t = normal(n, dtype, scale) if scale < 3e38 else torch.full((n,), scale).to(dtype)
+    small = normal(77, dtype, 1e-3 * scale, 2)
+    for place in PLACES:
+        expect([t, small], clip(mc, [t, small], limit, **place), limit)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_large_eps(mc, dtype):
+    """norm + eps is past fp32's largest value."""
+    t = normal(9, dtype, 1e38)
+    for place in PLACES:
+        for limit in (1e38, 1.0, 3.4e38):
+            expect([t], clip(mc, [t], limit, eps=3.3e38, **place), limit, eps=3.3e38)
