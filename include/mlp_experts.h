@@ -64,7 +64,8 @@ mlp_status mlp_route_backward(int64_t tokens, int64_t experts, int32_t top, cons
 /* ------------------------------------------------------------------------ dispatch and combine --
  * `tokens` token rows and `rows` expert rows of `cols` elements, all of one dtype (BF16 or F32); slots
  * int32 [tokens][top] as mlp_route_forward writes them, a slot outside [0, rows) means no row; gates fp32
- * [tokens][top].  tokens, rows >= 0, cols >= 1, 1 <= top <= MLP_MAX_TOP.  Sums are fp32, rounded once.
+ * [tokens][top].  tokens, rows >= 0, cols >= 1, 1 <= top <= MLP_MAX_TOP.  tokens * top, rows and cols are below
+ * 2^31, and so is tokens times the pieces of 128 bytes that a row of cols takes.  Sums are fp32, rounded once.
  * Expert rows that no slot names are neither read nor written.  Slots differ from one another.  Base
  * pointers aligned to their element; rows that are 16-byte aligned throughout run faster. */
 

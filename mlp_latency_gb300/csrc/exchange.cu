@@ -516,7 +516,7 @@ void run(bool gather, int word, Exchange &p, Stream &st)
 bool bad_sizes(int64_t tokens, int64_t cols, int32_t top, int64_t rows)
 {
     return tokens < 0 || rows < 0 || rows >= (int64_t{1} << 31) || cols < 1 || cols >= (int64_t{1} << 31) || top < 1 || top > MLP_MAX_TOP ||
-           tokens >= (int64_t{1} << 31) / top;
+           tokens > ((int64_t{1} << 31) - 1) / top;
 }
 
 mlp_status start(bool gather, Exchange &p, mlp_dtype dtype, void *stream)

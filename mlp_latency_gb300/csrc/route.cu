@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(kGradThreads<N>) route_grad_kernel(const Route
 bool bad_sizes(int64_t tokens, int64_t experts, int32_t top)
 {
     return tokens < 0 || experts < 1 || experts > MLP_MAX_EXPERTS || top < 1 || top > MLP_MAX_TOP || top > experts ||
-           tokens >= (int64_t{1} << 31) / top;
+           tokens > ((int64_t{1} << 31) - 1) / top;
 }
 
 // Tables of the clusters' counts, and of their sums of p: cells of each.

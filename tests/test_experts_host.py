@@ -121,6 +121,24 @@ def test_an_exchange_refuses(lib, what, kw, want):
     assert call(lib, what, **kw) == want
 
 
+def test_the_most_choices(lib):
+    """tokens * top up to 2^31 - 1, whether top divides it or not.  (Sizes are looked at before the type, and that before anything else.)"""
+    for top in (1, 2, 3, 5, 7, 31, 32):
+        most = ((1 << 31) - 1) // top
+        for tokens, want in ((most, UNSUPPORTED), (most + 1, INVALID)):
+            assert route(lib, tokens=tokens, top=top, experts=64, ldl=64, dt=0) == want
+            assert route_back(lib, tokens=tokens, top=top, experts=64, ldl=64, ldd=64, dt=0) == want
+            for what in EXCHANGES:
+                assert call(lib, what, tokens=tokens, top=top, dt=0) == want
+
+
+@pytest.mark.parametrize("what", EXCHANGES)
+def test_the_largest_exchanges_are_refused(lib, what):
+    """Tokens times a row's pieces of 128 bytes from 2^31 on."""
+    assert call(lib, what, tokens=1 << 26, cols=64 * 32, lda=64 * 32, ldb=64 * 32) == INVALID
+    assert call(lib, what, tokens=1 << 26, cols=32 * 31 + 1, lda=64 * 32, ldb=64 * 32, dt=F32) == INVALID
+
+
 def clip(lib, spans, max_norm=1.0, eps=1e-6, norm=P, ws=P, clipped=True, count=None):
     """spans: (data, out, elements, dtype)"""
     a = (_lib.Tensor * max(len(spans), 1))(*(_lib.Tensor(*s) for s in spans))
