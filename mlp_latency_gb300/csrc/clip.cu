@@ -33,7 +33,7 @@ struct Partial {
     int32_t from;
 };
 
-// One tensor: `head` elements, `words` words of 16 bytes, `tail` elements; or, where out lies differently in its words
+// One tensor: `head` elements, `words` words of 16 bytes, `tail` elements; or, for the second pass where out lies differently in its words
 // than data, elements throughout (`words` counts elements then).
 struct Part {
     const char *data;
@@ -196,11 +196,6 @@ __global__ void __launch_bounds__(kThreads, 8) norm_kernel(const __grid_constant
         const Part &t = l.part[k];
         const int64_t w0 = static_cast<int64_t>(piece - (k ? l.part[k - 1].last : 0)) * kPiece;
         const bool f32 = t.f32;
-        if (t.by_element) {
-            for (int64_t i = w0 + threadIdx.x; i < min(w0 + kPiece, t.words); i += kThreads)
-                add_element(q, element(t.data, f32, i));
-            continue;
-        }
         const char *body = t.data + static_cast<int>(t.head) * (f32 ? 4 : 2);
         uint4 w[kWords];
 #pragma unroll
