@@ -183,11 +183,11 @@ struct Logits {
     }
 };
 
-// Exclusive sums of total[0 .. experts) in place, by all threads of a block (a multiple of 32, no fewer than experts / 8); returns the
-// sum of all.  Starts and ends with the block in step.
+// Exclusive sums of total[0 .. experts) in place, by all threads of a block (a multiple of 32), as many experts at a time; returns the sum
+// of all.  Starts and ends with the block in step.
 __device__ __forceinline__ int32_t scan_experts(int32_t *total, int experts)
 {
-    __shared__ int32_t of_warp[33];
+    __shared__ int32_t of_warp[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     int32_t carry = 0;
     for (int e0 = 0; e0 < experts; e0 += blockDim.x) {
