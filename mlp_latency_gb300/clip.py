@@ -2,8 +2,9 @@
 
 Argument checks and marshalling only, as in block.py.  ``grads`` is a list or tuple of contiguous CUDA tensors of any
 shape, bfloat16 or float32, all on norm's device; ``norm`` is float32 [1], ``workspace`` at least
-``clip_workspace_size(len(grads))`` bytes.  A call enqueues work on ``stream`` (default: torch's current stream of that
-device) without synchronising: a step that depends on the norm reads it when it likes.
+``clip_workspace_size(len(grads))`` bytes.  The workspace lies within no tensor of the lists, nor does the norm when they
+are clipped.  A call enqueues work on ``stream`` (default: torch's current stream of that device) without synchronising: a
+step that depends on the norm reads it when it likes.
 """
 from __future__ import annotations
 

@@ -12,6 +12,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <sstream>
 #include <stdexcept>
 
@@ -586,6 +587,21 @@ struct Sequence {
     PyObject *operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(o, i); }
 };
 
+// Bytes at an address.
+struct Span {
+    uintptr_t from, to;
+    Span(const void *p, size_t bytes) : from(reinterpret_cast<uintptr_t>(p)), to(from + bytes) {}
+    bool meets(const Span &o) const { return from < o.to && o.from < to && from < to && o.from < o.to; }
+    void take(const Span &o)
+    {
+        from = std::min(from, o.from);
+        to = std::max(to, o.to);
+    }
+};
+
+Span data_of(const mlp_tensor &t) { return {t.data, static_cast<size_t>(t.count) * (t.dtype == MLP_DT_BF16 ? 2 : 4)}; }
+Span out_of(const mlp_tensor &t) { return {t.out, static_cast<size_t>(t.count) * (t.dtype == MLP_DT_BF16 ? 2 : 4)}; }
+
 // grads, out (None: in place), max_norm (None: the norm only), norm, eps, workspace, stream
 PyObject *clip(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
@@ -595,11 +611,14 @@ PyObject *clip(PyObject *, PyObject *const *a, Py_ssize_t n)
         const Tensors on{static_cast<int>(tensor(a[3], "norm").get_device())};
         float *norm = static_cast<float *>(on.dense(a[3], "norm", {1}, kF32));
         c10::SmallVector<mlp_tensor, 64> list(static_cast<size_t>(grads.size()));
+        Span all(reinterpret_cast<void *>(UINTPTR_MAX), 0);   // from the first byte of a tensor to the last
+        all.to = 0;
         for (Py_ssize_t i = 0; i < grads.size(); ++i) {
             const at::Tensor &t = tensor(grads[i], "grads");
             if ((t.scalar_type() != kBf16 && t.scalar_type() != kF32) || elsewhere(t, on.device) || !t.is_contiguous())
                 throw Refused("grads[" + std::to_string(i) + "]: expected a contiguous CUDA tensor of bfloat16 or float32 on cuda:" + std::to_string(on.device));
             list[i] = {t.data_ptr(), t.data_ptr(), t.numel(), code(t.scalar_type())};
+            all.take(data_of(list[i]));
         }
         if (elsewhere_out) {
             const Sequence out(a[1], "out");
@@ -608,6 +627,7 @@ PyObject *clip(PyObject *, PyObject *const *a, Py_ssize_t n)
             for (Py_ssize_t i = 0; i < grads.size(); ++i) {
                 const at::Tensor &t = THPVariable_Unpack(grads[i]);
                 list[i].out = on.dense(out[i], "out", t.sizes(), t.scalar_type());
+                all.take(out_of(list[i]));
             }
         }
         const float max_norm = clipped ? static_cast<float>(PyFloat_AsDouble(a[2])) : 0.0f, eps = static_cast<float>(PyFloat_AsDouble(a[4]));
@@ -617,6 +637,16 @@ PyObject *clip(PyObject *, PyObject *const *a, Py_ssize_t n)
         void *ws = on.workspace(a[5], need), *st = stream_of(a[6], on.device);
         if (PyErr_Occurred())
             return 0;
+        // Nothing that is written may be read by others meanwhile.  (Each tensor is looked at where one of the two lies among them: 2 us for
+        // 1000, which take 30 otherwise.)
+        const Span used(ws, ws ? need : 0), result(norm, clipped ? sizeof(float) : 0);
+        bool bad = result.meets(used);
+        if (all.meets(used) || all.meets(result))
+            for (const mlp_tensor &t : list)
+                for (const Span &s : {data_of(t), out_of(t)})
+                    bad = bad || s.meets(used) || s.meets(result);
+        if (bad)
+            throw Refused("norm and workspace: one overlaps the other or a tensor of the list");
         const CurrentDevice current(on.device);
         return unlocked([&]() -> int {
             const int64_t count = static_cast<int64_t>(list.size());

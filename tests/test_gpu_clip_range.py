@@ -102,3 +102,19 @@ def test_a_large_eps(mc, dtype):
     for place in PLACES:
         for limit in (1e38, 1.0, 3.4e38):
             expect([t], clip(mc, [t], limit, eps=3.3e38, **place), limit, eps=3.3e38)
+
+
+def test_a_norm_or_a_workspace_within_the_tensors_is_refused(mc):
+    size = mc.clip_workspace_size(2)
+    buf = torch.zeros(size // 4 + 512, device=DEV)
+    a, b, norm, ws = buf[:128], buf[128:256], buf[256:257], buf[512:]
+    mc.clip_gradients([a], 1.0, norm, out=[b], workspace=ws)
+    mc.gradient_norm([a, b], a[:1], workspace=ws)
+    for call in (lambda: mc.clip_gradients([a, b], 1.0, b[127:], workspace=ws), lambda: mc.clip_gradients([a], 1.0, b[:1], out=[b], workspace=ws),
+                 lambda: mc.clip_gradients([a], 1.0, a[7:8], out=[b], workspace=ws), lambda: mc.clip_gradients([a], 1.0, ws[5:6], workspace=ws),
+                 lambda: mc.clip_gradients([a, ws[:1]], 1.0, norm, workspace=ws), lambda: mc.clip_gradients([a], 1.0, norm, out=[ws[64:192]], workspace=ws),
+                 lambda: mc.gradient_norm([ws[100:228]], norm, workspace=ws)):
+        with pytest.raises(ValueError, match="overlaps"):
+            call()
+    torch.cuda.synchronize()
+    assert not buf[:512].any()
