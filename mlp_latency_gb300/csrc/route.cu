@@ -314,7 +314,8 @@ __global__ void __launch_bounds__(N <= 8 ? 1024 : 256) route_few_kernel(const Ro
             most = __reduce_max_sync(kAll, left.first);
         }
         gate = mine >= 0 ? expf(left.value(my_key) - top) : 0.0f;
-        gate = gate / (p.normalize ? warp_sum(gate) : all);
+        const float sum = p.normalize ? warp_sum(gate) : all;
+        gate = mine >= 0 ? gate / sum : 0.0f;   // (the sum may be NaN)
     }
     if (p.loss)
 #pragma unroll

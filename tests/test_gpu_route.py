@@ -289,3 +289,19 @@ def test_logits_past_32_bits(mc):
     mc.route_backward(l.to(DEV), got["experts"], got["offsets"], a, dgates=G)
     mc.route_backward(wide, got["experts"], got["offsets"], wide, dgates=G)
     assert torch.equal(wide, a)
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T,E", [(4, 6), (32, 70), (8, 300), (33, 6), (700, 70), (40, 300)])
+def test_without_a_choice_a_gate_is_zero(mc, T, E, dtype, normalize):
+    """Also next to gates that are NaN, in rows with fewer logits than choices."""
+    l = torch.full((T, E), -INF)
+    l[0, 2], l[1, 3], l[1, 1], l[2, 4] = NAN, INF, 1.0, -INF
+    l[3:] = logits_for(T - 3, E, F32, 1)
+    got = forward(mc, l.to(dtype).to(DEV), 4, normalize=normalize)
+    want = ref.choose(l.to(dtype).double().numpy(), 4, None)
+    assert np.array_equal(got["experts"].cpu().numpy(), want) and list(want[1]) == [3, 1, -1, -1] and list(want[2]) == [-1] * 4
+    gates = got["gates"].cpu()
+    assert not gates[torch.from_numpy(want) < 0].any()
+    assert torch.isnan(gates[0, 0]) and torch.isnan(gates[1]).any() and not torch.isnan(gates[3:]).any()
