@@ -118,3 +118,36 @@ def test_a_norm_or_a_workspace_within_the_tensors_is_refused(mc):
             call()
     torch.cuda.synchronize()
     assert not buf[:512].any()
+
+
+@pytest.mark.parametrize("limit", [0.3, 5.0])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_some_in_place(mc, dtype, limit):
+    """Lists of tensors in place, elsewhere and elsewhere in their words, in turn; the gradients of the last two stay."""
+    for n in (5, 66, 1003):
+        kept = [normal(1 + 977 * (i % 23), dtype, 1.0, i) for i in range(n)]
+        size = sum(t.numel() for t in kept) ** 0.5
+        bufs = [torch.empty(t.numel() + 1, dtype=dtype, device=DEV) for t in kept]
+        src = [b[i % 2:i % 2 + t.numel()] for i, (b, t) in enumerate(zip(bufs, kept))]
+        for s, t in zip(src, kept):
+            s.copy_(t)
+        outs = [torch.zeros(t.numel() + 1, dtype=dtype, device=DEV) for t in kept]
+        out = [s if i % 3 == 0 else o[(i + i // 2) % 2:][:s.numel()] for i, (s, o) in enumerate(zip(src, outs))]
+        norm = torch.empty(1, device=DEV)
+        ws = torch.empty(mc.clip_workspace_size(n), dtype=torch.uint8, device=DEV)
+        mc.clip_gradients(src, limit * size, norm, out=out, eps=0.0, workspace=ws)
+        expect(kept, (float(norm), out), limit * size)
+        for i, (s, t) in enumerate(zip(src, kept)):
+            assert i % 3 == 0 or torch.equal(s.cpu(), t)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [9_000, 10_000_019, 300_000_007])
+def test_long_sums_of_equal_values(mc, n, dtype):
+    """Their roundings all go the same way."""
+    for value in (0.1, 0.7):
+        t = torch.full((n,), value, dtype=dtype, device=DEV)
+        want = float(t[:1].double()) * n ** 0.5
+        norm, ws = torch.empty(1, device=DEV), torch.empty(mc.clip_workspace_size(1), dtype=torch.uint8, device=DEV)
+        mc.gradient_norm([t], norm, workspace=ws)
+        assert abs(float(norm) - want) <= units([t]) * U * want, abs(float(norm) / want - 1) / U
