@@ -424,7 +424,6 @@ int64_t launches_of(int64_t tensors) { return std::max<int64_t>(1, cdiv(tensors,
 
 struct Span {
     uintptr_t lo, hi;
-    int64_t tensor;
     bool out;
 };
 
@@ -449,9 +448,9 @@ bool overlap(int64_t tensors, const mlp_tensor *list)
         const uintptr_t from = reinterpret_cast<uintptr_t>(list[i].data), to = reinterpret_cast<uintptr_t>(list[i].out);
         if (!bytes)
             continue;
-        s[n++] = {to, to + bytes, i, true};
+        s[n++] = {to, to + bytes, true};
         if (from != to)
-            s[n++] = {from, from + bytes, i, false};
+            s[n++] = {from, from + bytes, false};
     }
     std::sort(s, s + n, [](const Span &a, const Span &b) { return a.lo < b.lo; });
     bool bad = false;
