@@ -7,12 +7,13 @@
 // Backward, with g_e = dloss E k counts_e / M^2 (+ dgate at a chosen e, without normalize):
 //   dl = p (g - sum_e g_e p_e) (+ gate (dgate - sum gate dgate) at the chosen ones, with normalize).
 //
-// A few instructions per logit and a table of counts: what bounds it is latency for few tokens (one to 2 of 8 experts 2.5 us, of
-// which an empty launch is 2.3; 2048 in one launch 4.6) and the rate of instructions for many (8192 to 8 of 256, 4.2 MB of logits,
-// 13.6 us: 6.3 million instructions of a warp, some 560 a token of 256 experts, at half the rate of issue; then 2.3 us of the second
-// launch).  A group of lanes takes a token, 8 experts a lane (16 or 32 where there are more than 256), so a warp has up to 32 tokens
-// at a time.  The rows are a counting sort: a warp ranks its tokens' choices, a block adds its warps' counts up, a cluster its
-// blocks', and a second launch the clusters' (none where one cluster has all tokens).
+// A few instructions per logit and a table of counts: what bounds it is latency for few tokens (one to 2 of 8 experts 2.4 us, of
+// which an empty launch is 2.3; 2048 in one launch 4.5) and the rate of instructions for many (8192 to 8 of 256, 4.2 MB of logits,
+// 14.4 us, or 13.5 where the same logits are read again and L2 has them: 6.3 million instructions of a warp, some 560 a token of 256
+// experts, at half the rate of issue; then 2.3 us of the second launch).  A group of lanes takes a token, 8 experts a lane (16 or 32
+// where there are more than 256), so a warp has up to 32 tokens at a time.  The rows are a counting sort: a warp ranks its tokens'
+// choices, a block adds its warps' counts up, a cluster its blocks', and a second launch the clusters' (none where one cluster has all
+// tokens).  The times below are of calls in a row with the same logits.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -28,8 +29,9 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kCluster = 8;           // blocks that add their counts up through each other's shared memory
-// Clusters of a launch: as many as run at a time (of 512 threads with 64 registers two blocks share an SM, with more one).  8192 tokens to 8
-// of 256 experts: 20 clusters 21.0 us, 30 16.8, 32 18.6; 4096 tokens to 8 of 512: 12 18.9, 15 17.6, 18 27.2.
+// Clusters of a launch: as many as run at a time on the one device there is code for (of 512 threads with 64 registers two blocks share
+// an SM, with more one); where fewer ran, the others would come after them.  8192 tokens to 8 of 256 experts: 20 clusters 21.0 us,
+// 30 16.8, 32 18.6; 4096 tokens to 8 of 512: 12 18.9, 15 17.6, 18 27.2.
 constexpr int kMostClusters = 30, kMostWideClusters = 15;
 constexpr int kStageBytes = 48 * 1024;   // a block's choices, kept until their rows are known
 constexpr int kPlaceThreads = 1024;
@@ -268,7 +270,7 @@ __device__ __forceinline__ float group_sum(float v)
 }
 
 // Up to 32 tokens (8 where there are more than 256 experts) in one block, a warp each: which tokens chose an expert is a word, so a row
-// is a count of bits.  All of it is latency: one token to 2 of 8 experts 2.5 us, 32 tokens 3.4 (route_kernel: 4.0 and 4.1).
+// is a count of bits.  All of it is latency: one token to 2 of 8 experts 2.4 us, 32 tokens 3.3 (route_kernel: 4.0 and 4.1).
 template <typename T, int N>
 __global__ void __launch_bounds__(N <= 8 ? 1024 : 256) route_few_kernel(const Route p)
 {
@@ -686,8 +688,9 @@ __device__ __forceinline__ float group_most(float v)   // NaN where there is one
 template <int N>
 constexpr int kGradThreads = N <= 16 ? 256 : 128;
 
-// Lanes have tokens and experts as in route_kernel.  Reads the logits once and writes as much: 16000 x 32 fp32 (4.6 MB) 3.6 us, of
-// which 1.3 are more than an empty launch; 8192 x 256 bf16 7.1, with normalize 9.2: the rate of instructions again.
+// Lanes have tokens and experts as in route_kernel.  Reads the logits once and writes as much: 16000 x 32 fp32 (4.6 MB) 3.6 us (4.0 with
+// other logits each time), of which 1.3 are more than an empty launch; 8192 x 256 bf16 7.1, with normalize 9.2: the rate of instructions
+// again.
 template <typename T, int N, int G, int V>
 __global__ void __launch_bounds__(kGradThreads<N>) route_grad_kernel(const RouteGrad p)
 {
@@ -815,6 +818,8 @@ void forward_as(Route &p, Stream &st)
 {
     constexpr int V = std::min(N, 16 / static_cast<int>(sizeof(T))), kTokens = 32 / G;
     const int most = kRouteThreads<N> / 32;   // warps of a block
+    // Rows of whole vectors, or else one value at a time: 8192 tokens to 8 of 256 bf16 13.5 and 13.9 us, 16384 to 4 of 64 11.1 and 11.4 (of
+    // 60 11.4).
     const bool wide = p.experts % V == 0 && aligned(p.logits, p.ldl, sizeof(T), V * sizeof(T));
     const int64_t units = cdiv(p.tokens, kTokens);   // of a warp's tokens at a time
     int cluster = kCluster;
@@ -877,6 +882,7 @@ template <typename T, int N, int G>
 void backward_as(const RouteGrad &p, Stream &st)
 {
     constexpr int V = std::min(N, 16 / static_cast<int>(sizeof(T)));
+    // (as above: 8192 x 256 bf16 7.1 and 10.0 us, 16384 x 64 3.7 and 6.2, 16384 x 60 5.8)
     const bool wide = p.experts % V == 0 && aligned(p.logits, p.ldl, sizeof(T), V * sizeof(T)) && aligned(p.dlogits, p.ldd, sizeof(T), V * sizeof(T));
     const int64_t blocks = cdiv(p.tokens, 32 / G * (kGradThreads<N> / 32));
     launch(wide ? route_grad_kernel<T, N, G, V> : route_grad_kernel<T, N, G, 1>, static_cast<unsigned>(std::min<int64_t>(blocks, 8 * kSms)),
